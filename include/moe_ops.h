@@ -124,14 +124,13 @@ moe_status moe_unpermute_backward(int32_t dtype, int64_t T, int32_t d, int32_t k
  * gets the scale byte 255 (NaN), so whatever it enters becomes NaN.
  * Two codes a byte, the element of lower index in the low bits.  K is a
  * multiple of 32.  Scale bytes (s + 127) lie in 512-byte tiles of up to 128
- * rows x 4 blocks (ceil(K / 128) tiles side by side along K): row r of the
- * tile, block kb at byte 16*(r%32) + 4*(r/32) + kb%4.
- *   Weights [batch, N, K]: ceil(N / 128) runs of tiles an expert.
- *   Rows [rows, K] in expert order, offsets [G+1] as above: an expert's rows
- *   in blocks of MOE_FP4_TOKENS, each two runs of tiles (128 rows and the
- *   rest); block i of expert g is block offsets[g] / MOE_FP4_TOKENS + g + i.
- * Codes and scales are 128-byte aligned. */
-#define MOE_FP4_TOKENS 224
+ * rows x 4 blocks, ceil(K / 128) tiles side by side along K (a run): row r of
+ * the tile, block kb at byte 16*(r%32) + 4*(r/32) + kb%4.
+ *   Weights [batch, N, K]: ceil(N / 128) runs an expert, expert by expert.
+ *   Rows [rows, K] in expert order, offsets [G+1] as above: rows
+ *   [128 i, 128 i + 128) of expert g are run offsets[g] / 128 + g + i.
+ * The bytes of blocks past K in a row's last tile are read: any but 255 (the
+ * quantisers write 127).  Codes and scales are 128-byte aligned. */
 enum { MOE_ACT_NONE = 0, MOE_ACT_SWIGLU = 1 };
 
 size_t moe_mxfp4_weight_scale_bytes(int64_t batch, int32_t K, int32_t N);

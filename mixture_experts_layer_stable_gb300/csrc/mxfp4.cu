@@ -15,8 +15,6 @@ namespace moe {
 
 namespace {
 
-constexpr int kTok = MOE_FP4_TOKENS;
-
 // Scale exponent of a block with max |v| = amax (finite).
 __device__ __forceinline__ int fp4_scale_exp(float amax) {
   const uint32_t b = __float_as_uint(amax);
@@ -43,11 +41,12 @@ __device__ __forceinline__ float fp4_value(uint32_t c) {
   return (c & 8u) ? -v : v;
 }
 
-// Offset of the scale of row i of expert g (whose rows start at off), block kb.
+// Offset of the scale of row i of expert g (whose rows start at off), block kb:
+// off / 128 + g leaves every expert room for its rows rounded up to 128.
 __host__ __device__ inline size_t fp4_row_scale_at(int64_t off, int g, int64_t i, int kb, int KT) {
-  const int64_t blk = off / kTok + g + i / kTok;
-  const int r = (int)(i % kTok);
-  return ((size_t)(blk * 2 + (r >> 7)) * KT + (kb >> 2)) * 512u + 16 * (r & 31) + 4 * ((r & 127) >> 5) + (kb & 3);
+  const int64_t run = off / 128 + g + i / 128;
+  const int r = (int)(i % 128);
+  return ((size_t)run * KT + (kb >> 2)) * 512u + 16 * (r & 31) + 4 * (r >> 5) + (kb & 3);
 }
 __host__ __device__ inline size_t fp4_weight_scale_at(int64_t e, int n, int kb, int N, int KT) {
   return ((size_t)(e * ((N + 127) / 128) + (n >> 7)) * KT + (kb >> 2)) * 512u + 16 * (n & 31) +
@@ -172,71 +171,305 @@ __global__ void __launch_bounds__(256) dequant_weights_kernel(const uint8_t* __r
   }
 }
 
-// The product on the CUDA cores: tiles of 64 rows x 64 features, a block of K
-// at a time decoded into shared memory, 4 x 4 sums a thread.
-template <typename T>
-__global__ void __launch_bounds__(256) product_simt_kernel(const uint8_t* __restrict__ xq,
-                                                           const uint8_t* __restrict__ xs,
-                                                           const uint8_t* __restrict__ wq,
-                                                           const uint8_t* __restrict__ ws, int64_t rows, int N, int K,
-                                                           int G, const int* __restrict__ off, bool swiglu,
-                                                           T* __restrict__ out, int64_t ldo,
-                                                           int* __restrict__ status) {
-  __shared__ float A[64][33], B[64][33];
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 2) status[threadIdx.x] = 0;
-  const int KT = (K + 127) / 128;
-  const int g = find_group_block(off, G, blockIdx.x, 64);
-  const int64_t o = off ? off[g] : 0, cnt = (off ? off[g + 1] : rows) - o;
-  const int64_t i0 = (blockIdx.x - (o / 64 + g)) * (int64_t)64;
-  if (i0 >= cnt) return;
-  const int n0 = blockIdx.y * 64, tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  float acc[4][4] = {};
-  for (int kb = 0; kb < K / 32; ++kb) {
-    __syncthreads();
-    for (int j = threadIdx.x; j < 64 * 16; j += 256) {
-      const int r = j / 16, c = j % 16;
-      float s = 0.f;
-      uint32_t b = 0;
-      if (i0 + r < cnt) {
-        s = fp4_scale_of(xs[fp4_row_scale_at(o, g, i0 + r, kb, KT)]);
-        b = xq[(o + i0 + r) * (K / 2) + kb * 16 + c];
-      }
-      A[r][2 * c] = fp4_value(b & 15u) * s;
-      A[r][2 * c + 1] = fp4_value(b >> 4) * s;
-      s = 0.f;
-      b = 0;
-      if (n0 + r < N) {
-        s = fp4_scale_of(ws[fp4_weight_scale_at(g, n0 + r, kb, N, KT)]);
-        b = wq[((int64_t)g * N + n0 + r) * (K / 2) + kb * 16 + c];
-      }
-      B[r][2 * c] = fp4_value(b & 15u) * s;
-      B[r][2 * c + 1] = fp4_value(b >> 4) * s;
-    }
-    __syncthreads();
-    for (int c = 0; c < 32; ++c)
+// ------------------------------------------------------------------ the product
+// Warp-specialised, persistent, one CTA per SM: warp 0 issues the copies, one
+// thread of warp 1 the tensor-core instructions, warps 2..5 the epilogue.
+//
+// The weights are the MMA's A operand (M = 128 features) and the rows its B
+// (N = rows of the tile rounded up to 16, at most kMaxTok): the accumulator
+// holds features on TMEM lanes and rows on TMEM columns, so an expert with a
+// few rows costs its weight stream and little else.  A unit of work is (expert,
+// 128 features, tile of rows); a stage of the ring holds 256 elements of K:
+//   weights 128 x 128 B, rows up to 224 x 128 B (both 128-byte swizzled), their
+//   scale tiles (2 x 512 B for the features and for each 128 rows).
+// The stage's scale tiles are copied to TMEM (tcgen05.cp) right before its four
+// MMAs of K = 64, into one of two column sets; the stage that used a set last
+// has completed before it is written again.
+// TMEM: two accumulators of 224 columns, two scale sets of 32.
+constexpr int kThreads4 = 192;
+constexpr int kMaxTok = 224;
+constexpr int kMaxStages = 12;
+constexpr int kWBytes = 128 * 128;      // weights of a stage
+constexpr int kSmem4 = 232448;          // all of an SM's
+constexpr uint32_t kSfCol = 448;        // scale sets: 32 columns each
+
+// D (+)= (A * sfa) (B * sfb): E2M1 operands, a UE8M0 scale per 32 elements, K = 64.
+MOE_DEV void tc_mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+// Instruction descriptor: E2M1 A and B (K-major), UE8M0 scales taken from bytes
+// sf, sf + 1 of a 32-bit scale column (sf 0 or 2).
+MOE_DEV uint32_t idesc_mxf4(int N, int sf) {
+  return ((uint32_t)sf << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
+         ((uint32_t)(128 >> 4) << 24) | ((uint32_t)sf << 29);
+}
+
+struct P4 {
+  const int* off;      // [G+1] or NULL (one segment of `rows`)
+  const uint8_t* xs;
+  const uint8_t* ws;
+  void* out;
+  int64_t ldo;
+  int* status;
+  int rows, G, N, K, NT, KT, stages_k;
+};
+
+// Tiles of an expert's c rows: one of up to kMaxTok, else of up to 192 that start
+// on multiples of 64 (so a tile's scales lie in at most two 128-row tiles, from
+// column 0 or 2 of the first).
+MOE_DEV int tok_tiles(int c) { return c <= kMaxTok ? (c > 0) : (c + 191) / 192; }
+MOE_DEV int tok_start(int c, int tiles, int t) { return (int)((int64_t)t * ((c + 63) / 64) / tiles) * 64; }
+
+struct Unit4 {
+  int e, n, row0, first, nt;  // expert, feature tile, first row of the expert, first row in it, rows
+};
+
+template <typename T, bool SWIGLU>
+__global__ void __launch_bounds__(kThreads4, 1)
+    product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, const P4 p) {
+  extern __shared__ uint8_t smem_raw[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ int s_off[kMaxE + 1];    // first row of each expert
+  __shared__ int s_unit[kMaxE + 1];   // first unit of each expert
+  __shared__ alignas(8) uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2], drain;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort, s_most;
+  if (blockIdx.x == 0 && threadIdx.x < 2) p.status[threadIdx.x] = 0;
+
+  // experts' rows and units
+  for (int i = threadIdx.x; i <= p.G; i += blockDim.x) s_off[i] = p.off ? p.off[i] : (i ? p.rows : 0);
+  __syncthreads();
+  if (warp == 0) {
+    int run = 0, most = 0;
+    for (int base = 0; base < p.G; base += 32) {
+      const int e = base + lane;
+      const int c = e < p.G ? s_off[e + 1] - s_off[e] : 0;
+      const int tt = tok_tiles(c);
+      most = max(most, tt > 1 ? 192 : c);
+      int inc = tt * p.NT;
+      const int mine = inc;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(A[ty * 4 + i][c], B[tx * 4 + j][c], acc[i][j]);
-  }
-  for (int i = 0; i < 4; ++i) {
-    if (i0 + ty * 4 + i >= cnt) break;
-    T* dst = out + (o + i0 + ty * 4 + i) * ldo;
-    const int n = n0 + tx * 4;
-    if (swiglu) {
-      for (int j = 0; j < 4; j += 2)
-        if (n + j < N) dst[(n + j) / 2] = from_f32<T>(silu_f(acc[i][j]) * acc[i][j + 1]);
-    } else {
-      for (int j = 0; j < 4; ++j)
-        if (n + j < N) dst[n + j] = from_f32<T>(acc[i][j]);
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      if (e < p.G) s_unit[e] = run + inc - mine;
+      run += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) {
+      s_unit[p.G] = run;
+      s_most = most;
+      for (int i = 0; i < kMaxStages; ++i) {
+        mbar_init(&full[i], 1);
+        mbar_init(&empty[i], 1);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&tfull[i], 1);
+        mbar_init(&tempty[i], 4);
+      }
+      mbar_init(&drain, 1);
+      s_abort = 0;
+      fence_mbar_init();
+      tma_prefetch_desc(&tm_x);
+      tma_prefetch_desc(&tm_w);
     }
   }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&s_tmem), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  const int total = s_unit[p.G];
+  volatile int* abort_flag = &s_abort;
+
+  // stage layout for the largest tile there is: weights, rows, scales
+  const int cap = (s_most + 31) & ~31;
+  const uint32_t sfb_runs = cap > 128 ? 2 : 1;
+  const uint32_t stage_bytes = (uint32_t)kWBytes + (uint32_t)cap * 128u + 1024u + sfb_runs * 1024u;
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t room = kSmem4 - 16384u - (base - smem_u32(smem_raw));
+  const int S = min(kMaxStages, (int)(room / stage_bytes));
+
+  auto unit_at = [&](int u) {
+    int lo = 0, hi = p.G - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_unit[mid] <= u) lo = mid;
+      else hi = mid - 1;
+    }
+    Unit4 t;
+    t.e = lo;
+    t.row0 = s_off[lo];
+    const int c = s_off[lo + 1] - t.row0, tt = tok_tiles(c), r = u - s_unit[lo];
+    t.n = r / tt;
+    const int i = r - t.n * tt;
+    t.first = tok_start(c, tt, i);
+    t.nt = (i + 1 < tt ? tok_start(c, tt, i + 1) : c) - t.first;
+    return t;
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0, used = 0, last = 0;
+      for (int u = blockIdx.x; u < total; u += gridDim.x) {
+        const Unit4 t = unit_at(u);
+        const int boxes = (t.nt + 31) / 32;
+        const int runs = ((t.first & 127) + t.nt + 127) / 128;
+        const uint8_t* wsp = p.ws + ((size_t)t.e * p.NT + t.n) * p.KT * 512u;
+        const uint8_t* xsp = p.xs + (size_t)(t.row0 / 128 + t.e + t.first / 128) * p.KT * 512u;
+        for (int kb = 0; kb < p.stages_k; ++kb) {
+          if (!mbar_wait(&empty[s], ph ^ 1u, abort_flag, p.status, 1000 + s)) goto produced;
+          const uint32_t sa = base + (uint32_t)s * stage_bytes, sb = sa + kWBytes, sf = sb + (uint32_t)cap * 128u;
+          const uint32_t fb = smem_u32(&full[s]);
+          const uint32_t sfn = 512u * (uint32_t)min(2, p.KT - 2 * kb);
+          mbar_arrive_expect_tx(&full[s], (uint32_t)kWBytes + (uint32_t)boxes * 4096u + sfn * (1u + runs));
+          tma_load_3d(sa, &tm_w, fb, kb * 128, t.n * 128, t.e);
+          bulk_load(sf, wsp + (size_t)kb * 1024u, sfn, fb);
+          for (int i = 0; i < boxes; ++i) tma_load_2d(sb + i * 4096u, &tm_x, fb, kb * 128, t.row0 + t.first + i * 32);
+          for (int i = 0; i < runs; ++i)
+            bulk_load(sf + 1024u * (1 + i), xsp + ((size_t)i * p.KT + 2 * kb) * 512u, sfn, fb);
+          used |= 1u << s;
+          last = (last & ~(1u << s)) | (ph << s);
+          if (++s == S) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+    produced:
+      // every issued copy has landed before the CTA can exit
+      for (int i = 0; i < kMaxStages; ++i)
+        if ((used >> i) & 1u) mbar_wait_drain(&full[i], (last >> i) & 1u);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int s = 0, acc = 0;
+      uint32_t ph = 0, aph = 0, it = 0;
+      int s2 = 0;           // the stage issued two before this one, and its phase
+      uint32_t ph2 = 0;
+      for (int u = blockIdx.x; u < total; u += gridDim.x) {
+        const Unit4 t = unit_at(u);
+        const int n16 = (t.nt + 15) & ~15;
+        const int runs = ((t.first & 127) + t.nt + 127) / 128;
+        const uint32_t shift = (uint32_t)(t.first & 127) / 32u;  // 0 or 2 columns
+        const uint32_t id0 = idesc_mxf4(n16, 0), id2 = idesc_mxf4(n16, 2);
+        if (!mbar_wait(&tempty[acc], aph ^ 1u, abort_flag, p.status, 1100 + acc)) goto issued;
+        tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)acc * kMaxTok;
+        for (int kb = 0; kb < p.stages_k; ++kb, ++it) {
+          if (!mbar_wait(&full[s], ph, abort_flag, p.status, 1200 + s)) goto issued;
+          // the scale columns are free once the stage two back has completed
+          if (it >= 2) {
+            if (!mbar_wait(&empty[s2], ph2, abort_flag, p.status, 1300 + s2)) goto issued;
+            if (++s2 == S) {
+              s2 = 0;
+              ph2 ^= 1u;
+            }
+          }
+          tc_fence_after();
+          const uint32_t sa = base + (uint32_t)s * stage_bytes, sb = sa + kWBytes, sf = sb + (uint32_t)cap * 128u;
+          const uint32_t tsf = tmem + kSfCol + (it & 1u) * 32u;
+          const int tiles = min(2, p.KT - 2 * kb);
+          for (int j = 0; j < tiles; ++j) {
+            tc_cp_32x128b_warpx4(tsf + j * 16u, sdesc_plain(sf + j * 512u, 16, 128));
+            for (int i = 0; i < runs; ++i)
+              tc_cp_32x128b_warpx4(tsf + j * 16u + 8u + i * 4u, sdesc_plain(sf + 1024u * (1 + i) + j * 512u, 16, 128));
+          }
+          const int steps = min(4, (p.K - kb * 256 + 63) / 64);
+          for (int j = 0; j < steps; ++j) {
+            const uint32_t c = tsf + (uint32_t)(j >> 1) * 16u;
+            tc_mma_mxf4(d, sdesc_sw128(sa + j * 32, 16, 1024), sdesc_sw128(sb + j * 32, 16, 1024),
+                        (j & 1) ? id2 : id0, c, c + 8u + shift, (kb > 0 || j > 0) ? 1u : 0u);
+          }
+          tc_commit(smem_u32(&empty[s]));
+          if (++s == S) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        tc_commit(smem_u32(&tfull[acc]));
+        if (++acc == 2) {
+          acc = 0;
+          aph ^= 1u;
+        }
+      }
+    issued:
+      tc_commit(smem_u32(&drain));
+      mbar_wait_drain(&drain, 0);
+    }
+  } else {
+    const int q = warp & 3;  // TMEM lane quarter of this warp
+    int acc = 0;
+    uint32_t aph = 0;
+    T* out = static_cast<T*>(p.out);
+    for (int u = blockIdx.x; u < total; u += gridDim.x) {
+      const Unit4 t = unit_at(u);
+      if (!mbar_wait(&tfull[acc], aph, abort_flag, p.status, 1400 + acc)) break;
+      tc_fence_after();
+      const int n = t.n * 128 + q * 32 + lane;
+      T* dst = out + (int64_t)(t.row0 + t.first) * p.ldo + (SWIGLU ? n >> 1 : n);
+      for (int c0 = 0; c0 < t.nt; c0 += 32) {
+        float v[32];
+        tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kMaxTok + c0), v);
+        if (SWIGLU) {
+          // even lanes hold gates, odd lanes the matching up products: of each
+          // pair of rows an even lane finishes the first, an odd lane the second
+          const bool odd = lane & 1;
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            const float y = __shfl_xor_sync(0xffffffffu, odd ? v[c] : v[c + 1], 1);
+            const float r = odd ? silu_f(y) * v[c + 1] : silu_f(v[c]) * y;
+            const int row = c0 + c + (odd ? 1 : 0);
+            if (row < t.nt && n < p.N) dst[(int64_t)row * p.ldo] = from_f32<T>(r);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (c0 + c < t.nt && n < p.N) dst[(int64_t)(c0 + c) * p.ldo] = from_f32<T>(v[c]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tempty[acc]);
+      if (++acc == 2) {
+        acc = 0;
+        aph ^= 1u;
+      }
+    }
+  }
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
 int grid_for(int64_t n) {
   const int64_t b = (n + 255) / 256;
   return (int)(b < 1 ? 1 : b < (1 << 20) ? b : (1 << 20));
 }
+template <typename T, bool SWIGLU>
+cudaError_t launch_product(const CUtensorMap& tm_x, const CUtensorMap& tm_w, const P4& p, cudaStream_t st) {
+  auto kern = product_kernel<T, SWIGLU>;
+  const int smem = kSmem4 - 12288;  // beside the experts' table and the barriers
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  // units: at most NT for every expert with a row and every 192 rows
+  const int64_t units = (int64_t)p.NT * ((int64_t)p.rows / 192 + (p.G < p.rows ? p.G : p.rows));
+  const int grid = units < num_sms() ? (int)units : num_sms();
+  TraceScope ts("mxfp4_product", st);
+  kern<<<grid, kThreads4, smem, st>>>(tm_x, tm_w, p);
+  return cudaGetLastError();
+}
+
 bool fp4_k(int32_t K) { return K >= 32 && K % 32 == 0 && K <= (1 << 24); }
 bool fp4_weights(int64_t batch, int32_t K, int32_t N) {
   return batch >= 0 && batch <= (1 << 20) && fp4_k(K) && N >= 1 && N <= (1 << 22);
@@ -261,7 +494,7 @@ size_t moe_mxfp4_weight_scale_bytes(int64_t batch, int32_t K, int32_t N) {
 
 size_t moe_mxfp4_row_scale_bytes(int64_t rows, int32_t K, int32_t G) {
   if (!fp4_rows(rows, K, G)) return 0;
-  return (size_t)(rows / kTok + G) * 2 * ((K + 127) / 128) * 512;
+  return (size_t)(rows / 128 + G) * ((K + 127) / 128) * 512;
 }
 
 moe_status moe_quantize_mxfp4(int32_t dtype, const void* w, int64_t batch, int32_t K, int32_t N, int32_t paired,
@@ -348,13 +581,27 @@ moe_status moe_mxfp4_product(int32_t dtype, int64_t rows, int32_t N, int32_t K, 
       !elem_ok(out, dtype_bytes(dtype)) || !elem_ok_or_null(offsets, 4))
     return MOE_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  CUtensorMap tm_x, tm_w;
+  if (!map2d(&tm_x, xq, (uint64_t)K / 2, (uint64_t)rows, 128, 32, true) ||
+      !map3d(&tm_w, wq, (uint64_t)K / 2, (uint64_t)N, (uint64_t)G, 128, 128, true))
+    return MOE_ERR_CUDA;
+  P4 p;
+  p.off = offsets;
+  p.xs = xscales;
+  p.ws = wscales;
+  p.out = out;
+  p.ldo = ldo;
+  p.status = static_cast<int*>(ws);
+  p.rows = (int)rows;
+  p.G = G;
+  p.N = N;
+  p.K = K;
+  p.NT = (N + 127) / 128;
+  p.KT = (K + 127) / 128;
+  p.stages_k = (K + 255) / 256;
   return ops_status(with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
-    TraceScope ts("mxfp4_product", st);
-    product_simt_kernel<T><<<dim3((unsigned)(rows / 64 + G), (N + 63) / 64), 256, 0, st>>>(
-        xq, xscales, wq, wscales, rows, N, K, G, offsets, act == MOE_ACT_SWIGLU, static_cast<T*>(out), ldo,
-        static_cast<int*>(ws));
-    return cudaGetLastError();
+    return act == MOE_ACT_SWIGLU ? launch_product<T, true>(tm_x, tm_w, p, st) : launch_product<T, false>(tm_x, tm_w, p, st);
   }));
 }
 

@@ -18,7 +18,6 @@ from .binding import MOE_ERR_INVALID_ARG, MoeError, _check, _stream, lib as _bas
 MOE_DT_F32 = 0
 MOE_DT_BF16 = 1
 MOE_DT_F16 = 2
-MOE_FP4_TOKENS = 224
 MOE_ACT_NONE = 0
 MOE_ACT_SWIGLU = 1
 

@@ -17,7 +17,6 @@ from ops_util import DT, close, empty_strided, gen, randn, strided
 
 pytestmark = pytest.mark.gpu
 GRID = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6], dtype=torch.float64)
-TOK = ops.MOE_FP4_TOKENS
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -58,9 +57,9 @@ def row_tiles(byte, offsets):
     out = {}
     for g in range(len(offsets) - 1):
         for i in range(offsets[g + 1] - offsets[g]):
-            blk, r = offsets[g] // TOK + g + i // TOK, i % TOK
+            run, r = offsets[g] // 128 + g + i // 128, i % 128
             for kb in range(KT * 4):
-                at = ((blk * 2 + r // 128) * KT + kb // 4) * 512 + 16 * (r % 128 % 32) + 4 * (r % 128 // 32) + kb % 4
+                at = (run * KT + kb // 4) * 512 + 16 * (r % 32) + 4 * (r // 32) + kb % 4
                 assert at not in out
                 out[at] = int(byte[offsets[g] + i, kb]) if kb < nb else 127
     return out
