@@ -5,8 +5,6 @@
 // s is the smallest exponent with max |v| <= 6 * 2^s, so no element saturates:
 // with max |v| = m * 2^q, m in [0.5, 1), 6 * 2^s = 0.75 * 2^(s+3) gives
 // s = q - 3 for m <= 0.75 and q - 2 otherwise.
-#include <cuda_fp4.h>
-
 #include "gemm_common.cuh"
 #include "mx.cuh"
 #include "ops_common.cuh"
@@ -30,15 +28,25 @@ __device__ __forceinline__ float fp4_scale_of(uint32_t byte) {
   return byte == 255 ? __uint_as_float(0x7FFFFFFFu) : byte == 0 ? __uint_as_float(0x400000u)
                                                                : __uint_as_float(byte << 23);
 }
-// Two values as a byte of codes (lower index in the low bits), to nearest, ties to even.
-__device__ __forceinline__ uint32_t fp4_pack2(float lo, float hi) {
-  return __nv_cvt_float2_to_fp4x2(make_float2(lo, hi), __NV_E2M1, cudaRoundNearest);
+// Eight values as 4-bit codes (lowest index in the lowest bits), to nearest, ties to even.
+__device__ __forceinline__ uint32_t fp4_pack8(const float* v) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return r;
 }
-// Value of a 4-bit code: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives.
+// Value of a 4-bit code (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives): codes
+// 2..7 are a two-bit exponent and one mantissa bit, 1 is 0.5.
 __device__ __forceinline__ float fp4_value(uint32_t c) {
   const uint32_t m = c & 7u;
-  const float v = m < 2 ? 0.5f * m : (m & 1u ? 1.5f : 1.0f) * (float)(1u << ((m >> 1) - 1));
-  return (c & 8u) ? -v : v;
+  const uint32_t b = m >= 2 ? (m << 22) + 0x3F000000u : m * 0x3F000000u;
+  return __uint_as_float(b | ((c & 8u) << 28));
 }
 
 // Offset of the scale of row i of expert g (whose rows start at off), block kb:
@@ -53,80 +61,159 @@ __host__ __device__ inline size_t fp4_weight_scale_at(int64_t e, int n, int kb, 
          4 * ((n & 127) >> 5) + (kb & 3);
 }
 
-// Largest g in [0, G) with off[g] / div + g <= key (off NULL: 0).
-__device__ __forceinline__ int find_group_block(const int* off, int G, int key, int div) {
-  if (off == nullptr) return 0;
-  int lo = 0, hi = G - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(off + mid) / div + mid <= key) lo = mid;
-    else hi = mid - 1;
-  }
-  return lo;
-}
-// Expert of row p < off[G]: the largest g with off[g] <= p.
-__device__ __forceinline__ int find_group(const int* off, int G, int p) {
-  return off == nullptr ? 0 : find_expert(off, G, p);
-}
-
 // One block of 32 values: 16 bytes of codes and the scale byte.
-__device__ __forceinline__ uint32_t fp4_quant_block(const float* v, uint8_t* q) {
+__device__ __forceinline__ uint32_t fp4_quant_block(float* v, uint8_t* q) {
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 32; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-  if (m >= 0x7F800000u) {
+  uint4 code = make_uint4(0, 0, 0, 0);
+  uint32_t byte = 255;
+  if (m < 0x7F800000u) {
+    const int s = fp4_scale_exp(__uint_as_float(m));
+    const float f = fp4_inv_scale(s);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) q[i] = 0;
-    return 255u;
+    for (int i = 0; i < 32; ++i) v[i] *= f;
+    code = make_uint4(fp4_pack8(v), fp4_pack8(v + 8), fp4_pack8(v + 16), fp4_pack8(v + 24));
+    byte = (uint32_t)(s + 127);
   }
-  const int s = fp4_scale_exp(__uint_as_float(m));
-  const float f = fp4_inv_scale(s);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) q[i] = (uint8_t)fp4_pack2(v[2 * i] * f, v[2 * i + 1] * f);
-  return (uint32_t)(s + 127);
+  *reinterpret_cast<uint4*>(q) = code;
+  return byte;
 }
 
-// One thread per block of a row, the padding blocks (scale 1) included.
-template <typename T>
+// ------------------------------------------------------------------ rows
+// A warp takes up to kSegPasses passes of 256 elements of one row: every lane 8
+// elements a pass, four lanes a block, half a warp the four blocks that share a
+// word of a scale tile (the padding blocks past K included, scale 1).  All the
+// loads go out before the first is used; the expert lookup runs in their shadow.
+constexpr int kSegPasses = 7;
+
+// Expert of row p: every lane compares 1/32 of the offsets, twice.
+__device__ __forceinline__ int warp_find_group(const int* __restrict__ off, int G, int p, int lane) {
+  if (off == nullptr) return 0;
+  const int stride = (G + 31) >> 5;
+  const int i = lane * stride;
+  const uint32_t b = __ballot_sync(0xffffffffu, i < G && __ldg(off + i) <= p);
+  const int lo = (31 - __clz(b | 1u)) * stride;
+  const bool in = lane < stride && lo + lane < G && __ldg(off + lo + lane) <= p;
+  return lo + 31 - __clz(__ballot_sync(0xffffffffu, in) | 1u);
+}
+
+// 8 elements of a row as loaded: 16 bytes (32 for fp32) when V, else one by one.
+template <typename T, bool V>
+struct Raw8 {
+  Vec<T, V ? 16 / sizeof(T) : 1> e[V ? sizeof(T) / 2 : 8];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(e) / sizeof(e[0])); ++i) e[i] = load_vec<T, V ? 16 / sizeof(T) : 1>(p + i * (V ? 16 / sizeof(T) : 1));
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) reinterpret_cast<T*>(e)[i] = from_f32<T>(0.f);
+  }
+  __device__ __forceinline__ float at(int i) const { return to_f32(reinterpret_cast<const T*>(e)[i]); }
+};
+
+template <typename T, bool V>
 __global__ void __launch_bounds__(256) quant_rows_kernel(const T* __restrict__ x, int64_t ldx, int64_t rows, int K,
                                                          int G, const int* __restrict__ off,
-                                                         const int* __restrict__ perm, int k,
+                                                         const int* __restrict__ perm, int k, int segs, int per,
                                                          uint8_t* __restrict__ q, uint8_t* __restrict__ sc) {
-  const int KT = (K + 127) / 128, nb = KT * 4;
-  const int64_t n = (off ? off[G] : rows) * (int64_t)nb;
-  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t p = i / nb;
-    const int kb = (int)(i % nb);
-    const int g = find_group(off, G, (int)p);
-    const int64_t o = off ? off[g] : 0;
-    uint32_t s = 127;
-    if (kb * 32 < K) {
-      const T* src = x + (perm ? (int64_t)(perm[p] / k) : p) * ldx + kb * 32;
-      float v[32];
-      for (int j = 0; j < 32; ++j) v[j] = to_f32(src[j]);
-      s = fp4_quant_block(v, q + p * (K / 2) + kb * 16);
-    }
-    sc[fp4_row_scale_at(o, g, p - o, kb, KT)] = (uint8_t)s;
+  const int lane = threadIdx.x & 31, KT = (K + 127) / 128;
+  const int64_t w = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5;
+  const int64_t p = w / segs;
+  const int pass0 = (int)(w % segs) * per;
+  if (p >= rows) return;
+  const int64_t src_row = perm ? (int64_t)(__ldg(perm + p) / k) : p;
+  const T* src = x + src_row * ldx;
+  Raw8<T, V> v[kSegPasses];
+#pragma unroll
+  for (int i = 0; i < kSegPasses; ++i) {
+    const int c = (pass0 + i) * 256 + lane * 8;
+    if (i < per && c < K) v[i].load(src + c);
+    else v[i].zero();
+  }
+  if (off != nullptr && p >= __ldg(off + G)) return;
+  const int g = warp_find_group(off, G, (int)p, lane);
+  const int64_t o = off ? __ldg(off + g) : 0;
+#pragma unroll
+  for (int i = 0; i < kSegPasses; ++i) {
+    const int c = (pass0 + i) * 256 + lane * 8;
+    if (i >= per || (pass0 + i) * 2 >= KT) break;
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[i].at(j)) & 0x7FFFFFFFu);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const bool fin = m < 0x7F800000u;
+    const int s = fin ? fp4_scale_exp(__uint_as_float(m)) : 0;
+    const float f = fp4_inv_scale(s);
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = v[i].at(j) * f;
+    const uint32_t code = fp4_pack8(y);
+    if (c < K) *reinterpret_cast<uint32_t*>(q + p * (K / 2) + c / 2) = fin ? code : 0u;
+    uint32_t word = (c < K ? (fin ? (uint32_t)(s + 127) : 255u) : 127u) << (8 * ((lane >> 2) & 3));
+    word |= __shfl_xor_sync(0xffffffffu, word, 4);
+    word |= __shfl_xor_sync(0xffffffffu, word, 8);
+    const int kt = (pass0 + i) * 2 + (lane >> 4);
+    if ((lane & 15) == 0 && kt < KT)
+      *reinterpret_cast<uint32_t*>(sc + fp4_row_scale_at(o, g, p - o, kt * 4, KT)) = word;
   }
 }
 
-template <typename T>
+template <typename T, bool V>
 __global__ void __launch_bounds__(256) dequant_rows_kernel(const uint8_t* __restrict__ q,
                                                            const uint8_t* __restrict__ sc, int64_t rows, int K,
-                                                           int G, const int* __restrict__ off, T* __restrict__ y,
-                                                           int64_t ldy) {
-  const int KT = (K + 127) / 128, h = K / 2;
-  const int64_t n = (off ? off[G] : rows) * (int64_t)h;
-  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t p = i / h;
-    const int c = (int)(i % h);
-    const int g = find_group(off, G, (int)p);
-    const int64_t o = off ? off[g] : 0;
-    const float s = fp4_scale_of(sc[fp4_row_scale_at(o, g, p - o, c / 16, KT)]);
-    const uint32_t b = q[i];
-    y[p * ldy + 2 * c] = from_f32<T>(fp4_value(b & 15u) * s);
-    y[p * ldy + 2 * c + 1] = from_f32<T>(fp4_value(b >> 4) * s);
+                                                           int G, const int* __restrict__ off, int segs, int per,
+                                                           T* __restrict__ y, int64_t ldy) {
+  const int lane = threadIdx.x & 31, KT = (K + 127) / 128;
+  const int64_t w = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5;
+  const int64_t p = w / segs;
+  const int pass0 = (int)(w % segs) * per;
+  if (p >= rows || (off != nullptr && p >= __ldg(off + G))) return;
+  uint32_t code[kSegPasses];
+#pragma unroll
+  for (int i = 0; i < kSegPasses; ++i) {
+    const int c = (pass0 + i) * 256 + lane * 8;
+    code[i] = i < per && c < K ? *reinterpret_cast<const uint32_t*>(q + p * (K / 2) + c / 2) : 0u;
   }
+  const int g = warp_find_group(off, G, (int)p, lane);
+  const int64_t o = off ? __ldg(off + g) : 0;
+  uint32_t sb[kSegPasses];
+#pragma unroll
+  for (int i = 0; i < kSegPasses; ++i) {
+    const int c = (pass0 + i) * 256 + lane * 8;
+    sb[i] = i < per && c < K ? sc[fp4_row_scale_at(o, g, p - o, c / 32, KT)] : 0u;
+  }
+#pragma unroll
+  for (int i = 0; i < kSegPasses; ++i) {
+    const int c = (pass0 + i) * 256 + lane * 8;
+    if (i >= per || c >= K) break;
+    const float s = fp4_scale_of(sb[i]);
+    constexpr int W = V ? 16 / sizeof(T) : 1;
+    Vec<T, W> o8[8 / W];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      reinterpret_cast<T*>(o8)[j] = from_f32<T>(fp4_value((code[i] >> (4 * j)) & 15u) * s);
+#pragma unroll
+    for (int j = 0; j < 8 / W; ++j) store_vec<T, W>(y + p * ldy + c + j * W, o8[j]);
+  }
+}
+
+// Segments of a row, and passes of each.
+struct Segs {
+  int n, per;
+};
+Segs row_segs(int K) {
+  const int passes = (K + 255) / 256;
+  Segs s;
+  s.n = (passes + kSegPasses - 1) / kSegPasses;
+  s.per = (passes + s.n - 1) / s.n;
+  return s;
+}
+// Rows whose 8-element groups are 16-byte aligned.
+bool rows16(const void* p, int64_t ld, int dt) {
+  return aligned_to(p, 16) && ld * (int64_t)dtype_bytes(dt) % 16 == 0;
 }
 
 // Column of w that row n of the codes holds.
@@ -183,15 +270,16 @@ __global__ void __launch_bounds__(256) dequant_weights_kernel(const uint8_t* __r
 //   weights 128 x 128 B, rows up to 224 x 128 B (both 128-byte swizzled), their
 //   scale tiles (2 x 512 B for the features and for each 128 rows).
 // The stage's scale tiles are copied to TMEM (tcgen05.cp) right before its four
-// MMAs of K = 64, into one of two column sets; the stage that used a set last
+// MMAs of K = 64, into one of `sets` column sets; the stage that used a set last
 // has completed before it is written again.
-// TMEM: two accumulators of 224 columns, two scale sets of 32.
+// TMEM: two accumulators as wide as the largest tile of rows (at most 224
+// columns), then scale sets of 32 columns: two beside the widest accumulators, one
+// for every stage where tiles are narrow.
 constexpr int kThreads4 = 192;
 constexpr int kMaxTok = 224;
 constexpr int kMaxStages = 12;
 constexpr int kWBytes = 128 * 128;      // weights of a stage
 constexpr int kSmem4 = 232448;          // all of an SM's
-constexpr uint32_t kSfCol = 448;        // scale sets: 32 columns each
 
 // D (+)= (A * sfa) (B * sfb): E2M1 operands, a UE8M0 scale per 32 elements, K = 64.
 MOE_DEV void tc_mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
@@ -209,6 +297,19 @@ MOE_DEV uint32_t idesc_mxf4(int N, int sf) {
   return ((uint32_t)sf << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
          ((uint32_t)(128 >> 4) << 24) | ((uint32_t)sf << 29);
 }
+
+// One lane of a converged warp.
+MOE_DEV bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+// The same value in every lane, known to be so.
+MOE_DEV int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 struct P4 {
   const int* off;      // [G+1] or NULL (one segment of `rows`)
@@ -234,7 +335,7 @@ template <typename T, bool SWIGLU>
 __global__ void __launch_bounds__(kThreads4, 1)
     product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, const P4 p) {
   extern __shared__ uint8_t smem_raw[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   __shared__ int s_off[kMaxE + 1];    // first row of each expert
   __shared__ int s_unit[kMaxE + 1];   // first unit of each expert
   __shared__ alignas(8) uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2], drain;
@@ -288,17 +389,18 @@ __global__ void __launch_bounds__(kThreads4, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem;
-  const int total = s_unit[p.G];
+  const uint32_t tmem = (uint32_t)uniform((int)s_tmem);
+  const int total = uniform(s_unit[p.G]);
   volatile int* abort_flag = &s_abort;
 
   // stage layout for the largest tile there is: weights, rows, scales
-  const int cap = (s_most + 31) & ~31;
+  const int cap = uniform((s_most + 31) & ~31);
   const uint32_t sfb_runs = cap > 128 ? 2 : 1;
   const uint32_t stage_bytes = (uint32_t)kWBytes + (uint32_t)cap * 128u + 1024u + sfb_runs * 1024u;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t room = kSmem4 - 16384u - (base - smem_u32(smem_raw));
   const int S = min(kMaxStages, (int)(room / stage_bytes));
+  const int sets = min(S, (512 - 2 * cap) / 32);
 
   auto unit_at = [&](int u) {
     int lo = 0, hi = p.G - 1;
@@ -307,10 +409,11 @@ __global__ void __launch_bounds__(kThreads4, 1)
       if (s_unit[mid] <= u) lo = mid;
       else hi = mid - 1;
     }
+    lo = uniform(lo);
     Unit4 t;
     t.e = lo;
-    t.row0 = s_off[lo];
-    const int c = s_off[lo + 1] - t.row0, tt = tok_tiles(c), r = u - s_unit[lo];
+    t.row0 = uniform(s_off[lo]);
+    const int c = uniform(s_off[lo + 1]) - t.row0, tt = tok_tiles(c), r = u - uniform(s_unit[lo]);
     t.n = r / tt;
     const int i = r - t.n * tt;
     t.first = tok_start(c, tt, i);
@@ -318,96 +421,108 @@ __global__ void __launch_bounds__(kThreads4, 1)
     return t;
   };
 
+  // The copy and MMA warps run their loops in all lanes, so that addresses and
+  // descriptors are warp-uniform values (they live in uniform registers, which
+  // those instructions take); one elected lane issues.
+  const bool leader = warp < 2 && elect_one();
+  auto wait_all = [&](uint64_t* bar, uint32_t parity, int where) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.status, where));
+  };
   if (warp == 0) {
-    if (lane == 0) {
-      int s = 0;
-      uint32_t ph = 0, used = 0, last = 0;
-      for (int u = blockIdx.x; u < total; u += gridDim.x) {
-        const Unit4 t = unit_at(u);
-        const int boxes = (t.nt + 31) / 32;
-        const int runs = ((t.first & 127) + t.nt + 127) / 128;
-        const uint8_t* wsp = p.ws + ((size_t)t.e * p.NT + t.n) * p.KT * 512u;
-        const uint8_t* xsp = p.xs + (size_t)(t.row0 / 128 + t.e + t.first / 128) * p.KT * 512u;
-        for (int kb = 0; kb < p.stages_k; ++kb) {
-          if (!mbar_wait(&empty[s], ph ^ 1u, abort_flag, p.status, 1000 + s)) goto produced;
-          const uint32_t sa = base + (uint32_t)s * stage_bytes, sb = sa + kWBytes, sf = sb + (uint32_t)cap * 128u;
-          const uint32_t fb = smem_u32(&full[s]);
-          const uint32_t sfn = 512u * (uint32_t)min(2, p.KT - 2 * kb);
+    int s = 0;
+    uint32_t ph = 0, used = 0, last = 0;
+    for (int u = blockIdx.x; u < total; u += gridDim.x) {
+      const Unit4 t = unit_at(u);
+      const int boxes = (t.nt + 31) / 32;
+      const int runs = ((t.first & 127) + t.nt + 127) / 128;
+      const uint8_t* wsp = p.ws + ((size_t)t.e * p.NT + t.n) * p.KT * 512u;
+      const uint8_t* xsp = p.xs + (size_t)(t.row0 / 128 + t.e + t.first / 128) * p.KT * 512u;
+      for (int kb = 0; kb < p.stages_k; ++kb) {
+        if (!wait_all(&empty[s], ph ^ 1u, 1000 + s)) goto produced;
+        const uint32_t sa = base + (uint32_t)s * stage_bytes, sb = sa + kWBytes, sf = sb + (uint32_t)cap * 128u;
+        const uint32_t fb = smem_u32(&full[s]);
+        const uint32_t sfn = 512u * (uint32_t)min(2, p.KT - 2 * kb);
+        if (leader) {
           mbar_arrive_expect_tx(&full[s], (uint32_t)kWBytes + (uint32_t)boxes * 4096u + sfn * (1u + runs));
           tma_load_3d(sa, &tm_w, fb, kb * 128, t.n * 128, t.e);
           bulk_load(sf, wsp + (size_t)kb * 1024u, sfn, fb);
           for (int i = 0; i < boxes; ++i) tma_load_2d(sb + i * 4096u, &tm_x, fb, kb * 128, t.row0 + t.first + i * 32);
           for (int i = 0; i < runs; ++i)
             bulk_load(sf + 1024u * (1 + i), xsp + ((size_t)i * p.KT + 2 * kb) * 512u, sfn, fb);
-          used |= 1u << s;
-          last = (last & ~(1u << s)) | (ph << s);
-          if (++s == S) {
-            s = 0;
-            ph ^= 1u;
-          }
+        }
+        __syncwarp();
+        used |= 1u << s;
+        last = (last & ~(1u << s)) | (ph << s);
+        if (++s == S) {
+          s = 0;
+          ph ^= 1u;
         }
       }
-    produced:
-      // every issued copy has landed before the CTA can exit
-      for (int i = 0; i < kMaxStages; ++i)
-        if ((used >> i) & 1u) mbar_wait_drain(&full[i], (last >> i) & 1u);
     }
+  produced:
+    // every issued copy has landed before the CTA can exit
+    for (int i = 0; i < kMaxStages; ++i)
+      if ((used >> i) & 1u) mbar_wait_drain(&full[i], (last >> i) & 1u);
   } else if (warp == 1) {
-    if (lane == 0) {
-      int s = 0, acc = 0;
-      uint32_t ph = 0, aph = 0, it = 0;
-      int s2 = 0;           // the stage issued two before this one, and its phase
-      uint32_t ph2 = 0;
-      for (int u = blockIdx.x; u < total; u += gridDim.x) {
-        const Unit4 t = unit_at(u);
-        const int n16 = (t.nt + 15) & ~15;
-        const int runs = ((t.first & 127) + t.nt + 127) / 128;
-        const uint32_t shift = (uint32_t)(t.first & 127) / 32u;  // 0 or 2 columns
-        const uint32_t id0 = idesc_mxf4(n16, 0), id2 = idesc_mxf4(n16, 2);
-        if (!mbar_wait(&tempty[acc], aph ^ 1u, abort_flag, p.status, 1100 + acc)) goto issued;
+    int s = 0, acc = 0;
+    uint32_t ph = 0, aph = 0, ph2 = 0;
+    int set = 0, it = 0, s2 = 0;  // s2, ph2: the stage issued `sets` before this one
+    for (int u = blockIdx.x; u < total; u += gridDim.x) {
+      const Unit4 t = unit_at(u);
+      const int n16 = (t.nt + 15) & ~15;
+      const int runs = ((t.first & 127) + t.nt + 127) / 128;
+      const uint32_t shift = (uint32_t)(t.first & 127) / 32u;  // 0 or 2 columns
+      const uint32_t id0 = idesc_mxf4(n16, 0), id2 = idesc_mxf4(n16, 2);
+      if (!wait_all(&tempty[acc], aph ^ 1u, 1100 + acc)) goto issued;
+      tc_fence_after();
+      const uint32_t d = tmem + (uint32_t)(acc * cap);
+      for (int kb = 0; kb < p.stages_k; ++kb, ++it) {
+        if (!wait_all(&full[s], ph, 1200 + s)) goto issued;
+        // the scale columns are free once the stage that used them has
+        // completed (with a set for every stage its refill has shown that)
+        if (sets < S && it >= sets) {
+          if (!wait_all(&empty[s2], ph2, 1300 + s2)) goto issued;
+          if (++s2 == S) {
+            s2 = 0;
+            ph2 ^= 1u;
+          }
+        }
         tc_fence_after();
-        const uint32_t d = tmem + (uint32_t)acc * kMaxTok;
-        for (int kb = 0; kb < p.stages_k; ++kb, ++it) {
-          if (!mbar_wait(&full[s], ph, abort_flag, p.status, 1200 + s)) goto issued;
-          // the scale columns are free once the stage two back has completed
-          if (it >= 2) {
-            if (!mbar_wait(&empty[s2], ph2, abort_flag, p.status, 1300 + s2)) goto issued;
-            if (++s2 == S) {
-              s2 = 0;
-              ph2 ^= 1u;
-            }
-          }
-          tc_fence_after();
-          const uint32_t sa = base + (uint32_t)s * stage_bytes, sb = sa + kWBytes, sf = sb + (uint32_t)cap * 128u;
-          const uint32_t tsf = tmem + kSfCol + (it & 1u) * 32u;
-          const int tiles = min(2, p.KT - 2 * kb);
+        const uint32_t sa = base + (uint32_t)s * stage_bytes, sb = sa + kWBytes, sf = sb + (uint32_t)cap * 128u;
+        const uint32_t tsf = tmem + 2u * (uint32_t)cap + (uint32_t)set * 32u;
+        const uint64_t da = sdesc_sw128(sa, 16, 1024), db = sdesc_sw128(sb, 16, 1024), dsf = sdesc_plain(sf, 16, 128);
+        const int tiles = min(2, p.KT - 2 * kb);
+        const int steps = min(4, (p.K - kb * 256 + 63) / 64);
+        if (leader) {
+          // descriptors advance in units of 16 bytes
           for (int j = 0; j < tiles; ++j) {
-            tc_cp_32x128b_warpx4(tsf + j * 16u, sdesc_plain(sf + j * 512u, 16, 128));
-            for (int i = 0; i < runs; ++i)
-              tc_cp_32x128b_warpx4(tsf + j * 16u + 8u + i * 4u, sdesc_plain(sf + 1024u * (1 + i) + j * 512u, 16, 128));
+            tc_cp_32x128b_warpx4(tsf + j * 16u, dsf + j * 32u);
+            for (int i = 0; i < runs; ++i) tc_cp_32x128b_warpx4(tsf + j * 16u + 8u + i * 4u, dsf + 64u * (1 + i) + j * 32u);
           }
-          const int steps = min(4, (p.K - kb * 256 + 63) / 64);
           for (int j = 0; j < steps; ++j) {
             const uint32_t c = tsf + (uint32_t)(j >> 1) * 16u;
-            tc_mma_mxf4(d, sdesc_sw128(sa + j * 32, 16, 1024), sdesc_sw128(sb + j * 32, 16, 1024),
-                        (j & 1) ? id2 : id0, c, c + 8u + shift, (kb > 0 || j > 0) ? 1u : 0u);
+            tc_mma_mxf4(d, da + j * 2u, db + j * 2u, (j & 1) ? id2 : id0, c, c + 8u + shift, (kb > 0 || j > 0) ? 1u : 0u);
           }
           tc_commit(smem_u32(&empty[s]));
-          if (++s == S) {
-            s = 0;
-            ph ^= 1u;
-          }
         }
-        tc_commit(smem_u32(&tfull[acc]));
-        if (++acc == 2) {
-          acc = 0;
-          aph ^= 1u;
+        __syncwarp();
+        if (++set == sets) set = 0;
+        if (++s == S) {
+          s = 0;
+          ph ^= 1u;
         }
       }
-    issued:
-      tc_commit(smem_u32(&drain));
-      mbar_wait_drain(&drain, 0);
+      if (leader) tc_commit(smem_u32(&tfull[acc]));
+      __syncwarp();
+      if (++acc == 2) {
+        acc = 0;
+        aph ^= 1u;
+      }
     }
+  issued:
+    if (leader) tc_commit(smem_u32(&drain));
+    __syncwarp();
+    mbar_wait_drain(&drain, 0);
   } else {
     const int q = warp & 3;  // TMEM lane quarter of this warp
     int acc = 0;
@@ -421,7 +536,7 @@ __global__ void __launch_bounds__(kThreads4, 1)
       T* dst = out + (int64_t)(t.row0 + t.first) * p.ldo + (SWIGLU ? n >> 1 : n);
       for (int c0 = 0; c0 < t.nt; c0 += 32) {
         float v[32];
-        tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kMaxTok + c0), v);
+        tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * cap + c0), v);
         if (SWIGLU) {
           // even lanes hold gates, odd lanes the matching up products: of each
           // pair of rows an even lane finishes the first, an odd lane the second
@@ -540,8 +655,10 @@ moe_status moe_quantize_mxfp4_rows(int32_t dtype, int64_t rows, int32_t K, const
   return ops_status(with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
     TraceScope ts("quantize_mxfp4_rows", st);
-    quant_rows_kernel<T><<<grid_for(rows * ((K + 127) / 128) * 4), 256, 0, st>>>(
-        static_cast<const T*>(x), ldx, rows, K, G, offsets, perm, k, q, scales);
+    const Segs sg = row_segs(K);
+    const unsigned grid = (unsigned)((rows * sg.n + 7) / 8);
+    auto kern = rows16(x, ldx, dtype) ? quant_rows_kernel<T, true> : quant_rows_kernel<T, false>;
+    kern<<<grid, 256, 0, st>>>(static_cast<const T*>(x), ldx, rows, K, G, offsets, perm, k, sg.n, sg.per, q, scales);
     return cudaGetLastError();
   }));
 }
@@ -557,8 +674,10 @@ moe_status moe_dequantize_mxfp4_rows(int32_t dtype, int64_t rows, int32_t K, con
   return ops_status(with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
     TraceScope ts("dequantize_mxfp4_rows", st);
-    dequant_rows_kernel<T><<<grid_for(rows * (K / 2)), 256, 0, st>>>(q, scales, rows, K, G, offsets,
-                                                                      static_cast<T*>(y), ldy);
+    const Segs sg = row_segs(K);
+    const unsigned grid = (unsigned)((rows * sg.n + 7) / 8);
+    auto kern = rows16(y, ldy, dtype) ? dequant_rows_kernel<T, true> : dequant_rows_kernel<T, false>;
+    kern<<<grid, 256, 0, st>>>(q, scales, rows, K, G, offsets, sg.n, sg.per, static_cast<T*>(y), ldy);
     return cudaGetLastError();
   }));
 }
