@@ -333,7 +333,8 @@ struct Unit4 {
 
 template <typename T, bool SWIGLU>
 __global__ void __launch_bounds__(kThreads4, 1)
-    product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, const P4 p) {
+    product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_x128,
+                   const __grid_constant__ CUtensorMap tm_w, const P4 p) {
   extern __shared__ uint8_t smem_raw[];
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   __shared__ int s_off[kMaxE + 1];    // first row of each expert
@@ -435,6 +436,7 @@ __global__ void __launch_bounds__(kThreads4, 1)
       const Unit4 t = unit_at(u);
       const int boxes = (t.nt + 31) / 32;
       const int runs = ((t.first & 127) + t.nt + 127) / 128;
+      const int row = t.row0 + t.first;
       const uint8_t* wsp = p.ws + ((size_t)t.e * p.NT + t.n) * p.KT * 512u;
       const uint8_t* xsp = p.xs + (size_t)(t.row0 / 128 + t.e + t.first / 128) * p.KT * 512u;
       for (int kb = 0; kb < p.stages_k; ++kb) {
@@ -446,9 +448,14 @@ __global__ void __launch_bounds__(kThreads4, 1)
           mbar_arrive_expect_tx(&full[s], (uint32_t)kWBytes + (uint32_t)boxes * 4096u + sfn * (1u + runs));
           tma_load_3d(sa, &tm_w, fb, kb * 128, t.n * 128, t.e);
           bulk_load(sf, wsp + (size_t)kb * 1024u, sfn, fb);
-          for (int i = 0; i < boxes; ++i) tma_load_2d(sb + i * 4096u, &tm_x, fb, kb * 128, t.row0 + t.first + i * 32);
-          for (int i = 0; i < runs; ++i)
-            bulk_load(sf + 1024u * (1 + i), xsp + ((size_t)i * p.KT + 2 * kb) * 512u, sfn, fb);
+          int i = 0;  // rows in boxes of 128, the rest in boxes of 32
+          if (boxes >= 4) {
+            tma_load_2d(sb, &tm_x128, fb, kb * 128, row);
+            i = 4;
+          }
+          for (; i < boxes; ++i) tma_load_2d(sb + i * 4096u, &tm_x, fb, kb * 128, row + i * 32);
+          bulk_load(sf + 1024u, xsp + (size_t)kb * 1024u, sfn, fb);
+          if (runs > 1) bulk_load(sf + 2048u, xsp + (size_t)p.KT * 512u + (size_t)kb * 1024u, sfn, fb);
         }
         __syncwarp();
         used |= 1u << s;
@@ -491,17 +498,29 @@ __global__ void __launch_bounds__(kThreads4, 1)
         const uint32_t sa = base + (uint32_t)s * stage_bytes, sb = sa + kWBytes, sf = sb + (uint32_t)cap * 128u;
         const uint32_t tsf = tmem + 2u * (uint32_t)cap + (uint32_t)set * 32u;
         const uint64_t da = sdesc_sw128(sa, 16, 1024), db = sdesc_sw128(sb, 16, 1024), dsf = sdesc_plain(sf, 16, 128);
-        const int tiles = min(2, p.KT - 2 * kb);
         const int steps = min(4, (p.K - kb * 256 + 63) / 64);
         if (leader) {
           // descriptors advance in units of 16 bytes
-          for (int j = 0; j < tiles; ++j) {
+          auto scales = [&](int j) {
             tc_cp_32x128b_warpx4(tsf + j * 16u, dsf + j * 32u);
-            for (int i = 0; i < runs; ++i) tc_cp_32x128b_warpx4(tsf + j * 16u + 8u + i * 4u, dsf + 64u * (1 + i) + j * 32u);
-          }
-          for (int j = 0; j < steps; ++j) {
+            tc_cp_32x128b_warpx4(tsf + j * 16u + 8u, dsf + 64u + j * 32u);
+            if (runs > 1) tc_cp_32x128b_warpx4(tsf + j * 16u + 12u, dsf + 128u + j * 32u);
+          };
+          auto mma = [&](int j) {
             const uint32_t c = tsf + (uint32_t)(j >> 1) * 16u;
             tc_mma_mxf4(d, da + j * 2u, db + j * 2u, (j & 1) ? id2 : id0, c, c + 8u + shift, (kb > 0 || j > 0) ? 1u : 0u);
+          };
+          if (steps == 4) {  // straight-line: a loop costs as much again per instruction
+            scales(0);
+            scales(1);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mma(j);
+          } else {
+            scales(0);
+            if (steps > 2) scales(1);
+            mma(0);
+            if (steps > 1) mma(1);
+            if (steps > 2) mma(2);
           }
           tc_commit(smem_u32(&empty[s]));
         }
@@ -572,7 +591,7 @@ int grid_for(int64_t n) {
   return (int)(b < 1 ? 1 : b < (1 << 20) ? b : (1 << 20));
 }
 template <typename T, bool SWIGLU>
-cudaError_t launch_product(const CUtensorMap& tm_x, const CUtensorMap& tm_w, const P4& p, cudaStream_t st) {
+cudaError_t launch_product(const CUtensorMap& tm_x, const CUtensorMap& tm_x128, const CUtensorMap& tm_w, const P4& p, cudaStream_t st) {
   auto kern = product_kernel<T, SWIGLU>;
   const int smem = kSmem4 - 12288;  // beside the experts' table and the barriers
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -581,7 +600,7 @@ cudaError_t launch_product(const CUtensorMap& tm_x, const CUtensorMap& tm_w, con
   const int64_t units = (int64_t)p.NT * ((int64_t)p.rows / 192 + (p.G < p.rows ? p.G : p.rows));
   const int grid = units < num_sms() ? (int)units : num_sms();
   TraceScope ts("mxfp4_product", st);
-  kern<<<grid, kThreads4, smem, st>>>(tm_x, tm_w, p);
+  kern<<<grid, kThreads4, smem, st>>>(tm_x, tm_x128, tm_w, p);
   return cudaGetLastError();
 }
 
@@ -700,8 +719,9 @@ moe_status moe_mxfp4_product(int32_t dtype, int64_t rows, int32_t N, int32_t K, 
       !elem_ok(out, dtype_bytes(dtype)) || !elem_ok_or_null(offsets, 4))
     return MOE_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  CUtensorMap tm_x, tm_w;
+  CUtensorMap tm_x, tm_x128, tm_w;
   if (!map2d(&tm_x, xq, (uint64_t)K / 2, (uint64_t)rows, 128, 32, true) ||
+      !map2d(&tm_x128, xq, (uint64_t)K / 2, (uint64_t)rows, 128, 128, true) ||
       !map3d(&tm_w, wq, (uint64_t)K / 2, (uint64_t)N, (uint64_t)G, 128, 128, true))
     return MOE_ERR_CUDA;
   P4 p;
@@ -720,7 +740,7 @@ moe_status moe_mxfp4_product(int32_t dtype, int64_t rows, int32_t N, int32_t K, 
   p.stages_k = (K + 255) / 256;
   return ops_status(with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
-    return act == MOE_ACT_SWIGLU ? launch_product<T, true>(tm_x, tm_w, p, st) : launch_product<T, false>(tm_x, tm_w, p, st);
+    return act == MOE_ACT_SWIGLU ? launch_product<T, true>(tm_x, tm_x128, tm_w, p, st) : launch_product<T, false>(tm_x, tm_x128, tm_w, p, st);
   }));
 }
 
