@@ -81,13 +81,7 @@ __device__ __forceinline__ uint32_t fp4_quant_block(float* v, uint8_t* q) {
 }
 
 // ------------------------------------------------------------------ rows
-// A warp takes up to kSegPasses passes of 256 elements of one row: every lane 8
-// elements a pass, four lanes a block, half a warp the four blocks that share a
-// word of a scale tile (the padding blocks past K included, scale 1).  All the
-// loads go out before the first is used; the expert lookup runs in their shadow.
-constexpr int kSegPasses = 7;
-
-// Expert of row p: every lane compares 1/32 of the offsets, twice.
+// Expert of row p, the same in every lane: each compares 1/32 of the offsets, twice.
 __device__ __forceinline__ int warp_find_group(const int* __restrict__ off, int G, int p, int lane) {
   if (off == nullptr) return 0;
   const int stride = (G + 31) >> 5;
@@ -98,68 +92,92 @@ __device__ __forceinline__ int warp_find_group(const int* __restrict__ off, int 
   return lo + 31 - __clz(__ballot_sync(0xffffffffu, in) | 1u);
 }
 
-// 8 elements of a row as loaded: 16 bytes (32 for fp32) when V, else one by one.
+// A block of 32 elements as loaded: 16 bytes at a time when V, else one by one.
 template <typename T, bool V>
-struct Raw8 {
-  Vec<T, V ? 16 / sizeof(T) : 1> e[V ? sizeof(T) / 2 : 8];
+struct Block32 {
+  static constexpr int W = V ? 16 / sizeof(T) : 1;
+  Vec<T, W> e[32 / W];
   __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-    for (int i = 0; i < (int)(sizeof(e) / sizeof(e[0])); ++i) e[i] = load_vec<T, V ? 16 / sizeof(T) : 1>(p + i * (V ? 16 / sizeof(T) : 1));
+    for (int i = 0; i < 32 / W; ++i) e[i] = load_vec<T, W>(p + i * W);
   }
-  __device__ __forceinline__ void zero() {
+  __device__ __forceinline__ float at(int i) const { return to_f32(e[i / W].e[i % W]); }
+  // Bits of the largest magnitude as fp32 (of a NaN or infinity: 0x7F800000 or more).
+  __device__ __forceinline__ uint32_t max_bits() const {
+    uint32_t m = 0;
+    if constexpr (V && sizeof(T) == 2) {
+      // magnitudes order as their bits do: 16-bit integer maxima, two at a time
+      const uint32_t* u = reinterpret_cast<const uint32_t*>(e);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) reinterpret_cast<T*>(e)[i] = from_f32<T>(0.f);
+      for (int i = 0; i < 16; ++i) m = __vmaxu2(m, u[i] & 0x7FFF7FFFu);
+      const uint16_t h = (uint16_t)max(m & 0xFFFFu, m >> 16);
+      return __float_as_uint(to_f32(*reinterpret_cast<const T*>(&h)));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) m = max(m, __float_as_uint(at(i)) & 0x7FFFFFFFu);
+      return m;
+    }
   }
-  __device__ __forceinline__ float at(int i) const { return to_f32(reinterpret_cast<const T*>(e)[i]); }
 };
 
+// One lane a block (the blocks that pad a row's last scale tile included, scale 1):
+// the block's maximum needs no exchange, its codes leave as 16 bytes, and four lanes
+// join their scale bytes into a word of the tile.
 template <typename T, bool V>
 __global__ void __launch_bounds__(256) quant_rows_kernel(const T* __restrict__ x, int64_t ldx, int64_t rows, int K,
                                                          int G, const int* __restrict__ off,
-                                                         const int* __restrict__ perm, int k, int segs, int per,
-                                                         uint8_t* __restrict__ q, uint8_t* __restrict__ sc) {
-  const int lane = threadIdx.x & 31, KT = (K + 127) / 128;
-  const int64_t w = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5;
-  const int64_t p = w / segs;
-  const int pass0 = (int)(w % segs) * per;
-  if (p >= rows) return;
-  const int64_t src_row = perm ? (int64_t)(__ldg(perm + p) / k) : p;
-  const T* src = x + src_row * ldx;
-  Raw8<T, V> v[kSegPasses];
-#pragma unroll
-  for (int i = 0; i < kSegPasses; ++i) {
-    const int c = (pass0 + i) * 256 + lane * 8;
-    if (i < per && c < K) v[i].load(src + c);
-    else v[i].zero();
-  }
-  if (off != nullptr && p >= __ldg(off + G)) return;
-  const int g = warp_find_group(off, G, (int)p, lane);
+                                                         const int* __restrict__ perm, int k, uint8_t* __restrict__ q,
+                                                         uint8_t* __restrict__ sc) {
+  const int lane = threadIdx.x & 31, KT = (K + 127) / 128, nb = KT * 4;
+  const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+  const int64_t first = i - lane;                  // the warp's first block
+  if (first >= rows * nb) return;
+  const int64_t p = min(rows - 1, i / nb);
+  const int kb = (int)(i - p * nb);                // past the last row: beyond nb
+  const bool in = kb * 32 < K;
+  Block32<T, V> v;
+  if (in) v.load(x + (perm ? (int64_t)(__ldg(perm + p) / k) : p) * ldx + kb * 32);
+  int g;
+  if (first / nb == min(rows - 1, (first + 31) / nb)) g = warp_find_group(off, G, (int)p, lane);
+  else g = off ? find_expert(off, G, (int)p) : 0;
   const int64_t o = off ? __ldg(off + g) : 0;
-#pragma unroll
-  for (int i = 0; i < kSegPasses; ++i) {
-    const int c = (pass0 + i) * 256 + lane * 8;
-    if (i >= per || (pass0 + i) * 2 >= KT) break;
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[i].at(j)) & 0x7FFFFFFFu);
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const bool fin = m < 0x7F800000u;
-    const int s = fin ? fp4_scale_exp(__uint_as_float(m)) : 0;
+  const bool live = kb < nb && (off == nullptr || p < __ldg(off + G));
+  uint32_t byte = 127;
+  if (in && live) {
+    const uint32_t m = v.max_bits();
+    const int s = m < 0x7F800000u ? fp4_scale_exp(__uint_as_float(m)) : 0;
     const float f = fp4_inv_scale(s);
-    float y[8];
+    byte = m < 0x7F800000u ? (uint32_t)(s + 127) : 255u;
+    uint32_t c[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = v[i].at(j) * f;
-    const uint32_t code = fp4_pack8(y);
-    if (c < K) *reinterpret_cast<uint32_t*>(q + p * (K / 2) + c / 2) = fin ? code : 0u;
-    uint32_t word = (c < K ? (fin ? (uint32_t)(s + 127) : 255u) : 127u) << (8 * ((lane >> 2) & 3));
-    word |= __shfl_xor_sync(0xffffffffu, word, 4);
-    word |= __shfl_xor_sync(0xffffffffu, word, 8);
-    const int kt = (pass0 + i) * 2 + (lane >> 4);
-    if ((lane & 15) == 0 && kt < KT)
-      *reinterpret_cast<uint32_t*>(sc + fp4_row_scale_at(o, g, p - o, kt * 4, KT)) = word;
+    for (int w = 0; w < 4; ++w) {
+      float y[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = v.at(w * 8 + j) * f;
+      c[w] = byte != 255u ? fp4_pack8(y) : 0u;
+    }
+    *reinterpret_cast<uint4*>(q + p * (K / 2) + kb * 16) = make_uint4(c[0], c[1], c[2], c[3]);
   }
+  byte <<= 8 * (lane & 3);
+  byte |= __shfl_xor_sync(0xffffffffu, byte, 1);
+  byte |= __shfl_xor_sync(0xffffffffu, byte, 2);
+  if ((lane & 3) == 0 && live) *reinterpret_cast<uint32_t*>(sc + fp4_row_scale_at(o, g, p - o, kb, KT)) = byte;
 }
+
+// Two values of a byte of codes.
+__device__ __forceinline__ float2 fp4_values2(uint32_t byte) {
+  uint32_t h;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t}"
+      : "=r"(h)
+      : "r"(byte));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// A warp takes up to kSegPasses passes of 256 elements of one row, a lane 8
+// elements a pass (four lanes a block), so that stores are whole lines.
+constexpr int kSegPasses = 7;
 
 template <typename T, bool V>
 __global__ void __launch_bounds__(256) dequant_rows_kernel(const uint8_t* __restrict__ q,
@@ -193,8 +211,11 @@ __global__ void __launch_bounds__(256) dequant_rows_kernel(const uint8_t* __rest
     constexpr int W = V ? 16 / sizeof(T) : 1;
     Vec<T, W> o8[8 / W];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      reinterpret_cast<T*>(o8)[j] = from_f32<T>(fp4_value((code[i] >> (4 * j)) & 15u) * s);
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = fp4_values2(code[i] >> (8 * j));
+      o8[2 * j / W].e[2 * j % W] = from_f32<T>(f.x * s);
+      o8[(2 * j + 1) / W].e[(2 * j + 1) % W] = from_f32<T>(f.y * s);
+    }
 #pragma unroll
     for (int j = 0; j < 8 / W; ++j) store_vec<T, W>(y + p * ldy + c + j * W, o8[j]);
   }
@@ -281,14 +302,31 @@ constexpr int kMaxStages = 12;
 constexpr int kWBytes = 128 * 128;      // weights of a stage
 constexpr int kSmem4 = 232448;          // all of an SM's
 
+// Shared-memory descriptors as their low words (address in units of 16 bytes and
+// the leading offset, so that adding moves the address); the high words are
+// constants: 128-byte swizzle with 1024 bytes between 8-row groups, or none with 128.
+constexpr uint32_t kDescSw128 = (1024 >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t kDescPlain = (128 >> 4) | (1u << 14);
+MOE_DEV uint32_t desc_lo(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
+
 // D (+)= (A * sfa) (B * sfb): E2M1 operands, a UE8M0 scale per 32 elements, K = 64.
-MOE_DEV void tc_mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+MOE_DEV void tc_mma_mxf4(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
                          uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
       "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      "mov.b64 a, {%1, %7};\n\t"
+      "mov.b64 b, {%2, %7};\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], a, b, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "n"(kDescSw128)
+      : "memory");
+}
+// A 512-byte scale tile into four TMEM columns (its 32 rows of 16 bytes in every lane quarter).
+MOE_DEV void tc_cp_scales(uint32_t taddr, uint32_t lo) {
+  asm volatile(
+      "{\n\t.reg .b64 s;\n\t"
+      "mov.b64 s, {%1, %2};\n\t"
+      "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], s;\n\t}" ::"r"(taddr), "r"(lo), "n"(kDescPlain)
       : "memory");
 }
 // Instruction descriptor: E2M1 A and B (K-major), UE8M0 scales taken from bytes
@@ -308,8 +346,9 @@ MOE_DEV bool elect_one() {
       : "=r"(p));
   return p != 0;
 }
-// The same value in every lane, known to be so.
-MOE_DEV int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+// A value that is the same in every lane, as one the compiler knows to be: a
+// warp reduction's result is warp-uniform (a shuffle's is not).
+MOE_DEV int uniform(int v) { return (int)__reduce_max_sync(0xffffffffu, (unsigned)v); }
 
 struct P4 {
   const int* off;      // [G+1] or NULL (one segment of `rows`)
@@ -473,6 +512,7 @@ __global__ void __launch_bounds__(kThreads4, 1)
   } else if (warp == 1) {
     int s = 0, acc = 0;
     uint32_t ph = 0, aph = 0, ph2 = 0;
+    const uint32_t da0 = desc_lo(base), step = stage_bytes / 16u;
     int set = 0, it = 0, s2 = 0;  // s2, ph2: the stage issued `sets` before this one
     for (int u = blockIdx.x; u < total; u += gridDim.x) {
       const Unit4 t = unit_at(u);
@@ -495,16 +535,15 @@ __global__ void __launch_bounds__(kThreads4, 1)
           }
         }
         tc_fence_after();
-        const uint32_t sa = base + (uint32_t)s * stage_bytes, sb = sa + kWBytes, sf = sb + (uint32_t)cap * 128u;
+        const uint32_t da = da0 + (uint32_t)s * step, db = da + kWBytes / 16u, dsf = db + (uint32_t)cap * 8u;
         const uint32_t tsf = tmem + 2u * (uint32_t)cap + (uint32_t)set * 32u;
-        const uint64_t da = sdesc_sw128(sa, 16, 1024), db = sdesc_sw128(sb, 16, 1024), dsf = sdesc_plain(sf, 16, 128);
         const int steps = min(4, (p.K - kb * 256 + 63) / 64);
         if (leader) {
           // descriptors advance in units of 16 bytes
           auto scales = [&](int j) {
-            tc_cp_32x128b_warpx4(tsf + j * 16u, dsf + j * 32u);
-            tc_cp_32x128b_warpx4(tsf + j * 16u + 8u, dsf + 64u + j * 32u);
-            if (runs > 1) tc_cp_32x128b_warpx4(tsf + j * 16u + 12u, dsf + 128u + j * 32u);
+            tc_cp_scales(tsf + j * 16u, dsf + j * 32u);
+            tc_cp_scales(tsf + j * 16u + 8u, dsf + 64u + j * 32u);
+            if (runs > 1) tc_cp_scales(tsf + j * 16u + 12u, dsf + 128u + j * 32u);
           };
           auto mma = [&](int j) {
             const uint32_t c = tsf + (uint32_t)(j >> 1) * 16u;
@@ -674,10 +713,9 @@ moe_status moe_quantize_mxfp4_rows(int32_t dtype, int64_t rows, int32_t K, const
   return ops_status(with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
     TraceScope ts("quantize_mxfp4_rows", st);
-    const Segs sg = row_segs(K);
-    const unsigned grid = (unsigned)((rows * sg.n + 7) / 8);
     auto kern = rows16(x, ldx, dtype) ? quant_rows_kernel<T, true> : quant_rows_kernel<T, false>;
-    kern<<<grid, 256, 0, st>>>(static_cast<const T*>(x), ldx, rows, K, G, offsets, perm, k, sg.n, sg.per, q, scales);
+    const unsigned grid = (unsigned)((rows * ((K + 127) / 128) * 4 + 255) / 256);
+    kern<<<grid, 256, 0, st>>>(static_cast<const T*>(x), ldx, rows, K, G, offsets, perm, k, q, scales);
     return cudaGetLastError();
   }));
 }
