@@ -288,16 +288,19 @@ __global__ void __launch_bounds__(256) dequant_weights_kernel(const uint8_t* __r
 // holds features on TMEM lanes and rows on TMEM columns, so an expert with a
 // few rows costs its weight stream and little else.  A unit of work is (expert,
 // 128 features, tile of rows); a stage of the ring holds 256 elements of K:
-//   weights 128 x 128 B, rows up to 224 x 128 B (both 128-byte swizzled), their
+//   weights 128 x 128 B, rows up to 192 x 128 B (both 128-byte swizzled), their
 //   scale tiles (2 x 512 B for the features and for each 128 rows).
 // The stage's scale tiles are copied to TMEM (tcgen05.cp) right before its four
-// MMAs of K = 64, into one of `sets` column sets; the stage that used a set last
-// has completed before it is written again.
-// TMEM: two accumulators as wide as the largest tile of rows (at most 224
-// columns), then scale sets of 32 columns: two beside the widest accumulators, one
-// for every stage where tiles are narrow.
+// MMAs of K = 64, into the stage's own columns.
+// TMEM: two accumulators as wide as the largest tile of rows (at most 192
+// columns), then 32 scale columns for every stage.
+//
+// The copy and MMA warps are bound by instruction issue when experts have few
+// rows (a stage is then 17 KB of weights, 0.38 us of an SM's share of HBM): their
+// loops run in all lanes without branches, every copy and MMA predicated on one
+// elected lane and on what the stage needs, and give up waiting out of line.
 constexpr int kThreads4 = 192;
-constexpr int kMaxTok = 224;
+constexpr int kMaxTok = 192;
 constexpr int kMaxStages = 12;
 constexpr int kWBytes = 128 * 128;      // weights of a stage
 constexpr int kSmem4 = 232448;          // all of an SM's
@@ -309,25 +312,95 @@ constexpr uint32_t kDescSw128 = (1024 >> 4) | (1u << 14) | (2u << 29);
 constexpr uint32_t kDescPlain = (128 >> 4) | (1u << 14);
 MOE_DEV uint32_t desc_lo(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
 
+// The following do nothing in lanes where `on` is 0.
 // D (+)= (A * sfa) (B * sfb): E2M1 operands, a UE8M0 scale per 32 elements, K = 64.
-MOE_DEV void tc_mma_mxf4(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+MOE_DEV void tc_mma_mxf4(int on, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
                          uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
       "setp.ne.b32 p, %6, 0;\n\t"
+      "setp.ne.b32 q, %8, 0;\n\t"
       "mov.b64 a, {%1, %7};\n\t"
       "mov.b64 b, {%2, %7};\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], a, b, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "n"(kDescSw128)
+      "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], a, b, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "n"(kDescSw128), "r"(on)
       : "memory");
 }
 // A 512-byte scale tile into four TMEM columns (its 32 rows of 16 bytes in every lane quarter).
-MOE_DEV void tc_cp_scales(uint32_t taddr, uint32_t lo) {
+MOE_DEV void tc_cp_scales(int on, uint32_t taddr, uint32_t lo) {
   asm volatile(
-      "{\n\t.reg .b64 s;\n\t"
+      "{\n\t.reg .pred q;\n\t.reg .b64 s;\n\t"
+      "setp.ne.b32 q, %3, 0;\n\t"
       "mov.b64 s, {%1, %2};\n\t"
-      "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], s;\n\t}" ::"r"(taddr), "r"(lo), "n"(kDescPlain)
+      "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], s;\n\t}" ::"r"(taddr), "r"(lo), "n"(kDescPlain), "r"(on)
       : "memory");
+}
+MOE_DEV void tc_commit_on(int on, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(on)
+      : "memory");
+}
+MOE_DEV void expect_tx_on(int on, uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %2, 0;\n\t"
+      "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes), "r"(on)
+      : "memory");
+}
+MOE_DEV void tma_load_2d_on(int on, uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(on)
+      : "memory");
+}
+MOE_DEV void tma_load_3d_on(int on, uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %6, 0;\n\t"
+      "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(on)
+      : "memory");
+}
+MOE_DEV void bulk_load_on(int on, uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %4, 0;\n\t"
+      "@q cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar), "r"(on)
+      : "memory");
+}
+MOE_DEV bool try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// The rest of a wait whose first try failed: gives up (false) on the abort flag
+// or after kWaitLimitNs, which it reports.
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status, int where) {
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (try_wait(bar, parity)) return true;
+    if ((it & 63u) == 0) {
+      if (*abort_flag) return false;
+      if (global_timer_ns() - t0 > kWaitLimitNs) {
+        *abort_flag = 1;
+        report_status(status, kStatusTimeout, where);
+        return false;
+      }
+    }
+  }
 }
 // Instruction descriptor: E2M1 A and B (K-major), UE8M0 scales taken from bytes
 // sf, sf + 1 of a 32-bit scale column (sf 0 or 2).
@@ -360,11 +433,11 @@ struct P4 {
   int rows, G, N, K, NT, KT, stages_k;
 };
 
-// Tiles of an expert's c rows: one of up to kMaxTok, else of up to 192 that start
-// on multiples of 64 (so a tile's scales lie in at most two 128-row tiles, from
-// column 0 or 2 of the first).
-MOE_DEV int tok_tiles(int c) { return c <= kMaxTok ? (c > 0) : (c + 191) / 192; }
-MOE_DEV int tok_start(int c, int tiles, int t) { return (int)((int64_t)t * ((c + 63) / 64) / tiles) * 64; }
+// Tiles of an expert's c rows: as few as kMaxTok allows, starting on multiples of
+// 64 (so a tile's scales lie in at most two 128-row tiles, from column 0 or 2 of
+// the first).
+MOE_DEV int tok_tiles(int c) { return (c + kMaxTok - 1) / kMaxTok; }
+MOE_DEV int tok_start(int c, int tiles, int t) { return t * ((c + 63) / 64) / tiles * 64; }
 
 struct Unit4 {
   int e, n, row0, first, nt;  // expert, feature tile, first row of the expert, first row in it, rows
@@ -392,7 +465,7 @@ __global__ void __launch_bounds__(kThreads4, 1)
       const int e = base + lane;
       const int c = e < p.G ? s_off[e + 1] - s_off[e] : 0;
       const int tt = tok_tiles(c);
-      most = max(most, tt > 1 ? 192 : c);
+      most = max(most, tt > 1 ? kMaxTok : c);
       int inc = tt * p.NT;
       const int mine = inc;
 #pragma unroll
@@ -439,8 +512,7 @@ __global__ void __launch_bounds__(kThreads4, 1)
   const uint32_t stage_bytes = (uint32_t)kWBytes + (uint32_t)cap * 128u + 1024u + sfb_runs * 1024u;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t room = kSmem4 - 16384u - (base - smem_u32(smem_raw));
-  const int S = min(kMaxStages, (int)(room / stage_bytes));
-  const int sets = min(S, (512 - 2 * cap) / 32);
+  const int S = min(min(kMaxStages, (int)(room / stage_bytes)), (512 - 2 * cap) / 32);
 
   auto unit_at = [&](int u) {
     int lo = 0, hi = p.G - 1;
@@ -461,12 +533,12 @@ __global__ void __launch_bounds__(kThreads4, 1)
     return t;
   };
 
-  // The copy and MMA warps run their loops in all lanes, so that addresses and
-  // descriptors are warp-uniform values (they live in uniform registers, which
-  // those instructions take); one elected lane issues.
-  const bool leader = warp < 2 && elect_one();
-  auto wait_all = [&](uint64_t* bar, uint32_t parity, int where) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.status, where));
+  const int leader = warp < 2 && elect_one();
+  const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty);
+  // All lanes wait; the result is the same in each.
+  auto wait_all = [&](uint32_t bar, uint32_t parity, int where) {
+    if (__all_sync(0xffffffffu, try_wait(bar, parity))) return true;
+    return __all_sync(0xffffffffu, wait_on(bar, parity, abort_flag, p.status, where)) != 0;
   };
   if (warp == 0) {
     int s = 0;
@@ -478,25 +550,25 @@ __global__ void __launch_bounds__(kThreads4, 1)
       const int row = t.row0 + t.first;
       const uint8_t* wsp = p.ws + ((size_t)t.e * p.NT + t.n) * p.KT * 512u;
       const uint8_t* xsp = p.xs + (size_t)(t.row0 / 128 + t.e + t.first / 128) * p.KT * 512u;
+      const uint8_t* xsp2 = xsp + (size_t)p.KT * 512u;
+      const uint32_t bytes = (uint32_t)kWBytes + (uint32_t)boxes * 4096u;
+      // rows in boxes of 128, the rest in boxes of 32
+      const int big = leader && boxes >= 4, small0 = boxes >= 4 ? 4 : 0;
       for (int kb = 0; kb < p.stages_k; ++kb) {
-        if (!wait_all(&empty[s], ph ^ 1u, 1000 + s)) goto produced;
+        if (!wait_all(empty0 + 8u * s, ph ^ 1u, 1000 + s)) goto produced;
         const uint32_t sa = base + (uint32_t)s * stage_bytes, sb = sa + kWBytes, sf = sb + (uint32_t)cap * 128u;
-        const uint32_t fb = smem_u32(&full[s]);
+        const uint32_t fb = full0 + 8u * s;
         const uint32_t sfn = 512u * (uint32_t)min(2, p.KT - 2 * kb);
-        if (leader) {
-          mbar_arrive_expect_tx(&full[s], (uint32_t)kWBytes + (uint32_t)boxes * 4096u + sfn * (1u + runs));
-          tma_load_3d(sa, &tm_w, fb, kb * 128, t.n * 128, t.e);
-          bulk_load(sf, wsp + (size_t)kb * 1024u, sfn, fb);
-          int i = 0;  // rows in boxes of 128, the rest in boxes of 32
-          if (boxes >= 4) {
-            tma_load_2d(sb, &tm_x128, fb, kb * 128, row);
-            i = 4;
-          }
-          for (; i < boxes; ++i) tma_load_2d(sb + i * 4096u, &tm_x, fb, kb * 128, row + i * 32);
-          bulk_load(sf + 1024u, xsp + (size_t)kb * 1024u, sfn, fb);
-          if (runs > 1) bulk_load(sf + 2048u, xsp + (size_t)p.KT * 512u + (size_t)kb * 1024u, sfn, fb);
-        }
-        __syncwarp();
+        expect_tx_on(leader, fb, bytes + sfn * (1u + runs));
+        tma_load_3d_on(leader, sa, &tm_w, fb, kb * 128, t.n * 128, t.e);
+        bulk_load_on(leader, sf, wsp, sfn, fb);
+        tma_load_2d_on(big, sb, &tm_x128, fb, kb * 128, row);
+        for (int i = small0; i < boxes; ++i) tma_load_2d_on(leader, sb + i * 4096u, &tm_x, fb, kb * 128, row + i * 32);
+        bulk_load_on(leader, sf + 1024u, xsp, sfn, fb);
+        bulk_load_on(leader && runs > 1, sf + 2048u, xsp2, sfn, fb);
+        wsp += 1024;
+        xsp += 1024;
+        xsp2 += 1024;
         used |= 1u << s;
         last = (last & ~(1u << s)) | (ph << s);
         if (++s == S) {
@@ -511,75 +583,53 @@ __global__ void __launch_bounds__(kThreads4, 1)
       if ((used >> i) & 1u) mbar_wait_drain(&full[i], (last >> i) & 1u);
   } else if (warp == 1) {
     int s = 0, acc = 0;
-    uint32_t ph = 0, aph = 0, ph2 = 0;
-    const uint32_t da0 = desc_lo(base), step = stage_bytes / 16u;
-    int set = 0, it = 0, s2 = 0;  // s2, ph2: the stage issued `sets` before this one
+    uint32_t ph = 0, aph = 0;
+    const uint32_t da0 = desc_lo(base), step = stage_bytes / 16u, sf0 = tmem + 2u * (uint32_t)cap;
+    const uint32_t b_off = kWBytes / 16u, s_off16 = b_off + (uint32_t)cap * 8u;
     for (int u = blockIdx.x; u < total; u += gridDim.x) {
       const Unit4 t = unit_at(u);
       const int n16 = (t.nt + 15) & ~15;
-      const int runs = ((t.first & 127) + t.nt + 127) / 128;
-      const uint32_t shift = (uint32_t)(t.first & 127) / 32u;  // 0 or 2 columns
+      const int two = leader && (t.first & 127) + t.nt > 128;
+      const uint32_t shift = 8u + (uint32_t)(t.first & 127) / 32u;  // scale columns of the rows: 0 or 2 in
       const uint32_t id0 = idesc_mxf4(n16, 0), id2 = idesc_mxf4(n16, 2);
-      if (!wait_all(&tempty[acc], aph ^ 1u, 1100 + acc)) goto issued;
-      tc_fence_after();
       const uint32_t d = tmem + (uint32_t)(acc * cap);
-      for (int kb = 0; kb < p.stages_k; ++kb, ++it) {
-        if (!wait_all(&full[s], ph, 1200 + s)) goto issued;
-        // the scale columns are free once the stage that used them has
-        // completed (with a set for every stage its refill has shown that)
-        if (sets < S && it >= sets) {
-          if (!wait_all(&empty[s2], ph2, 1300 + s2)) goto issued;
-          if (++s2 == S) {
-            s2 = 0;
-            ph2 ^= 1u;
-          }
-        }
+      if (!wait_all(smem_u32(&tempty[acc]), aph ^ 1u, 1100 + acc)) goto issued;
+      tc_fence_after();
+      int left = p.K;  // elements of K still to come
+      uint32_t more = 0;
+      for (int kb = 0; kb < p.stages_k; ++kb) {
+        if (!wait_all(full0 + 8u * s, ph, 1200 + s)) goto issued;
         tc_fence_after();
-        const uint32_t da = da0 + (uint32_t)s * step, db = da + kWBytes / 16u, dsf = db + (uint32_t)cap * 8u;
-        const uint32_t tsf = tmem + 2u * (uint32_t)cap + (uint32_t)set * 32u;
-        const int steps = min(4, (p.K - kb * 256 + 63) / 64);
-        if (leader) {
-          // descriptors advance in units of 16 bytes
-          auto scales = [&](int j) {
-            tc_cp_scales(tsf + j * 16u, dsf + j * 32u);
-            tc_cp_scales(tsf + j * 16u + 8u, dsf + 64u + j * 32u);
-            if (runs > 1) tc_cp_scales(tsf + j * 16u + 12u, dsf + 128u + j * 32u);
-          };
-          auto mma = [&](int j) {
-            const uint32_t c = tsf + (uint32_t)(j >> 1) * 16u;
-            tc_mma_mxf4(d, da + j * 2u, db + j * 2u, (j & 1) ? id2 : id0, c, c + 8u + shift, (kb > 0 || j > 0) ? 1u : 0u);
-          };
-          if (steps == 4) {  // straight-line: a loop costs as much again per instruction
-            scales(0);
-            scales(1);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) mma(j);
-          } else {
-            scales(0);
-            if (steps > 2) scales(1);
-            mma(0);
-            if (steps > 1) mma(1);
-            if (steps > 2) mma(2);
-          }
-          tc_commit(smem_u32(&empty[s]));
-        }
-        __syncwarp();
-        if (++set == sets) set = 0;
+        // descriptors advance in units of 16 bytes
+        const uint32_t da = da0 + (uint32_t)s * step, db = da + b_off, ds = da + s_off16;
+        const uint32_t tsf = sf0 + (uint32_t)s * 32u, tsb = tsf + shift;
+        const int half = leader && left > 128;
+        tc_cp_scales(leader, tsf, ds);
+        tc_cp_scales(leader, tsf + 8u, ds + 64u);
+        tc_cp_scales(two, tsf + 12u, ds + 128u);
+        tc_cp_scales(half, tsf + 16u, ds + 32u);
+        tc_cp_scales(half, tsf + 24u, ds + 96u);
+        tc_cp_scales(two && half, tsf + 28u, ds + 160u);
+        tc_mma_mxf4(leader, d, da, db, id0, tsf, tsb, more);
+        tc_mma_mxf4(leader && left > 64, d, da + 2u, db + 2u, id2, tsf, tsb, 1u);
+        tc_mma_mxf4(half, d, da + 4u, db + 4u, id0, tsf + 16u, tsb + 16u, 1u);
+        tc_mma_mxf4(leader && left > 192, d, da + 6u, db + 6u, id2, tsf + 16u, tsb + 16u, 1u);
+        tc_commit_on(leader, empty0 + 8u * s);
+        left -= 256;
+        more = 1u;
         if (++s == S) {
           s = 0;
           ph ^= 1u;
         }
       }
-      if (leader) tc_commit(smem_u32(&tfull[acc]));
-      __syncwarp();
+      tc_commit_on(leader, smem_u32(&tfull[acc]));
       if (++acc == 2) {
         acc = 0;
         aph ^= 1u;
       }
     }
   issued:
-    if (leader) tc_commit(smem_u32(&drain));
-    __syncwarp();
+    tc_commit_on(leader, smem_u32(&drain));
     mbar_wait_drain(&drain, 0);
   } else {
     const int q = warp & 3;  // TMEM lane quarter of this warp
@@ -588,7 +638,7 @@ __global__ void __launch_bounds__(kThreads4, 1)
     T* out = static_cast<T*>(p.out);
     for (int u = blockIdx.x; u < total; u += gridDim.x) {
       const Unit4 t = unit_at(u);
-      if (!mbar_wait(&tfull[acc], aph, abort_flag, p.status, 1400 + acc)) break;
+      if (!wait_all(smem_u32(&tfull[acc]), aph, 1400 + acc)) break;
       tc_fence_after();
       const int n = t.n * 128 + q * 32 + lane;
       T* dst = out + (int64_t)(t.row0 + t.first) * p.ldo + (SWIGLU ? n >> 1 : n);
