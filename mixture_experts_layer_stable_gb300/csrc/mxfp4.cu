@@ -295,10 +295,14 @@ __global__ void __launch_bounds__(256) dequant_weights_kernel(const uint8_t* __r
 // TMEM: two accumulators as wide as the largest tile of rows (at most 192
 // columns), then 32 scale columns for every stage.
 //
-// The copy and MMA warps are bound by instruction issue when experts have few
-// rows (a stage is then 17 KB of weights, 0.38 us of an SM's share of HBM): their
-// loops run in all lanes without branches, every copy and MMA predicated on one
-// elected lane and on what the stage needs, and give up waiting out of line.
+// When experts have few rows a stage is 17 KB of weights, 0.38 us of an SM's share
+// of HBM, and issuing its copies and MMAs must not take longer: the copy and MMA
+// warps run their loops in all lanes without branches, every copy and MMA
+// predicated on one elected lane and on what the stage needs, and wait out of
+// line.  The election has to stand in the role's own branch: with its result
+// merged across branches (or with lane == 0 instead) every one of these
+// instructions took 70 cycles or more, against 10 to 20, and a stage 850 cycles
+// instead of what its bytes take.
 constexpr int kThreads4 = 192;
 constexpr int kMaxTok = 192;
 constexpr int kMaxStages = 12;
@@ -533,7 +537,6 @@ __global__ void __launch_bounds__(kThreads4, 1)
     return t;
   };
 
-  const int leader = warp < 2 && elect_one();
   const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty);
   // All lanes wait; the result is the same in each.
   auto wait_all = [&](uint32_t bar, uint32_t parity, int where) {
@@ -541,6 +544,7 @@ __global__ void __launch_bounds__(kThreads4, 1)
     return __all_sync(0xffffffffu, wait_on(bar, parity, abort_flag, p.status, where)) != 0;
   };
   if (warp == 0) {
+    const int leader = elect_one();
     int s = 0;
     uint32_t ph = 0, used = 0, last = 0;
     for (int u = blockIdx.x; u < total; u += gridDim.x) {
@@ -582,6 +586,7 @@ __global__ void __launch_bounds__(kThreads4, 1)
     for (int i = 0; i < kMaxStages; ++i)
       if ((used >> i) & 1u) mbar_wait_drain(&full[i], (last >> i) & 1u);
   } else if (warp == 1) {
+    const int leader = elect_one();
     int s = 0, acc = 0;
     uint32_t ph = 0, aph = 0;
     const uint32_t da0 = desc_lo(base), step = stage_bytes / 16u, sf0 = tmem + 2u * (uint32_t)cap;
