@@ -4,69 +4,292 @@
 //   y  = (x - mean) * rstd * w + b
 //   dx = rstd * (g - mean(g) - xh * mean(g * xh)) + dadd,  g = dy * w, xh = (x - mean) * rstd
 //   dw = sum over rows of dy * xh,  db = sum over rows of dy
+//
+// Every call is bound by HBM (about ten operations an element), so a row is read
+// once: a group of threads (a warp or a block) holds it in registers, the mean and
+// then the sum of squared distances from it are taken from there (two passes over
+// registers cost nothing and keep the variance of rows whose mean is large), and
+// the groups are persistent with the next row's loads in flight while a row is
+// reduced.  The backward's groups add their rows' dw and db in registers and leave
+// one partial sum a block; a second kernel adds those in block order.
 #include "ops_common.cuh"
 
 namespace moe {
 
 namespace {
 
-constexpr int kLnThreads = 256;
-constexpr int kLnRows = 256;  // rows of one partial sum of dw and db
+constexpr int kElems = 16;       // elements of a row that a thread holds
+constexpr int kWarpRowMax = 32 * kElems;    // a warp takes a row up to this
+constexpr int kBlockRowMax = 512 * kElems;  // a block up to this
+constexpr int kLnWarps = 8;      // warps (rows) of a block in the warp form
+constexpr int kLoopThreads = 512;
 
-// Sum over the block, the same value in every thread.
-__device__ __forceinline__ float block_sum(float v, float* sh) {
+// Sum over the group's threads, the same in each.
+template <bool BLOCK>
+__device__ __forceinline__ float2 group_sum2(float a, float b, float2* sh) {
+  a = warp_sum(a);
+  b = warp_sum(b);
+  if constexpr (!BLOCK) return make_float2(a, b);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  v = warp_sum(v);
+  __syncthreads();  // the last sum's values have been read
+  if (lane == 0) sh[warp] = make_float2(a, b);
   __syncthreads();
-  if (lane == 0) sh[warp] = v;
+  const float2 v = lane < nw ? sh[lane] : make_float2(0.f, 0.f);
+  return make_float2(warp_sum(v.x), warp_sum(v.y));
+}
+template <bool BLOCK>
+__device__ __forceinline__ float group_sum(float a, float* sh) {
+  a = warp_sum(a);
+  if constexpr (!BLOCK) return a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
   __syncthreads();
-  float s = 0.f;
-  for (int i = 0; i < nw; ++i) s += sh[i];
-  return s;
+  if (lane == 0) sh[warp] = a;
+  __syncthreads();
+  return warp_sum(lane < nw ? sh[lane] : 0.f);
 }
 
-template <typename T, typename W>
-__global__ void __launch_bounds__(kLnThreads) ln_forward_kernel(
-    const T* __restrict__ x, int64_t ldx, const W* __restrict__ w, const W* __restrict__ b, float eps,
-    T* __restrict__ y, int64_t ldy, float* __restrict__ mean, float* __restrict__ rstd, int64_t rows, int d) {
-  __shared__ float sh[kLnThreads / 32];
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-    const T* xr = x + r * ldx;
-    float s = 0.f;
-    for (int i = threadIdx.x; i < d; i += blockDim.x) s += to_f32(xr[i]);
-    const float mu = block_sum(s, sh) / d;
-    s = 0.f;
-    for (int i = threadIdx.x; i < d; i += blockDim.x) {
-      const float c = to_f32(xr[i]) - mu;
-      s += c * c;
+// The part of a row that one thread holds: N vectors of V elements, vector i at
+// (i * threads + thread) * V; elements past d read as zeros.
+template <typename T, int V, int N>
+struct Part {
+  Vec<T, V> v[N];
+  __device__ __forceinline__ void load(const T* __restrict__ row, int d, int tid, int nt) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = (i * nt + tid) * V;
+      if (c < d) v[i] = load_vec<T, V>(row + c);
+      else
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[i].e[j] = from_f32<T>(0.f);
     }
-    const float rs = 1.0f / sqrtf(block_sum(s, sh) / d + eps);
-    if (threadIdx.x == 0 && mean != nullptr) {
+  }
+  __device__ __forceinline__ float at(int i, int j) const { return to_f32(v[i].e[j]); }
+};
+
+// V consecutive values of an optional array (NULL: all `other`).
+template <typename W, int V>
+__device__ __forceinline__ void weights_at(const W* __restrict__ w, int c, float other, float (&o)[V]) {
+  if (w == nullptr) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) o[j] = other;
+    return;
+  }
+  constexpr int P = V * sizeof(W) > 16 ? 16 / sizeof(W) : V;  // at most 16 bytes a load
+#pragma unroll
+  for (int j = 0; j < V; j += P) {
+    const Vec<W, P> v = load_vec<W, P>(w + c + j);
+#pragma unroll
+    for (int q = 0; q < P; ++q) o[j + q] = to_f32(v.e[q]);
+  }
+}
+
+template <typename T, typename W, int V, bool BLOCK>
+__global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
+    ln_forward_kernel(const T* x, int64_t ldx, const W* __restrict__ w, const W* __restrict__ b, float eps, T* y,
+                      int64_t ldy, float* __restrict__ mean, float* __restrict__ rstd, int64_t rows, int d) {
+  constexpr int N = kElems / V;
+  __shared__ float sh[32];
+  const int tid = BLOCK ? threadIdx.x : threadIdx.x & 31, nt = BLOCK ? blockDim.x : 32;
+  const int64_t first = BLOCK ? blockIdx.x : blockIdx.x * (int64_t)kLnWarps + (threadIdx.x >> 5);
+  const int64_t step = BLOCK ? gridDim.x : gridDim.x * (int64_t)kLnWarps;
+  const float inv_d = 1.0f / (float)d;
+  Part<T, V, N> cur, next;
+  if (first < rows) next.load(x + first * ldx, d, tid, nt);
+  for (int64_t r = first; r < rows; r += step) {
+    cur = next;
+    if (r + step < rows) next.load(x + (r + step) * ldx, d, tid, nt);
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < V; ++j) s += cur.at(i, j);
+    const float mu = group_sum<BLOCK>(s, sh) / (float)d;
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if ((i * nt + tid) * V >= d) break;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float c = cur.at(i, j) - mu;
+        s = fmaf(c, c, s);
+      }
+    }
+    const float rs = 1.0f / sqrtf(group_sum<BLOCK>(s, sh) * inv_d + eps);
+    if (tid == 0 && mean != nullptr) {
       mean[r] = mu;
       rstd[r] = rs;
     }
-    for (int i = threadIdx.x; i < d; i += blockDim.x) {
-      const float xh = (to_f32(xr[i]) - mu) * rs;
-      y[r * ldy + i] = from_f32<T>(xh * (w ? to_f32(w[i]) : 1.f) + (b ? to_f32(b[i]) : 0.f));
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = (i * nt + tid) * V;
+      if (c >= d) break;
+      float wv[V], bv[V];
+      weights_at<W, V>(w, c, 1.f, wv);
+      weights_at<W, V>(b, c, 0.f, bv);
+      Vec<T, V> o;
+#pragma unroll
+      for (int j = 0; j < V; ++j) o.e[j] = from_f32<T>(fmaf((cur.at(i, j) - mu) * rs, wv[j], bv[j]));
+      store_vec<T, V>(y + r * ldy + c, o);
     }
   }
 }
 
+// dx of the group's rows; with part, the rows' sums of dy * xh and dy to
+// part[block][0 / 1][d].
+template <typename T, typename W, int V, bool BLOCK>
+__global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
+    ln_backward_kernel(const T* dy, int64_t lddy, const T* __restrict__ x, int64_t ldx, const W* __restrict__ w,
+                       const float* __restrict__ mean, const float* __restrict__ rstd, const T* dadd, int64_t ldadd,
+                       T* dx, int64_t lddx, float* __restrict__ part, int64_t rows, int d) {
+  constexpr int N = kElems / V;
+  __shared__ float2 sh[32];
+  const int tid = BLOCK ? threadIdx.x : threadIdx.x & 31, nt = BLOCK ? blockDim.x : 32;
+  const int64_t first = BLOCK ? blockIdx.x : blockIdx.x * (int64_t)kLnWarps + (threadIdx.x >> 5);
+  const int64_t step = BLOCK ? gridDim.x : gridDim.x * (int64_t)kLnWarps;
+  const float inv_d = 1.0f / (float)d;
+  float aw[N][V] = {}, ab[N][V] = {};
+  Part<T, V, N> cx, cy, nx, ny;
+  float nmu = 0.f, nrs = 0.f;
+  if (first < rows) {
+    nx.load(x + first * ldx, d, tid, nt);
+    ny.load(dy + first * lddy, d, tid, nt);
+    nmu = __ldg(mean + first);
+    nrs = __ldg(rstd + first);
+  }
+  for (int64_t r = first; r < rows; r += step) {
+    cx = nx;
+    cy = ny;
+    const float mu = nmu, rs = nrs;
+    if (r + step < rows) {
+      nx.load(x + (r + step) * ldx, d, tid, nt);
+      ny.load(dy + (r + step) * lddy, d, tid, nt);
+      nmu = __ldg(mean + r + step);
+      nrs = __ldg(rstd + r + step);
+    }
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = (i * nt + tid) * V;
+      if (c >= d) break;
+      float wv[V];
+      weights_at<W, V>(w, c, 1.f, wv);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float xh = (cx.at(i, j) - mu) * rs, t = cy.at(i, j), g = t * wv[j];
+        s1 += g;
+        s2 = fmaf(g, xh, s2);
+        aw[i][j] = fmaf(t, xh, aw[i][j]);
+        ab[i][j] += t;
+      }
+    }
+    const float2 m = group_sum2<BLOCK>(s1, s2, sh);
+    const float m1 = m.x * inv_d, m2 = m.y * inv_d;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = (i * nt + tid) * V;
+      if (c >= d) break;
+      float wv[V];
+      weights_at<W, V>(w, c, 1.f, wv);
+      Vec<T, V> a, o;
+      if (dadd) a = load_vec<T, V>(dadd + r * ldadd + c);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float xh = (cx.at(i, j) - mu) * rs, g = cy.at(i, j) * wv[j];
+        float v = rs * (g - m1 - xh * m2);
+        if (dadd) v += to_f32(a.e[j]);
+        o.e[j] = from_f32<T>(v);
+      }
+      store_vec<T, V>(dx + r * lddx + c, o);
+    }
+  }
+  if (part == nullptr) return;
+  float* mine = part + (size_t)blockIdx.x * 2 * d;
+  if constexpr (BLOCK) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = (i * nt + tid) * V;
+      if (c >= d) break;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        mine[c + j] = aw[i][j];
+        mine[d + c + j] = ab[i][j];
+      }
+    }
+  } else {
+    // the warps add theirs one after the other
+    __shared__ float acc[2][kWarpRowMax];
+    for (int k = 0; k < kLnWarps; ++k) {
+      if ((threadIdx.x >> 5) == k) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int c = (i * nt + tid) * V;
+          if (c >= d) break;
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            acc[0][c + j] = (k ? acc[0][c + j] : 0.f) + aw[i][j];
+            acc[1][c + j] = (k ? acc[1][c + j] : 0.f) + ab[i][j];
+          }
+        }
+      }
+      __syncthreads();
+    }
+    for (int c = threadIdx.x; c < d; c += blockDim.x) {
+      mine[c] = acc[0][c];
+      mine[d + c] = acc[1][c];
+    }
+  }
+}
+
+// Rows too wide for a block's registers: three passes over the row (it stays in
+// L1 / L2), one element at a time.
 template <typename T, typename W>
-__global__ void __launch_bounds__(kLnThreads) ln_backward_kernel(
-    const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* w, const float* mean, const float* rstd,
-    const T* dadd, int64_t ldadd, T* dx, int64_t lddx, int64_t rows, int d) {
-  __shared__ float sh[kLnThreads / 32];
+__global__ void __launch_bounds__(kLoopThreads)
+    ln_forward_loop_kernel(const T* x, int64_t ldx, const W* __restrict__ w, const W* __restrict__ b, float eps, T* y,
+                           int64_t ldy, float* __restrict__ mean, float* __restrict__ rstd, int64_t rows, int d) {
+  __shared__ float sh[32];
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+    const T* xr = x + r * ldx;
+    float s = 0.f;
+    for (int i = threadIdx.x; i < d; i += blockDim.x) s += to_f32(xr[i]);
+    const float mu = group_sum<true>(s, sh) / (float)d;
+    s = 0.f;
+    for (int i = threadIdx.x; i < d; i += blockDim.x) {
+      const float c = to_f32(xr[i]) - mu;
+      s = fmaf(c, c, s);
+    }
+    const float rs = 1.0f / sqrtf(group_sum<true>(s, sh) / (float)d + eps);
+    if (threadIdx.x == 0 && mean != nullptr) {
+      mean[r] = mu;
+      rstd[r] = rs;
+    }
+    for (int i = threadIdx.x; i < d; i += blockDim.x)
+      y[r * ldy + i] = from_f32<T>(fmaf((to_f32(xr[i]) - mu) * rs, w ? to_f32(w[i]) : 1.f, b ? to_f32(b[i]) : 0.f));
+  }
+}
+
+template <typename T, typename W>
+__global__ void __launch_bounds__(kLoopThreads)
+    ln_backward_loop_kernel(const T* dy, int64_t lddy, const T* __restrict__ x, int64_t ldx, const W* __restrict__ w,
+                            const float* __restrict__ mean, const float* __restrict__ rstd, const T* dadd,
+                            int64_t ldadd, T* dx, int64_t lddx, float* __restrict__ part, int64_t rows, int d) {
+  __shared__ float2 sh[32];
+  float* mine = part ? part + (size_t)blockIdx.x * 2 * d : nullptr;
+  bool begun = false;
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x, begun = true) {
     const float mu = mean[r], rs = rstd[r];
     float s1 = 0.f, s2 = 0.f;
     for (int i = threadIdx.x; i < d; i += blockDim.x) {
-      const float g = to_f32(dy[r * lddy + i]) * (w ? to_f32(w[i]) : 1.f);
+      const float t = to_f32(dy[r * lddy + i]), g = t * (w ? to_f32(w[i]) : 1.f);
+      const float xh = (to_f32(x[r * ldx + i]) - mu) * rs;
       s1 += g;
-      s2 += g * ((to_f32(x[r * ldx + i]) - mu) * rs);
+      s2 = fmaf(g, xh, s2);
+      if (mine) {  // a column is one thread's
+        mine[i] = fmaf(t, xh, begun ? mine[i] : 0.f);
+        mine[d + i] = (begun ? mine[d + i] : 0.f) + t;
+      }
     }
-    const float m1 = block_sum(s1, sh) / d;
-    const float m2 = block_sum(s2, sh) / d;
+    const float2 m = group_sum2<true>(s1, s2, sh);
+    const float m1 = m.x / (float)d, m2 = m.y / (float)d;
     for (int i = threadIdx.x; i < d; i += blockDim.x) {
       const float g = to_f32(dy[r * lddy + i]) * (w ? to_f32(w[i]) : 1.f);
       const float xh = (to_f32(x[r * ldx + i]) - mu) * rs;
@@ -77,45 +300,38 @@ __global__ void __launch_bounds__(kLnThreads) ln_backward_kernel(
   }
 }
 
-// part[c][0 / 1][i]: dw and db summed over rows [c kLnRows, (c + 1) kLnRows).
-template <typename T>
-__global__ void __launch_bounds__(kLnThreads) ln_partial_kernel(
-    const T* __restrict__ dy, int64_t lddy, const T* __restrict__ x, int64_t ldx,
-    const float* __restrict__ mean, const float* __restrict__ rstd, float* __restrict__ part, int64_t rows,
-    int d) {
-  const int i = blockIdx.x * kLnThreads + threadIdx.x;
-  const int64_t r0 = (int64_t)blockIdx.y * kLnRows, r1 = min(rows, r0 + kLnRows);
-  if (i >= d) return;
-  float a = 0.f, s = 0.f;
-  for (int64_t r = r0; r < r1; ++r) {
-    const float g = to_f32(dy[r * lddy + i]);
-    a += g * ((to_f32(x[r * ldx + i]) - mean[r]) * rstd[r]);
-    s += g;
-  }
-  part[(size_t)blockIdx.y * 2 * d + i] = a;
-  part[(size_t)blockIdx.y * 2 * d + d + i] = s;
-}
-
+// dw and db from the blocks' partial sums: 32 columns a block, its 8 warps each
+// a run of the partials, joined in order.
 template <typename W>
-__global__ void __launch_bounds__(kLnThreads) ln_reduce_kernel(const float* __restrict__ part, int np,
-                                                               W* __restrict__ dw, W* __restrict__ db, int d) {
-  const int i = blockIdx.x * kLnThreads + threadIdx.x;
-  if (i >= d) return;
-  float a = 0.f, s = 0.f;
-  for (int p = 0; p < np; ++p) {
-    a += part[(size_t)p * 2 * d + i];
-    s += part[(size_t)p * 2 * d + d + i];
+__global__ void __launch_bounds__(256) ln_reduce_kernel(const float* __restrict__ part, int np, W* __restrict__ dw,
+                                                        W* __restrict__ db, int d) {
+  __shared__ float sh[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;  // column of [2 d]: dw's, then db's
+  const int per = (np + 7) / 8, p1 = min(np, (warp + 1) * per);
+  float s = 0.f;
+  if (c < 2 * d) {
+#pragma unroll 8
+    for (int p = warp * per; p < p1; ++p) s += __ldcg(part + (size_t)p * 2 * d + c);
   }
-  if (dw) dw[i] = from_f32<W>(a);
-  if (db) db[i] = from_f32<W>(s);
+  sh[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && c < 2 * d) {
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += sh[i][lane];
+    if (c < d) {
+      if (dw) dw[c] = from_f32<W>(s);
+    } else if (db) {
+      db[c - d] = from_f32<W>(s);
+    }
+  }
 }
 
 bool ln_args(int32_t dtype, int32_t wdtype, int64_t rows, int32_t d) {
   return dtype_valid(dtype) && (wdtype == dtype || wdtype == MOE_DT_F32) && rows >= 0 &&
          rows <= ((int64_t)1 << 40) && d >= 1 && d <= 65536;
 }
-
-int64_t ln_parts(int64_t rows) { return (rows + kLnRows - 1) / kLnRows; }
 
 // f(T{}, W{}) for the element types of the rows and of the weights.
 template <typename F>
@@ -124,6 +340,39 @@ cudaError_t ln_types(int dtype, int wdtype, F f) {
     if (wdtype == MOE_DT_F32) return f(t, float());
     return f(t, t);
   });
+}
+
+// Elements a thread moves at once: 16 bytes where every row and d allow it, else
+// 4 bytes, else one element.  `a`: the or of the addresses and row strides in
+// bytes; `aw`: of the weights' addresses, which are read V elements at a time too.
+int ln_vec(size_t es, size_t wes, int d, uintptr_t a, uintptr_t aw) {
+  auto fits = [&](int v) {
+    const size_t wb = v * wes > 16 ? 16 : v * wes;
+    return d % v == 0 && a % (v * es) == 0 && aw % wb == 0;
+  };
+  if (fits((int)(16 / es))) return (int)(16 / es);
+  if (es == 2 && fits(2)) return 2;
+  return 1;
+}
+uintptr_t bits(const void* p) { return reinterpret_cast<uintptr_t>(p); }
+
+// f(integral_constant V) for the vector widths of T.
+template <typename T, typename F>
+void ln_with_vec(int v, F f) {
+  if (v == (int)(16 / sizeof(T))) f(std::integral_constant<int, 16 / sizeof(T)>());
+  else if (v == 1) f(std::integral_constant<int, 1>());
+  else if constexpr (sizeof(T) == 2) f(std::integral_constant<int, 2>());
+}
+
+// Threads of a block that takes a row.
+int ln_block_threads(int d) { return ((d + kElems - 1) / kElems + 31) / 32 * 32; }
+// Blocks: about as many as fit on the GPU at once (1024 threads an SM), so that
+// each stays on its rows.
+int ln_blocks(int64_t rows, int d) {
+  const int threads = d <= kWarpRowMax ? 32 * kLnWarps : d <= kBlockRowMax ? ln_block_threads(d) : kLoopThreads;
+  const int64_t need = d <= kWarpRowMax ? (rows + kLnWarps - 1) / kLnWarps : rows;
+  const int64_t most = (int64_t)num_sms() * (1024 / threads);
+  return (int)(need < most ? need : most);
 }
 
 }  // namespace
@@ -139,28 +388,42 @@ moe_status moe_layernorm_forward(int32_t dtype, int32_t wdtype, int64_t rows, in
                                  int64_t ldy, float* mean, float* rstd, moe_stream_t stream) {
   if (!ln_args(dtype, wdtype, rows, d) || ldx < d || ldy < d || !(eps >= 0.f) || !isfinite(eps))
     return MOE_ERR_INVALID_ARG;
-  const size_t es = dtype_bytes(dtype), ws = dtype_bytes(wdtype);
-  if (!elem_ok_or_null(weight, ws) || !elem_ok_or_null(bias, ws) || (mean == nullptr) != (rstd == nullptr) ||
+  const size_t es = dtype_bytes(dtype), wes = dtype_bytes(wdtype);
+  if (!elem_ok_or_null(weight, wes) || !elem_ok_or_null(bias, wes) || (mean == nullptr) != (rstd == nullptr) ||
       !elem_ok_or_null(mean, 4) || !elem_ok_or_null(rstd, 4))
     return MOE_ERR_INVALID_ARG;
   if (rows == 0) return MOE_OK;
   if (!elem_ok(x, es) || !elem_ok(y, es)) return MOE_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int v = ln_vec(es, wes, d, bits(x) | bits(y) | (uintptr_t)(ldx * es) | (uintptr_t)(ldy * es),
+                       bits(weight) | bits(bias));
+  const int grid = ln_blocks(rows, d);
   return ops_status(ln_types(dtype, wdtype, [&](auto t, auto wt) {
     using T = decltype(t);
     using W = decltype(wt);
-    const int grid = (int)(rows < 65535 ? rows : 65535);
+    const T* xp = static_cast<const T*>(x);
+    const W *wp = static_cast<const W*>(weight), *bp = static_cast<const W*>(bias);
+    T* yp = static_cast<T*>(y);
     TraceScope ts("layernorm_forward", st);
-    ln_forward_kernel<T, W><<<grid, kLnThreads, 0, st>>>(
-        static_cast<const T*>(x), ldx, static_cast<const W*>(weight), static_cast<const W*>(bias), eps,
-        static_cast<T*>(y), ldy, mean, rstd, rows, d);
+    if (d > kBlockRowMax)
+      ln_forward_loop_kernel<T, W><<<grid, kLoopThreads, 0, st>>>(xp, ldx, wp, bp, eps, yp, ldy, mean, rstd, rows, d);
+    else
+      ln_with_vec<T>(v, [&](auto vc) {
+        constexpr int V = decltype(vc)::value;
+        if (d <= kWarpRowMax)
+          ln_forward_kernel<T, W, V, false><<<grid, 32 * kLnWarps, 0, st>>>(xp, ldx, wp, bp, eps, yp, ldy, mean, rstd,
+                                                                            rows, d);
+        else
+          ln_forward_kernel<T, W, V, true><<<grid, ln_block_threads(d), 0, st>>>(xp, ldx, wp, bp, eps, yp, ldy, mean,
+                                                                                 rstd, rows, d);
+      });
     return cudaGetLastError();
   }));
 }
 
 size_t moe_layernorm_workspace_bytes(int64_t rows, int32_t d) {
   if (!ln_args(MOE_DT_F32, MOE_DT_F32, rows, d)) return 0;
-  return ((size_t)(ln_parts(rows) + 1) * 2 * d * sizeof(float) + 127) / 128 * 128;
+  return ((size_t)(ln_blocks(rows, d) + 1) * 2 * d * sizeof(float) + 127) / 128 * 128;
 }
 
 moe_status moe_layernorm_backward(int32_t dtype, int32_t wdtype, int64_t rows, int32_t d, const void* dy,
@@ -170,9 +433,9 @@ moe_status moe_layernorm_backward(int32_t dtype, int32_t wdtype, int64_t rows, i
                                   size_t ws_bytes, moe_stream_t stream) {
   if (!ln_args(dtype, wdtype, rows, d) || lddy < d || ldx < d || lddx < d || (dadd != nullptr && ldadd < d))
     return MOE_ERR_INVALID_ARG;
-  const size_t es = dtype_bytes(dtype), wb = dtype_bytes(wdtype);
-  if (!elem_ok_or_null(weight, wb) || !elem_ok_or_null(dadd, es) || !elem_ok_or_null(dweight, wb) ||
-      !elem_ok_or_null(dbias, wb))
+  const size_t es = dtype_bytes(dtype), wes = dtype_bytes(wdtype);
+  if (!elem_ok_or_null(weight, wes) || !elem_ok_or_null(dadd, es) || !elem_ok_or_null(dweight, wes) ||
+      !elem_ok_or_null(dbias, wes))
     return MOE_ERR_INVALID_ARG;
   const bool sums = dweight != nullptr || dbias != nullptr;
   if (sums && (ws == nullptr || !aligned_to(ws, 128))) return MOE_ERR_INVALID_ARG;
@@ -181,33 +444,40 @@ moe_status moe_layernorm_backward(int32_t dtype, int32_t wdtype, int64_t rows, i
     return MOE_ERR_INVALID_ARG;
   if (rows == 0 && !sums) return MOE_OK;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int v = ln_vec(es, wes, d,
+                       bits(dy) | bits(x) | bits(dx) | bits(dadd) | (uintptr_t)(lddy * es) | (uintptr_t)(ldx * es) |
+                           (uintptr_t)(lddx * es) | (uintptr_t)((dadd ? ldadd : 0) * es),
+                       bits(weight));
+  const int grid = ln_blocks(rows, d);
   return ops_status(ln_types(dtype, wdtype, [&](auto t, auto wt) {
     using T = decltype(t);
     using W = decltype(wt);
-    float* part = static_cast<float*>(ws);
-    const int np = (int)ln_parts(rows), nc = (d + kLnThreads - 1) / kLnThreads;
+    const T *dyp = static_cast<const T*>(dy), *xp = static_cast<const T*>(x), *ap = static_cast<const T*>(dadd);
+    const W* wp = static_cast<const W*>(weight);
+    T* dxp = static_cast<T*>(dx);
+    float* part = sums ? static_cast<float*>(ws) : nullptr;
     cudaError_t e = cudaSuccess;
-    if (sums && rows > 0) {
-      TraceScope ts("layernorm_partial", st);
-      for (int p = 0; p < np && e == cudaSuccess; p += 65535) {
-        const int n = np - p < 65535 ? np - p : 65535;
-        ln_partial_kernel<T><<<dim3(nc, n), kLnThreads, 0, st>>>(
-            static_cast<const T*>(dy) + (size_t)p * kLnRows * lddy, lddy,
-            static_cast<const T*>(x) + (size_t)p * kLnRows * ldx, ldx, mean + (size_t)p * kLnRows,
-            rstd + (size_t)p * kLnRows, part + (size_t)p * 2 * d, rows - (int64_t)p * kLnRows, d);
-        e = cudaGetLastError();
-      }
+    if (rows > 0) {
+      TraceScope ts("layernorm_backward", st);
+      if (d > kBlockRowMax)
+        ln_backward_loop_kernel<T, W><<<grid, kLoopThreads, 0, st>>>(dyp, lddy, xp, ldx, wp, mean, rstd, ap, ldadd, dxp,
+                                                                     lddx, part, rows, d);
+      else
+        ln_with_vec<T>(v, [&](auto vc) {
+          constexpr int V = decltype(vc)::value;
+          if (d <= kWarpRowMax)
+            ln_backward_kernel<T, W, V, false><<<grid, 32 * kLnWarps, 0, st>>>(
+                dyp, lddy, xp, ldx, wp, mean, rstd, ap, ldadd, dxp, lddx, part, rows, d);
+          else
+            ln_backward_kernel<T, W, V, true><<<grid, ln_block_threads(d), 0, st>>>(
+                dyp, lddy, xp, ldx, wp, mean, rstd, ap, ldadd, dxp, lddx, part, rows, d);
+        });
+      e = cudaGetLastError();
     }
     if (e == cudaSuccess && sums) {
       TraceScope ts("layernorm_reduce", st);
-      ln_reduce_kernel<W><<<nc, kLnThreads, 0, st>>>(part, np, static_cast<W*>(dweight), static_cast<W*>(dbias), d);
-      e = cudaGetLastError();
-    }
-    if (e == cudaSuccess && rows > 0) {
-      TraceScope ts("layernorm_backward", st);
-      ln_backward_kernel<T, W><<<(int)(rows < 65535 ? rows : 65535), kLnThreads, 0, st>>>(
-          static_cast<const T*>(dy), lddy, static_cast<const T*>(x), ldx, static_cast<const W*>(weight), mean,
-          rstd, static_cast<const T*>(dadd), ldadd, static_cast<T*>(dx), lddx, rows, d);
+      ln_reduce_kernel<W><<<(2 * d + 31) / 32, 256, 0, st>>>(part, grid, static_cast<W*>(dweight),
+                                                             static_cast<W*>(dbias), d);
       e = cudaGetLastError();
     }
     return e;
