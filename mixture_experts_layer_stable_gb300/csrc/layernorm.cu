@@ -8,10 +8,13 @@
 // Every call is bound by HBM (about ten operations an element), so a row is read
 // once: a group of threads (a warp or a block) holds it in registers, the mean and
 // then the sum of squared distances from it are taken from there (two passes over
-// registers cost nothing and keep the variance of rows whose mean is large), and
-// the groups are persistent with the next row's loads in flight while a row is
-// reduced.  The backward's groups add their rows' dw and db in registers and leave
-// one partial sum a block; a second kernel adds those in block order.
+// registers cost little and keep the variance of rows whose mean is large).  The
+// groups are persistent.  Where rows are 16-byte aligned a block copies the rows
+// that follow into a ring in shared memory (cp.async, every thread its own
+// elements, so the ring needs no barrier): with only the next row in flight, in
+// registers, an SM has 28 KB of the backward's rows under way, half of what HBM's
+// latency asks for.  The backward's groups add their rows' dw and db in registers
+// and leave one partial sum a block; a second kernel adds those in block order.
 #include "ops_common.cuh"
 
 namespace moe {
@@ -66,44 +69,94 @@ struct Part {
   __device__ __forceinline__ float at(int i, int j) const { return to_f32(v[i].e[j]); }
 };
 
-// V consecutive values of an optional array (NULL: all `other`).
-template <typename W, int V>
-__device__ __forceinline__ void weights_at(const W* __restrict__ w, int c, float other, float (&o)[V]) {
-  if (w == nullptr) {
+// The weights of the same elements (NULL: all `other`).
+template <typename W, int V, int N>
+struct Weights {
+  static constexpr int P = V * sizeof(W) > 16 ? 16 / sizeof(W) : V;  // at most 16 bytes a load
+  Vec<W, P> v[N][V / P];
+  __device__ __forceinline__ void load(const W* __restrict__ w, float other, int d, int tid, int nt) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) o[j] = other;
-    return;
+    for (int i = 0; i < N; ++i) {
+      const int c = (i * nt + tid) * V;
+#pragma unroll
+      for (int j = 0; j < V / P; ++j) {
+        if (w != nullptr && c < d) v[i][j] = load_vec<W, P>(w + c + j * P);
+        else
+#pragma unroll
+          for (int q = 0; q < P; ++q) v[i][j].e[q] = from_f32<W>(other);
+      }
+    }
   }
-  constexpr int P = V * sizeof(W) > 16 ? 16 / sizeof(W) : V;  // at most 16 bytes a load
+  __device__ __forceinline__ float at(int i, int j) const { return to_f32(v[i][j / P].e[j % P]); }
+};
+
+// Copies of one thread's vectors of a row into its places of a ring slot.
+template <typename T, int V, int N>
+__device__ __forceinline__ void ring_copy(T* slot, const T* __restrict__ row, int d, int tid, int nt) {
 #pragma unroll
-  for (int j = 0; j < V; j += P) {
-    const Vec<W, P> v = load_vec<W, P>(w + c + j);
-#pragma unroll
-    for (int q = 0; q < P; ++q) o[j + q] = to_f32(v.e[q]);
+  for (int i = 0; i < N; ++i) {
+    const int c = (i * nt + tid) * V;
+    if (c < d)  // (only instances with V * sizeof(T) = 16 have a ring)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                       static_cast<uint32_t>(__cvta_generic_to_shared(slot + c))),
+                   "l"(row + c)
+                   : "memory");
   }
 }
+__device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void ring_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
-template <typename T, typename W, int V, bool BLOCK>
+// RING: rows of the ring in shared memory (block form, 16-byte vectors), or 0: the
+// next row is loaded into registers.
+template <typename T, typename W, int V, bool BLOCK, int RING>
 __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
     ln_forward_kernel(const T* x, int64_t ldx, const W* __restrict__ w, const W* __restrict__ b, float eps, T* y,
                       int64_t ldy, float* __restrict__ mean, float* __restrict__ rstd, int64_t rows, int d) {
   constexpr int N = kElems / V;
+  extern __shared__ __align__(16) uint8_t ring_mem[];
   __shared__ float sh[32];
   const int tid = BLOCK ? threadIdx.x : threadIdx.x & 31, nt = BLOCK ? blockDim.x : 32;
   const int64_t first = BLOCK ? blockIdx.x : blockIdx.x * (int64_t)kLnWarps + (threadIdx.x >> 5);
   const int64_t step = BLOCK ? gridDim.x : gridDim.x * (int64_t)kLnWarps;
   const float inv_d = 1.0f / (float)d;
+  T* ring = reinterpret_cast<T*>(ring_mem);
   Part<T, V, N> cur, next;
-  if (first < rows) next.load(x + first * ldx, d, tid, nt);
+  Weights<W, V, N> wv, bv;
+  int slot = 0;
+  if constexpr (RING > 0) {
+#pragma unroll
+    for (int i = 0; i < RING; ++i) {
+      if (first + i * step < rows) ring_copy<T, V, N>(ring + i * d, x + (first + i * step) * ldx, d, tid, nt);
+      ring_commit();
+    }
+  } else if (first < rows) {
+    next.load(x + first * ldx, d, tid, nt);
+  }
+  wv.load(w, 1.f, d, tid, nt);
+  bv.load(b, 0.f, d, tid, nt);
   for (int64_t r = first; r < rows; r += step) {
-    cur = next;
-    if (r + step < rows) next.load(x + (r + step) * ldx, d, tid, nt);
+    if constexpr (RING > 0) {
+      ring_wait<RING - 1>();
+      cur.load(ring + slot * d, d, tid, nt);
+    } else {
+      cur = next;
+      if (r + step < rows) next.load(x + (r + step) * ldx, d, tid, nt);
+    }
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
       for (int j = 0; j < V; ++j) s += cur.at(i, j);
     const float mu = group_sum<BLOCK>(s, sh) / (float)d;
+    if constexpr (RING > 0) {
+      // this thread's elements have been read: the row that takes their place
+      if (r + RING * step < rows) ring_copy<T, V, N>(ring + slot * d, x + (r + RING * step) * ldx, d, tid, nt);
+      ring_commit();
+      if (++slot == RING) slot = 0;
+    }
     s = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -123,12 +176,9 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
     for (int i = 0; i < N; ++i) {
       const int c = (i * nt + tid) * V;
       if (c >= d) break;
-      float wv[V], bv[V];
-      weights_at<W, V>(w, c, 1.f, wv);
-      weights_at<W, V>(b, c, 0.f, bv);
       Vec<T, V> o;
 #pragma unroll
-      for (int j = 0; j < V; ++j) o.e[j] = from_f32<T>(fmaf((cur.at(i, j) - mu) * rs, wv[j], bv[j]));
+      for (int j = 0; j < V; ++j) o.e[j] = from_f32<T>(fmaf((cur.at(i, j) - mu) * rs, wv.at(i, j), bv.at(i, j)));
       store_vec<T, V>(y + r * ldy + c, o);
     }
   }
@@ -136,46 +186,69 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
 
 // dx of the group's rows; with part, the rows' sums of dy * xh and dy to
 // part[block][0 / 1][d].
-template <typename T, typename W, int V, bool BLOCK>
+template <typename T, typename W, int V, bool BLOCK, int RING>
 __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
     ln_backward_kernel(const T* dy, int64_t lddy, const T* __restrict__ x, int64_t ldx, const W* __restrict__ w,
                        const float* __restrict__ mean, const float* __restrict__ rstd, const T* dadd, int64_t ldadd,
                        T* dx, int64_t lddx, float* __restrict__ part, int64_t rows, int d) {
   constexpr int N = kElems / V;
+  extern __shared__ __align__(16) uint8_t ring_mem[];
   __shared__ float2 sh[32];
   const int tid = BLOCK ? threadIdx.x : threadIdx.x & 31, nt = BLOCK ? blockDim.x : 32;
   const int64_t first = BLOCK ? blockIdx.x : blockIdx.x * (int64_t)kLnWarps + (threadIdx.x >> 5);
   const int64_t step = BLOCK ? gridDim.x : gridDim.x * (int64_t)kLnWarps;
   const float inv_d = 1.0f / (float)d;
+  T* ring = reinterpret_cast<T*>(ring_mem);
   float aw[N][V] = {}, ab[N][V] = {};
   Part<T, V, N> cx, cy, nx, ny;
+  Weights<W, V, N> wv;
   float nmu = 0.f, nrs = 0.f;
-  if (first < rows) {
+  int slot = 0;
+  auto copy_in = [&](int sl, int64_t r) {
+    ring_copy<T, V, N>(ring + (2 * sl) * d, x + r * ldx, d, tid, nt);
+    ring_copy<T, V, N>(ring + (2 * sl + 1) * d, dy + r * lddy, d, tid, nt);
+  };
+  if constexpr (RING > 0) {
+#pragma unroll
+    for (int i = 0; i < RING; ++i) {
+      if (first + i * step < rows) copy_in(i, first + i * step);
+      ring_commit();
+    }
+  } else if (first < rows) {
     nx.load(x + first * ldx, d, tid, nt);
     ny.load(dy + first * lddy, d, tid, nt);
+  }
+  if (first < rows) {
     nmu = __ldg(mean + first);
     nrs = __ldg(rstd + first);
   }
+  wv.load(w, 1.f, d, tid, nt);
   for (int64_t r = first; r < rows; r += step) {
-    cx = nx;
-    cy = ny;
     const float mu = nmu, rs = nrs;
     if (r + step < rows) {
-      nx.load(x + (r + step) * ldx, d, tid, nt);
-      ny.load(dy + (r + step) * lddy, d, tid, nt);
       nmu = __ldg(mean + r + step);
       nrs = __ldg(rstd + r + step);
+    }
+    if constexpr (RING > 0) {
+      ring_wait<RING - 1>();
+      cx.load(ring + (2 * slot) * d, d, tid, nt);
+      cy.load(ring + (2 * slot + 1) * d, d, tid, nt);
+    } else {
+      cx = nx;
+      cy = ny;
+      if (r + step < rows) {
+        nx.load(x + (r + step) * ldx, d, tid, nt);
+        ny.load(dy + (r + step) * lddy, d, tid, nt);
+      }
     }
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int c = (i * nt + tid) * V;
       if (c >= d) break;
-      float wv[V];
-      weights_at<W, V>(w, c, 1.f, wv);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const float xh = (cx.at(i, j) - mu) * rs, t = cy.at(i, j), g = t * wv[j];
+        const float xh = (cx.at(i, j) - mu) * rs, t = cy.at(i, j), g = t * wv.at(i, j);
         s1 += g;
         s2 = fmaf(g, xh, s2);
         aw[i][j] = fmaf(t, xh, aw[i][j]);
@@ -183,18 +256,22 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
       }
     }
     const float2 m = group_sum2<BLOCK>(s1, s2, sh);
+    if constexpr (RING > 0) {
+      // this thread's elements have been read: the row that takes their place
+      if (r + RING * step < rows) copy_in(slot, r + RING * step);
+      ring_commit();
+      if (++slot == RING) slot = 0;
+    }
     const float m1 = m.x * inv_d, m2 = m.y * inv_d;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int c = (i * nt + tid) * V;
       if (c >= d) break;
-      float wv[V];
-      weights_at<W, V>(w, c, 1.f, wv);
       Vec<T, V> a, o;
       if (dadd) a = load_vec<T, V>(dadd + r * ldadd + c);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const float xh = (cx.at(i, j) - mu) * rs, g = cy.at(i, j) * wv[j];
+        const float xh = (cx.at(i, j) - mu) * rs, g = cy.at(i, j) * wv.at(i, j);
         float v = rs * (g - m1 - xh * m2);
         if (dadd) v += to_f32(a.e[j]);
         o.e[j] = from_f32<T>(v);
@@ -356,23 +433,48 @@ int ln_vec(size_t es, size_t wes, int d, uintptr_t a, uintptr_t aw) {
 }
 uintptr_t bits(const void* p) { return reinterpret_cast<uintptr_t>(p); }
 
-// f(integral_constant V) for the vector widths of T.
-template <typename T, typename F>
-void ln_with_vec(int v, F f) {
-  if (v == (int)(16 / sizeof(T))) f(std::integral_constant<int, 16 / sizeof(T)>());
-  else if (v == 1) f(std::integral_constant<int, 1>());
-  else if constexpr (sizeof(T) == 2) f(std::integral_constant<int, 2>());
-}
-
 // Threads of a block that takes a row.
 int ln_block_threads(int d) { return ((d + kElems - 1) / kElems + 31) / 32 * 32; }
-// Blocks: about as many as fit on the GPU at once (1024 threads an SM), so that
-// each stays on its rows.
+// Blocks an SM holds at once, for the registers the kernels need (1024 threads).
+int ln_blocks_per_sm(int d) {
+  return 1024 / (d <= kWarpRowMax ? 32 * kLnWarps : d <= kBlockRowMax ? ln_block_threads(d) : kLoopThreads);
+}
+// Blocks of a call: about as many as fit on the GPU, so that each stays on its rows.
 int ln_blocks(int64_t rows, int d) {
-  const int threads = d <= kWarpRowMax ? 32 * kLnWarps : d <= kBlockRowMax ? ln_block_threads(d) : kLoopThreads;
   const int64_t need = d <= kWarpRowMax ? (rows + kLnWarps - 1) / kLnWarps : rows;
-  const int64_t most = (int64_t)num_sms() * (1024 / threads);
+  const int64_t most = (int64_t)num_sms() * ln_blocks_per_sm(d);
   return (int)(need < most ? need : most);
+}
+
+// Launches kern<T, W, V, BLOCK, RING> for the vector width v and the row length,
+// f(kernel tag) doing the launch: block rows of 16-byte vectors go through a ring
+// of 4 rows, 3 where 4 would not fit into the SM's shared memory beside its other
+// blocks.  row_bytes: of all arrays that a ring row holds.
+template <int V_, bool BLOCK_, int RING_>
+struct LnTag {
+  static constexpr int V = V_, RING = RING_;
+  static constexpr bool BLOCK = BLOCK_;
+};
+template <typename T, typename F>
+void ln_pick(int v, int d, size_t row_bytes, F f) {
+  constexpr int VF = 16 / sizeof(T);
+  if (v == VF) {
+    if (d <= kWarpRowMax) return f(LnTag<VF, false, 0>(), (size_t)0);
+    const size_t share = 225 * 1024 / ln_blocks_per_sm(d) - 1024;
+    if (4 * row_bytes <= share) return f(LnTag<VF, true, 4>(), 4 * row_bytes);
+    return f(LnTag<VF, true, 3>(), 3 * row_bytes);
+  }
+  auto plain = [&](auto vc) {
+    constexpr int V = decltype(vc)::value;
+    if (d <= kWarpRowMax) f(LnTag<V, false, 0>(), (size_t)0);
+    else f(LnTag<V, true, 0>(), (size_t)0);
+  };
+  if (v == 1) return plain(std::integral_constant<int, 1>());
+  if constexpr (sizeof(T) == 2) plain(std::integral_constant<int, 2>());
+}
+template <typename K>
+void ln_allow_smem(K kern, size_t bytes) {
+  if (bytes > 40 * 1024) cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
 }  // namespace
@@ -408,14 +510,12 @@ moe_status moe_layernorm_forward(int32_t dtype, int32_t wdtype, int64_t rows, in
     if (d > kBlockRowMax)
       ln_forward_loop_kernel<T, W><<<grid, kLoopThreads, 0, st>>>(xp, ldx, wp, bp, eps, yp, ldy, mean, rstd, rows, d);
     else
-      ln_with_vec<T>(v, [&](auto vc) {
-        constexpr int V = decltype(vc)::value;
-        if (d <= kWarpRowMax)
-          ln_forward_kernel<T, W, V, false><<<grid, 32 * kLnWarps, 0, st>>>(xp, ldx, wp, bp, eps, yp, ldy, mean, rstd,
-                                                                            rows, d);
-        else
-          ln_forward_kernel<T, W, V, true><<<grid, ln_block_threads(d), 0, st>>>(xp, ldx, wp, bp, eps, yp, ldy, mean,
-                                                                                 rstd, rows, d);
+      ln_pick<T>(v, d, d * sizeof(T), [&](auto tag, size_t smem) {
+        using K = decltype(tag);
+        auto kern = ln_forward_kernel<T, W, K::V, K::BLOCK, K::RING>;
+        ln_allow_smem(kern, smem);
+        kern<<<grid, K::BLOCK ? ln_block_threads(d) : 32 * kLnWarps, smem, st>>>(xp, ldx, wp, bp, eps, yp, ldy, mean,
+                                                                               rstd, rows, d);
       });
     return cudaGetLastError();
   }));
@@ -463,14 +563,12 @@ moe_status moe_layernorm_backward(int32_t dtype, int32_t wdtype, int64_t rows, i
         ln_backward_loop_kernel<T, W><<<grid, kLoopThreads, 0, st>>>(dyp, lddy, xp, ldx, wp, mean, rstd, ap, ldadd, dxp,
                                                                      lddx, part, rows, d);
       else
-        ln_with_vec<T>(v, [&](auto vc) {
-          constexpr int V = decltype(vc)::value;
-          if (d <= kWarpRowMax)
-            ln_backward_kernel<T, W, V, false><<<grid, 32 * kLnWarps, 0, st>>>(
-                dyp, lddy, xp, ldx, wp, mean, rstd, ap, ldadd, dxp, lddx, part, rows, d);
-          else
-            ln_backward_kernel<T, W, V, true><<<grid, ln_block_threads(d), 0, st>>>(
-                dyp, lddy, xp, ldx, wp, mean, rstd, ap, ldadd, dxp, lddx, part, rows, d);
+        ln_pick<T>(v, d, 2 * d * sizeof(T), [&](auto tag, size_t smem) {
+          using K = decltype(tag);
+          auto kern = ln_backward_kernel<T, W, K::V, K::BLOCK, K::RING>;
+          ln_allow_smem(kern, smem);
+          kern<<<grid, K::BLOCK ? ln_block_threads(d) : 32 * kLnWarps, smem, st>>>(
+              dyp, lddy, xp, ldx, wp, mean, rstd, ap, ldadd, dxp, lddx, part, rows, d);
         });
       e = cudaGetLastError();
     }

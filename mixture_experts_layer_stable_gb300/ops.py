@@ -13,7 +13,7 @@ import ctypes
 
 import torch
 
-from .binding import MOE_ERR_INVALID_ARG, MoeError, _check, _stream, lib as _base_lib
+from .binding import MOE_ERR_INVALID_ARG, MoeError, _check, _stream as _given_stream, lib as _base_lib
 
 MOE_DT_F32 = 0
 MOE_DT_BF16 = 1
@@ -61,6 +61,16 @@ def lib():
     return _lib
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream, t):
+    """`stream`, or the current stream of t's device."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(t.get_device())
+    return _given_stream(stream)
+
+
 def _need(ok, where):
     if not ok:
         raise MoeError(MOE_ERR_INVALID_ARG, where)
@@ -74,15 +84,18 @@ def _dt(t, where):
 
 def _rows(t, n, d, dtype, where):
     """Row stride of a [n, d] tensor with contiguous rows."""
-    _need(t.dtype == dtype and t.shape == (n, d) and (d == 1 or t.stride(1) == 1), where)
-    return t.stride(0) if n > 1 else max(d, t.stride(0))
+    ld, one = t.stride()
+    if t.dtype != dtype or t.shape != (n, d) or (one != 1 and d != 1):
+        raise MoeError(MOE_ERR_INVALID_ARG, where)
+    return ld if n > 1 else max(d, ld)
 
 
 def _flat(t, n, dtype, where):
     """Pointer of a contiguous tensor of n elements; None stays None."""
     if t is None:
         return None
-    _need(t.dtype == dtype and t.numel() == n and t.is_contiguous(), where)
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        raise MoeError(MOE_ERR_INVALID_ARG, where)
     return t.data_ptr()
 
 
@@ -105,7 +118,7 @@ def moe_layernorm_forward(x, weight, bias, eps, y, mean=None, rstd=None, stream=
     _check(lib().moe_layernorm_forward(
         dt, dt if wt is None else _dt(wt, w), n, d, x.data_ptr(), _rows(x, n, d, x.dtype, w),
         _flat(weight, d, wdtype, w), _flat(bias, d, wdtype, w), eps, y.data_ptr(), _rows(y, n, d, x.dtype, w),
-        _flat(mean, n, torch.float32, w), _flat(rstd, n, torch.float32, w), _stream(stream)), w)
+        _flat(mean, n, torch.float32, w), _flat(rstd, n, torch.float32, w), _stream(stream, x)), w)
 
 
 def moe_layernorm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, ws, dadd=None, stream=None):
@@ -120,7 +133,7 @@ def moe_layernorm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, ws, da
         None if dadd is None else dadd.data_ptr(), 0 if dadd is None else _rows(dadd, n, d, x.dtype, w),
         dx.data_ptr(), _rows(dx, n, d, x.dtype, w), _flat(dweight, d, wt.dtype, w), _flat(dbias, d, wt.dtype, w),
         None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size(),
-        _stream(stream)), w)
+        _stream(stream, x)), w)
 
 
 # ---------------------------------------------------------------- rows by expert
@@ -135,7 +148,7 @@ def moe_sort_rows(ids, counts, offsets, perm, inv, ws, stream=None):
     i32 = torch.int32
     _check(lib().moe_sort_rows(_flat(ids, R, i32, w), R, E, _flat(counts, E, i32, w), _flat(offsets, E + 1, i32, w),
                                _flat(perm, R, i32, w), _flat(inv, R, i32, w), ws.data_ptr(),
-                               ws.numel() * ws.element_size(), _stream(stream)), w)
+                               ws.numel() * ws.element_size(), _stream(stream, ids)), w)
 
 
 def moe_permute(x, k, inv, offsets, xp, stream=None):
@@ -144,7 +157,7 @@ def moe_permute(x, k, inv, offsets, xp, stream=None):
     T, d = x.shape
     _check(lib().moe_permute(_dt(x, w), T, d, k, offsets.numel() - 1, x.data_ptr(), _rows(x, T, d, x.dtype, w),
                              _flat(inv, T * k, torch.int32, w), _flat(offsets, offsets.numel(), torch.int32, w),
-                             _flat(xp, T * k * d, x.dtype, w), _stream(stream)), w)
+                             _flat(xp, T * k * d, x.dtype, w), _stream(stream, x)), w)
 
 
 def moe_unpermute(y, weights, k, inv, offsets, out, base=None, stream=None):
@@ -156,7 +169,7 @@ def moe_unpermute(y, weights, k, inv, offsets, out, base=None, stream=None):
                                _flat(offsets, offsets.numel(), torch.int32, w),
                                None if base is None else base.data_ptr(),
                                0 if base is None else _rows(base, T, d, out.dtype, w), out.data_ptr(),
-                               _rows(out, T, d, out.dtype, w), _stream(stream)), w)
+                               _rows(out, T, d, out.dtype, w), _stream(stream, out)), w)
 
 
 def moe_unpermute_backward(dout, y, weights, k, inv, offsets, dy, dw, stream=None):
@@ -167,7 +180,7 @@ def moe_unpermute_backward(dout, y, weights, k, inv, offsets, dy, dw, stream=Non
         _dt(dout, w), T, d, k, offsets.numel() - 1, dout.data_ptr(), _rows(dout, T, d, dout.dtype, w),
         _flat(y, T * k * d, dout.dtype, w), _flat(weights, T * k, torch.float32, w),
         _flat(inv, T * k, torch.int32, w), _flat(offsets, offsets.numel(), torch.int32, w),
-        _flat(dy, T * k * d, dout.dtype, w), _flat(dw, T * k, torch.float32, w), _stream(stream)), w)
+        _flat(dy, T * k * d, dout.dtype, w), _flat(dw, T * k, torch.float32, w), _stream(stream, dout)), w)
 
 
 # ---------------------------------------------------------------- MXFP4
@@ -189,7 +202,7 @@ def moe_quantize_mxfp4(weights, q, scales, paired=False, stream=None):
     b, K, N = weights.shape
     _check(lib().moe_quantize_mxfp4(_dt(weights, w), _flat(weights, b * K * N, weights.dtype, w), b, K, N, int(paired),
                                     _bytes(q, b * N * (K // 2), w),
-                                    _bytes(scales, moe_mxfp4_weight_scale_bytes(b, K, N), w), _stream(stream)), w)
+                                    _bytes(scales, moe_mxfp4_weight_scale_bytes(b, K, N), w), _stream(stream, weights)), w)
 
 
 def moe_dequantize_mxfp4(q, scales, weights, paired=False, stream=None):
@@ -198,7 +211,7 @@ def moe_dequantize_mxfp4(q, scales, weights, paired=False, stream=None):
     b, K, N = weights.shape
     _check(lib().moe_dequantize_mxfp4(_dt(weights, w), _bytes(q, b * N * (K // 2), w),
                                       _bytes(scales, moe_mxfp4_weight_scale_bytes(b, K, N), w), b, K, N, int(paired),
-                                      _flat(weights, b * K * N, weights.dtype, w), _stream(stream)), w)
+                                      _flat(weights, b * K * N, weights.dtype, w), _stream(stream, weights)), w)
 
 
 def _segments(offsets, where):
@@ -217,7 +230,7 @@ def moe_quantize_mxfp4_rows(x, q, scales, offsets=None, perm=None, k=1, stream=N
     _need(perm is None or rows <= n * k, w)
     _check(lib().moe_quantize_mxfp4_rows(_dt(x, w), rows, K, x.data_ptr(), _rows(x, n, K, x.dtype, w), G, off,
                                          _flat(perm, rows, torch.int32, w), k, _bytes(q, rows * (K // 2), w),
-                                         _bytes(scales, moe_mxfp4_row_scale_bytes(rows, K, G), w), _stream(stream)), w)
+                                         _bytes(scales, moe_mxfp4_row_scale_bytes(rows, K, G), w), _stream(stream, x)), w)
 
 
 def moe_dequantize_mxfp4_rows(q, scales, y, offsets=None, stream=None):
@@ -227,7 +240,7 @@ def moe_dequantize_mxfp4_rows(q, scales, y, offsets=None, stream=None):
     rows, K = y.shape
     _check(lib().moe_dequantize_mxfp4_rows(_dt(y, w), rows, K, _bytes(q, rows * (K // 2), w),
                                            _bytes(scales, moe_mxfp4_row_scale_bytes(rows, K, G), w), G, off,
-                                           y.data_ptr(), _rows(y, rows, K, y.dtype, w), _stream(stream)), w)
+                                           y.data_ptr(), _rows(y, rows, K, y.dtype, w), _stream(stream, y)), w)
 
 
 def moe_mxfp4_product(q, scales, offsets, wq, wscales, act, out, ws, stream=None):
@@ -243,4 +256,4 @@ def moe_mxfp4_product(q, scales, offsets, wq, wscales, act, out, ws, stream=None
                                    _bytes(wq, G * N * (K // 2), w),
                                    _bytes(wscales, moe_mxfp4_weight_scale_bytes(G, K, N), w), act, out.data_ptr(),
                                    _rows(out, rows, n_out, out.dtype, w), ws.data_ptr(),
-                                   ws.numel() * ws.element_size(), _stream(stream)), w)
+                                   ws.numel() * ws.element_size(), _stream(stream, out)), w)
