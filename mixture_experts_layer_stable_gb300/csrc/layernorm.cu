@@ -66,7 +66,8 @@ struct Part {
         for (int j = 0; j < V; ++j) v[i].e[j] = from_f32<T>(0.f);
     }
   }
-  __device__ __forceinline__ float at(int i, int j) const { return to_f32(v[i].e[j]); }
+  // Elements 2k and 2k + 1 of the thread's kElems.
+  __device__ __forceinline__ F2 pair(int k) const { return pair_f32(reinterpret_cast<const T*>(v) + 2 * k); }
 };
 
 // The weights of the same elements (NULL: all `other`).
@@ -87,7 +88,7 @@ struct Weights {
       }
     }
   }
-  __device__ __forceinline__ float at(int i, int j) const { return to_f32(v[i][j / P].e[j % P]); }
+  __device__ __forceinline__ F2 pair(int k) const { return pair_f32(reinterpret_cast<const W*>(v) + 2 * k); }
 };
 
 // Copies of one thread's vectors of a row into its places of a ring slot.
@@ -145,41 +146,47 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
       cur = next;
       if (r + step < rows) next.load(x + (r + step) * ldx, d, tid, nt);
     }
-    float s = 0.f;
+    F2 v[kElems / 2], s(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-#pragma unroll
-      for (int j = 0; j < V; ++j) s += cur.at(i, j);
-    const float mu = group_sum<BLOCK>(s, sh) / (float)d;
+    for (int k = 0; k < kElems / 2; ++k) {
+      v[k] = cur.pair(k);
+      s = add2(s, v[k]);
+    }
+    const float mu = group_sum<BLOCK>(sum2(s), sh) / (float)d;
     if constexpr (RING > 0) {
       // this thread's elements have been read: the row that takes their place
       if (r + RING * step < rows) ring_copy<T, V, N>(ring + slot * d, x + (r + RING * step) * ldx, d, tid, nt);
       ring_commit();
       if (++slot == RING) slot = 0;
     }
-    s = 0.f;
+    s = F2(0.f, 0.f);
+    const F2 neg_mu(-mu, -mu);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if ((i * nt + tid) * V >= d) break;
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float c = cur.at(i, j) - mu;
-        s = fmaf(c, c, s);
+    for (int k = 0; k < kElems / 2; ++k) {
+      const F2 c = add2(v[k], neg_mu);
+      v[k] = c;
+      if (V == 1) {  // the pair's elements are of different vectors
+        const float2 f = c.get();
+        const float c0 = (2 * k * nt + tid) < d ? f.x : 0.f, c1 = ((2 * k + 1) * nt + tid) < d ? f.y : 0.f;
+        s = fma2(F2(c0, c1), F2(c0, c1), s);
+      } else if ((2 * k / V * nt + tid) * V < d) {
+        s = fma2(c, c, s);
       }
     }
-    const float rs = 1.0f / sqrtf(group_sum<BLOCK>(s, sh) * inv_d + eps);
+    const float rs = 1.0f / sqrtf(group_sum<BLOCK>(sum2(s), sh) * inv_d + eps);
     if (tid == 0 && mean != nullptr) {
       mean[r] = mu;
       rstd[r] = rs;
     }
+    Part<T, V, N> o;
+    const F2 rs2(rs, rs);
+#pragma unroll
+    for (int k = 0; k < kElems / 2; ++k)
+      pair_to(reinterpret_cast<T*>(o.v) + 2 * k, fma2(mul2(v[k], rs2), wv.pair(k), bv.pair(k)));
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int c = (i * nt + tid) * V;
-      if (c >= d) break;
-      Vec<T, V> o;
-#pragma unroll
-      for (int j = 0; j < V; ++j) o.e[j] = from_f32<T>(fmaf((cur.at(i, j) - mu) * rs, wv.at(i, j), bv.at(i, j)));
-      store_vec<T, V>(y + r * ldy + c, o);
+      if (c < d) store_vec<T, V>(y + r * ldy + c, o.v[i]);
     }
   }
 }
@@ -199,7 +206,9 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
   const int64_t step = BLOCK ? gridDim.x : gridDim.x * (int64_t)kLnWarps;
   const float inv_d = 1.0f / (float)d;
   T* ring = reinterpret_cast<T*>(ring_mem);
-  float aw[N][V] = {}, ab[N][V] = {};
+  F2 aw[kElems / 2], ab[kElems / 2];
+#pragma unroll
+  for (int k = 0; k < kElems / 2; ++k) aw[k] = ab[k] = F2(0.f, 0.f);
   Part<T, V, N> cx, cy, nx, ny;
   Weights<W, V, N> wv;
   float nmu = 0.f, nrs = 0.f;
@@ -241,70 +250,71 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
         ny.load(dy + (r + step) * lddy, d, tid, nt);
       }
     }
-    float s1 = 0.f, s2 = 0.f;
+    // elements past d: dy and so g are zero
+    F2 xh[kElems / 2], g[kElems / 2], s1(0.f, 0.f), s2(0.f, 0.f);
+    const F2 rs2(rs, rs), off(-mu * rs, -mu * rs);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int c = (i * nt + tid) * V;
-      if (c >= d) break;
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float xh = (cx.at(i, j) - mu) * rs, t = cy.at(i, j), g = t * wv.at(i, j);
-        s1 += g;
-        s2 = fmaf(g, xh, s2);
-        aw[i][j] = fmaf(t, xh, aw[i][j]);
-        ab[i][j] += t;
-      }
+    for (int k = 0; k < kElems / 2; ++k) {
+      const F2 t = cy.pair(k);
+      xh[k] = fma2(cx.pair(k), rs2, off);
+      g[k] = mul2(t, wv.pair(k));
+      s1 = add2(s1, g[k]);
+      s2 = fma2(g[k], xh[k], s2);
+      aw[k] = fma2(t, xh[k], aw[k]);
+      ab[k] = add2(ab[k], t);
     }
-    const float2 m = group_sum2<BLOCK>(s1, s2, sh);
+    const float2 m = group_sum2<BLOCK>(sum2(s1), sum2(s2), sh);
     if constexpr (RING > 0) {
       // this thread's elements have been read: the row that takes their place
       if (r + RING * step < rows) copy_in(slot, r + RING * step);
       ring_commit();
       if (++slot == RING) slot = 0;
     }
-    const float m1 = m.x * inv_d, m2 = m.y * inv_d;
+    // dx = rs g - rs m1 - xh rs m2
+    const float m1 = -rs * (m.x * inv_d), m2 = -rs * (m.y * inv_d);
+    const F2 m1s(m1, m1), m2s(m2, m2);
+    Part<T, V, N> o;
+    if (dadd != nullptr) o.load(dadd + r * ldadd, d, tid, nt);
+#pragma unroll
+    for (int k = 0; k < kElems / 2; ++k) {
+      F2 v = fma2(xh[k], m2s, fma2(g[k], rs2, m1s));
+      if (dadd != nullptr) v = add2(v, o.pair(k));
+      pair_to(reinterpret_cast<T*>(o.v) + 2 * k, v);
+    }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int c = (i * nt + tid) * V;
-      if (c >= d) break;
-      Vec<T, V> a, o;
-      if (dadd) a = load_vec<T, V>(dadd + r * ldadd + c);
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float xh = (cx.at(i, j) - mu) * rs, g = cy.at(i, j) * wv.at(i, j);
-        float v = rs * (g - m1 - xh * m2);
-        if (dadd) v += to_f32(a.e[j]);
-        o.e[j] = from_f32<T>(v);
-      }
-      store_vec<T, V>(dx + r * lddx + c, o);
+      if (c < d) store_vec<T, V>(dx + r * lddx + c, o.v[i]);
     }
   }
   if (part == nullptr) return;
   float* mine = part + (size_t)blockIdx.x * 2 * d;
+  float fw[kElems], fb[kElems];
+#pragma unroll
+  for (int k = 0; k < kElems / 2; ++k) {
+    pair_to(fw + 2 * k, aw[k]);
+    pair_to(fb + 2 * k, ab[k]);
+  }
   if constexpr (BLOCK) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int c = (i * nt + tid) * V;
-      if (c >= d) break;
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        mine[c + j] = aw[i][j];
-        mine[d + c + j] = ab[i][j];
+    for (int k = 0; k < kElems; ++k) {
+      const int c = (k / V * nt + tid) * V + k % V;
+      if (c < d) {
+        mine[c] = fw[k];
+        mine[d + c] = fb[k];
       }
     }
   } else {
     // the warps add theirs one after the other
     __shared__ float acc[2][kWarpRowMax];
-    for (int k = 0; k < kLnWarps; ++k) {
-      if ((threadIdx.x >> 5) == k) {
+    for (int q = 0; q < kLnWarps; ++q) {
+      if ((threadIdx.x >> 5) == q) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int c = (i * nt + tid) * V;
-          if (c >= d) break;
-#pragma unroll
-          for (int j = 0; j < V; ++j) {
-            acc[0][c + j] = (k ? acc[0][c + j] : 0.f) + aw[i][j];
-            acc[1][c + j] = (k ? acc[1][c + j] : 0.f) + ab[i][j];
+        for (int k = 0; k < kElems; ++k) {
+          const int c = (k / V * nt + tid) * V + k % V;
+          if (c < d) {
+            acc[0][c] = (q ? acc[0][c] : 0.f) + fw[k];
+            acc[1][c] = (q ? acc[1][c] : 0.f) + fb[k];
           }
         }
       }

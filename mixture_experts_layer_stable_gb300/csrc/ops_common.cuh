@@ -47,6 +47,65 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// Two fp32 values in a register pair: one instruction does both (each rounded
+// as its scalar form).
+struct F2 {
+  unsigned long long v;
+  __device__ __forceinline__ F2() {}
+  __device__ __forceinline__ F2(float x, float y) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y)); }
+  __device__ __forceinline__ float2 get() const {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+  }
+};
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ float sum2(F2 a) {
+  const float2 f = a.get();
+  return f.x + f.y;
+}
+// Elements 2k and 2k + 1 of an array of T as fp32, and back.
+__device__ __forceinline__ F2 pair_f32(const float* p) { return F2(p[0], p[1]); }
+__device__ __forceinline__ F2 pair_f32(const __nv_bfloat16* p) {
+  const uint32_t u = (uint32_t)__bfloat16_as_ushort(p[0]) | ((uint32_t)__bfloat16_as_ushort(p[1]) << 16);
+  return F2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+}
+__device__ __forceinline__ F2 pair_f32(const __half* p) {
+  const float2 f = __half22float2(__halves2half2(p[0], p[1]));
+  return F2(f.x, f.y);
+}
+__device__ __forceinline__ void pair_to(float* p, F2 v) {
+  const float2 f = v.get();
+  p[0] = f.x;
+  p[1] = f.y;
+}
+__device__ __forceinline__ void pair_to(__nv_bfloat16* p, F2 v) {
+  const float2 f = v.get();
+  const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+  p[0] = h.x;
+  p[1] = h.y;
+}
+__device__ __forceinline__ void pair_to(__half* p, F2 v) {
+  const float2 f = v.get();
+  const __half2 h = __floats2half2_rn(f.x, f.y);
+  p[0] = __low2half(h);
+  p[1] = __high2half(h);
+}
+
 // ------------------------------------------------------------------ host side
 inline size_t dtype_bytes(int dt) { return dt == MOE_DT_F32 ? 4 : 2; }
 inline bool dtype_valid(int dt) { return dt == MOE_DT_F32 || dt == MOE_DT_BF16 || dt == MOE_DT_F16; }
