@@ -27,68 +27,62 @@ constexpr int kBlockRowMax = 512 * kElems;  // a block up to this
 constexpr int kLnWarps = 8;      // warps (rows) of a block in the warp form
 constexpr int kLoopThreads = 512;
 
-// Sum over the group's threads, the same in each.
-template <bool BLOCK>
-__device__ __forceinline__ float2 group_sum2(float a, float b, float2* sh) {
-  a = warp_sum(a);
-  b = warp_sum(b);
-  if constexpr (!BLOCK) return make_float2(a, b);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  __syncthreads();  // the last sum's values have been read
-  if (lane == 0) sh[warp] = make_float2(a, b);
-  __syncthreads();
-  const float2 v = lane < nw ? sh[lane] : make_float2(0.f, 0.f);
-  return make_float2(warp_sum(v.x), warp_sum(v.y));
-}
-template <bool BLOCK>
-__device__ __forceinline__ float group_sum(float a, float* sh) {
-  a = warp_sum(a);
-  if constexpr (!BLOCK) return a;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  __syncthreads();
-  if (lane == 0) sh[warp] = a;
-  __syncthreads();
-  return warp_sum(lane < nw ? sh[lane] : 0.f);
+// Sums of M values over the group's threads, the same in each.
+template <bool BLOCK, int M>
+__device__ __forceinline__ void group_sum(float (&v)[M], float (*sh)[M]) {
+#pragma unroll
+  for (int m = 0; m < M; ++m) v[m] = warp_sum(v[m]);
+  if constexpr (BLOCK) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    __syncthreads();  // the last sums' values have been read
+    if (lane == 0) {
+#pragma unroll
+      for (int m = 0; m < M; ++m) sh[warp][m] = v[m];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < M; ++m) v[m] = warp_sum(lane < nw ? sh[lane][m] : 0.f);
+  }
 }
 
 // The part of a row that one thread holds: N vectors of V elements, vector i at
 // (i * threads + thread) * V; elements past d read as zeros.
 template <typename T, int V, int N>
-struct Part {
-  Vec<T, V> v[N];
+struct Part : Words<T, V * N> {
   __device__ __forceinline__ void load(const T* __restrict__ row, int d, int tid, int nt) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int c = (i * nt + tid) * V;
-      if (c < d) v[i] = load_vec<T, V>(row + c);
-      else
-#pragma unroll
-        for (int j = 0; j < V; ++j) v[i].e[j] = from_f32<T>(0.f);
+      if (c < d) Words<T, V * N>::template load<V>(i, row + c);
+      else Words<T, V * N>::template zero<V>(i);
     }
   }
-  // Elements 2k and 2k + 1 of the thread's kElems.
-  __device__ __forceinline__ F2 pair(int k) const { return pair_f32(reinterpret_cast<const T*>(v) + 2 * k); }
+  __device__ __forceinline__ void store(T* __restrict__ row, int d, int tid, int nt) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = (i * nt + tid) * V;
+      if (c < d) Words<T, V * N>::template store<V>(i, row + c);
+    }
+  }
 };
 
 // The weights of the same elements (NULL: all `other`).
 template <typename W, int V, int N>
-struct Weights {
+struct Weights : Words<W, V * N> {
   static constexpr int P = V * sizeof(W) > 16 ? 16 / sizeof(W) : V;  // at most 16 bytes a load
-  Vec<W, P> v[N][V / P];
   __device__ __forceinline__ void load(const W* __restrict__ w, float other, int d, int tid, int nt) {
+#pragma unroll
+    for (int k = 0; k < V * N / 2; ++k) Words<W, V * N>::set(k, F2(other, other));
+    if (w == nullptr) return;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int c = (i * nt + tid) * V;
+      if (c < d) {
 #pragma unroll
-      for (int j = 0; j < V / P; ++j) {
-        if (w != nullptr && c < d) v[i][j] = load_vec<W, P>(w + c + j * P);
-        else
-#pragma unroll
-          for (int q = 0; q < P; ++q) v[i][j].e[q] = from_f32<W>(other);
+        for (int j = 0; j < V / P; ++j) Words<W, V * N>::template load<P>(i * (V / P) + j, w + c + j * P);
       }
     }
   }
-  __device__ __forceinline__ F2 pair(int k) const { return pair_f32(reinterpret_cast<const W*>(v) + 2 * k); }
 };
 
 // Copies of one thread's vectors of a row into its places of a ring slot.
@@ -110,15 +104,16 @@ __device__ __forceinline__ void ring_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// RING: rows of the ring in shared memory (block form, 16-byte vectors), or 0: the
-// next row is loaded into registers.
+// RING: rows that the ring in shared memory holds (block form, 16-byte vectors), or
+// 0: the next row is loaded into registers.  A slot is filled again after the first
+// barrier of the row that follows its own.
 template <typename T, typename W, int V, bool BLOCK, int RING>
 __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
     ln_forward_kernel(const T* x, int64_t ldx, const W* __restrict__ w, const W* __restrict__ b, float eps, T* y,
                       int64_t ldy, float* __restrict__ mean, float* __restrict__ rstd, int64_t rows, int d) {
   constexpr int N = kElems / V;
   extern __shared__ __align__(16) uint8_t ring_mem[];
-  __shared__ float sh[32];
+  __shared__ float sh[32][1];
   const int tid = BLOCK ? threadIdx.x : threadIdx.x & 31, nt = BLOCK ? blockDim.x : 32;
   const int64_t first = BLOCK ? blockIdx.x : blockIdx.x * (int64_t)kLnWarps + (threadIdx.x >> 5);
   const int64_t step = BLOCK ? gridDim.x : gridDim.x * (int64_t)kLnWarps;
@@ -127,12 +122,13 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
   Part<T, V, N> cur, next;
   Weights<W, V, N> wv, bv;
   int slot = 0;
+  auto copy_in = [&](int sl, int64_t r) {
+    if (r < rows) ring_copy<T, V, N>(ring + sl * d, x + r * ldx, d, tid, nt);
+    ring_commit();
+  };
   if constexpr (RING > 0) {
 #pragma unroll
-    for (int i = 0; i < RING; ++i) {
-      if (first + i * step < rows) ring_copy<T, V, N>(ring + i * d, x + (first + i * step) * ldx, d, tid, nt);
-      ring_commit();
-    }
+    for (int i = 0; i < RING - 1; ++i) copy_in(i, first + i * step);
   } else if (first < rows) {
     next.load(x + first * ldx, d, tid, nt);
   }
@@ -140,26 +136,26 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
   bv.load(b, 0.f, d, tid, nt);
   for (int64_t r = first; r < rows; r += step) {
     if constexpr (RING > 0) {
-      ring_wait<RING - 1>();
+      ring_wait<RING - 2>();
       cur.load(ring + slot * d, d, tid, nt);
     } else {
       cur = next;
       if (r + step < rows) next.load(x + (r + step) * ldx, d, tid, nt);
     }
-    F2 v[kElems / 2], s(0.f, 0.f);
+    F2 v[kElems / 2], t(0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < kElems / 2; ++k) {
       v[k] = cur.pair(k);
-      s = add2(s, v[k]);
+      t = add2(t, v[k]);
     }
-    const float mu = group_sum<BLOCK>(sum2(s), sh) / (float)d;
+    float s[1] = {sum2(t)};
+    group_sum<BLOCK>(s, sh);
     if constexpr (RING > 0) {
-      // this thread's elements have been read: the row that takes their place
-      if (r + RING * step < rows) ring_copy<T, V, N>(ring + slot * d, x + (r + RING * step) * ldx, d, tid, nt);
-      ring_commit();
+      copy_in(slot == 0 ? RING - 1 : slot - 1, r + (RING - 1) * step);
       if (++slot == RING) slot = 0;
     }
-    s = F2(0.f, 0.f);
+    const float mu = s[0] / (float)d;
+    t = F2(0.f, 0.f);
     const F2 neg_mu(-mu, -mu);
 #pragma unroll
     for (int k = 0; k < kElems / 2; ++k) {
@@ -168,26 +164,22 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
       if (V == 1) {  // the pair's elements are of different vectors
         const float2 f = c.get();
         const float c0 = (2 * k * nt + tid) < d ? f.x : 0.f, c1 = ((2 * k + 1) * nt + tid) < d ? f.y : 0.f;
-        s = fma2(F2(c0, c1), F2(c0, c1), s);
+        t = fma2(F2(c0, c1), F2(c0, c1), t);
       } else if ((2 * k / V * nt + tid) * V < d) {
-        s = fma2(c, c, s);
+        t = fma2(c, c, t);
       }
     }
-    const float rs = 1.0f / sqrtf(group_sum<BLOCK>(sum2(s), sh) * inv_d + eps);
+    s[0] = sum2(t);
+    group_sum<BLOCK>(s, sh);
+    const float rs = 1.0f / sqrtf(s[0] * inv_d + eps);
     if (tid == 0 && mean != nullptr) {
       mean[r] = mu;
       rstd[r] = rs;
     }
-    Part<T, V, N> o;
     const F2 rs2(rs, rs);
 #pragma unroll
-    for (int k = 0; k < kElems / 2; ++k)
-      pair_to(reinterpret_cast<T*>(o.v) + 2 * k, fma2(mul2(v[k], rs2), wv.pair(k), bv.pair(k)));
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int c = (i * nt + tid) * V;
-      if (c < d) store_vec<T, V>(y + r * ldy + c, o.v[i]);
-    }
+    for (int k = 0; k < kElems / 2; ++k) cur.set(k, fma2(mul2(v[k], rs2), wv.pair(k), bv.pair(k)));
+    cur.store(y + r * ldy, d, tid, nt);
   }
 }
 
@@ -200,7 +192,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
                        T* dx, int64_t lddx, float* __restrict__ part, int64_t rows, int d) {
   constexpr int N = kElems / V;
   extern __shared__ __align__(16) uint8_t ring_mem[];
-  __shared__ float2 sh[32];
+  __shared__ float sh[32][2];
   const int tid = BLOCK ? threadIdx.x : threadIdx.x & 31, nt = BLOCK ? blockDim.x : 32;
   const int64_t first = BLOCK ? blockIdx.x : blockIdx.x * (int64_t)kLnWarps + (threadIdx.x >> 5);
   const int64_t step = BLOCK ? gridDim.x : gridDim.x * (int64_t)kLnWarps;
@@ -214,15 +206,15 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
   float nmu = 0.f, nrs = 0.f;
   int slot = 0;
   auto copy_in = [&](int sl, int64_t r) {
-    ring_copy<T, V, N>(ring + (2 * sl) * d, x + r * ldx, d, tid, nt);
-    ring_copy<T, V, N>(ring + (2 * sl + 1) * d, dy + r * lddy, d, tid, nt);
+    if (r < rows) {
+      ring_copy<T, V, N>(ring + 2 * sl * d, x + r * ldx, d, tid, nt);
+      ring_copy<T, V, N>(ring + (2 * sl + 1) * d, dy + r * lddy, d, tid, nt);
+    }
+    ring_commit();
   };
   if constexpr (RING > 0) {
 #pragma unroll
-    for (int i = 0; i < RING; ++i) {
-      if (first + i * step < rows) copy_in(i, first + i * step);
-      ring_commit();
-    }
+    for (int i = 0; i < RING - 1; ++i) copy_in(i, first + i * step);
   } else if (first < rows) {
     nx.load(x + first * ldx, d, tid, nt);
     ny.load(dy + first * lddy, d, tid, nt);
@@ -239,8 +231,8 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
       nrs = __ldg(rstd + r + step);
     }
     if constexpr (RING > 0) {
-      ring_wait<RING - 1>();
-      cx.load(ring + (2 * slot) * d, d, tid, nt);
+      ring_wait<RING - 2>();
+      cx.load(ring + 2 * slot * d, d, tid, nt);
       cy.load(ring + (2 * slot + 1) * d, d, tid, nt);
     } else {
       cx = nx;
@@ -263,37 +255,34 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
       aw[k] = fma2(t, xh[k], aw[k]);
       ab[k] = add2(ab[k], t);
     }
-    const float2 m = group_sum2<BLOCK>(sum2(s1), sum2(s2), sh);
+    float s[2] = {sum2(s1), sum2(s2)};
+    group_sum<BLOCK>(s, sh);
     if constexpr (RING > 0) {
-      // this thread's elements have been read: the row that takes their place
-      if (r + RING * step < rows) copy_in(slot, r + RING * step);
-      ring_commit();
+      copy_in(slot == 0 ? RING - 1 : slot - 1, r + (RING - 1) * step);
       if (++slot == RING) slot = 0;
     }
     // dx = rs g - rs m1 - xh rs m2
-    const float m1 = -rs * (m.x * inv_d), m2 = -rs * (m.y * inv_d);
+    const float m1 = -rs * (s[0] * inv_d), m2 = -rs * (s[1] * inv_d);
     const F2 m1s(m1, m1), m2s(m2, m2);
-    Part<T, V, N> o;
-    if (dadd != nullptr) o.load(dadd + r * ldadd, d, tid, nt);
+    if (dadd != nullptr) cy.load(dadd + r * ldadd, d, tid, nt);
 #pragma unroll
     for (int k = 0; k < kElems / 2; ++k) {
       F2 v = fma2(xh[k], m2s, fma2(g[k], rs2, m1s));
-      if (dadd != nullptr) v = add2(v, o.pair(k));
-      pair_to(reinterpret_cast<T*>(o.v) + 2 * k, v);
+      if (dadd != nullptr) v = add2(v, cy.pair(k));
+      cx.set(k, v);
     }
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int c = (i * nt + tid) * V;
-      if (c < d) store_vec<T, V>(dx + r * lddx + c, o.v[i]);
-    }
+    cx.store(dx + r * lddx, d, tid, nt);
   }
   if (part == nullptr) return;
   float* mine = part + (size_t)blockIdx.x * 2 * d;
   float fw[kElems], fb[kElems];
 #pragma unroll
   for (int k = 0; k < kElems / 2; ++k) {
-    pair_to(fw + 2 * k, aw[k]);
-    pair_to(fb + 2 * k, ab[k]);
+    const float2 a = aw[k].get(), c = ab[k].get();
+    fw[2 * k] = a.x;
+    fw[2 * k + 1] = a.y;
+    fb[2 * k] = c.x;
+    fb[2 * k + 1] = c.y;
   }
   if constexpr (BLOCK) {
 #pragma unroll
@@ -333,18 +322,20 @@ template <typename T, typename W>
 __global__ void __launch_bounds__(kLoopThreads)
     ln_forward_loop_kernel(const T* x, int64_t ldx, const W* __restrict__ w, const W* __restrict__ b, float eps, T* y,
                            int64_t ldy, float* __restrict__ mean, float* __restrict__ rstd, int64_t rows, int d) {
-  __shared__ float sh[32];
+  __shared__ float sh[32][1];
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
     const T* xr = x + r * ldx;
-    float s = 0.f;
-    for (int i = threadIdx.x; i < d; i += blockDim.x) s += to_f32(xr[i]);
-    const float mu = group_sum<true>(s, sh) / (float)d;
-    s = 0.f;
+    float s[1] = {0.f};
+    for (int i = threadIdx.x; i < d; i += blockDim.x) s[0] += to_f32(xr[i]);
+    group_sum<true>(s, sh);
+    const float mu = s[0] / (float)d;
+    s[0] = 0.f;
     for (int i = threadIdx.x; i < d; i += blockDim.x) {
       const float c = to_f32(xr[i]) - mu;
-      s = fmaf(c, c, s);
+      s[0] = fmaf(c, c, s[0]);
     }
-    const float rs = 1.0f / sqrtf(group_sum<true>(s, sh) / (float)d + eps);
+    group_sum<true>(s, sh);
+    const float rs = 1.0f / sqrtf(s[0] / (float)d + eps);
     if (threadIdx.x == 0 && mean != nullptr) {
       mean[r] = mu;
       rstd[r] = rs;
@@ -359,24 +350,24 @@ __global__ void __launch_bounds__(kLoopThreads)
     ln_backward_loop_kernel(const T* dy, int64_t lddy, const T* __restrict__ x, int64_t ldx, const W* __restrict__ w,
                             const float* __restrict__ mean, const float* __restrict__ rstd, const T* dadd,
                             int64_t ldadd, T* dx, int64_t lddx, float* __restrict__ part, int64_t rows, int d) {
-  __shared__ float2 sh[32];
+  __shared__ float sh[32][2];
   float* mine = part ? part + (size_t)blockIdx.x * 2 * d : nullptr;
   bool begun = false;
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x, begun = true) {
     const float mu = mean[r], rs = rstd[r];
-    float s1 = 0.f, s2 = 0.f;
+    float s[2] = {0.f, 0.f};
     for (int i = threadIdx.x; i < d; i += blockDim.x) {
       const float t = to_f32(dy[r * lddy + i]), g = t * (w ? to_f32(w[i]) : 1.f);
       const float xh = (to_f32(x[r * ldx + i]) - mu) * rs;
-      s1 += g;
-      s2 = fmaf(g, xh, s2);
+      s[0] += g;
+      s[1] = fmaf(g, xh, s[1]);
       if (mine) {  // a column is one thread's
         mine[i] = fmaf(t, xh, begun ? mine[i] : 0.f);
         mine[d + i] = (begun ? mine[d + i] : 0.f) + t;
       }
     }
-    const float2 m = group_sum2<true>(s1, s2, sh);
-    const float m1 = m.x / (float)d, m2 = m.y / (float)d;
+    group_sum<true>(s, sh);
+    const float m1 = s[0] / (float)d, m2 = s[1] / (float)d;
     for (int i = threadIdx.x; i < d; i += blockDim.x) {
       const float g = to_f32(dy[r * lddy + i]) * (w ? to_f32(w[i]) : 1.f);
       const float xh = (to_f32(x[r * ldx + i]) - mu) * rs;
@@ -445,33 +436,35 @@ uintptr_t bits(const void* p) { return reinterpret_cast<uintptr_t>(p); }
 
 // Threads of a block that takes a row.
 int ln_block_threads(int d) { return ((d + kElems - 1) / kElems + 31) / 32 * 32; }
-// Blocks an SM holds at once, for the registers the kernels need (1024 threads).
-int ln_blocks_per_sm(int d) {
-  return 1024 / (d <= kWarpRowMax ? 32 * kLnWarps : d <= kBlockRowMax ? ln_block_threads(d) : kLoopThreads);
+// Threads an SM holds of each kernel, for the registers they need.
+constexpr int kForwardThreads = 1024, kBackwardThreads = 640;
+int ln_blocks_per_sm(int d, int threads) {
+  const int t = d <= kWarpRowMax ? 32 * kLnWarps : d <= kBlockRowMax ? ln_block_threads(d) : kLoopThreads;
+  return t > threads / 2 ? 1 : threads / t;
 }
 // Blocks of a call: about as many as fit on the GPU, so that each stays on its rows.
-int ln_blocks(int64_t rows, int d) {
+int ln_blocks(int64_t rows, int d, int threads) {
   const int64_t need = d <= kWarpRowMax ? (rows + kLnWarps - 1) / kLnWarps : rows;
-  const int64_t most = (int64_t)num_sms() * ln_blocks_per_sm(d);
+  const int64_t most = (int64_t)num_sms() * ln_blocks_per_sm(d, threads);
   return (int)(need < most ? need : most);
 }
 
-// Launches kern<T, W, V, BLOCK, RING> for the vector width v and the row length,
-// f(kernel tag) doing the launch: block rows of 16-byte vectors go through a ring
-// of 4 rows, 3 where 4 would not fit into the SM's shared memory beside its other
-// blocks.  row_bytes: of all arrays that a ring row holds.
+// The kernel form for the vector width v and the row length, f(tag, ring bytes)
+// doing the launch.  Block rows of 16-byte vectors go through a ring of six rows,
+// three where six would not fit into the block's share of shared memory (row_bytes:
+// of all arrays that a ring row holds).
 template <int V_, bool BLOCK_, int RING_>
 struct LnTag {
   static constexpr int V = V_, RING = RING_;
   static constexpr bool BLOCK = BLOCK_;
 };
 template <typename T, typename F>
-void ln_pick(int v, int d, size_t row_bytes, F f) {
+void ln_pick(int v, int d, int per_sm, size_t row_bytes, F f) {
   constexpr int VF = 16 / sizeof(T);
   if (v == VF) {
     if (d <= kWarpRowMax) return f(LnTag<VF, false, 0>(), (size_t)0);
-    const size_t share = 225 * 1024 / ln_blocks_per_sm(d) - 1024;
-    if (4 * row_bytes <= share) return f(LnTag<VF, true, 4>(), 4 * row_bytes);
+    const size_t share = 225 * 1024 / per_sm - 1024;
+    if (6 * row_bytes <= share) return f(LnTag<VF, true, 6>(), 6 * row_bytes);
     return f(LnTag<VF, true, 3>(), 3 * row_bytes);
   }
   auto plain = [&](auto vc) {
@@ -509,7 +502,7 @@ moe_status moe_layernorm_forward(int32_t dtype, int32_t wdtype, int64_t rows, in
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int v = ln_vec(es, wes, d, bits(x) | bits(y) | (uintptr_t)(ldx * es) | (uintptr_t)(ldy * es),
                        bits(weight) | bits(bias));
-  const int grid = ln_blocks(rows, d);
+  const int grid = ln_blocks(rows, d, kForwardThreads);
   return ops_status(ln_types(dtype, wdtype, [&](auto t, auto wt) {
     using T = decltype(t);
     using W = decltype(wt);
@@ -520,7 +513,7 @@ moe_status moe_layernorm_forward(int32_t dtype, int32_t wdtype, int64_t rows, in
     if (d > kBlockRowMax)
       ln_forward_loop_kernel<T, W><<<grid, kLoopThreads, 0, st>>>(xp, ldx, wp, bp, eps, yp, ldy, mean, rstd, rows, d);
     else
-      ln_pick<T>(v, d, d * sizeof(T), [&](auto tag, size_t smem) {
+      ln_pick<T>(v, d, ln_blocks_per_sm(d, kForwardThreads), d * sizeof(T), [&](auto tag, size_t smem) {
         using K = decltype(tag);
         auto kern = ln_forward_kernel<T, W, K::V, K::BLOCK, K::RING>;
         ln_allow_smem(kern, smem);
@@ -533,7 +526,7 @@ moe_status moe_layernorm_forward(int32_t dtype, int32_t wdtype, int64_t rows, in
 
 size_t moe_layernorm_workspace_bytes(int64_t rows, int32_t d) {
   if (!ln_args(MOE_DT_F32, MOE_DT_F32, rows, d)) return 0;
-  return ((size_t)(ln_blocks(rows, d) + 1) * 2 * d * sizeof(float) + 127) / 128 * 128;
+  return ((size_t)(ln_blocks(rows, d, kBackwardThreads) + 1) * 2 * d * sizeof(float) + 127) / 128 * 128;
 }
 
 moe_status moe_layernorm_backward(int32_t dtype, int32_t wdtype, int64_t rows, int32_t d, const void* dy,
@@ -558,7 +551,7 @@ moe_status moe_layernorm_backward(int32_t dtype, int32_t wdtype, int64_t rows, i
                        bits(dy) | bits(x) | bits(dx) | bits(dadd) | (uintptr_t)(lddy * es) | (uintptr_t)(ldx * es) |
                            (uintptr_t)(lddx * es) | (uintptr_t)((dadd ? ldadd : 0) * es),
                        bits(weight));
-  const int grid = ln_blocks(rows, d);
+  const int grid = ln_blocks(rows, d, kBackwardThreads);
   return ops_status(ln_types(dtype, wdtype, [&](auto t, auto wt) {
     using T = decltype(t);
     using W = decltype(wt);
@@ -573,7 +566,7 @@ moe_status moe_layernorm_backward(int32_t dtype, int32_t wdtype, int64_t rows, i
         ln_backward_loop_kernel<T, W><<<grid, kLoopThreads, 0, st>>>(dyp, lddy, xp, ldx, wp, mean, rstd, ap, ldadd, dxp,
                                                                      lddx, part, rows, d);
       else
-        ln_pick<T>(v, d, 2 * d * sizeof(T), [&](auto tag, size_t smem) {
+        ln_pick<T>(v, d, ln_blocks_per_sm(d, kBackwardThreads), 2 * d * sizeof(T), [&](auto tag, size_t smem) {
           using K = decltype(tag);
           auto kern = ln_backward_kernel<T, W, K::V, K::BLOCK, K::RING>;
           ln_allow_smem(kern, smem);

@@ -78,33 +78,84 @@ __device__ __forceinline__ float sum2(F2 a) {
   const float2 f = a.get();
   return f.x + f.y;
 }
-// Elements 2k and 2k + 1 of an array of T as fp32, and back.
-__device__ __forceinline__ F2 pair_f32(const float* p) { return F2(p[0], p[1]); }
-__device__ __forceinline__ F2 pair_f32(const __nv_bfloat16* p) {
-  const uint32_t u = (uint32_t)__bfloat16_as_ushort(p[0]) | ((uint32_t)__bfloat16_as_ushort(p[1]) << 16);
-  return F2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+// Two elements of T, as the 32-bit words they lie in (one word of two, or two of
+// one), to fp32 and back.  (Arrays of 16-bit values would be taken apart and put
+// together again around every use.)
+template <typename T>
+__device__ __forceinline__ F2 pair_f32(const uint32_t* w);
+template <>
+__device__ __forceinline__ F2 pair_f32<float>(const uint32_t* w) {
+  return F2(__uint_as_float(w[0]), __uint_as_float(w[1]));
 }
-__device__ __forceinline__ F2 pair_f32(const __half* p) {
-  const float2 f = __half22float2(__halves2half2(p[0], p[1]));
+template <>
+__device__ __forceinline__ F2 pair_f32<__nv_bfloat16>(const uint32_t* w) {
+  return F2(__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xFFFF0000u));
+}
+template <>
+__device__ __forceinline__ F2 pair_f32<__half>(const uint32_t* w) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(w));
   return F2(f.x, f.y);
 }
-__device__ __forceinline__ void pair_to(float* p, F2 v) {
+template <typename T>
+__device__ __forceinline__ void pair_to(uint32_t* w, F2 v);
+template <>
+__device__ __forceinline__ void pair_to<float>(uint32_t* w, F2 v) {
   const float2 f = v.get();
-  p[0] = f.x;
-  p[1] = f.y;
+  w[0] = __float_as_uint(f.x);
+  w[1] = __float_as_uint(f.y);
 }
-__device__ __forceinline__ void pair_to(__nv_bfloat16* p, F2 v) {
+template <>
+__device__ __forceinline__ void pair_to<__nv_bfloat16>(uint32_t* w, F2 v) {
   const float2 f = v.get();
-  const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
-  p[0] = h.x;
-  p[1] = h.y;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[0]) : "f"(f.y), "f"(f.x));
 }
-__device__ __forceinline__ void pair_to(__half* p, F2 v) {
+template <>
+__device__ __forceinline__ void pair_to<__half>(uint32_t* w, F2 v) {
   const float2 f = v.get();
-  const __half2 h = __floats2half2_rn(f.x, f.y);
-  p[0] = __low2half(h);
-  p[1] = __high2half(h);
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[0]) : "f"(f.y), "f"(f.x));
 }
+
+// E elements of T in registers, moved V at a time (V * sizeof(T) is 16, 4 or the
+// element's size; 8 for loads too): vector i of them from or to memory at p.
+template <typename T, int E>
+struct Words {
+  static constexpr int kWords = E * (int)sizeof(T) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ F2 pair(int k) const { return pair_f32<T>(w + k * (int)sizeof(T) / 2); }
+  __device__ __forceinline__ void set(int k, F2 v) { pair_to<T>(w + k * (int)sizeof(T) / 2, v); }
+  template <int V>
+  __device__ __forceinline__ void load(int i, const T* p) {
+    if constexpr (V * sizeof(T) == 16) {
+      const uint4 u = *reinterpret_cast<const uint4*>(p);
+      w[4 * i] = u.x;
+      w[4 * i + 1] = u.y;
+      w[4 * i + 2] = u.z;
+      w[4 * i + 3] = u.w;
+    } else if constexpr (V * sizeof(T) == 8) {
+      const uint2 u = *reinterpret_cast<const uint2*>(p);
+      w[2 * i] = u.x;
+      w[2 * i + 1] = u.y;
+    } else if constexpr (V * sizeof(T) == 4) {
+      w[i] = *reinterpret_cast<const uint32_t*>(p);
+    } else {  // one 16-bit element
+      const uint32_t u = *reinterpret_cast<const uint16_t*>(p);
+      w[i / 2] = i % 2 ? w[i / 2] | (u << 16) : u;
+    }
+  }
+  template <int V>
+  __device__ __forceinline__ void zero(int i) {
+    if constexpr (V * sizeof(T) == 16) w[4 * i] = w[4 * i + 1] = w[4 * i + 2] = w[4 * i + 3] = 0;
+    else if constexpr (V * sizeof(T) == 4) w[i] = 0;
+    else if (i % 2 == 0) w[i / 2] = 0;
+  }
+  template <int V>
+  __device__ __forceinline__ void store(int i, T* p) const {
+    if constexpr (V * sizeof(T) == 16)
+      *reinterpret_cast<uint4*>(p) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    else if constexpr (V * sizeof(T) == 4) *reinterpret_cast<uint32_t*>(p) = w[i];
+    else *reinterpret_cast<uint16_t*>(p) = (uint16_t)(w[i / 2] >> (16 * (i % 2)));
+  }
+};
 
 // ------------------------------------------------------------------ host side
 inline size_t dtype_bytes(int dt) { return dt == MOE_DT_F32 ? 4 : 2; }
