@@ -111,6 +111,7 @@ template <typename T, typename W, int V, bool BLOCK, int RING>
 __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
     ln_forward_kernel(const T* x, int64_t ldx, const W* __restrict__ w, const W* __restrict__ b, float eps, T* y,
                       int64_t ldy, float* __restrict__ mean, float* __restrict__ rstd, int64_t rows, int d) {
+  ops_begin();
   constexpr int N = kElems / V;
   extern __shared__ __align__(16) uint8_t ring_mem[];
   __shared__ float sh[32][1];
@@ -190,6 +191,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
     ln_backward_kernel(const T* dy, int64_t lddy, const T* __restrict__ x, int64_t ldx, const W* __restrict__ w,
                        const float* __restrict__ mean, const float* __restrict__ rstd, const T* dadd, int64_t ldadd,
                        T* dx, int64_t lddx, float* __restrict__ part, int64_t rows, int d) {
+  ops_begin();
   constexpr int N = kElems / V;
   extern __shared__ __align__(16) uint8_t ring_mem[];
   __shared__ float sh[32][2];
@@ -323,6 +325,7 @@ __global__ void __launch_bounds__(kLoopThreads)
     ln_forward_loop_kernel(const T* x, int64_t ldx, const W* __restrict__ w, const W* __restrict__ b, float eps, T* y,
                            int64_t ldy, float* __restrict__ mean, float* __restrict__ rstd, int64_t rows, int d) {
   __shared__ float sh[32][1];
+  ops_begin();
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
     const T* xr = x + r * ldx;
     float s[1] = {0.f};
@@ -351,6 +354,7 @@ __global__ void __launch_bounds__(kLoopThreads)
                             const float* __restrict__ mean, const float* __restrict__ rstd, const T* dadd,
                             int64_t ldadd, T* dx, int64_t lddx, float* __restrict__ part, int64_t rows, int d) {
   __shared__ float sh[32][2];
+  ops_begin();
   float* mine = part ? part + (size_t)blockIdx.x * 2 * d : nullptr;
   bool begun = false;
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x, begun = true) {
@@ -378,15 +382,16 @@ __global__ void __launch_bounds__(kLoopThreads)
   }
 }
 
-// dw and db from the blocks' partial sums: 32 columns a block, its 8 warps each
-// a run of the partials, joined in order.
+// dw and db from the blocks' partial sums: 32 columns a block, its 32 warps each a
+// run of the partials, joined in order.
 template <typename W>
-__global__ void __launch_bounds__(256) ln_reduce_kernel(const float* __restrict__ part, int np, W* __restrict__ dw,
-                                                        W* __restrict__ db, int d) {
-  __shared__ float sh[8][32];
+__global__ void __launch_bounds__(1024) ln_reduce_kernel(const float* __restrict__ part, int np, W* __restrict__ dw,
+                                                         W* __restrict__ db, int d) {
+  __shared__ float sh[32][33];
+  ops_begin();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;  // column of [2 d]: dw's, then db's
-  const int per = (np + 7) / 8, p1 = min(np, (warp + 1) * per);
+  const int per = (np + 31) / 32, p1 = min(np, (warp + 1) * per);
   float s = 0.f;
   if (c < 2 * d) {
 #pragma unroll 8
@@ -394,14 +399,14 @@ __global__ void __launch_bounds__(256) ln_reduce_kernel(const float* __restrict_
   }
   sh[warp][lane] = s;
   __syncthreads();
-  if (warp == 0 && c < 2 * d) {
-    s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s += sh[i][lane];
-    if (c < d) {
-      if (dw) dw[c] = from_f32<W>(s);
+  // column `warp` of the block: its 32 sums, one a lane
+  const int cc = blockIdx.x * 32 + warp;
+  s = warp_sum(sh[lane][warp]);
+  if (lane == 0 && cc < 2 * d) {
+    if (cc < d) {
+      if (dw) dw[cc] = from_f32<W>(s);
     } else if (db) {
-      db[c - d] = from_f32<W>(s);
+      db[cc - d] = from_f32<W>(s);
     }
   }
 }
@@ -509,18 +514,19 @@ moe_status moe_layernorm_forward(int32_t dtype, int32_t wdtype, int64_t rows, in
     const T* xp = static_cast<const T*>(x);
     const W *wp = static_cast<const W*>(weight), *bp = static_cast<const W*>(bias);
     T* yp = static_cast<T*>(y);
-    TraceScope ts("layernorm_forward", st);
+    cudaError_t e = cudaSuccess;
     if (d > kBlockRowMax)
-      ln_forward_loop_kernel<T, W><<<grid, kLoopThreads, 0, st>>>(xp, ldx, wp, bp, eps, yp, ldy, mean, rstd, rows, d);
+      e = launch_ops("layernorm_forward", ln_forward_loop_kernel<T, W>, dim3(grid), dim3(kLoopThreads), 0, st, xp, ldx, wp,
+                     bp, eps, yp, ldy, mean, rstd, rows, d);
     else
       ln_pick<T>(v, d, ln_blocks_per_sm(d, kForwardThreads), d * sizeof(T), [&](auto tag, size_t smem) {
         using K = decltype(tag);
         auto kern = ln_forward_kernel<T, W, K::V, K::BLOCK, K::RING>;
         ln_allow_smem(kern, smem);
-        kern<<<grid, K::BLOCK ? ln_block_threads(d) : 32 * kLnWarps, smem, st>>>(xp, ldx, wp, bp, eps, yp, ldy, mean,
-                                                                               rstd, rows, d);
+        e = launch_ops("layernorm_forward", kern, dim3(grid), dim3(K::BLOCK ? ln_block_threads(d) : 32 * kLnWarps), smem,
+                       st, xp, ldx, wp, bp, eps, yp, ldy, mean, rstd, rows, d);
       });
-    return cudaGetLastError();
+    return e;
   }));
 }
 
@@ -561,26 +567,21 @@ moe_status moe_layernorm_backward(int32_t dtype, int32_t wdtype, int64_t rows, i
     float* part = sums ? static_cast<float*>(ws) : nullptr;
     cudaError_t e = cudaSuccess;
     if (rows > 0) {
-      TraceScope ts("layernorm_backward", st);
       if (d > kBlockRowMax)
-        ln_backward_loop_kernel<T, W><<<grid, kLoopThreads, 0, st>>>(dyp, lddy, xp, ldx, wp, mean, rstd, ap, ldadd, dxp,
-                                                                     lddx, part, rows, d);
+        e = launch_ops("layernorm_backward", ln_backward_loop_kernel<T, W>, dim3(grid), dim3(kLoopThreads), 0, st, dyp,
+                       lddy, xp, ldx, wp, mean, rstd, ap, ldadd, dxp, lddx, part, rows, d);
       else
         ln_pick<T>(v, d, ln_blocks_per_sm(d, kBackwardThreads), 2 * d * sizeof(T), [&](auto tag, size_t smem) {
           using K = decltype(tag);
           auto kern = ln_backward_kernel<T, W, K::V, K::BLOCK, K::RING>;
           ln_allow_smem(kern, smem);
-          kern<<<grid, K::BLOCK ? ln_block_threads(d) : 32 * kLnWarps, smem, st>>>(
-              dyp, lddy, xp, ldx, wp, mean, rstd, ap, ldadd, dxp, lddx, part, rows, d);
+          e = launch_ops("layernorm_backward", kern, dim3(grid), dim3(K::BLOCK ? ln_block_threads(d) : 32 * kLnWarps),
+                         smem, st, dyp, lddy, xp, ldx, wp, mean, rstd, ap, ldadd, dxp, lddx, part, rows, d);
         });
-      e = cudaGetLastError();
     }
-    if (e == cudaSuccess && sums) {
-      TraceScope ts("layernorm_reduce", st);
-      ln_reduce_kernel<W><<<(2 * d + 31) / 32, 256, 0, st>>>(part, grid, static_cast<W*>(dweight),
-                                                             static_cast<W*>(dbias), d);
-      e = cudaGetLastError();
-    }
+    if (e == cudaSuccess && sums)
+      e = launch_ops("layernorm_reduce", ln_reduce_kernel<W>, dim3((2 * d + 31) / 32), dim3(1024), 0, st, part, grid,
+                     static_cast<W*>(dweight), static_cast<W*>(dbias), d);
     return e;
   }));
 }

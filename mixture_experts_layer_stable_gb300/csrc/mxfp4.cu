@@ -128,6 +128,7 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const T* __restrict__ x
                                                          int G, const int* __restrict__ off,
                                                          const int* __restrict__ perm, int k, uint8_t* __restrict__ q,
                                                          uint8_t* __restrict__ sc) {
+  ops_begin();
   const int lane = threadIdx.x & 31, KT = (K + 127) / 128, nb = KT * 4;
   const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
   const int64_t first = i - lane;                  // the warp's first block
@@ -184,6 +185,7 @@ __global__ void __launch_bounds__(256) dequant_rows_kernel(const uint8_t* __rest
                                                            const uint8_t* __restrict__ sc, int64_t rows, int K,
                                                            int G, const int* __restrict__ off, int segs, int per,
                                                            T* __restrict__ y, int64_t ldy) {
+  ops_begin();
   const int lane = threadIdx.x & 31, KT = (K + 127) / 128;
   const int64_t w = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5;
   const int64_t p = w / segs;
@@ -458,6 +460,27 @@ __global__ void __launch_bounds__(kThreads4, 1)
   __shared__ alignas(8) uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2], drain;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_most;
+  if (warp == 0 && lane == 0) {
+    for (int i = 0; i < kMaxStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tempty[i], 4);
+    }
+    mbar_init(&drain, 1);
+    s_abort = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_x);
+    tma_prefetch_desc(&tm_x128);
+    tma_prefetch_desc(&tm_w);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&s_tmem), 512);
+    tmem_relinquish();
+  }
+  ops_begin();
   if (blockIdx.x == 0 && threadIdx.x < 2) p.status[threadIdx.x] = 0;
 
   // experts' rows and units
@@ -484,24 +507,7 @@ __global__ void __launch_bounds__(kThreads4, 1)
     if (lane == 0) {
       s_unit[p.G] = run;
       s_most = most;
-      for (int i = 0; i < kMaxStages; ++i) {
-        mbar_init(&full[i], 1);
-        mbar_init(&empty[i], 1);
-      }
-      for (int i = 0; i < 2; ++i) {
-        mbar_init(&tfull[i], 1);
-        mbar_init(&tempty[i], 4);
-      }
-      mbar_init(&drain, 1);
-      s_abort = 0;
-      fence_mbar_init();
-      tma_prefetch_desc(&tm_x);
-      tma_prefetch_desc(&tm_w);
     }
-  }
-  if (warp == 1) {
-    tmem_alloc(smem_u32(&s_tmem), 512);
-    tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
@@ -693,9 +699,7 @@ cudaError_t launch_product(const CUtensorMap& tm_x, const CUtensorMap& tm_x128, 
   // units: at most NT for every expert with a row and every 192 rows
   const int64_t units = (int64_t)p.NT * ((int64_t)p.rows / 192 + (p.G < p.rows ? p.G : p.rows));
   const int grid = units < num_sms() ? (int)units : num_sms();
-  TraceScope ts("mxfp4_product", st);
-  kern<<<grid, kThreads4, smem, st>>>(tm_x, tm_x128, tm_w, p);
-  return cudaGetLastError();
+  return launch_ops("mxfp4_product", kern, dim3(grid), dim3(kThreads4), smem, st, tm_x, tm_x128, tm_w, p);
 }
 
 bool fp4_k(int32_t K) { return K >= 32 && K % 32 == 0 && K <= (1 << 24); }
@@ -767,11 +771,10 @@ moe_status moe_quantize_mxfp4_rows(int32_t dtype, int64_t rows, int32_t K, const
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return ops_status(with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
-    TraceScope ts("quantize_mxfp4_rows", st);
     auto kern = rows16(x, ldx, dtype) ? quant_rows_kernel<T, true> : quant_rows_kernel<T, false>;
     const unsigned grid = (unsigned)((rows * ((K + 127) / 128) * 4 + 255) / 256);
-    kern<<<grid, 256, 0, st>>>(static_cast<const T*>(x), ldx, rows, K, G, offsets, perm, k, q, scales);
-    return cudaGetLastError();
+    return launch_ops("quantize_mxfp4_rows", kern, dim3(grid), dim3(256), 0, st, static_cast<const T*>(x), ldx, rows, K,
+                      G, offsets, perm, k, q, scales);
   }));
 }
 
@@ -785,12 +788,11 @@ moe_status moe_dequantize_mxfp4_rows(int32_t dtype, int64_t rows, int32_t K, con
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return ops_status(with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
-    TraceScope ts("dequantize_mxfp4_rows", st);
     const Segs sg = row_segs(K);
     const unsigned grid = (unsigned)((rows * sg.n + 7) / 8);
     auto kern = rows16(y, ldy, dtype) ? dequant_rows_kernel<T, true> : dequant_rows_kernel<T, false>;
-    kern<<<grid, 256, 0, st>>>(q, scales, rows, K, G, offsets, sg.n, sg.per, static_cast<T*>(y), ldy);
-    return cudaGetLastError();
+    return launch_ops("dequantize_mxfp4_rows", kern, dim3(grid), dim3(256), 0, st, q, scales, rows, K, G, offsets, sg.n,
+                      sg.per, static_cast<T*>(y), ldy);
   }));
 }
 

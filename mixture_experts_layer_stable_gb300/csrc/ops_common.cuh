@@ -142,6 +142,10 @@ struct Words {
       w[i / 2] = i % 2 ? w[i / 2] | (u << 16) : u;
     }
   }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0;
+  }
   template <int V>
   __device__ __forceinline__ void zero(int i) {
     if constexpr (V * sizeof(T) == 16) w[4 * i] = w[4 * i + 1] = w[4 * i + 2] = w[4 * i + 3] = 0;
@@ -157,7 +161,35 @@ struct Words {
   }
 };
 
+// Programmatic dependent launch: a kernel launched by launch_ops may start while the
+// kernel before it in the stream still runs, as soon as every block of that one has
+// started and called ops_begin (or has ended).  ops_begin lets the next kernel in
+// and waits until everything before this one has completed and is visible; it comes
+// before a kernel's first access to global memory.  In a chain of small operators
+// this hides the launch latency of each.
+__device__ __forceinline__ void ops_begin() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // ------------------------------------------------------------------ host side
+template <typename... P, typename... A>
+cudaError_t launch_ops(const char* name, void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                       A... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  TraceScope ts(name, st);
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
 inline size_t dtype_bytes(int dt) { return dt == MOE_DT_F32 ? 4 : 2; }
 inline bool dtype_valid(int dt) { return dt == MOE_DT_F32 || dt == MOE_DT_BF16 || dt == MOE_DT_F16; }
 inline bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }

@@ -1,172 +1,394 @@
 // permute.cu -- rows sorted by expert and back (include/moe_ops.h:
 // moe_sort_rows, moe_permute, moe_unpermute, moe_unpermute_backward).
+//
+// The sort is a counting sort over E + 1 buckets (the last: rows without an
+// expert) and is bound by latency; the moves are bound by HBM.
 #include "ops_common.cuh"
+#include "ptx.cuh"
 
 namespace moe {
 
 namespace {
 
-constexpr int kPmThreads = 256;
-constexpr int kSortChunk = 1024;  // routed rows of one histogram / scatter block
-constexpr int kSortWarps = kPmThreads / 32;
+// ------------------------------------------------------------------ sort
+constexpr int kSortIters = 8;                     // rows a lane holds
+constexpr int kSortBlockRows = 32 * 32 * kSortIters;
+constexpr int kSortCluster = 8;
 
 // Expert of a row, or E for one without an expert.
 __device__ __forceinline__ int bucket(int id, int E) { return (unsigned)id < (unsigned)E ? id : E; }
 
-// hist[b][e]: rows of chunk b in bucket e (e = E: dropped rows).
-__global__ void __launch_bounds__(kPmThreads) sort_hist_kernel(const int* __restrict__ ids, int64_t R, int E,
-                                                               int* __restrict__ hist) {
-  __shared__ int sh[kMaxE + 1];
-  for (int e = threadIdx.x; e <= E; e += blockDim.x) sh[e] = 0;
-  __syncthreads();
-  const int64_t r0 = (int64_t)blockIdx.x * kSortChunk, r1 = min(R, r0 + kSortChunk);
-  for (int64_t r = r0 + threadIdx.x; r < r1; r += blockDim.x) atomicAdd(&sh[bucket(ids[r], E)], 1);
-  __syncthreads();
-  for (int e = threadIdx.x; e <= E; e += blockDim.x) hist[(size_t)blockIdx.x * (E + 1) + e] = sh[e];
+__device__ __forceinline__ int ld_cluster(uint32_t saddr, uint32_t rank) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(saddr, rank)) : "memory");
+  return v;
 }
 
-// One block: hist[b][e] becomes the position of chunk b's first row of bucket e.
-__global__ void __launch_bounds__(1024) sort_scan_kernel(int* __restrict__ hist, int nb, int E,
-                                                         int* __restrict__ counts, int* __restrict__ offsets) {
-  __shared__ int sh[kMaxE + 1];
-  for (int e = threadIdx.x; e <= E; e += blockDim.x) {
+// Rows [blockIdx.x * per_block, ...) of the sort, at most kSortBlockRows, in W
+// warps of whole groups of 32 rows.  Each warp counts its rows by bucket while it
+// ranks them (the rows of a group that share a bucket by warp match, in order);
+// exclusive prefixes over the warps, the blocks and the buckets then give every
+// row its place.  No atomics decide a place, so the order is stable.
+// The blocks' totals: of the one cluster that does the whole sort, from its shared
+// memories; else from `before` [blocks, E + 1], rows in earlier blocks by bucket,
+// and `total` [E + 1].
+template <bool CLUSTER>
+__global__ void __launch_bounds__(1024) sort_kernel(const int* __restrict__ ids, int64_t R, int E, int W, int per_block,
+                                                    const int* __restrict__ before, const int* __restrict__ total,
+                                                    int* __restrict__ counts, int* __restrict__ offsets,
+                                                    int* __restrict__ perm, int* __restrict__ inv) {
+  extern __shared__ int sort_mem[];
+  int* wcnt = sort_mem;                  // [W][E + 1]
+  int* tot = sort_mem + W * (E + 1);     // [E + 1] rows of this block
+  int* start = tot + (E + 1);            // [E + 1] place of this block's first row
+  __shared__ int wsum[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nb = E + 1;
+  for (int i = tid; i < W * nb; i += blockDim.x) wcnt[i] = 0;
+  __syncthreads();
+  ops_begin();
+  const int64_t b0 = blockIdx.x * (int64_t)per_block, b1 = min(R, b0 + per_block);
+  const int per_warp = per_block / W;    // a multiple of 32
+  const int64_t w0 = b0 + warp * per_warp, w1 = min(b1, w0 + per_warp);
+  int e[kSortIters], at[kSortIters];
+  if (warp < W) {
+#pragma unroll
+    for (int i = 0; i < kSortIters; ++i) {
+      const int64_t r = w0 + i * 32 + lane;
+      e[i] = r < w1 ? bucket(__ldg(ids + r), E) : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kSortIters; ++i) {
+      if (w0 + i * 32 >= w1) break;
+      const uint32_t peers = __match_any_sync(0xffffffffu, e[i]);
+      const int first = __ffs(peers) - 1;
+      int base = 0;
+      if (lane == first && e[i] >= 0) {
+        base = wcnt[warp * nb + e[i]];
+        wcnt[warp * nb + e[i]] = base + __popc(peers);
+      }
+      __syncwarp();
+      at[i] = __shfl_sync(0xffffffffu, base, first) + __popc(peers & ((1u << lane) - 1u));
+    }
+  }
+  __syncthreads();
+  for (int b = tid; b < nb; b += blockDim.x) {
     int run = 0;
-    for (int b = 0; b < nb; ++b) {
-      const int c = hist[(size_t)b * (E + 1) + e];
-      hist[(size_t)b * (E + 1) + e] = run;
+    for (int w = 0; w < W; ++w) {
+      const int c = wcnt[w * nb + b];
+      wcnt[w * nb + b] = run;
       run += c;
     }
-    sh[e] = run;
-    if (e < E) counts[e] = run;
+    tot[b] = run;
   }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    int run = 0;
-    for (int e = 0; e <= E; ++e) {
-      const int c = sh[e];
-      sh[e] = run;
-      offsets[e] = run;  // offsets[E]: the rows kept
-      run += c;
+  if constexpr (CLUSTER) cluster_sync();
+  else __syncthreads();
+  // every bucket's rows in all blocks, and in the blocks before this one
+  int all = 0, pre = 0;  // of bucket tid (E <= 1024 threads; the dropped rows' apart)
+  if (tid < E) {
+    if constexpr (CLUSTER) {
+      const uint32_t me = cluster_ctarank(), a = smem_u32(tot + tid);
+#pragma unroll
+      for (uint32_t c = 0; c < kSortCluster; ++c) {
+        const int v = c < gridDim.x ? ld_cluster(a, c) : 0;
+        all += v;
+        if (c < me) pre += v;
+      }
+    } else if (total != nullptr) {
+      all = __ldg(total + tid);
+      pre = __ldg(before + (size_t)blockIdx.x * nb + tid);
+    } else {
+      all = tot[tid];
     }
   }
-  __syncthreads();
-  for (int e = threadIdx.x; e <= E; e += blockDim.x)
-    for (int b = 0; b < nb; ++b) hist[(size_t)b * (E + 1) + e] += sh[e];
-}
-
-// Stable positions of a chunk's rows: each warp counts its rows by bucket,
-// prefixes over the warps, then every row ranks among the equal ones before it.
-__global__ void __launch_bounds__(kPmThreads) sort_scatter_kernel(const int* __restrict__ ids, int64_t R, int E,
-                                                                  const int* __restrict__ hist,
-                                                                  int* __restrict__ perm, int* __restrict__ inv) {
-  __shared__ int wcnt[kSortWarps][kMaxE + 1];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int i = tid; i < kSortWarps * (E + 1); i += blockDim.x) wcnt[i / (E + 1)][i % (E + 1)] = 0;
-  __syncthreads();
-  constexpr int kPerWarp = kSortChunk / kSortWarps;
-  const int64_t w0 = (int64_t)blockIdx.x * kSortChunk + warp * kPerWarp;
-  const int64_t w1 = min(R, w0 + kPerWarp);
-  for (int64_t base = w0; base < w1; base += 32) {
-    const int64_t r = base + lane;
-    const int e = r < w1 ? bucket(ids[r], E) : -1;
-    const uint32_t peers = __match_any_sync(0xffffffffu, e);
-    if (e >= 0 && lane == __ffs(peers) - 1) wcnt[warp][e] += __popc(peers);
-    __syncwarp();
+  int inc = all;  // inclusive scan over the buckets
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
   }
+  if (lane == 31) wsum[warp] = inc;
   __syncthreads();
-  for (int e = tid; e <= E; e += blockDim.x) {
-    int run = hist[(size_t)blockIdx.x * (E + 1) + e];
-    for (int w = 0; w < kSortWarps; ++w) {
-      const int c = wcnt[w][e];
-      wcnt[w][e] = run;
-      run += c;
+  const int nw = blockDim.x >> 5;
+  int below = lane < warp && lane < nw ? wsum[lane] : 0;
+  below = __reduce_add_sync(0xffffffffu, below);
+  const int kept = __reduce_add_sync(0xffffffffu, lane < nw ? wsum[lane] : 0);
+  if (tid < E) {
+    start[tid] = below + inc - all + pre;
+    if (blockIdx.x == 0) {
+      counts[tid] = all;
+      offsets[tid] = below + inc - all;
     }
   }
-  __syncthreads();
-  for (int64_t base = w0; base < w1; base += 32) {
-    const int64_t r = base + lane;
-    const int e = r < w1 ? bucket(ids[r], E) : -1;
-    const uint32_t peers = __match_any_sync(0xffffffffu, e);
-    int p = 0;
-    if (e >= 0) p = wcnt[warp][e] + __popc(peers & ((1u << lane) - 1u));
-    __syncwarp();
-    if (e >= 0 && lane == __ffs(peers) - 1) wcnt[warp][e] += __popc(peers);
-    __syncwarp();
-    if (e >= 0) {
-      perm[p] = (int)r;
+  if (tid == 0) {
+    int drop = 0;
+    if constexpr (CLUSTER) {
+      const uint32_t me = cluster_ctarank(), a = smem_u32(tot + E);
+      for (uint32_t c = 0; c < me; ++c) drop += ld_cluster(a, c);
+    } else if (total != nullptr) {
+      drop = __ldg(before + (size_t)blockIdx.x * nb + E);
+    }
+    start[E] = kept + drop;
+    if (blockIdx.x == 0) offsets[E] = kept;
+  }
+  if constexpr (CLUSTER) cluster_sync();  // no block leaves while others read its totals
+  else __syncthreads();
+  if (warp < W) {
+#pragma unroll
+    for (int i = 0; i < kSortIters; ++i) {
+      if (e[i] < 0) continue;
+      const int r = (int)(w0 + i * 32 + lane);
+      const int p = start[e[i]] + wcnt[warp * nb + e[i]] + at[i];
+      perm[p] = r;
       inv[r] = p;
     }
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kPmThreads) permute_kernel(const T* __restrict__ x, int64_t ldx,
-                                                             const int* __restrict__ inv,
-                                                             const int* __restrict__ kept_p, int k, int d,
-                                                             int64_t T_, T* __restrict__ xp) {
-  const int kept = *kept_p;
-  for (int64_t t = blockIdx.x; t < T_; t += gridDim.x)
-    for (int i = threadIdx.x; i < d; i += blockDim.x) {
-      const T v = x[t * ldx + i];
-      for (int j = 0; j < k; ++j) {
-        const int p = inv[t * k + j];
-        xp[(int64_t)p * d + i] = p < kept ? v : from_f32<T>(0.f);
-      }
-    }
+// More rows than a cluster takes: the blocks' histograms ...
+__global__ void __launch_bounds__(1024) sort_hist_kernel(const int* __restrict__ ids, int64_t R, int E,
+                                                         int* __restrict__ hist) {
+  __shared__ int sh[kMaxE + 1];
+  for (int e = threadIdx.x; e <= E; e += blockDim.x) sh[e] = 0;
+  __syncthreads();
+  ops_begin();
+  const int64_t r0 = blockIdx.x * (int64_t)kSortBlockRows, r1 = min(R, r0 + kSortBlockRows);
+  for (int64_t r = r0 + threadIdx.x; r < r1; r += blockDim.x) atomicAdd(&sh[bucket(__ldg(ids + r), E)], 1);
+  __syncthreads();
+  for (int e = threadIdx.x; e <= E; e += blockDim.x) hist[(size_t)blockIdx.x * (E + 1) + e] = sh[e];
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kPmThreads) unpermute_kernel(const T* __restrict__ y,
-                                                               const float* __restrict__ w,
-                                                               const int* __restrict__ inv,
-                                                               const int* __restrict__ kept_p, int k, int d,
-                                                               int64_t T_, const T* base, int64_t ldbase, T* out,
-                                                               int64_t ldout) {
-  const int kept = *kept_p;
-  for (int64_t t = blockIdx.x; t < T_; t += gridDim.x)
-    for (int i = threadIdx.x; i < d; i += blockDim.x) {
-      float s = base ? to_f32(base[t * ldbase + i]) : 0.f;
-      for (int j = 0; j < k; ++j) {
-        const int p = inv[t * k + j];
-        if (p < kept) s = fmaf(w ? w[t * k + j] : 1.f, to_f32(y[(int64_t)p * d + i]), s);
-      }
-      out[t * ldout + i] = from_f32<T>(s);
-    }
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kPmThreads) unpermute_backward_kernel(
-    const T* __restrict__ dout, int64_t lddout, const T* __restrict__ y, const float* __restrict__ w,
-    const int* __restrict__ inv, const int* __restrict__ kept_p, int k, int d, int64_t R, T* __restrict__ dy,
-    float* __restrict__ dw) {
-  __shared__ float sh[kPmThreads / 32];
-  const int kept = *kept_p;
-  for (int64_t r = blockIdx.x; r < R; r += gridDim.x) {
-    const int64_t t = r / k;
-    const int p = inv[r];
-    const bool live = p < kept;
-    const float wr = live ? (w ? w[r] : 1.f) : 0.f;
-    float s = 0.f;
-    for (int i = threadIdx.x; i < d; i += blockDim.x) {
-      const float g = to_f32(dout[t * lddout + i]);
-      if (dw && live) s = fmaf(g, to_f32(y[(int64_t)p * d + i]), s);
-      dy[(int64_t)p * d + i] = from_f32<T>(live ? wr * g : 0.f);
-    }
-    if (dw) {
-      s = warp_sum(s);
-      __syncthreads();
-      if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = s;
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        float v = 0.f;
-        for (int i = 0; i < kPmThreads / 32; ++i) v += sh[i];
-        dw[r] = v;
-      }
+// ... and their exclusive prefixes over the blocks, in place, with the totals: 32
+// buckets a block, its 32 warps each a run of the histograms.
+__global__ void __launch_bounds__(1024) sort_scan_kernel(int* __restrict__ hist, int blocks, int nb,
+                                                         int* __restrict__ total) {
+  __shared__ int sh[32][33];
+  ops_begin();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
+  const int per = (blocks + 31) / 32, p0 = min(blocks, warp * per), p1 = min(blocks, p0 + per);
+  int sum = 0;
+  if (e < nb) {
+#pragma unroll 8
+    for (int p = p0; p < p1; ++p) sum += __ldcg(hist + (size_t)p * nb + e);
+  }
+  sh[warp][lane] = sum;
+  __syncthreads();
+  if (e >= nb) return;
+  int run = 0, all = 0;
+  for (int w = 0; w < 32; ++w) {
+    if (w == warp) run = all;
+    all += sh[w][lane];
+  }
+  if (warp == 0) total[e] = all;
+  for (int p = p0; p < p1; p += 8) {
+    int c[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) c[u] = p + u < p1 ? __ldcg(hist + (size_t)(p + u) * nb + e) : 0;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (p + u < p1) hist[(size_t)(p + u) * nb + e] = run;
+      run += c[u];
     }
   }
 }
 
-int grid_rows(int64_t n) { return (int)(n < (1 << 30) ? n : (1 << 30)); }
+// ------------------------------------------------------------------ moves
+// Threads are laid over (token, vector of V elements): a block takes `tpb` tokens,
+// or 1 / chunks of one.
+struct Lay {
+  int nv;      // vectors of a row
+  int tpb;     // tokens of a block
+  int chunks;  // blocks of a token (1 when tpb > 1)
+};
+__device__ __forceinline__ bool lay_at(const Lay& l, int64_t T, int64_t& t, int& c) {
+  if (l.chunks > 1) {
+    t = blockIdx.x / l.chunks;
+    c = (int)(blockIdx.x - t * l.chunks) * blockDim.x + threadIdx.x;
+  } else {
+    const int a = threadIdx.x / l.nv;
+    t = blockIdx.x * (int64_t)l.tpb + a;
+    c = threadIdx.x - a * l.nv;
+    if (a >= l.tpb) return false;
+  }
+  return t < T && c < l.nv;
+}
+
+// A token's vector is read once and written to the k places.
+template <typename T, int V>
+__global__ void __launch_bounds__(256) permute_kernel(const T* __restrict__ x, int64_t ldx, const int* __restrict__ inv,
+                                                      const int* __restrict__ kept_p, int k, int d, int64_t tokens,
+                                                      Lay lay, T* __restrict__ xp) {
+  ops_begin();
+  int64_t t;
+  int c;
+  if (!lay_at(lay, tokens, t, c)) return;
+  const int kept = __ldg(kept_p);
+  Words<T, V == 1 ? 2 : V> v, z;
+  z.clear();
+  v.template load<V>(0, x + t * ldx + c * V);
+  const int* pi = inv + t * k;
+#pragma unroll 8
+  for (int j = 0; j < k; ++j) {
+    const int p = __ldg(pi + j);
+    T* dst = xp + (int64_t)p * d + c * V;
+    if (p < kept) v.template store<V>(0, dst);
+    else z.template store<V>(0, dst);
+  }
+}
+
+// The k rows' vectors of a token, eight loads in flight, summed in slot order.
+template <typename T, int V>
+__global__ void __launch_bounds__(256) unpermute_kernel(const T* __restrict__ y, const float* __restrict__ w,
+                                                        const int* __restrict__ inv, const int* __restrict__ kept_p,
+                                                        int k, int d, int64_t tokens, Lay lay, const T* base,
+                                                        int64_t ldbase, T* out, int64_t ldout) {
+  constexpr int E = V == 1 ? 2 : V;  // (a single element is half a pair)
+  ops_begin();
+  int64_t t;
+  int c;
+  if (!lay_at(lay, tokens, t, c)) return;
+  const int kept = __ldg(kept_p);
+  F2 s[E / 2];
+#pragma unroll
+  for (int q = 0; q < E / 2; ++q) s[q] = F2(0.f, 0.f);
+  Words<T, E> v[8];
+  if (base != nullptr) {
+    v[0].clear();
+    v[0].template load<V>(0, base + t * ldbase + c * V);
+#pragma unroll
+    for (int q = 0; q < E / 2; ++q) s[q] = v[0].pair(q);
+  }
+  for (int j0 = 0; j0 < k; j0 += 8) {
+    float wj[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int j = j0 + u;
+      const int p = j < k ? __ldg(inv + t * k + j) : kept;
+      v[u].clear();
+      wj[u] = 0.f;
+      if (p < kept) {
+        v[u].template load<V>(0, y + (int64_t)p * d + c * V);
+        wj[u] = w ? __ldg(w + t * k + j) : 1.f;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (j0 + u >= k) break;
+      const F2 ww(wj[u], wj[u]);
+#pragma unroll
+      for (int q = 0; q < E / 2; ++q) s[q] = fma2(ww, v[u].pair(q), s[q]);
+    }
+  }
+  Words<T, E> o;
+#pragma unroll
+  for (int q = 0; q < E / 2; ++q) o.set(q, s[q]);
+  o.template store<V>(0, out + t * ldout + c * V);
+}
+
+// A block a token: its gradient in registers (kBwdVec vectors a thread, in turns
+// for wider rows), written to the k places with their weights while the k rows of y
+// are read for the scalar products; those are summed over each warp's lanes, then
+// over the warps in order.
+constexpr int kBwdVec = 4;
+template <typename T, int V>
+__global__ void __launch_bounds__(256) unpermute_backward_kernel(
+    const T* __restrict__ dout, int64_t lddout, const T* __restrict__ y, const float* __restrict__ w,
+    const int* __restrict__ inv, const int* __restrict__ kept_p, int k, int d, T* __restrict__ dy,
+    float* __restrict__ dw) {
+  constexpr int E = V == 1 ? 2 : V;
+  __shared__ float sh[8][kMaxK];
+  ops_begin();
+  const int64_t t = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, nw = nt >> 5;
+  const int kept = __ldg(kept_p), span = nt * V * kBwdVec;
+  for (int c0 = 0; c0 < d; c0 += span) {
+    Words<T, E> g[kBwdVec];
+#pragma unroll
+    for (int i = 0; i < kBwdVec; ++i) {
+      const int c = c0 + (i * nt + tid) * V;
+      g[i].clear();
+      if (c < d) g[i].template load<V>(0, dout + t * lddout + c);
+    }
+#pragma unroll 2
+    for (int j = 0; j < k; ++j) {
+      const int p = __ldg(inv + t * k + j);
+      const bool live = p < kept;
+      const float wr = live ? (w ? __ldg(w + t * k + j) : 1.f) : 0.f;
+      const int64_t row = (int64_t)p * d;
+      Words<T, E> v[kBwdVec];
+      if (dw != nullptr && live) {
+#pragma unroll
+        for (int i = 0; i < kBwdVec; ++i) {
+          const int c = c0 + (i * nt + tid) * V;
+          v[i].clear();
+          if (c < d) v[i].template load<V>(0, y + row + c);
+        }
+      }
+      const F2 w2(wr, wr);
+#pragma unroll
+      for (int i = 0; i < kBwdVec; ++i) {
+        const int c = c0 + (i * nt + tid) * V;
+        Words<T, E> o;
+#pragma unroll
+        for (int q = 0; q < E / 2; ++q) o.set(q, live ? mul2(g[i].pair(q), w2) : F2(0.f, 0.f));
+        if (c < d) o.template store<V>(0, dy + row + c);
+      }
+      if (dw != nullptr) {
+        F2 s(0.f, 0.f);
+        if (live) {
+#pragma unroll
+          for (int i = 0; i < kBwdVec; ++i)
+#pragma unroll
+            for (int q = 0; q < E / 2; ++q) s = fma2(g[i].pair(q), v[i].pair(q), s);
+        }
+        const float r = warp_sum(sum2(s));
+        if (lane == 0) sh[warp][j] = c0 ? sh[warp][j] + r : r;
+      }
+    }
+  }
+  if (dw == nullptr) return;
+  __syncthreads();
+  if (tid < k) {
+    float s = 0.f;
+    for (int i = 0; i < nw; ++i) s += sh[i][tid];
+    dw[t * k + tid] = s;
+  }
+}
+
+// Elements moved at once: 16 bytes where every row starts on 16 bytes and d is
+// whole, else 4 bytes, else one.  bits: the or of addresses and row strides.
+int pm_vec(size_t es, int d, uintptr_t bits) {
+  bits |= (uintptr_t)d * es;
+  return bits % 16 == 0 ? (int)(16 / es) : bits % 4 == 0 ? (int)(4 / es) : 1;
+}
+uintptr_t addr(const void* p) { return reinterpret_cast<uintptr_t>(p); }
+
+// f(T{}, integral_constant V).
+template <typename F>
+cudaError_t pm_types(int dtype, int v, F f) {
+  return with_dtype(dtype, [&](auto t) {
+    using T = decltype(t);
+    if (v == (int)(16 / sizeof(T))) return f(t, std::integral_constant<int, 16 / sizeof(T)>());
+    if constexpr (sizeof(T) == 2)
+      if (v == 2) return f(t, std::integral_constant<int, 2>());
+    return f(t, std::integral_constant<int, 1>());
+  });
+}
+
+struct LayLaunch {
+  Lay lay;
+  int threads;
+  int64_t blocks;
+};
+LayLaunch pm_lay(int64_t T, int d, int v) {
+  LayLaunch l;
+  l.lay.nv = d / v;
+  l.lay.chunks = (l.lay.nv + 255) / 256;
+  l.lay.tpb = l.lay.chunks > 1 ? 1 : 256 / l.lay.nv;
+  if (l.lay.tpb > T) l.lay.tpb = (int)T;
+  l.threads = ((l.lay.chunks > 1 ? (l.lay.nv + l.lay.chunks - 1) / l.lay.chunks : l.lay.nv * l.lay.tpb) + 31) / 32 * 32;
+  l.blocks = l.lay.chunks > 1 ? T * l.lay.chunks : (T + l.lay.tpb - 1) / l.lay.tpb;
+  return l;
+}
 
 bool pm_args(int32_t dtype, int64_t T, int32_t d, int32_t k, int32_t E) {
   return dtype_valid(dtype) && T >= 0 && d >= 1 && d <= (1 << 24) && k >= 1 && k <= kMaxK && E >= 1 && E <= kMaxE &&
@@ -174,8 +396,7 @@ bool pm_args(int32_t dtype, int64_t T, int32_t d, int32_t k, int32_t E) {
 }
 
 bool sort_args(int64_t R, int32_t E) { return R >= 0 && R <= ((int64_t)1 << 28) && E >= 1 && E <= kMaxE; }
-
-int64_t sort_chunks(int64_t R) { return (R + kSortChunk - 1) / kSortChunk; }
+int64_t sort_blocks(int64_t R) { return (R + kSortBlockRows - 1) / kSortBlockRows; }
 
 }  // namespace
 
@@ -187,7 +408,7 @@ extern "C" {
 
 size_t moe_sort_workspace_bytes(int64_t R, int32_t E) {
   if (!sort_args(R, E)) return 0;
-  return ((size_t)(sort_chunks(R) + 1) * (E + 1) * sizeof(int) + 127) / 128 * 128;
+  return ((size_t)(sort_blocks(R) + 2) * (E + 1) * sizeof(int) + 127) / 128 * 128;
 }
 
 moe_status moe_sort_rows(const int32_t* ids, int64_t R, int32_t E, int32_t* counts, int32_t* offsets,
@@ -197,21 +418,54 @@ moe_status moe_sort_rows(const int32_t* ids, int64_t R, int32_t E, int32_t* coun
   if (R > 0 && (!elem_ok(ids, 4) || !elem_ok(perm, 4) || !elem_ok(inv, 4))) return MOE_ERR_INVALID_ARG;
   if (ws_bytes < moe_sort_workspace_bytes(R, E)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  // one block up to 1024 rows, one cluster of 8 up to 65536, else a histogram, its
+  // scan and a block for every 8192 rows
+  const bool big = R > (int64_t)kSortCluster * kSortBlockRows, cluster = !big && R > 1024;
+  const int64_t share = big ? kSortBlockRows : cluster ? (R + kSortCluster - 1) / kSortCluster : R;
+  const int groups = (int)((share + 31) / 32);
+  const int W = groups < 1 ? 1 : groups < 32 ? groups : 32;
+  const int per_block = (groups + W - 1) / W * W * 32;
+  const int threads = W * 32 > E ? W * 32 : (E + 31) / 32 * 32;
+  const size_t smem = (size_t)(W + 2) * (E + 1) * sizeof(int);
   int* hist = static_cast<int*>(ws);
-  const int nb = (int)sort_chunks(R);
-  if (nb > 0) {
-    TraceScope ts("sort_hist", st);
-    sort_hist_kernel<<<nb, kPmThreads, 0, st>>>(ids, R, E, hist);
+  cudaError_t e = cudaSuccess;
+  if (cluster) {
+    auto kern = sort_kernel<true>;
+    if (smem > 40 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kSortCluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kSortCluster);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    TraceScope ts("sort_rows", st);
+    if (e == cudaSuccess)
+      e = cudaLaunchKernelEx(&cfg, kern, (const int*)ids, R, (int)E, W, per_block, (const int*)nullptr,
+                             (const int*)nullptr, (int*)counts, (int*)offsets, (int*)perm, (int*)inv);
+    return ops_status(e);
   }
-  {
-    TraceScope ts("sort_scan", st);
-    sort_scan_kernel<<<1, 1024, 0, st>>>(hist, nb, E, counts, offsets);
+  const int blocks = big ? (int)sort_blocks(R) : 1;
+  int* total = hist + (size_t)blocks * (E + 1);
+  if (big) {
+    e = launch_ops("sort_hist", sort_hist_kernel, dim3(blocks), dim3(1024), 0, st, ids, R, E, hist);
+    if (e == cudaSuccess)
+      e = launch_ops("sort_scan", sort_scan_kernel, dim3((E + 1 + 31) / 32), dim3(1024), 0, st, hist, blocks, E + 1,
+                     total);
   }
-  if (nb > 0) {
-    TraceScope ts("sort_scatter", st);
-    sort_scatter_kernel<<<nb, kPmThreads, 0, st>>>(ids, R, E, hist, perm, inv);
-  }
-  return ops_status(cudaGetLastError());
+  auto kern = sort_kernel<false>;
+  if (e == cudaSuccess && smem > 40 * 1024)
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess)
+    e = launch_ops("sort_rows", kern, dim3(blocks), dim3(threads), smem, st, ids, R, E, W, per_block,
+                   big ? hist : nullptr, big ? total : nullptr, counts, offsets, perm, inv);
+  return ops_status(e);
 }
 
 moe_status moe_permute(int32_t dtype, int64_t T, int32_t d, int32_t k, int32_t E, const void* x, int64_t ldx,
@@ -221,12 +475,12 @@ moe_status moe_permute(int32_t dtype, int64_t T, int32_t d, int32_t k, int32_t E
   const size_t es = dtype_bytes(dtype);
   if (!elem_ok(x, es) || !elem_ok(xp, es) || !elem_ok(inv, 4) || !elem_ok(offsets, 4)) return MOE_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return ops_status(with_dtype(dtype, [&](auto t) {
+  const int v = pm_vec(es, d, addr(x) | addr(xp) | (uintptr_t)(ldx * es));
+  const LayLaunch l = pm_lay(T, d, v);
+  return ops_status(pm_types(dtype, v, [&](auto t, auto vc) {
     using U = decltype(t);
-    TraceScope ts("permute", st);
-    permute_kernel<U><<<grid_rows(T), kPmThreads, 0, st>>>(static_cast<const U*>(x), ldx, inv, offsets + E, k, d, T,
-                                                           static_cast<U*>(xp));
-    return cudaGetLastError();
+    return launch_ops("permute", permute_kernel<U, decltype(vc)::value>, dim3((unsigned)l.blocks), dim3(l.threads), 0,
+                      st, static_cast<const U*>(x), ldx, inv, offsets + E, k, d, T, l.lay, static_cast<U*>(xp));
   }));
 }
 
@@ -240,13 +494,14 @@ moe_status moe_unpermute(int32_t dtype, int64_t T, int32_t d, int32_t k, int32_t
       !elem_ok(inv, 4) || !elem_ok(offsets, 4))
     return MOE_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return ops_status(with_dtype(dtype, [&](auto t) {
+  const int v = pm_vec(es, d, addr(y) | addr(out) | (uintptr_t)(ldout * es) | addr(base) |
+                                  (uintptr_t)((base ? ldbase : 0) * es));
+  const LayLaunch l = pm_lay(T, d, v);
+  return ops_status(pm_types(dtype, v, [&](auto t, auto vc) {
     using U = decltype(t);
-    TraceScope ts("unpermute", st);
-    unpermute_kernel<U><<<grid_rows(T), kPmThreads, 0, st>>>(static_cast<const U*>(y), w, inv, offsets + E, k, d, T,
-                                                             static_cast<const U*>(base), ldbase,
-                                                             static_cast<U*>(out), ldout);
-    return cudaGetLastError();
+    return launch_ops("unpermute", unpermute_kernel<U, decltype(vc)::value>, dim3((unsigned)l.blocks), dim3(l.threads),
+                      0, st, static_cast<const U*>(y), w, inv, offsets + E, k, d, T, l.lay,
+                      static_cast<const U*>(base), ldbase, static_cast<U*>(out), ldout);
   }));
 }
 
@@ -260,13 +515,14 @@ moe_status moe_unpermute_backward(int32_t dtype, int64_t T, int32_t d, int32_t k
       !elem_ok_or_null(dw, 4) || (dw != nullptr && !elem_ok(y, es)))
     return MOE_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return ops_status(with_dtype(dtype, [&](auto t) {
+  const int v = pm_vec(es, d, addr(dout) | (uintptr_t)(lddout * es) | addr(dy) | (dw ? addr(y) : 0));
+  const int need = ((d / v + kBwdVec - 1) / kBwdVec + 31) / 32 * 32;
+  const int threads = need < 256 ? need : 256;
+  return ops_status(pm_types(dtype, v, [&](auto t, auto vc) {
     using U = decltype(t);
-    TraceScope ts("unpermute_backward", st);
-    unpermute_backward_kernel<U><<<grid_rows(T * k), kPmThreads, 0, st>>>(
-        static_cast<const U*>(dout), lddout, static_cast<const U*>(y), w, inv, offsets + E, k, d, T * k,
-        static_cast<U*>(dy), dw);
-    return cudaGetLastError();
+    return launch_ops("unpermute_backward", unpermute_backward_kernel<U, decltype(vc)::value>, dim3((unsigned)T),
+                      dim3(threads), 0, st, static_cast<const U*>(dout), lddout, static_cast<const U*>(y), w, inv,
+                      offsets + E, k, d, static_cast<U*>(dy), dw);
   }));
 }
 

@@ -28,6 +28,8 @@ def sort(ids, E, stream=None):
     s = dict(counts=torch.full((E,), -7, **i32), offsets=torch.full((E + 1,), -7, **i32), perm=torch.full((R,), -7, **i32),
              inv=torch.full((R,), -7, **i32))
     ws = torch.full((ops.moe_sort_workspace_bytes(R, E),), 255, dtype=torch.uint8, device="cuda")
+    if stream is not None:
+        torch.cuda.synchronize()  # the fills above run on the current stream
     ops.moe_sort_rows(ids, s["counts"], s["offsets"], s["perm"], s["inv"], ws, stream=stream)
     return s
 
