@@ -192,10 +192,10 @@ __global__ void __launch_bounds__(1024) sort_scan_kernel(int* __restrict__ hist,
 }
 
 // ------------------------------------------------------------------ moves
-// Threads are laid over (token, vector of V elements): a block takes `tpb` tokens,
-// or 1 / chunks of one.
+// Threads are laid over (token, unit of its row): a block takes `tpb` tokens, or
+// 1 / chunks of one.
 struct Lay {
-  int nv;      // vectors of a row
+  int nv;      // threads of a token
   int tpb;     // tokens of a block
   int chunks;  // blocks of a token (1 when tpb > 1)
 };
@@ -212,7 +212,8 @@ __device__ __forceinline__ bool lay_at(const Lay& l, int64_t T, int64_t& t, int&
   return t < T && c < l.nv;
 }
 
-// A token's vector is read once and written to the k places.
+// Rows of whole 16-byte vectors: a token's vector is read once and written to the k
+// places.
 template <typename T, int V>
 __global__ void __launch_bounds__(256) permute_kernel(const T* __restrict__ x, int64_t ldx, const int* __restrict__ inv,
                                                       const int* __restrict__ kept_p, int k, int d, int64_t tokens,
@@ -222,7 +223,7 @@ __global__ void __launch_bounds__(256) permute_kernel(const T* __restrict__ x, i
   int c;
   if (!lay_at(lay, tokens, t, c)) return;
   const int kept = __ldg(kept_p);
-  Words<T, V == 1 ? 2 : V> v, z;
+  Words<T, V> v, z;
   z.clear();
   v.template load<V>(0, x + t * ldx + c * V);
   const int* pi = inv + t * k;
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(256) unpermute_kernel(const T* __restrict__ y,
                                                         const int* __restrict__ inv, const int* __restrict__ kept_p,
                                                         int k, int d, int64_t tokens, Lay lay, const T* base,
                                                         int64_t ldbase, T* out, int64_t ldout) {
-  constexpr int E = V == 1 ? 2 : V;  // (a single element is half a pair)
+  constexpr int E = V;
   ops_begin();
   int64_t t;
   int c;
@@ -288,14 +289,14 @@ __global__ void __launch_bounds__(256) unpermute_kernel(const T* __restrict__ y,
 // for wider rows), written to the k places with their weights while the k rows of y
 // are read for the scalar products; those are summed over each warp's lanes, then
 // over the warps in order.
-constexpr int kBwdVec = 4;
+constexpr int kBwdVec = 2, kBwdThreads = 512;
 template <typename T, int V>
-__global__ void __launch_bounds__(256) unpermute_backward_kernel(
+__global__ void __launch_bounds__(kBwdThreads, 2) unpermute_backward_kernel(
     const T* __restrict__ dout, int64_t lddout, const T* __restrict__ y, const float* __restrict__ w,
     const int* __restrict__ inv, const int* __restrict__ kept_p, int k, int d, T* __restrict__ dy,
     float* __restrict__ dw) {
-  constexpr int E = V == 1 ? 2 : V;
-  __shared__ float sh[8][kMaxK];
+  constexpr int E = V;
+  __shared__ float sh[kBwdThreads / 32][kMaxK];
   ops_begin();
   const int64_t t = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, nw = nt >> 5;
@@ -354,38 +355,207 @@ __global__ void __launch_bounds__(256) unpermute_backward_kernel(
   }
 }
 
-// Elements moved at once: 16 bytes where every row starts on 16 bytes and d is
-// whole, else 4 bytes, else one.  bits: the or of addresses and row strides.
-int pm_vec(size_t es, int d, uintptr_t bits) {
-  bits |= (uintptr_t)d * es;
-  return bits % 16 == 0 ? (int)(16 / es) : bits % 4 == 0 ? (int)(4 / es) : 1;
-}
-uintptr_t addr(const void* p) { return reinterpret_cast<uintptr_t>(p); }
+// ---- rows of any alignment, in 32-bit words: one fp32 element, or two 16-bit ones.
+// A row of 16-bit elements may start in the middle of a word.  Its word c (of d / 2 +
+// 1) is then elements 2c - 1 and 2c, else 2c and 2c + 1, so that whole words are
+// stored; its first and last may hold one element only.  A thread takes kWordsEach
+// words, a block apart, so that the lookups of a row's places serve them all.
+constexpr int kWordsEach = 4;
 
-// f(T{}, integral_constant V).
-template <typename F>
-cudaError_t pm_types(int dtype, int v, F f) {
-  return with_dtype(dtype, [&](auto t) {
-    using T = decltype(t);
-    if (v == (int)(16 / sizeof(T))) return f(t, std::integral_constant<int, 16 / sizeof(T)>());
-    if constexpr (sizeof(T) == 2)
-      if (v == 2) return f(t, std::integral_constant<int, 2>());
-    return f(t, std::integral_constant<int, 1>());
-  });
+// A word's elements at p as two fp32 values, 0 where `lo` / `hi` says there is none.
+// (fp32: one value, with lo.)
+template <typename T>
+__device__ __forceinline__ uint32_t load_word(const T* p, bool lo, bool hi) {
+  if constexpr (sizeof(T) == 4) {
+    return lo ? *reinterpret_cast<const uint32_t*>(p) : 0u;
+  } else {
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+    if (lo && hi && (reinterpret_cast<uintptr_t>(p) & 2) == 0) return *reinterpret_cast<const uint32_t*>(p);
+    const uint32_t a = lo ? h[0] : 0u, b = hi ? h[1] : 0u;
+    return a | (b << 16);
+  }
 }
+template <typename T>
+__device__ __forceinline__ void store_word(T* p, uint32_t w, bool lo, bool hi) {
+  if constexpr (sizeof(T) == 4) {
+    if (lo) *reinterpret_cast<uint32_t*>(p) = w;
+  } else {
+    uint16_t* h = reinterpret_cast<uint16_t*>(p);
+    if (lo && hi && (reinterpret_cast<uintptr_t>(p) & 2) == 0) {
+      *reinterpret_cast<uint32_t*>(p) = w;
+      return;
+    }
+    if (lo) h[0] = (uint16_t)w;
+    if (hi) h[1] = (uint16_t)(w >> 16);
+  }
+}
+template <typename T>
+__device__ __forceinline__ F2 word_f32(uint32_t w) {
+  if constexpr (sizeof(T) == 4) return F2(__uint_as_float(w), 0.f);
+  else return pair_f32<T>(&w);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t f32_word(F2 v) {
+  if constexpr (sizeof(T) == 4) return __float_as_uint(v.get().x);
+  uint32_t w;
+  if constexpr (sizeof(T) == 2) pair_to<T>(&w, v);
+  return w;
+}
+constexpr __host__ __device__ int words_of(int d, size_t es) { return es == 4 ? d : d / 2 + 1; }
+// Whether the row at p starts in the middle of a word.
+template <typename T>
+__device__ __forceinline__ int half_word(const T* p) {
+  return sizeof(T) == 4 ? 0 : (int)(reinterpret_cast<uintptr_t>(p) >> 1) & 1;
+}
+// The source elements around word c of a row: pairs (2c, 2c + 1) and (2c - 1, 2c).
+template <typename T>
+struct Around {
+  uint32_t even, odd;
+  __device__ __forceinline__ void load(const T* row, int c, int d) {
+    if constexpr (sizeof(T) == 4) {
+      even = odd = load_word(row + c, c < d, false);
+    } else {
+      const uint16_t* h = reinterpret_cast<const uint16_t*>(row);
+      const uint32_t m = c > 0 && 2 * c - 1 < d ? h[2 * c - 1] : 0u;
+      even = load_word(row + 2 * c, 2 * c < d, 2 * c + 1 < d);
+      odd = m | (even << 16);
+    }
+  }
+};
+
+template <typename T>
+__global__ void __launch_bounds__(256) permute_words_kernel(const T* __restrict__ x, int64_t ldx,
+                                                            const int* __restrict__ inv,
+                                                            const int* __restrict__ kept_p, int k, int d,
+                                                            int64_t tokens, Lay lay, T* __restrict__ xp) {
+  constexpr int E = 4 / sizeof(T);
+  ops_begin();
+  int64_t t;
+  int c0;
+  if (!lay_at(lay, tokens, t, c0)) return;
+  const int kept = __ldg(kept_p), n = words_of(d, sizeof(T));
+  Around<T> v[kWordsEach];
+#pragma unroll
+  for (int u = 0; u < kWordsEach; ++u) v[u].load(x + t * ldx, c0 + u * lay.nv, d);
+#pragma unroll 4
+  for (int j = 0; j < k; ++j) {
+    const int p = __ldg(inv + t * k + j);
+    T* row = xp + (int64_t)p * d;
+    const int a = half_word(row);
+#pragma unroll
+    for (int u = 0; u < kWordsEach; ++u) {
+      const int c = c0 + u * lay.nv, e = c * E - a;
+      if (c < n) store_word(row + e, p < kept ? (a ? v[u].odd : v[u].even) : 0u, e >= 0 && e < d, e + 1 < d);
+    }
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) unpermute_words_kernel(const T* __restrict__ y, const float* __restrict__ w,
+                                                              const int* __restrict__ inv,
+                                                              const int* __restrict__ kept_p, int k, int d,
+                                                              int64_t tokens, Lay lay, const T* base, int64_t ldbase,
+                                                              T* out, int64_t ldout) {
+  constexpr int E = 4 / sizeof(T);
+  ops_begin();
+  int64_t t;
+  int c0;
+  if (!lay_at(lay, tokens, t, c0)) return;
+  const int kept = __ldg(kept_p), n = words_of(d, sizeof(T));
+  T* row = out + t * ldout;
+  const int a = half_word(row);
+  F2 s[kWordsEach];
+  int e[kWordsEach];
+  bool lo[kWordsEach], hi[kWordsEach];
+#pragma unroll
+  for (int u = 0; u < kWordsEach; ++u) {
+    const int c = c0 + u * lay.nv;
+    e[u] = c * E - a;
+    lo[u] = c < n && e[u] >= 0 && e[u] < d;
+    hi[u] = E == 2 && c < n && e[u] + 1 < d;
+    s[u] = base ? word_f32<T>(load_word(base + t * ldbase + e[u], lo[u], hi[u])) : F2(0.f, 0.f);
+  }
+#pragma unroll 4
+  for (int j = 0; j < k; ++j) {
+    const int p = __ldg(inv + t * k + j);
+    if (p >= kept) continue;
+    const float wj = w ? __ldg(w + t * k + j) : 1.f;
+    const F2 ww(wj, wj);
+    const T* src = y + (int64_t)p * d;
+#pragma unroll
+    for (int u = 0; u < kWordsEach; ++u) s[u] = fma2(ww, word_f32<T>(load_word(src + e[u], lo[u], hi[u])), s[u]);
+  }
+#pragma unroll
+  for (int u = 0; u < kWordsEach; ++u) store_word(row + e[u], f32_word<T>(s[u]), lo[u], hi[u]);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kBwdThreads, 2) unpermute_backward_words_kernel(
+    const T* __restrict__ dout, int64_t lddout, const T* __restrict__ y, const float* __restrict__ w,
+    const int* __restrict__ inv, const int* __restrict__ kept_p, int k, int d, T* __restrict__ dy,
+    float* __restrict__ dw) {
+  constexpr int E = 4 / sizeof(T);
+  __shared__ float sh[kBwdThreads / 32][kMaxK];
+  ops_begin();
+  const int64_t t = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, nw = nt >> 5;
+  const int kept = __ldg(kept_p), n = words_of(d, sizeof(T));
+  for (int b0 = 0; b0 < n; b0 += nt * kWordsEach) {
+    Around<T> g[kWordsEach];
+#pragma unroll
+    for (int u = 0; u < kWordsEach; ++u) g[u].load(dout + t * lddout, b0 + u * nt + tid, d);
+#pragma unroll 2
+    for (int j = 0; j < k; ++j) {
+      const int p = __ldg(inv + t * k + j);
+      const bool live = p < kept;
+      const float wr = live ? (w ? __ldg(w + t * k + j) : 1.f) : 0.f;
+      const F2 w2(wr, wr);
+      T* row = dy + (int64_t)p * d;
+      const T* src = y + (int64_t)p * d;
+      const int a = half_word(row);
+      F2 s(0.f, 0.f);
+#pragma unroll
+      for (int u = 0; u < kWordsEach; ++u) {
+        const int c = b0 + u * nt + tid, e = c * E - a;
+        const bool lo = c < n && e >= 0 && e < d, hi = E == 2 && c < n && e + 1 < d;
+        const F2 gu = word_f32<T>(a ? g[u].odd : g[u].even);
+        if (dw != nullptr && live) s = fma2(gu, word_f32<T>(load_word(src + e, lo, hi)), s);
+        store_word(row + e, live ? f32_word<T>(mul2(gu, w2)) : 0u, lo, hi);
+      }
+      if (dw != nullptr) {
+        const float r = warp_sum(sum2(s));
+        if (lane == 0) sh[warp][j] = b0 ? sh[warp][j] + r : r;
+      }
+    }
+  }
+  if (dw == nullptr) return;
+  __syncthreads();
+  if (tid < k) {
+    float s = 0.f;
+    for (int i = 0; i < nw; ++i) s += sh[i][tid];
+    dw[t * k + tid] = s;
+  }
+}
+
+// Whether rows are whole 16-byte vectors: bits is the or of addresses and row
+// strides in bytes.
+bool pm_vec(size_t es, int d, uintptr_t bits) { return (bits | (uintptr_t)d * es) % 16 == 0; }
+uintptr_t addr(const void* p) { return reinterpret_cast<uintptr_t>(p); }
 
 struct LayLaunch {
   Lay lay;
   int threads;
   int64_t blocks;
 };
-LayLaunch pm_lay(int64_t T, int d, int v) {
+// n units of a row, `each` a thread: a token's lay.nv threads take unit c, c + nv, ...
+LayLaunch pm_lay(int64_t T, int n, int each) {
   LayLaunch l;
-  l.lay.nv = d / v;
-  l.lay.chunks = (l.lay.nv + 255) / 256;
-  l.lay.tpb = l.lay.chunks > 1 ? 1 : 256 / l.lay.nv;
+  const int need = (n + each - 1) / each;
+  l.lay.chunks = (need + 255) / 256;
+  l.lay.nv = need;
+  l.lay.tpb = l.lay.chunks > 1 ? 1 : 256 / need;
   if (l.lay.tpb > T) l.lay.tpb = (int)T;
-  l.threads = ((l.lay.chunks > 1 ? (l.lay.nv + l.lay.chunks - 1) / l.lay.chunks : l.lay.nv * l.lay.tpb) + 31) / 32 * 32;
+  l.threads = ((l.lay.chunks > 1 ? (need + l.lay.chunks - 1) / l.lay.chunks : need * l.lay.tpb) + 31) / 32 * 32;
   l.blocks = l.lay.chunks > 1 ? T * l.lay.chunks : (T + l.lay.tpb - 1) / l.lay.tpb;
   return l;
 }
@@ -475,12 +645,14 @@ moe_status moe_permute(int32_t dtype, int64_t T, int32_t d, int32_t k, int32_t E
   const size_t es = dtype_bytes(dtype);
   if (!elem_ok(x, es) || !elem_ok(xp, es) || !elem_ok(inv, 4) || !elem_ok(offsets, 4)) return MOE_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const int v = pm_vec(es, d, addr(x) | addr(xp) | (uintptr_t)(ldx * es));
-  const LayLaunch l = pm_lay(T, d, v);
-  return ops_status(pm_types(dtype, v, [&](auto t, auto vc) {
+  const bool vec = pm_vec(es, d, addr(x) | addr(xp) | (uintptr_t)(ldx * es));
+  return ops_status(with_dtype(dtype, [&](auto t) {
     using U = decltype(t);
-    return launch_ops("permute", permute_kernel<U, decltype(vc)::value>, dim3((unsigned)l.blocks), dim3(l.threads), 0,
-                      st, static_cast<const U*>(x), ldx, inv, offsets + E, k, d, T, l.lay, static_cast<U*>(xp));
+    constexpr int V = 16 / sizeof(U);
+    const LayLaunch l = vec ? pm_lay(T, d / V, 1) : pm_lay(T, words_of(d, es), kWordsEach);
+    return launch_ops("permute", vec ? permute_kernel<U, V> : permute_words_kernel<U>, dim3((unsigned)l.blocks),
+                      dim3(l.threads), 0, st, static_cast<const U*>(x), ldx, inv, offsets + E, k, d, T, l.lay,
+                      static_cast<U*>(xp));
   }));
 }
 
@@ -494,13 +666,14 @@ moe_status moe_unpermute(int32_t dtype, int64_t T, int32_t d, int32_t k, int32_t
       !elem_ok(inv, 4) || !elem_ok(offsets, 4))
     return MOE_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const int v = pm_vec(es, d, addr(y) | addr(out) | (uintptr_t)(ldout * es) | addr(base) |
-                                  (uintptr_t)((base ? ldbase : 0) * es));
-  const LayLaunch l = pm_lay(T, d, v);
-  return ops_status(pm_types(dtype, v, [&](auto t, auto vc) {
+  const bool vec = pm_vec(es, d, addr(y) | addr(out) | (uintptr_t)(ldout * es) | addr(base) |
+                                     (uintptr_t)((base ? ldbase : 0) * es));
+  return ops_status(with_dtype(dtype, [&](auto t) {
     using U = decltype(t);
-    return launch_ops("unpermute", unpermute_kernel<U, decltype(vc)::value>, dim3((unsigned)l.blocks), dim3(l.threads),
-                      0, st, static_cast<const U*>(y), w, inv, offsets + E, k, d, T, l.lay,
+    constexpr int V = 16 / sizeof(U);
+    const LayLaunch l = vec ? pm_lay(T, d / V, 1) : pm_lay(T, words_of(d, es), kWordsEach);
+    return launch_ops("unpermute", vec ? unpermute_kernel<U, V> : unpermute_words_kernel<U>, dim3((unsigned)l.blocks),
+                      dim3(l.threads), 0, st, static_cast<const U*>(y), w, inv, offsets + E, k, d, T, l.lay,
                       static_cast<const U*>(base), ldbase, static_cast<U*>(out), ldout);
   }));
 }
@@ -515,14 +688,15 @@ moe_status moe_unpermute_backward(int32_t dtype, int64_t T, int32_t d, int32_t k
       !elem_ok_or_null(dw, 4) || (dw != nullptr && !elem_ok(y, es)))
     return MOE_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const int v = pm_vec(es, d, addr(dout) | (uintptr_t)(lddout * es) | addr(dy) | (dw ? addr(y) : 0));
-  const int need = ((d / v + kBwdVec - 1) / kBwdVec + 31) / 32 * 32;
-  const int threads = need < 256 ? need : 256;
-  return ops_status(pm_types(dtype, v, [&](auto t, auto vc) {
+  const bool vec = pm_vec(es, d, addr(dout) | (uintptr_t)(lddout * es) | addr(dy) | (dw ? addr(y) : 0));
+  return ops_status(with_dtype(dtype, [&](auto t) {
     using U = decltype(t);
-    return launch_ops("unpermute_backward", unpermute_backward_kernel<U, decltype(vc)::value>, dim3((unsigned)T),
-                      dim3(threads), 0, st, static_cast<const U*>(dout), lddout, static_cast<const U*>(y), w, inv,
-                      offsets + E, k, d, static_cast<U*>(dy), dw);
+    constexpr int V = 16 / sizeof(U);
+    const int need = vec ? (d / V + kBwdVec - 1) / kBwdVec : (words_of(d, es) + kWordsEach - 1) / kWordsEach;
+    const int threads = need < kBwdThreads ? (need + 31) / 32 * 32 : kBwdThreads;
+    return launch_ops("unpermute_backward", vec ? unpermute_backward_kernel<U, V> : unpermute_backward_words_kernel<U>,
+                      dim3((unsigned)T), dim3(threads), 0, st, static_cast<const U*>(dout), lddout,
+                      static_cast<const U*>(y), w, inv, offsets + E, k, d, static_cast<U*>(dy), dw);
   }));
 }
 
