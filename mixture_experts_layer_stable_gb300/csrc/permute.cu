@@ -362,29 +362,36 @@ __global__ void __launch_bounds__(kBwdThreads, 2) unpermute_backward_kernel(
 // words, a block apart, so that the lookups of a row's places serve them all.
 constexpr int kWordsEach = 4;
 
-// A word's elements at p as two fp32 values, 0 where `lo` / `hi` says there is none.
-// (fp32: one value, with lo.)
-template <typename T>
-__device__ __forceinline__ uint32_t load_word(const T* p, bool lo, bool hi) {
+// A word as it is loaded: whole, or its two elements apart (the parts are joined
+// when the word is used, so that many loads can be under way).
+struct RawWord {
+  uint32_t lo, hi;
+  __device__ __forceinline__ uint32_t join() const { return lo | (hi << 16); }
+};
+// The word at p; EDGE: only the elements that lo / hi say there are, the others 0.
+// `whole`: p is aligned to words.
+template <typename T, bool EDGE>
+__device__ __forceinline__ RawWord load_word(const T* p, bool whole, bool lo, bool hi) {
+  RawWord r{0u, 0u};
   if constexpr (sizeof(T) == 4) {
-    return lo ? *reinterpret_cast<const uint32_t*>(p) : 0u;
+    if (!EDGE || lo) r.lo = *reinterpret_cast<const uint32_t*>(p);
   } else {
     const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
-    if (lo && hi && (reinterpret_cast<uintptr_t>(p) & 2) == 0) return *reinterpret_cast<const uint32_t*>(p);
-    const uint32_t a = lo ? h[0] : 0u, b = hi ? h[1] : 0u;
-    return a | (b << 16);
+    if (EDGE || !whole) {
+      if (!EDGE || lo) r.lo = h[0];
+      if (!EDGE || hi) r.hi = h[1];
+    } else {
+      r.lo = *reinterpret_cast<const uint32_t*>(p);
+    }
   }
+  return r;
 }
-template <typename T>
+template <typename T, bool EDGE>
 __device__ __forceinline__ void store_word(T* p, uint32_t w, bool lo, bool hi) {
-  if constexpr (sizeof(T) == 4) {
-    if (lo) *reinterpret_cast<uint32_t*>(p) = w;
+  if constexpr (!EDGE || sizeof(T) == 4) {
+    if (!EDGE || lo) *reinterpret_cast<uint32_t*>(p) = w;
   } else {
     uint16_t* h = reinterpret_cast<uint16_t*>(p);
-    if (lo && hi && (reinterpret_cast<uintptr_t>(p) & 2) == 0) {
-      *reinterpret_cast<uint32_t*>(p) = w;
-      return;
-    }
     if (lo) h[0] = (uint16_t)w;
     if (hi) h[1] = (uint16_t)(w >> 16);
   }
@@ -413,15 +420,25 @@ struct Around {
   uint32_t even, odd;
   __device__ __forceinline__ void load(const T* row, int c, int d) {
     if constexpr (sizeof(T) == 4) {
-      even = odd = load_word(row + c, c < d, false);
+      even = odd = c < d ? *reinterpret_cast<const uint32_t*>(row + c) : 0u;
     } else {
-      const uint16_t* h = reinterpret_cast<const uint16_t*>(row);
-      const uint32_t m = c > 0 && 2 * c - 1 < d ? h[2 * c - 1] : 0u;
-      even = load_word(row + 2 * c, 2 * c < d, 2 * c + 1 < d);
-      odd = m | (even << 16);
+      const uint16_t* h = reinterpret_cast<const uint16_t*>(row) + 2 * c;
+      const uint32_t m = c > 0 && 2 * c - 1 < d ? h[-1] : 0u;
+      const uint32_t a = 2 * c < d ? h[0] : 0u, b = 2 * c + 1 < d ? h[1] : 0u;
+      even = a | (b << 16);
+      odd = m | (a << 16);
     }
   }
 };
+// Whether a thread's words c0, c0 + stride, ... (kWordsEach of n) are inner ones,
+// both of whose elements exist however the row lies; f(true_type or false_type) for
+// words at the edges or not.
+template <typename F>
+__device__ __forceinline__ void at_edges(int c0, int stride, int n, size_t es, F f) {
+  const bool inner = es == 4 ? c0 + (kWordsEach - 1) * stride < n : c0 > 0 && c0 + (kWordsEach - 1) * stride < n - 1;
+  if (inner) f(std::false_type());
+  else f(std::true_type());
+}
 
 template <typename T>
 __global__ void __launch_bounds__(256) permute_words_kernel(const T* __restrict__ x, int64_t ldx,
@@ -434,20 +451,26 @@ __global__ void __launch_bounds__(256) permute_words_kernel(const T* __restrict_
   int c0;
   if (!lay_at(lay, tokens, t, c0)) return;
   const int kept = __ldg(kept_p), n = words_of(d, sizeof(T));
+  const int* pi = inv + t * k;
   Around<T> v[kWordsEach];
 #pragma unroll
   for (int u = 0; u < kWordsEach; ++u) v[u].load(x + t * ldx, c0 + u * lay.nv, d);
+  at_edges(c0, lay.nv, n, sizeof(T), [&](auto edge) {
+    constexpr bool EDGE = decltype(edge)::value;
 #pragma unroll 4
-  for (int j = 0; j < k; ++j) {
-    const int p = __ldg(inv + t * k + j);
-    T* row = xp + (int64_t)p * d;
-    const int a = half_word(row);
+    for (int j = 0; j < k; ++j) {
+      const int p = __ldg(pi + j);
+      const bool live = p < kept;
+      T* row = xp + (int64_t)p * d;
+      const int a = half_word(row), e0 = c0 * E - a;
+      T* dst = row + e0;
 #pragma unroll
-    for (int u = 0; u < kWordsEach; ++u) {
-      const int c = c0 + u * lay.nv, e = c * E - a;
-      if (c < n) store_word(row + e, p < kept ? (a ? v[u].odd : v[u].even) : 0u, e >= 0 && e < d, e + 1 < d);
+      for (int u = 0; u < kWordsEach; ++u) {
+        const int e = e0 + u * lay.nv * E;
+        store_word<T, EDGE>(dst + u * lay.nv * E, live ? (a ? v[u].odd : v[u].even) : 0u, e >= 0 && e < d, e + 1 < d);
+      }
     }
-  }
+  });
 }
 
 template <typename T>
@@ -461,32 +484,56 @@ __global__ void __launch_bounds__(256) unpermute_words_kernel(const T* __restric
   int64_t t;
   int c0;
   if (!lay_at(lay, tokens, t, c0)) return;
-  const int kept = __ldg(kept_p), n = words_of(d, sizeof(T));
+  const int kept = __ldg(kept_p), n = words_of(d, sizeof(T)), stride = lay.nv * E;
+  const int* pi = inv + t * k;
+  const float* pw = w + t * k;
   T* row = out + t * ldout;
-  const int a = half_word(row);
-  F2 s[kWordsEach];
-  int e[kWordsEach];
-  bool lo[kWordsEach], hi[kWordsEach];
+  const int e0 = c0 * E - half_word(row);
+  at_edges(c0, lay.nv, n, sizeof(T), [&](auto edge) {
+    constexpr bool EDGE = decltype(edge)::value;
+    auto lo = [&](int u) { return e0 + u * stride >= 0 && e0 + u * stride < d; };
+    auto hi = [&](int u) { return e0 + u * stride + 1 < d; };
+    F2 s[kWordsEach];
 #pragma unroll
-  for (int u = 0; u < kWordsEach; ++u) {
-    const int c = c0 + u * lay.nv;
-    e[u] = c * E - a;
-    lo[u] = c < n && e[u] >= 0 && e[u] < d;
-    hi[u] = E == 2 && c < n && e[u] + 1 < d;
-    s[u] = base ? word_f32<T>(load_word(base + t * ldbase + e[u], lo[u], hi[u])) : F2(0.f, 0.f);
-  }
-#pragma unroll 4
-  for (int j = 0; j < k; ++j) {
-    const int p = __ldg(inv + t * k + j);
-    if (p >= kept) continue;
-    const float wj = w ? __ldg(w + t * k + j) : 1.f;
-    const F2 ww(wj, wj);
-    const T* src = y + (int64_t)p * d;
+    for (int u = 0; u < kWordsEach; ++u) s[u] = F2(0.f, 0.f);
+    if (base != nullptr) {
+      const T* src = base + t * ldbase + e0;
 #pragma unroll
-    for (int u = 0; u < kWordsEach; ++u) s[u] = fma2(ww, word_f32<T>(load_word(src + e[u], lo[u], hi[u])), s[u]);
-  }
+      for (int u = 0; u < kWordsEach; ++u)
+        s[u] = word_f32<T>(load_word<T, EDGE>(src + u * stride, !half_word(src), lo(u), hi(u)).join());
+    }
+    for (int j0 = 0; j0 < k; j0 += 4) {  // four rows' words under way
+      RawWord v[4][kWordsEach];
+      float wj[4];
 #pragma unroll
-  for (int u = 0; u < kWordsEach; ++u) store_word(row + e[u], f32_word<T>(s[u]), lo[u], hi[u]);
+      for (int q = 0; q < 4; ++q) {
+        const int p = j0 + q < k ? __ldg(pi + j0 + q) : kept;
+        wj[q] = 0.f;
+#pragma unroll
+        for (int u = 0; u < kWordsEach; ++u) v[q][u] = RawWord{0u, 0u};
+        if (p < kept) {
+          wj[q] = w ? __ldg(pw + j0 + q) : 1.f;
+          const T* src = y + (int64_t)p * d + e0;
+          if (half_word(src)) {
+#pragma unroll
+            for (int u = 0; u < kWordsEach; ++u) v[q][u] = load_word<T, EDGE>(src + u * stride, false, lo(u), hi(u));
+          } else {
+#pragma unroll
+            for (int u = 0; u < kWordsEach; ++u) v[q][u] = load_word<T, EDGE>(src + u * stride, true, lo(u), hi(u));
+          }
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const F2 ww(wj[q], wj[q]);
+#pragma unroll
+        for (int u = 0; u < kWordsEach; ++u) s[u] = fma2(ww, word_f32<T>(v[q][u].join()), s[u]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kWordsEach; ++u)
+      store_word<T, EDGE>(row + e0 + u * stride, f32_word<T>(s[u]), lo(u), hi(u));
+  });
 }
 
 template <typename T>
@@ -499,31 +546,45 @@ __global__ void __launch_bounds__(kBwdThreads, 2) unpermute_backward_words_kerne
   ops_begin();
   const int64_t t = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, nw = nt >> 5;
-  const int kept = __ldg(kept_p), n = words_of(d, sizeof(T));
+  const int kept = __ldg(kept_p), n = words_of(d, sizeof(T)), stride = nt * E;
+  const int* pi = inv + t * k;
+  const float* pw = w + t * k;
   for (int b0 = 0; b0 < n; b0 += nt * kWordsEach) {
+    const int c0 = b0 + tid;
     Around<T> g[kWordsEach];
 #pragma unroll
-    for (int u = 0; u < kWordsEach; ++u) g[u].load(dout + t * lddout, b0 + u * nt + tid, d);
+    for (int u = 0; u < kWordsEach; ++u) g[u].load(dout + t * lddout, c0 + u * nt, d);
 #pragma unroll 2
     for (int j = 0; j < k; ++j) {
-      const int p = __ldg(inv + t * k + j);
+      const int p = __ldg(pi + j);
       const bool live = p < kept;
-      const float wr = live ? (w ? __ldg(w + t * k + j) : 1.f) : 0.f;
+      const float wr = live ? (w ? __ldg(pw + j) : 1.f) : 0.f;
       const F2 w2(wr, wr);
       T* row = dy + (int64_t)p * d;
-      const T* src = y + (int64_t)p * d;
-      const int a = half_word(row);
+      const int a = half_word(row), e0 = c0 * E - a;
+      const T* src = y + (int64_t)p * d + e0;
+      const bool aligned = !half_word(src);
       F2 s(0.f, 0.f);
+      at_edges(c0, nt, n, sizeof(T), [&](auto edge) {
+        constexpr bool EDGE = decltype(edge)::value;
+        auto lo = [&](int u) { return e0 + u * stride >= 0 && e0 + u * stride < d; };
+        auto hi = [&](int u) { return e0 + u * stride + 1 < d; };
+        RawWord v[kWordsEach];
 #pragma unroll
-      for (int u = 0; u < kWordsEach; ++u) {
-        const int c = b0 + u * nt + tid, e = c * E - a;
-        const bool lo = c < n && e >= 0 && e < d, hi = E == 2 && c < n && e + 1 < d;
-        const F2 gu = word_f32<T>(a ? g[u].odd : g[u].even);
-        if (dw != nullptr && live) s = fma2(gu, word_f32<T>(load_word(src + e, lo, hi)), s);
-        store_word(row + e, live ? f32_word<T>(mul2(gu, w2)) : 0u, lo, hi);
-      }
+        for (int u = 0; u < kWordsEach; ++u) v[u] = RawWord{0u, 0u};
+        if (dw != nullptr && live) {
+#pragma unroll
+          for (int u = 0; u < kWordsEach; ++u) v[u] = load_word<T, EDGE>(src + u * stride, aligned, lo(u), hi(u));
+        }
+#pragma unroll
+        for (int u = 0; u < kWordsEach; ++u) {
+          const F2 gu = word_f32<T>(a ? g[u].odd : g[u].even);
+          store_word<T, EDGE>(row + e0 + u * stride, live ? f32_word<T>(mul2(gu, w2)) : 0u, lo(u), hi(u));
+          s = fma2(gu, word_f32<T>(v[u].join()), s);
+        }
+      });
       if (dw != nullptr) {
-        const float r = warp_sum(sum2(s));
+        const float r = live ? warp_sum(sum2(s)) : 0.f;
         if (lane == 0) sh[warp][j] = b0 ? sh[warp][j] + r : r;
       }
     }
