@@ -480,11 +480,6 @@ void ln_pick(int v, int d, int per_sm, size_t row_bytes, F f) {
   if (v == 1) return plain(std::integral_constant<int, 1>());
   if constexpr (sizeof(T) == 2) plain(std::integral_constant<int, 2>());
 }
-template <typename K>
-void ln_allow_smem(K kern, size_t bytes) {
-  if (bytes > 40 * 1024) cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
 }  // namespace
 
 }  // namespace moe
@@ -522,8 +517,9 @@ moe_status moe_layernorm_forward(int32_t dtype, int32_t wdtype, int64_t rows, in
       ln_pick<T>(v, d, ln_blocks_per_sm(d, kForwardThreads), d * sizeof(T), [&](auto tag, size_t smem) {
         using K = decltype(tag);
         auto kern = ln_forward_kernel<T, W, K::V, K::BLOCK, K::RING>;
-        ln_allow_smem(kern, smem);
-        e = launch_ops("layernorm_forward", kern, dim3(grid), dim3(K::BLOCK ? ln_block_threads(d) : 32 * kLnWarps), smem,
+        static SmemAllowed allowed;
+        e = allow_smem(kern, smem, allowed);
+        if (e == cudaSuccess) e = launch_ops("layernorm_forward", kern, dim3(grid), dim3(K::BLOCK ? ln_block_threads(d) : 32 * kLnWarps), smem,
                        st, xp, ldx, wp, bp, eps, yp, ldy, mean, rstd, rows, d);
       });
     return e;
@@ -574,8 +570,9 @@ moe_status moe_layernorm_backward(int32_t dtype, int32_t wdtype, int64_t rows, i
         ln_pick<T>(v, d, ln_blocks_per_sm(d, kBackwardThreads), 2 * d * sizeof(T), [&](auto tag, size_t smem) {
           using K = decltype(tag);
           auto kern = ln_backward_kernel<T, W, K::V, K::BLOCK, K::RING>;
-          ln_allow_smem(kern, smem);
-          e = launch_ops("layernorm_backward", kern, dim3(grid), dim3(K::BLOCK ? ln_block_threads(d) : 32 * kLnWarps),
+          static SmemAllowed allowed;
+          e = allow_smem(kern, smem, allowed);
+          if (e == cudaSuccess) e = launch_ops("layernorm_backward", kern, dim3(grid), dim3(K::BLOCK ? ln_block_threads(d) : 32 * kLnWarps),
                          smem, st, dyp, lddy, xp, ldx, wp, mean, rstd, ap, ldadd, dxp, lddx, part, rows, d);
         });
     }

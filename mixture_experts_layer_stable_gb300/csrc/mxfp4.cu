@@ -694,7 +694,8 @@ template <typename T, bool SWIGLU>
 cudaError_t launch_product(const CUtensorMap& tm_x, const CUtensorMap& tm_x128, const CUtensorMap& tm_w, const P4& p, cudaStream_t st) {
   auto kern = product_kernel<T, SWIGLU>;
   const int smem = kSmem4 - 12288;  // beside the experts' table and the barriers
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static SmemAllowed allowed;
+  const cudaError_t e = allow_smem(kern, smem, allowed);
   if (e != cudaSuccess) return e;
   // units: at most NT for every expert with a row and every 192 rows
   const int64_t units = (int64_t)p.NT * ((int64_t)p.rows / 192 + (p.G < p.rows ? p.G : p.rows));

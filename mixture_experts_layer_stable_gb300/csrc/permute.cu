@@ -662,7 +662,8 @@ moe_status moe_sort_rows(const int32_t* ids, int64_t R, int32_t E, int32_t* coun
   cudaError_t e = cudaSuccess;
   if (cluster) {
     auto kern = sort_kernel<true>;
-    if (smem > 40 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static SmemAllowed allowed;
+    e = allow_smem(kern, smem, allowed);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = kSortCluster;
@@ -691,8 +692,8 @@ moe_status moe_sort_rows(const int32_t* ids, int64_t R, int32_t E, int32_t* coun
                      total);
   }
   auto kern = sort_kernel<false>;
-  if (e == cudaSuccess && smem > 40 * 1024)
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static SmemAllowed allowed;
+  if (e == cudaSuccess) e = allow_smem(kern, smem, allowed);
   if (e == cudaSuccess)
     e = launch_ops("sort_rows", kern, dim3(blocks), dim3(threads), smem, st, ids, R, E, W, per_block,
                    big ? hist : nullptr, big ? total : nullptr, counts, offsets, perm, inv);

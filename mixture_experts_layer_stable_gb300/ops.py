@@ -68,7 +68,7 @@ def _stream(stream, t):
     """`stream`, or the current stream of t's device."""
     if stream is None and _raw_stream is not None:
         return _raw_stream(t.get_device())
-    return _given_stream(stream)
+    return stream if type(stream) is int else _given_stream(stream)
 
 
 def _need(ok, where):
@@ -77,9 +77,10 @@ def _need(ok, where):
 
 
 def _dt(t, where):
-    dt = _DT.get(t.dtype)
-    _need(dt is not None, where)
-    return dt
+    try:
+        return _DT[t.dtype]
+    except KeyError:
+        raise MoeError(MOE_ERR_INVALID_ARG, where) from None
 
 
 def _rows(t, n, d, dtype, where):
@@ -99,9 +100,18 @@ def _flat(t, n, dtype, where):
     return t.data_ptr()
 
 
+_u8 = torch.uint8
+
+
 def _bytes(t, n, where):
-    _need(t.dtype == torch.uint8 and t.numel() >= n and t.is_contiguous(), where)
+    if t.dtype != _u8 or t.numel() < n or not t.is_contiguous():
+        raise MoeError(MOE_ERR_INVALID_ARG, where)
     return t.data_ptr()
+
+
+def _tiles(K):
+    """Bytes of a run of scale tiles along K."""
+    return (K + 127) // 128 * 512
 
 
 # ---------------------------------------------------------------- layer norm
@@ -115,7 +125,7 @@ def moe_layernorm_forward(x, weight, bias, eps, y, mean=None, rstd=None, stream=
     n, d = x.shape
     dt, wt = _dt(x, w), weight if weight is not None else bias
     wdtype = x.dtype if wt is None else wt.dtype
-    _check(lib().moe_layernorm_forward(
+    _check((_lib or lib()).moe_layernorm_forward(
         dt, dt if wt is None else _dt(wt, w), n, d, x.data_ptr(), _rows(x, n, d, x.dtype, w),
         _flat(weight, d, wdtype, w), _flat(bias, d, wdtype, w), eps, y.data_ptr(), _rows(y, n, d, x.dtype, w),
         _flat(mean, n, torch.float32, w), _flat(rstd, n, torch.float32, w), _stream(stream, x)), w)
@@ -127,12 +137,12 @@ def moe_layernorm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, ws, da
     n, d = x.shape
     dt = _dt(x, w)
     wt = next((t for t in (weight, dweight, dbias) if t is not None), x)
-    _check(lib().moe_layernorm_backward(
+    _check((_lib or lib()).moe_layernorm_backward(
         dt, _dt(wt, w), n, d, dy.data_ptr(), _rows(dy, n, d, x.dtype, w), x.data_ptr(), _rows(x, n, d, x.dtype, w),
         _flat(weight, d, wt.dtype, w), _flat(mean, n, torch.float32, w), _flat(rstd, n, torch.float32, w),
         None if dadd is None else dadd.data_ptr(), 0 if dadd is None else _rows(dadd, n, d, x.dtype, w),
         dx.data_ptr(), _rows(dx, n, d, x.dtype, w), _flat(dweight, d, wt.dtype, w), _flat(dbias, d, wt.dtype, w),
-        None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size(),
+        None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes,
         _stream(stream, x)), w)
 
 
@@ -146,27 +156,29 @@ def moe_sort_rows(ids, counts, offsets, perm, inv, ws, stream=None):
     w = "moe_sort_rows"
     R, E = ids.numel(), counts.numel()
     i32 = torch.int32
-    _check(lib().moe_sort_rows(_flat(ids, R, i32, w), R, E, _flat(counts, E, i32, w), _flat(offsets, E + 1, i32, w),
+    _check((_lib or lib()).moe_sort_rows(_flat(ids, R, i32, w), R, E, _flat(counts, E, i32, w), _flat(offsets, E + 1, i32, w),
                                _flat(perm, R, i32, w), _flat(inv, R, i32, w), ws.data_ptr(),
-                               ws.numel() * ws.element_size(), _stream(stream, ids)), w)
+                               ws.nbytes, _stream(stream, ids)), w)
 
 
 def moe_permute(x, k, inv, offsets, xp, stream=None):
     """xp[inv[t*k+j]] = x[t]; dropped rows are zeros."""
     w = "moe_permute"
+    E, off = _segments(offsets, w)
     T, d = x.shape
-    _check(lib().moe_permute(_dt(x, w), T, d, k, offsets.numel() - 1, x.data_ptr(), _rows(x, T, d, x.dtype, w),
-                             _flat(inv, T * k, torch.int32, w), _flat(offsets, offsets.numel(), torch.int32, w),
+    _check((_lib or lib()).moe_permute(_dt(x, w), T, d, k, E, x.data_ptr(), _rows(x, T, d, x.dtype, w),
+                             _flat(inv, T * k, torch.int32, w), off,
                              _flat(xp, T * k * d, x.dtype, w), _stream(stream, x)), w)
 
 
 def moe_unpermute(y, weights, k, inv, offsets, out, base=None, stream=None):
     """out[t] = base[t] + sum_j weights[t*k+j] * y[inv[t*k+j]]; weights None: all 1 (the backward of moe_permute)."""
     w = "moe_unpermute"
+    E, off = _segments(offsets, w)
     T, d = out.shape
-    _check(lib().moe_unpermute(_dt(out, w), T, d, k, offsets.numel() - 1, _flat(y, T * k * d, out.dtype, w),
+    _check((_lib or lib()).moe_unpermute(_dt(out, w), T, d, k, E, _flat(y, T * k * d, out.dtype, w),
                                _flat(weights, T * k, torch.float32, w), _flat(inv, T * k, torch.int32, w),
-                               _flat(offsets, offsets.numel(), torch.int32, w),
+                               off,
                                None if base is None else base.data_ptr(),
                                0 if base is None else _rows(base, T, d, out.dtype, w), out.data_ptr(),
                                _rows(out, T, d, out.dtype, w), _stream(stream, out)), w)
@@ -175,11 +187,12 @@ def moe_unpermute(y, weights, k, inv, offsets, out, base=None, stream=None):
 def moe_unpermute_backward(dout, y, weights, k, inv, offsets, dy, dw, stream=None):
     """dy and dw of moe_unpermute (dw, and y with it, may be None)."""
     w = "moe_unpermute_backward"
+    E, off = _segments(offsets, w)
     T, d = dout.shape
-    _check(lib().moe_unpermute_backward(
-        _dt(dout, w), T, d, k, offsets.numel() - 1, dout.data_ptr(), _rows(dout, T, d, dout.dtype, w),
+    _check((_lib or lib()).moe_unpermute_backward(
+        _dt(dout, w), T, d, k, E, dout.data_ptr(), _rows(dout, T, d, dout.dtype, w),
         _flat(y, T * k * d, dout.dtype, w), _flat(weights, T * k, torch.float32, w),
-        _flat(inv, T * k, torch.int32, w), _flat(offsets, offsets.numel(), torch.int32, w),
+        _flat(inv, T * k, torch.int32, w), off,
         _flat(dy, T * k * d, dout.dtype, w), _flat(dw, T * k, torch.float32, w), _stream(stream, dout)), w)
 
 
@@ -200,17 +213,17 @@ def moe_quantize_mxfp4(weights, q, scales, paired=False, stream=None):
     """weights [batch, K, N] -> codes q [batch, N, K/2] and scale tiles."""
     w = "moe_quantize_mxfp4"
     b, K, N = weights.shape
-    _check(lib().moe_quantize_mxfp4(_dt(weights, w), _flat(weights, b * K * N, weights.dtype, w), b, K, N, int(paired),
+    _check((_lib or lib()).moe_quantize_mxfp4(_dt(weights, w), _flat(weights, b * K * N, weights.dtype, w), b, K, N, int(paired),
                                     _bytes(q, b * N * (K // 2), w),
-                                    _bytes(scales, moe_mxfp4_weight_scale_bytes(b, K, N), w), _stream(stream, weights)), w)
+                                    _bytes(scales, b * ((N + 127) // 128) * _tiles(K), w), _stream(stream, weights)), w)
 
 
 def moe_dequantize_mxfp4(q, scales, weights, paired=False, stream=None):
     """The values of quantised weights, into weights [batch, K, N]."""
     w = "moe_dequantize_mxfp4"
     b, K, N = weights.shape
-    _check(lib().moe_dequantize_mxfp4(_dt(weights, w), _bytes(q, b * N * (K // 2), w),
-                                      _bytes(scales, moe_mxfp4_weight_scale_bytes(b, K, N), w), b, K, N, int(paired),
+    _check((_lib or lib()).moe_dequantize_mxfp4(_dt(weights, w), _bytes(q, b * N * (K // 2), w),
+                                      _bytes(scales, b * ((N + 127) // 128) * _tiles(K), w), b, K, N, int(paired),
                                       _flat(weights, b * K * N, weights.dtype, w), _stream(stream, weights)), w)
 
 
@@ -218,7 +231,8 @@ def _segments(offsets, where):
     """(G, pointer) of the experts' segments; offsets None: one segment."""
     if offsets is None:
         return 1, None
-    return offsets.numel() - 1, _flat(offsets, offsets.numel(), torch.int32, where)
+    n = offsets.numel()
+    return n - 1, _flat(offsets, n, torch.int32, where)
 
 
 def moe_quantize_mxfp4_rows(x, q, scales, offsets=None, perm=None, k=1, stream=None):
@@ -228,9 +242,9 @@ def moe_quantize_mxfp4_rows(x, q, scales, offsets=None, perm=None, k=1, stream=N
     n, K = x.shape
     rows = n if perm is None else perm.numel()
     _need(perm is None or rows <= n * k, w)
-    _check(lib().moe_quantize_mxfp4_rows(_dt(x, w), rows, K, x.data_ptr(), _rows(x, n, K, x.dtype, w), G, off,
+    _check((_lib or lib()).moe_quantize_mxfp4_rows(_dt(x, w), rows, K, x.data_ptr(), _rows(x, n, K, x.dtype, w), G, off,
                                          _flat(perm, rows, torch.int32, w), k, _bytes(q, rows * (K // 2), w),
-                                         _bytes(scales, moe_mxfp4_row_scale_bytes(rows, K, G), w), _stream(stream, x)), w)
+                                         _bytes(scales, (rows // 128 + G) * _tiles(K), w), _stream(stream, x)), w)
 
 
 def moe_dequantize_mxfp4_rows(q, scales, y, offsets=None, stream=None):
@@ -238,8 +252,8 @@ def moe_dequantize_mxfp4_rows(q, scales, y, offsets=None, stream=None):
     w = "moe_dequantize_mxfp4_rows"
     G, off = _segments(offsets, w)
     rows, K = y.shape
-    _check(lib().moe_dequantize_mxfp4_rows(_dt(y, w), rows, K, _bytes(q, rows * (K // 2), w),
-                                           _bytes(scales, moe_mxfp4_row_scale_bytes(rows, K, G), w), G, off,
+    _check((_lib or lib()).moe_dequantize_mxfp4_rows(_dt(y, w), rows, K, _bytes(q, rows * (K // 2), w),
+                                           _bytes(scales, (rows // 128 + G) * _tiles(K), w), G, off,
                                            y.data_ptr(), _rows(y, rows, K, y.dtype, w), _stream(stream, y)), w)
 
 
@@ -248,12 +262,13 @@ def moe_mxfp4_product(q, scales, offsets, wq, wscales, act, out, ws, stream=None
     w = "moe_mxfp4_product"
     G, off = _segments(offsets, w)
     rows, n_out = out.shape
-    _need(wq.dim() == 3 and wq.shape[0] == G, w)
-    N, K = wq.shape[1], wq.shape[2] * 2
-    _need(n_out == (N // 2 if act == MOE_ACT_SWIGLU else N), w)
-    _check(lib().moe_mxfp4_product(_dt(out, w), rows, N, K, G, off, _bytes(q, rows * (K // 2), w),
-                                   _bytes(scales, moe_mxfp4_row_scale_bytes(rows, K, G), w),
+    experts, N, half = wq.shape
+    K = 2 * half
+    if experts != G or n_out != (N // 2 if act == MOE_ACT_SWIGLU else N):
+        raise MoeError(MOE_ERR_INVALID_ARG, w)
+    _check((_lib or lib()).moe_mxfp4_product(_dt(out, w), rows, N, K, G, off, _bytes(q, rows * (K // 2), w),
+                                   _bytes(scales, (rows // 128 + G) * _tiles(K), w),
                                    _bytes(wq, G * N * (K // 2), w),
-                                   _bytes(wscales, moe_mxfp4_weight_scale_bytes(G, K, N), w), act, out.data_ptr(),
+                                   _bytes(wscales, G * ((N + 127) // 128) * _tiles(K), w), act, out.data_ptr(),
                                    _rows(out, rows, n_out, out.dtype, w), ws.data_ptr(),
-                                   ws.numel() * ws.element_size(), _stream(stream, out)), w)
+                                   ws.nbytes, _stream(stream, out)), w)
