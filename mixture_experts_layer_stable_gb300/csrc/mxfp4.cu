@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(kThreads4, 1)
     tmem_alloc(smem_u32(&s_tmem), 512);
     tmem_relinquish();
   }
-  ops_begin();
+  ops_wait();
   if (blockIdx.x == 0 && threadIdx.x < 2) p.status[threadIdx.x] = 0;
 
   // experts' rows and units
@@ -682,6 +682,7 @@ __global__ void __launch_bounds__(kThreads4, 1)
       }
     }
   }
+  ops_let_next();
   __syncthreads();
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
