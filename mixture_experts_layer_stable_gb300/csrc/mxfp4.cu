@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(256) dequant_weights_kernel(const uint8_t* __r
 
 // ------------------------------------------------------------------ the product
 // Warp-specialised, persistent, one CTA per SM: warp 0 issues the copies, one
-// thread of warp 1 the tensor-core instructions, warps 2..5 the epilogue.
+// thread of warp 1 the tensor-core instructions, warps 2..9 the epilogue.
 //
 // The weights are the MMA's A operand (M = 128 features) and the rows its B
 // (N = rows of the tile rounded up to 16, at most kMaxTok): the accumulator
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(256) dequant_weights_kernel(const uint8_t* __r
 // The stage's scale tiles are copied to TMEM (tcgen05.cp) right before its four
 // MMAs of K = 64, into the stage's own columns.
 // TMEM: two accumulators as wide as the largest tile of rows (at most 192
-// columns), then 32 scale columns for every stage.
+// columns), then 24 scale columns for every stage.
 //
 // When experts have few rows a stage is 17 KB of weights, 0.38 us of an SM's share
 // of HBM, and issuing its copies and MMAs must not take longer: the copy and MMA
@@ -305,11 +305,15 @@ __global__ void __launch_bounds__(256) dequant_weights_kernel(const uint8_t* __r
 // merged across branches (or with lane == 0 instead) every one of these
 // instructions took 70 cycles or more, against 10 to 20, and a stage 850 cycles
 // instead of what its bytes take.
-constexpr int kThreads4 = 192;
+constexpr int kEpiWarps4 = 8;          // two for each quarter of the TMEM lanes
+constexpr int kThreads4 = 64 + 32 * kEpiWarps4;
 constexpr int kMaxTok = 192;
 constexpr int kMaxStages = 12;
+constexpr int kSfCols = 24;             // TMEM columns of a stage's scales: features 2 x 4, rows 2 x 8
 constexpr int kWBytes = 128 * 128;      // weights of a stage
-constexpr int kSmem4 = 232448;          // all of an SM's
+constexpr int kTables4 = 8704;          // static shared memory: the experts' rows and units, barriers
+constexpr int kSmem4 = 232448 - kTables4;  // the rest of what a block may have: ring and staging
+constexpr int kStage4 = 1024;           // staging of an epilogue warp: 16 rows x 32 features of 16 bits
 
 // Shared-memory descriptors as their low words (address in units of 16 bytes and
 // the leading offset, so that adding moves the address); the high words are
@@ -320,33 +324,68 @@ MOE_DEV uint32_t desc_lo(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
 
 // The following do nothing in lanes where `on` is 0.
 // D (+)= (A * sfa) (B * sfb): E2M1 operands, a UE8M0 scale per 32 elements, K = 64.
+template <bool PAIR>
 MOE_DEV void tc_mma_mxf4(int on, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
                          uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "setp.ne.b32 q, %8, 0;\n\t"
-      "mov.b64 a, {%1, %7};\n\t"
-      "mov.b64 b, {%2, %7};\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], a, b, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "n"(kDescSw128), "r"(on)
-      : "memory");
+  if constexpr (PAIR) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "setp.ne.b32 q, %8, 0;\n\t"
+        "mov.b64 a, {%1, %7};\n\t"
+        "mov.b64 b, {%2, %7};\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], a, b, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "n"(kDescSw128), "r"(on)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "setp.ne.b32 q, %8, 0;\n\t"
+        "mov.b64 a, {%1, %7};\n\t"
+        "mov.b64 b, {%2, %7};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], a, b, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "n"(kDescSw128), "r"(on)
+        : "memory");
+  }
 }
 // A 512-byte scale tile into four TMEM columns (its 32 rows of 16 bytes in every lane quarter).
+// Of a pair: in each CTA, from its own shared memory into its own TMEM.
+template <bool PAIR>
 MOE_DEV void tc_cp_scales(int on, uint32_t taddr, uint32_t lo) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t.reg .b64 s;\n\t"
-      "setp.ne.b32 q, %3, 0;\n\t"
-      "mov.b64 s, {%1, %2};\n\t"
-      "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], s;\n\t}" ::"r"(taddr), "r"(lo), "n"(kDescPlain), "r"(on)
-      : "memory");
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t.reg .b64 s;\n\t"
+        "setp.ne.b32 q, %3, 0;\n\t"
+        "mov.b64 s, {%1, %2};\n\t"
+        "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], s;\n\t}" ::"r"(taddr), "r"(lo), "n"(kDescPlain), "r"(on)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t.reg .b64 s;\n\t"
+        "setp.ne.b32 q, %3, 0;\n\t"
+        "mov.b64 s, {%1, %2};\n\t"
+        "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], s;\n\t}" ::"r"(taddr), "r"(lo), "n"(kDescPlain), "r"(on)
+        : "memory");
 }
-MOE_DEV void tc_commit_on(int on, uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "setp.ne.b32 q, %1, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(on)
-      : "memory");
+// One arrival on the barrier (of a pair: at this place in each CTA of mask) when what
+// was issued so far has completed.
+template <bool PAIR>
+MOE_DEV void tc_commit_on(int on, uint32_t bar, uint16_t mask = 3) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n\t}" ::
+            "r"(bar),
+        "r"(on), "h"(mask)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(on)
+        : "memory");
 }
 MOE_DEV void expect_tx_on(int on, uint32_t bar, uint32_t bytes) {
   asm volatile(
@@ -355,23 +394,46 @@ MOE_DEV void expect_tx_on(int on, uint32_t bar, uint32_t bytes) {
       "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes), "r"(on)
       : "memory");
 }
+// (Of a pair: `bar` may be the other CTA's, by its shared::cluster address.)
+template <bool PAIR>
 MOE_DEV void tma_load_2d_on(int on, uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "setp.ne.b32 q, %5, 0;\n\t"
-      "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(on)
-      : "memory");
+  if constexpr (PAIR) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(on)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(on)
+        : "memory");
+  }
 }
+template <bool PAIR>
 MOE_DEV void tma_load_3d_on(int on, uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "setp.ne.b32 q, %6, 0;\n\t"
-      "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(on)
-      : "memory");
+  if constexpr (PAIR) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %6, 0;\n\t"
+        "@q cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(on)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %6, 0;\n\t"
+        "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(on)
+        : "memory");
+  }
 }
 MOE_DEV void bulk_load_on(int on, uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile(
@@ -410,9 +472,9 @@ __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int
 }
 // Instruction descriptor: E2M1 A and B (K-major), UE8M0 scales taken from bytes
 // sf, sf + 1 of a 32-bit scale column (sf 0 or 2).
-MOE_DEV uint32_t idesc_mxf4(int N, int sf) {
+MOE_DEV uint32_t idesc_mxf4(int M, int N, int sf) {
   return ((uint32_t)sf << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
-         ((uint32_t)(128 >> 4) << 24) | ((uint32_t)sf << 29);
+         ((uint32_t)(M >> 4) << 24) | ((uint32_t)sf << 29);
 }
 
 // One lane of a converged warp.
@@ -437,6 +499,7 @@ struct P4 {
   int64_t ldo;
   int* status;
   int rows, G, N, K, NT, KT, stages_k;
+  int n_units;  // units along the features: NT, of a pair half as many
 };
 
 // Tiles of an expert's c rows: as few as kMaxTok allows, starting on multiples of
@@ -444,15 +507,30 @@ struct P4 {
 // the first).
 MOE_DEV int tok_tiles(int c) { return (c + kMaxTok - 1) / kMaxTok; }
 MOE_DEV int tok_start(int c, int tiles, int t) { return t * ((c + 63) / 64) / tiles * 64; }
+// Rows of the largest of them (kMaxTok where there are many).
+MOE_DEV int tok_most(int c) {
+  const int tt = tok_tiles(c);
+  if (tt > 4) return kMaxTok;
+  int most = 0;
+  for (int t = 0; t < tt; ++t) most = max(most, (t + 1 < tt ? tok_start(c, tt, t + 1) : c) - tok_start(c, tt, t));
+  return most;
+}
 
 struct Unit4 {
   int e, n, row0, first, nt;  // expert, feature tile, first row of the expert, first row in it, rows
 };
 
-template <typename T, bool SWIGLU>
+// PAIR: two CTAs (a cluster) share each MMA of M = 256 features, 128 in each, and
+// each holds half of the rows, so that an SM takes in 28 KB a stage for 128 x 192
+// products instead of 40.  The even CTA's barriers count both CTAs' copies, its one
+// thread issues for both, and its commits arrive in both.
+// tm_x128: rows in boxes of 128; of a pair the scale tiles of the rows, and tm_ws of
+// the weights, as rows of 256 bytes (a plain bulk copy cannot arrive on the other
+// CTA's barrier).
+template <typename T, bool SWIGLU, bool PAIR>
 __global__ void __launch_bounds__(kThreads4, 1)
     product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_x128,
-                   const __grid_constant__ CUtensorMap tm_w, const P4 p) {
+                   const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_ws, const P4 p) {
   extern __shared__ uint8_t smem_raw[];
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   __shared__ int s_off[kMaxE + 1];    // first row of each expert
@@ -467,7 +545,7 @@ __global__ void __launch_bounds__(kThreads4, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull[i], 1);
-      mbar_init(&tempty[i], 4);
+      mbar_init(&tempty[i], (PAIR ? 2 : 1) * kEpiWarps4);
     }
     mbar_init(&drain, 1);
     s_abort = 0;
@@ -475,25 +553,32 @@ __global__ void __launch_bounds__(kThreads4, 1)
     tma_prefetch_desc(&tm_x);
     tma_prefetch_desc(&tm_x128);
     tma_prefetch_desc(&tm_w);
+    if (PAIR) tma_prefetch_desc(&tm_ws);
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(&s_tmem), 512);
-    tmem_relinquish();
+    if constexpr (PAIR) {
+      tmem_alloc_pair(smem_u32(&s_tmem), 512);  // both CTAs, collectively
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(&s_tmem), 512);
+      tmem_relinquish();
+    }
   }
   ops_wait();
   if (blockIdx.x == 0 && threadIdx.x < 2) p.status[threadIdx.x] = 0;
 
   // experts' rows and units
-  for (int i = threadIdx.x; i <= p.G; i += blockDim.x) s_off[i] = p.off ? p.off[i] : (i ? p.rows : 0);
+  // (offsets out of order or range give wrong rows, not accesses out of range)
+  for (int i = threadIdx.x; i <= p.G; i += blockDim.x) s_off[i] = p.off ? min(max(p.off[i], 0), p.rows) : (i ? p.rows : 0);
   __syncthreads();
   if (warp == 0) {
     int run = 0, most = 0;
     for (int base = 0; base < p.G; base += 32) {
       const int e = base + lane;
-      const int c = e < p.G ? s_off[e + 1] - s_off[e] : 0;
+      const int c = e < p.G ? max(0, s_off[e + 1] - s_off[e]) : 0;
       const int tt = tok_tiles(c);
-      most = max(most, tt > 1 ? kMaxTok : c);
-      int inc = tt * p.NT;
+      most = max(most, tok_most(c));
+      int inc = tt * p.n_units;
       const int mine = inc;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -511,6 +596,7 @@ __global__ void __launch_bounds__(kThreads4, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync();  // the other CTA's barriers exist before their use
   tc_fence_after();
   const uint32_t tmem = (uint32_t)uniform((int)s_tmem);
   const int total = uniform(s_unit[p.G]);
@@ -519,26 +605,27 @@ __global__ void __launch_bounds__(kThreads4, 1)
   // stage layout for the largest tile there is: weights, rows, scales
   const int cap = uniform((s_most + 31) & ~31);
   const uint32_t sfb_runs = cap > 128 ? 2 : 1;
-  const uint32_t stage_bytes = (uint32_t)kWBytes + (uint32_t)cap * 128u + 1024u + sfb_runs * 1024u;
+  const int cap_x = PAIR ? (cap / 2 + 31) & ~31 : cap;  // rows in this CTA's shared memory
+  const uint32_t stage_bytes = (uint32_t)kWBytes + (uint32_t)cap_x * 128u + 1024u + sfb_runs * 1024u;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t room = kSmem4 - 16384u - (base - smem_u32(smem_raw));
-  const int S = min(min(kMaxStages, (int)(room / stage_bytes)), (512 - 2 * cap) / 32);
+  const uint32_t room = kSmem4 - kEpiWarps4 * kStage4 - (base - smem_u32(smem_raw));
+  const uint32_t staging = base + room;  // (16-byte aligned: base and the sizes are)
+  const int S = min(min(kMaxStages, (int)(room / stage_bytes)), (512 - 2 * cap) / kSfCols);
 
+  const int rank = PAIR ? uniform((int)cluster_ctarank()) : 0;
+  const int unit0 = PAIR ? blockIdx.x / 2 : blockIdx.x, unit_step = PAIR ? gridDim.x / 2 : gridDim.x;
+
+  // Unit u; each role walks its units upwards and keeps its place in the experts.
+  int at_e = 0;
   auto unit_at = [&](int u) {
-    int lo = 0, hi = p.G - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (s_unit[mid] <= u) lo = mid;
-      else hi = mid - 1;
-    }
-    lo = uniform(lo);
+    while (u >= uniform(s_unit[at_e + 1])) ++at_e;
     Unit4 t;
-    t.e = lo;
-    t.row0 = uniform(s_off[lo]);
-    const int c = uniform(s_off[lo + 1]) - t.row0, tt = tok_tiles(c), r = u - uniform(s_unit[lo]);
-    t.n = r / tt;
-    const int i = r - t.n * tt;
-    t.first = tok_start(c, tt, i);
+    t.e = at_e;
+    t.row0 = uniform(s_off[at_e]);
+    const int c = uniform(s_off[at_e + 1]) - t.row0, tt = tok_tiles(c), r = u - uniform(s_unit[at_e]);
+    const int n = tt == 1 ? r : r / tt, i = r - n * tt;
+    t.n = PAIR ? 2 * n + rank : n;
+    t.first = tt == 1 ? 0 : tok_start(c, tt, i);
     t.nt = (i + 1 < tt ? tok_start(c, tt, i + 1) : c) - t.first;
     return t;
   };
@@ -553,32 +640,44 @@ __global__ void __launch_bounds__(kThreads4, 1)
     const int leader = elect_one();
     int s = 0;
     uint32_t ph = 0, used = 0, last = 0;
-    for (int u = blockIdx.x; u < total; u += gridDim.x) {
+    for (int u = unit0; u < total; u += unit_step) {
       const Unit4 t = unit_at(u);
-      const int boxes = (t.nt + 31) / 32;
       const int runs = ((t.first & 127) + t.nt + 127) / 128;
-      const int row = t.row0 + t.first;
-      const uint8_t* wsp = p.ws + ((size_t)t.e * p.NT + t.n) * p.KT * 512u;
-      const uint8_t* xsp = p.xs + (size_t)(t.row0 / 128 + t.e + t.first / 128) * p.KT * 512u;
+      // this CTA's rows: all, or its half of the MMA's N; in boxes of 128 (one CTA), the rest of 32
+      const int mine = PAIR ? ((t.nt + 31) & ~31) / 2 : t.nt;
+      const int boxes = (mine + 31) / 32;
+      const int row = t.row0 + t.first + (PAIR ? rank * mine : 0);
+      const int big = !PAIR && leader && boxes >= 4, small0 = !PAIR && boxes >= 4 ? 4 : 0;
+      const size_t wrun = (size_t)t.e * p.NT + t.n, xrun = (size_t)(t.row0 / 128 + t.e + t.first / 128);
+      const uint8_t* wsp = p.ws + wrun * p.KT * 512u;
+      const uint8_t* xsp = p.xs + xrun * p.KT * 512u;
       const uint8_t* xsp2 = xsp + (size_t)p.KT * 512u;
       const uint32_t bytes = (uint32_t)kWBytes + (uint32_t)boxes * 4096u;
-      // rows in boxes of 128, the rest in boxes of 32
-      const int big = leader && boxes >= 4, small0 = boxes >= 4 ? 4 : 0;
       for (int kb = 0; kb < p.stages_k; ++kb) {
         if (!wait_all(empty0 + 8u * s, ph ^ 1u, 1000 + s)) goto produced;
-        const uint32_t sa = base + (uint32_t)s * stage_bytes, sb = sa + kWBytes, sf = sb + (uint32_t)cap * 128u;
-        const uint32_t fb = full0 + 8u * s;
-        const uint32_t sfn = 512u * (uint32_t)min(2, p.KT - 2 * kb);
-        expect_tx_on(leader, fb, bytes + sfn * (1u + runs));
-        tma_load_3d_on(leader, sa, &tm_w, fb, kb * 128, t.n * 128, t.e);
-        bulk_load_on(leader, sf, wsp, sfn, fb);
-        tma_load_2d_on(big, sb, &tm_x128, fb, kb * 128, row);
-        for (int i = small0; i < boxes; ++i) tma_load_2d_on(leader, sb + i * 4096u, &tm_x, fb, kb * 128, row + i * 32);
-        bulk_load_on(leader, sf + 1024u, xsp, sfn, fb);
-        bulk_load_on(leader && runs > 1, sf + 2048u, xsp2, sfn, fb);
-        wsp += 1024;
-        xsp += 1024;
-        xsp2 += 1024;
+        const uint32_t sa = base + (uint32_t)s * stage_bytes, sb = sa + kWBytes, sf = sb + (uint32_t)cap_x * 128u;
+        if constexpr (PAIR) {
+          const uint32_t fb = mapa_shared(full0 + 8u * s, 0);
+          expect_tx_on(leader && rank == 0, full0 + 8u * s, 2u * (bytes + 1024u * (1u + runs)));
+          tma_load_3d_on<true>(leader, sa, &tm_w, fb, kb * 128, t.n * 128, t.e);
+          for (int i = 0; i < boxes; ++i) tma_load_2d_on<true>(leader, sb + i * 4096u, &tm_x, fb, kb * 128, row + i * 32);
+          tma_load_2d_on<true>(leader, sf, &tm_ws, fb, 0, (int)(wrun * p.KT * 2) + kb * 4);
+          tma_load_2d_on<true>(leader, sf + 1024u, &tm_x128, fb, 0, (int)(xrun * p.KT * 2) + kb * 4);
+          tma_load_2d_on<true>(leader && runs > 1, sf + 2048u, &tm_x128, fb, 0, (int)((xrun + 1) * p.KT * 2) + kb * 4);
+        } else {
+          const uint32_t fb = full0 + 8u * s;
+          const uint32_t sfn = 512u * (uint32_t)min(2, p.KT - 2 * kb);
+          expect_tx_on(leader, fb, bytes + sfn * (1u + runs));
+          tma_load_3d_on<false>(leader, sa, &tm_w, fb, kb * 128, t.n * 128, t.e);
+          bulk_load_on(leader, sf, wsp, sfn, fb);
+          tma_load_2d_on<false>(big, sb, &tm_x128, fb, kb * 128, row);
+          for (int i = small0; i < boxes; ++i) tma_load_2d_on<false>(leader, sb + i * 4096u, &tm_x, fb, kb * 128, row + i * 32);
+          bulk_load_on(leader, sf + 1024u, xsp, sfn, fb);
+          bulk_load_on(leader && runs > 1, sf + 2048u, xsp2, sfn, fb);
+          wsp += 1024;
+          xsp += 1024;
+          xsp2 += 1024;
+        }
         used |= 1u << s;
         last = (last & ~(1u << s)) | (ph << s);
         if (++s == S) {
@@ -588,21 +687,25 @@ __global__ void __launch_bounds__(kThreads4, 1)
       }
     }
   produced:
-    // every issued copy has landed before the CTA can exit
-    for (int i = 0; i < kMaxStages; ++i)
-      if ((used >> i) & 1u) mbar_wait_drain(&full[i], (last >> i) & 1u);
-  } else if (warp == 1) {
+    // every issued copy has landed before the CTA can exit (of a pair the even CTA's
+    // barriers count both CTAs'), and of a pair every commit has arrived
+    for (int i = 0; i < kMaxStages; ++i) {
+      if (((used >> i) & 1u) == 0) continue;
+      if (rank == 0 && !mbar_wait_drain(&full[i], (last >> i) & 1u)) break;
+      if (PAIR && !mbar_wait_drain(&empty[i], (last >> i) & 1u)) break;
+    }
+  } else if (warp == 1 && rank == 0) {
     const int leader = elect_one();
     int s = 0, acc = 0;
     uint32_t ph = 0, aph = 0;
     const uint32_t da0 = desc_lo(base), step = stage_bytes / 16u, sf0 = tmem + 2u * (uint32_t)cap;
-    const uint32_t b_off = kWBytes / 16u, s_off16 = b_off + (uint32_t)cap * 8u;
-    for (int u = blockIdx.x; u < total; u += gridDim.x) {
+    const uint32_t b_off = kWBytes / 16u, s_off16 = b_off + (uint32_t)cap_x * 8u;
+    for (int u = unit0; u < total; u += unit_step) {
       const Unit4 t = unit_at(u);
-      const int n16 = (t.nt + 15) & ~15;
+      const int mma_n = PAIR ? (t.nt + 31) & ~31 : (t.nt + 15) & ~15;
       const int two = leader && (t.first & 127) + t.nt > 128;
       const uint32_t shift = 8u + (uint32_t)(t.first & 127) / 32u;  // scale columns of the rows: 0 or 2 in
-      const uint32_t id0 = idesc_mxf4(n16, 0), id2 = idesc_mxf4(n16, 2);
+      const uint32_t id0 = idesc_mxf4(PAIR ? 256 : 128, mma_n, 0), id2 = idesc_mxf4(PAIR ? 256 : 128, mma_n, 2);
       const uint32_t d = tmem + (uint32_t)(acc * cap);
       if (!wait_all(smem_u32(&tempty[acc]), aph ^ 1u, 1100 + acc)) goto issued;
       tc_fence_after();
@@ -613,19 +716,19 @@ __global__ void __launch_bounds__(kThreads4, 1)
         tc_fence_after();
         // descriptors advance in units of 16 bytes
         const uint32_t da = da0 + (uint32_t)s * step, db = da + b_off, ds = da + s_off16;
-        const uint32_t tsf = sf0 + (uint32_t)s * 32u, tsb = tsf + shift;
+        const uint32_t tsf = sf0 + (uint32_t)s * kSfCols, tsb = tsf + shift;
         const int half = leader && left > 128;
-        tc_cp_scales(leader, tsf, ds);
-        tc_cp_scales(leader, tsf + 8u, ds + 64u);
-        tc_cp_scales(two, tsf + 12u, ds + 128u);
-        tc_cp_scales(half, tsf + 16u, ds + 32u);
-        tc_cp_scales(half, tsf + 24u, ds + 96u);
-        tc_cp_scales(two && half, tsf + 28u, ds + 160u);
-        tc_mma_mxf4(leader, d, da, db, id0, tsf, tsb, more);
-        tc_mma_mxf4(leader && left > 64, d, da + 2u, db + 2u, id2, tsf, tsb, 1u);
-        tc_mma_mxf4(half, d, da + 4u, db + 4u, id0, tsf + 16u, tsb + 16u, 1u);
-        tc_mma_mxf4(leader && left > 192, d, da + 6u, db + 6u, id2, tsf + 16u, tsb + 16u, 1u);
-        tc_commit_on(leader, empty0 + 8u * s);
+        tc_cp_scales<PAIR>(leader, tsf, ds);
+        tc_cp_scales<PAIR>(leader, tsf + 8u, ds + 64u);
+        tc_cp_scales<PAIR>(two, tsf + 12u, ds + 128u);
+        tc_cp_scales<PAIR>(half, tsf + 4u, ds + 32u);
+        tc_cp_scales<PAIR>(half, tsf + 16u, ds + 96u);
+        tc_cp_scales<PAIR>(two && half, tsf + 20u, ds + 160u);
+        tc_mma_mxf4<PAIR>(leader, d, da, db, id0, tsf, tsb, more);
+        tc_mma_mxf4<PAIR>(leader && left > 64, d, da + 2u, db + 2u, id2, tsf, tsb, 1u);
+        tc_mma_mxf4<PAIR>(half, d, da + 4u, db + 4u, id0, tsf + 4u, tsb + 8u, 1u);
+        tc_mma_mxf4<PAIR>(leader && left > 192, d, da + 6u, db + 6u, id2, tsf + 4u, tsb + 8u, 1u);
+        tc_commit_on<PAIR>(leader, empty0 + 8u * s);
         left -= 256;
         more = 1u;
         if (++s == S) {
@@ -633,49 +736,87 @@ __global__ void __launch_bounds__(kThreads4, 1)
           ph ^= 1u;
         }
       }
-      tc_commit_on(leader, smem_u32(&tfull[acc]));
+      tc_commit_on<PAIR>(leader, smem_u32(&tfull[acc]));
       if (++acc == 2) {
         acc = 0;
         aph ^= 1u;
       }
     }
   issued:
-    tc_commit_on(leader, smem_u32(&drain));
+    tc_commit_on<PAIR>(leader, smem_u32(&drain), 1);
     mbar_wait_drain(&drain, 0);
-  } else {
+  } else if (warp > 1) {
+    // A warp takes every other 32 rows of its quarter's 32 features.  A lane holds one
+    // feature: results of 16 bits go through the warp's staging, 16 rows at a time, and
+    // leave as 16-byte stores (as they are, 2 bytes a lane, they cost three times
+    // the MMAs' time at K = 2048).  Output rows that are not 16-byte aligned, features
+    // past N and fp32 results are stored from the lanes.
     const int q = warp & 3;  // TMEM lane quarter of this warp
+    const uint32_t stg = staging + (uint32_t)(warp - 2) * kStage4;
+    constexpr int kCols = SWIGLU ? 16 : 32;  // output columns of 32 features
     int acc = 0;
     uint32_t aph = 0;
     T* out = static_cast<T*>(p.out);
-    for (int u = blockIdx.x; u < total; u += gridDim.x) {
+    const bool rows16 = sizeof(T) == 2 && (reinterpret_cast<uintptr_t>(out) & 15) == 0 && p.ldo % 8 == 0;
+    for (int u = unit0; u < total; u += unit_step) {
       const Unit4 t = unit_at(u);
       if (!wait_all(smem_u32(&tfull[acc]), aph, 1400 + acc)) break;
       tc_fence_after();
-      const int n = t.n * 128 + q * 32 + lane;
-      T* dst = out + (int64_t)(t.row0 + t.first) * p.ldo + (SWIGLU ? n >> 1 : n);
-      for (int c0 = 0; c0 < t.nt; c0 += 32) {
+      const int n0 = t.n * 128 + q * 32, n = n0 + lane;
+      T* dst = out + (int64_t)(t.row0 + t.first) * p.ldo + (SWIGLU ? n0 >> 1 : n0);
+      const bool odd = lane & 1;
+      for (int c0 = 32 * ((warp - 2) >> 2); c0 < t.nt; c0 += 64) {
         float v[32];
         tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * cap + c0), v);
         if (SWIGLU) {
           // even lanes hold gates, odd lanes the matching up products: of each
-          // pair of rows an even lane finishes the first, an odd lane the second
-          const bool odd = lane & 1;
+          // pair of rows an even lane finishes the first (left in v[c]), an odd
+          // lane the second (left in v[c] too)
 #pragma unroll
           for (int c = 0; c < 32; c += 2) {
             const float y = __shfl_xor_sync(0xffffffffu, odd ? v[c] : v[c + 1], 1);
-            const float r = odd ? silu_f(y) * v[c + 1] : silu_f(v[c]) * y;
-            const int row = c0 + c + (odd ? 1 : 0);
-            if (row < t.nt && n < p.N) dst[(int64_t)row * p.ldo] = from_f32<T>(r);
+            v[c] = odd ? silu_f(y) * v[c + 1] : silu_f(v[c]) * y;
           }
-        } else {
+        }
+        if (rows16 && n0 + 32 <= p.N) {
+          if constexpr (sizeof(T) == 2) {
 #pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (c0 + c < t.nt && n < p.N) dst[(int64_t)(c0 + c) * p.ldo] = from_f32<T>(v[c]);
+            for (int h = 0; h < 32; h += 16) {
+#pragma unroll
+              for (int c = 0; c < 16; c += SWIGLU ? 2 : 1) {
+                const T r = from_f32<T>(v[h + c]);
+                const uint32_t at = SWIGLU ? stg + c * kCols * 2 + lane * 2 + (odd ? kCols * 2 - 2 - (lane >> 1) * 2 : -(lane >> 1) * 2)
+                                           : stg + c * kCols * 2 + lane * 2;
+                asm volatile("st.shared.b16 [%0], %1;" ::"r"(at), "h"(*reinterpret_cast<const uint16_t*>(&r)) : "memory");
+              }
+              __syncwarp();
+              constexpr int kLanes = kCols / 8;  // lanes of a row
+#pragma unroll
+              for (int i = 0; i < 16 * kLanes / 32; ++i) {
+                const int row = i * (32 / kLanes) + lane / kLanes, col = lane % kLanes * 8;
+                uint4 w;
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                             : "r"(stg + (uint32_t)(row * kCols + col) * 2u));
+                if (c0 + h + row < t.nt) *reinterpret_cast<uint4*>(dst + (int64_t)(c0 + h + row) * p.ldo + col) = w;
+              }
+              __syncwarp();
+            }
+          }
+        } else if (n < p.N) {
+#pragma unroll
+          for (int c = 0; c < 32; c += SWIGLU ? 2 : 1) {
+            const int row = c0 + c + (SWIGLU && odd ? 1 : 0);
+            if (row < t.nt) dst[(int64_t)row * p.ldo + (SWIGLU ? lane >> 1 : lane)] = from_f32<T>(v[c]);
+          }
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&tempty[acc]);
+      if (lane == 0) {
+        if constexpr (PAIR) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
+        else mbar_arrive(&tempty[acc]);
+      }
       if (++acc == 2) {
         acc = 0;
         aph ^= 1u;
@@ -683,26 +824,74 @@ __global__ void __launch_bounds__(kThreads4, 1)
     }
   }
   ops_let_next();
+  tc_fence_before();
   __syncthreads();
-  if (warp == 1) tmem_dealloc(tmem, 512);
+  if constexpr (PAIR) cluster_sync();  // the pair's MMAs and remote arrivals are done
+  if (warp == 1) {
+    tc_fence_after();
+    if constexpr (PAIR) tmem_dealloc_pair(tmem, 512);
+    else tmem_dealloc(tmem, 512);
+  }
 }
 
 int grid_for(int64_t n) {
   const int64_t b = (n + 255) / 256;
   return (int)(b < 1 ? 1 : b < (1 << 20) ? b : (1 << 20));
 }
-template <typename T, bool SWIGLU>
-cudaError_t launch_product(const CUtensorMap& tm_x, const CUtensorMap& tm_x128, const CUtensorMap& tm_w, const P4& p, cudaStream_t st) {
-  auto kern = product_kernel<T, SWIGLU>;
-  const int smem = kSmem4 - 12288;  // beside the experts' table and the barriers
+// Clusters of two CTAs of kern that the GPU holds at once (cached by device).
+template <typename K>
+int pair_clusters(K kern, const cudaLaunchConfig_t& cfg) {
+  static int resident[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
+  if (resident[dev] == 0) {
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) n = num_sms() / 2;
+    resident[dev] = n;
+  }
+  return resident[dev];
+}
+
+template <typename T, bool SWIGLU, bool PAIR>
+cudaError_t launch_product(const CUtensorMap* tm, const P4& p, cudaStream_t st) {
+  auto kern = product_kernel<T, SWIGLU, PAIR>;
+  const int smem = kSmem4;
   static SmemAllowed allowed;
   const cudaError_t e = allow_smem(kern, smem, allowed);
   if (e != cudaSuccess) return e;
-  // units: at most NT for every expert with a row and every 192 rows
-  const int64_t units = (int64_t)p.NT * ((int64_t)p.rows / 192 + (p.G < p.rows ? p.G : p.rows));
-  const int grid = units < num_sms() ? (int)units : num_sms();
-  return launch_ops("mxfp4_product", kern, dim3(grid), dim3(kThreads4), smem, st, tm_x, tm_x128, tm_w, p);
+  // units: at most n_units for every expert with a row and every 192 rows
+  const int64_t units = (int64_t)p.n_units * ((int64_t)p.rows / kMaxTok + (p.G < p.rows ? p.G : p.rows));
+  if constexpr (!PAIR) {
+    const int grid = units < num_sms() ? (int)units : num_sms();
+    return launch_ops("mxfp4_product", kern, dim3(grid), dim3(kThreads4), smem, st, tm[0], tm[1], tm[2], tm[3], p);
+  } else {
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(num_sms() & ~1));
+    cfg.blockDim = dim3(kThreads4);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const int most = pair_clusters(kern, cfg);
+    cfg.numAttrs = 2;
+    cfg.gridDim = dim3(2 * (unsigned)(units < most ? units : most));
+    TraceScope ts("mxfp4_product", st);
+    return cudaLaunchKernelEx(&cfg, kern, tm[0], tm[1], tm[2], tm[3], p);
+  }
 }
+
+// Whether the product runs on CTA pairs: where it is bound by what the SMs take in,
+// that is experts with many rows, and K long enough that the pairs' hand-overs between
+// units do not cost more.  us, one CTA / pairs: 2048 rows an expert (8 experts, N =
+// 4096) K = 7168: 174 / 151, 4096: 109 / 97, 2048: 70 / 73; K = 7168, 512 rows (32):
+// 197 / 174, 204 (80): 299 / 273, 128 (256): 641 / 643.
+bool product_pairs(int64_t rows, int G, int K, int NT) { return NT > 1 && K >= 4096 && rows >= 160 * (int64_t)G; }
 
 bool fp4_k(int32_t K) { return K >= 32 && K % 32 == 0 && K <= (1 << 24); }
 bool fp4_weights(int64_t batch, int32_t K, int32_t N) {
@@ -816,11 +1005,19 @@ moe_status moe_mxfp4_product(int32_t dtype, int64_t rows, int32_t N, int32_t K, 
       !elem_ok(out, dtype_bytes(dtype)) || !elem_ok_or_null(offsets, 4))
     return MOE_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  CUtensorMap tm_x, tm_x128, tm_w;
-  if (!map2d(&tm_x, xq, (uint64_t)K / 2, (uint64_t)rows, 128, 32, true) ||
-      !map2d(&tm_x128, xq, (uint64_t)K / 2, (uint64_t)rows, 128, 128, true) ||
-      !map3d(&tm_w, wq, (uint64_t)K / 2, (uint64_t)N, (uint64_t)G, 128, 128, true))
-    return MOE_ERR_CUDA;
+  const int NT = (N + 127) / 128, KT = (K + 127) / 128;
+  const bool pair = product_pairs(rows, G, K, NT);
+  CUtensorMap tm[4];
+  bool ok = map2d(&tm[0], xq, (uint64_t)K / 2, (uint64_t)rows, 128, 32, true) &&
+            map3d(&tm[2], wq, (uint64_t)K / 2, (uint64_t)N, (uint64_t)G, 128, 128, true);
+  if (pair) {
+    ok = ok && map2d(&tm[1], xscales, 256, (uint64_t)(rows / 128 + G) * KT * 2, 256, 4, true, CU_TENSOR_MAP_SWIZZLE_NONE) &&
+         map2d(&tm[3], wscales, 256, (uint64_t)G * NT * KT * 2, 256, 4, true, CU_TENSOR_MAP_SWIZZLE_NONE);
+  } else {
+    ok = ok && map2d(&tm[1], xq, (uint64_t)K / 2, (uint64_t)rows, 128, 128, true);
+    tm[3] = tm[1];
+  }
+  if (!ok) return MOE_ERR_CUDA;
   P4 p;
   p.off = offsets;
   p.xs = xscales;
@@ -832,12 +1029,15 @@ moe_status moe_mxfp4_product(int32_t dtype, int64_t rows, int32_t N, int32_t K, 
   p.G = G;
   p.N = N;
   p.K = K;
-  p.NT = (N + 127) / 128;
-  p.KT = (K + 127) / 128;
+  p.NT = NT;
+  p.KT = KT;
+  p.n_units = pair ? (NT + 1) / 2 : NT;
   p.stages_k = (K + 255) / 256;
   return ops_status(with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
-    return act == MOE_ACT_SWIGLU ? launch_product<T, true>(tm_x, tm_x128, tm_w, p, st) : launch_product<T, false>(tm_x, tm_x128, tm_w, p, st);
+    if (act == MOE_ACT_SWIGLU)
+      return pair ? launch_product<T, true, true>(tm, p, st) : launch_product<T, true, false>(tm, p, st);
+    return pair ? launch_product<T, false, true>(tm, p, st) : launch_product<T, false, false>(tm, p, st);
   }));
 }
 

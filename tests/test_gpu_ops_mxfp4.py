@@ -193,7 +193,9 @@ def want_of(xv, wv, off, act):
 PRODUCTS = [([1], 32, 1), ([1], 64, 8), ([3], 96, 7), ([0, 5, 0], 128, 127), ([16, 1], 160, 128), ([17, 33], 256, 129),
             ([128], 288, 256), ([129, 0, 2], 512, 300), ([223, 224, 225], 224, 130), ([449, 1], 1056, 999),
             ([1] * 40, 512, 64), ([0] * 30 + [700], 992, 260), ([1, 1, 1, 1, 1, 1, 1, 1], 7168, 512),
-            ([300, 40, 0, 90], 2048, 1536), ([13], 4096, 4096), ([8], 7168, 2048)]
+            ([300, 40, 0, 90], 2048, 1536), ([13], 4096, 4096), ([8], 7168, 2048),
+            # long K and many rows: CTA pairs
+            ([160], 4096, 256), ([0, 449, 1, 300], 4128, 389), ([193, 200, 1025], 4224, 130), ([320, 0], 7168, 1000)]
 
 
 @pytest.mark.parametrize("act", [False, True])
