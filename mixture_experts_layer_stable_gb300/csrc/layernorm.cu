@@ -46,30 +46,78 @@ __device__ __forceinline__ void group_sum(float (&v)[M], float (*sh)[M]) {
 }
 
 // The part of a row that one thread holds: N vectors of V elements, vector i at
-// (i * threads + thread) * V; elements past d read as zeros.
-template <typename T, int V, int N>
+// (i * threads + thread) * V; elements past d read as zeros.  LOOSE (V = 2): rows of
+// 16-bit elements that may start in the middle of a 32-bit word or end with half of
+// one; in those that do the elements are moved one by one, and the loaded halves
+// joined by join(), before the first use, so that loads stay under way.
+template <typename T, int V, int N, bool LOOSE>
 struct Part : Words<T, V * N> {
+  using Base = Words<T, V * N>;
+  static constexpr bool kLoose = LOOSE;
+  uint32_t high[kLoose ? N : 1];
   __device__ __forceinline__ void load(const T* __restrict__ row, int d, int tid, int nt) {
+    if constexpr (kLoose) {
+      const uint16_t* p = reinterpret_cast<const uint16_t*>(row);
+      if (reinterpret_cast<uintptr_t>(row) & 2) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int c = (i * nt + tid) * V;
-      if (c < d) Words<T, V * N>::template load<V>(i, row + c);
-      else Words<T, V * N>::template zero<V>(i);
+        for (int i = 0; i < N; ++i) {
+          const int c = (i * nt + tid) * 2;
+          Base::w[i] = c < d ? p[c] : 0u;
+          high[i] = c + 1 < d ? p[c + 1] : 0u;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int c = (i * nt + tid) * 2;
+          if (c + 1 < d) Base::w[i] = *reinterpret_cast<const uint32_t*>(p + c);
+          else Base::w[i] = c < d ? p[c] : 0u;
+          high[i] = 0;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int c = (i * nt + tid) * V;
+        if (c < d) Base::template load<V>(i, row + c);
+        else Base::template zero<V>(i);
+      }
+    }
+  }
+  __device__ __forceinline__ void join() {
+    if constexpr (kLoose) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) Base::w[i] |= high[i] << 16;
     }
   }
   __device__ __forceinline__ void store(T* __restrict__ row, int d, int tid, int nt) const {
+    if constexpr (kLoose) {
+      uint16_t* p = reinterpret_cast<uint16_t*>(row);
+      const bool half = reinterpret_cast<uintptr_t>(row) & 2;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int c = (i * nt + tid) * V;
-      if (c < d) Words<T, V * N>::template store<V>(i, row + c);
+      for (int i = 0; i < N; ++i) {
+        const int c = (i * nt + tid) * 2;
+        if (!half && c + 1 < d) {
+          *reinterpret_cast<uint32_t*>(p + c) = Base::w[i];
+        } else {
+          if (c < d) p[c] = (uint16_t)Base::w[i];
+          if (c + 1 < d) p[c + 1] = (uint16_t)(Base::w[i] >> 16);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int c = (i * nt + tid) * V;
+        if (c < d) Base::template store<V>(i, row + c);
+      }
     }
   }
 };
 
-// The weights of the same elements (NULL: all `other`).
+// The weights of the same elements (NULL: all `other`): 16 bytes at a time where rows
+// are, else one by one.
 template <typename W, int V, int N>
 struct Weights : Words<W, V * N> {
-  static constexpr int P = V * sizeof(W) > 16 ? 16 / sizeof(W) : V;  // at most 16 bytes a load
+  static constexpr int P = V <= 2 ? 1 : V * sizeof(W) > 16 ? 16 / sizeof(W) : V;
   __device__ __forceinline__ void load(const W* __restrict__ w, float other, int d, int tid, int nt) {
 #pragma unroll
     for (int k = 0; k < V * N / 2; ++k) Words<W, V * N>::set(k, F2(other, other));
@@ -77,10 +125,9 @@ struct Weights : Words<W, V * N> {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int c = (i * nt + tid) * V;
-      if (c < d) {
 #pragma unroll
-        for (int j = 0; j < V / P; ++j) Words<W, V * N>::template load<P>(i * (V / P) + j, w + c + j * P);
-      }
+      for (int j = 0; j < V / P; ++j)
+        if (c + j * P < d) Words<W, V * N>::template load<P>(i * (V / P) + j, w + c + j * P);
     }
   }
 };
@@ -91,7 +138,7 @@ __device__ __forceinline__ void ring_copy(T* slot, const T* __restrict__ row, in
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int c = (i * nt + tid) * V;
-    if (c < d)  // (only instances with V * sizeof(T) = 16 have a ring)
+    if (c < d)  // (only vectors of 16 bytes have a ring)
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
                        static_cast<uint32_t>(__cvta_generic_to_shared(slot + c))),
                    "l"(row + c)
@@ -104,10 +151,10 @@ __device__ __forceinline__ void ring_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// RING: rows that the ring in shared memory holds (block form, 16-byte vectors), or
-// 0: the next row is loaded into registers.  A slot is filled again after the first
+// RING: rows that the ring in shared memory holds (block form), or 0: the next row is
+// loaded into registers.  A slot is filled again after the first
 // barrier of the row that follows its own.
-template <typename T, typename W, int V, bool BLOCK, int RING>
+template <typename T, typename W, int V, bool LOOSE, bool BLOCK, int RING>
 __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
     ln_forward_kernel(const T* x, int64_t ldx, const W* __restrict__ w, const W* __restrict__ b, float eps, T* y,
                       int64_t ldy, float* __restrict__ mean, float* __restrict__ rstd, int64_t rows, int d) {
@@ -120,7 +167,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
   const int64_t step = BLOCK ? gridDim.x : gridDim.x * (int64_t)kLnWarps;
   const float inv_d = 1.0f / (float)d;
   T* ring = reinterpret_cast<T*>(ring_mem);
-  Part<T, V, N> cur, next;
+  Part<T, V, N, LOOSE> cur, next;
   Weights<W, V, N> wv, bv;
   int slot = 0;
   auto copy_in = [&](int sl, int64_t r) {
@@ -141,6 +188,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
       cur.load(ring + slot * d, d, tid, nt);
     } else {
       cur = next;
+      cur.join();
       if (r + step < rows) next.load(x + (r + step) * ldx, d, tid, nt);
     }
     F2 v[kElems / 2], t(0.f, 0.f);
@@ -166,6 +214,11 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
         const float2 f = c.get();
         const float c0 = (2 * k * nt + tid) < d ? f.x : 0.f, c1 = ((2 * k + 1) * nt + tid) < d ? f.y : 0.f;
         t = fma2(F2(c0, c1), F2(c0, c1), t);
+      } else if (LOOSE) {  // d may be odd
+        const int e = (k * nt + tid) * 2;
+        const float2 f = c.get();
+        const F2 m(e < d ? f.x : 0.f, e + 1 < d ? f.y : 0.f);
+        t = fma2(m, m, t);
       } else if ((2 * k / V * nt + tid) * V < d) {
         t = fma2(c, c, t);
       }
@@ -186,7 +239,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
 
 // dx of the group's rows; with part, the rows' sums of dy * xh and dy to
 // part[block][0 / 1][d].
-template <typename T, typename W, int V, bool BLOCK, int RING>
+template <typename T, typename W, int V, bool LOOSE, bool BLOCK, int RING>
 __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
     ln_backward_kernel(const T* dy, int64_t lddy, const T* __restrict__ x, int64_t ldx, const W* __restrict__ w,
                        const float* __restrict__ mean, const float* __restrict__ rstd, const T* dadd, int64_t ldadd,
@@ -203,7 +256,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
   F2 aw[kElems / 2], ab[kElems / 2];
 #pragma unroll
   for (int k = 0; k < kElems / 2; ++k) aw[k] = ab[k] = F2(0.f, 0.f);
-  Part<T, V, N> cx, cy, nx, ny;
+  Part<T, V, N, LOOSE> cx, cy, nx, ny;
   Weights<W, V, N> wv;
   float nmu = 0.f, nrs = 0.f;
   int slot = 0;
@@ -239,6 +292,8 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
     } else {
       cx = nx;
       cy = ny;
+      cx.join();
+      cy.join();
       if (r + step < rows) {
         nx.load(x + (r + step) * ldx, d, tid, nt);
         ny.load(dy + (r + step) * lddy, d, tid, nt);
@@ -266,7 +321,10 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
     // dx = rs g - rs m1 - xh rs m2
     const float m1 = -rs * (s[0] * inv_d), m2 = -rs * (s[1] * inv_d);
     const F2 m1s(m1, m1), m2s(m2, m2);
-    if (dadd != nullptr) cy.load(dadd + r * ldadd, d, tid, nt);
+    if (dadd != nullptr) {
+      cy.load(dadd + r * ldadd, d, tid, nt);
+      cy.join();
+    }
 #pragma unroll
     for (int k = 0; k < kElems / 2; ++k) {
       F2 v = fma2(xh[k], m2s, fma2(g[k], rs2, m1s));
@@ -425,17 +483,14 @@ cudaError_t ln_types(int dtype, int wdtype, F f) {
   });
 }
 
-// Elements a thread moves at once: 16 bytes where every row and d allow it, else
-// 4 bytes, else one element.  `a`: the or of the addresses and row strides in
-// bytes; `aw`: of the weights' addresses, which are read V elements at a time too.
-int ln_vec(size_t es, size_t wes, int d, uintptr_t a, uintptr_t aw) {
-  auto fits = [&](int v) {
-    const size_t wb = v * wes > 16 ? 16 : v * wes;
-    return d % v == 0 && a % (v * es) == 0 && aw % wb == 0;
-  };
-  if (fits((int)(16 / es))) return (int)(16 / es);
-  if (es == 2 && fits(2)) return 2;
-  return 1;
+// How a thread moves elements: 16 bytes at once where every row and d allow it, else
+// words of 32 bits, else 16-bit elements wherever they lie.  `a`: the or of the
+// addresses and row strides in bytes; `aw`: of the weights' addresses, which are read
+// 16 bytes at a time too.
+enum LnMove { LN_VECTORS, LN_WORDS, LN_LOOSE };
+LnMove ln_move(size_t es, int d, uintptr_t a, uintptr_t aw) {
+  a |= (uintptr_t)d * es;
+  return (a | aw) % 16 == 0 ? LN_VECTORS : a % 4 == 0 ? LN_WORDS : LN_LOOSE;
 }
 uintptr_t bits(const void* p) { return reinterpret_cast<uintptr_t>(p); }
 
@@ -454,32 +509,35 @@ int ln_blocks(int64_t rows, int d, int threads) {
   return (int)(need < most ? need : most);
 }
 
-// The kernel form for the vector width v and the row length, f(tag, ring bytes)
-// doing the launch.  Block rows of 16-byte vectors go through a ring of six rows,
-// three where six would not fit into the block's share of shared memory (row_bytes:
-// of all arrays that a ring row holds).
-template <int V_, bool BLOCK_, int RING_>
+// The kernel form for the way elements move and the row length, f(tag, ring bytes)
+// doing the launch.  Block rows of vectors go through a ring of six rows, three where
+// six would not fit into the block's share of shared memory (row_bytes: of all arrays
+// that a ring row holds).  Words do not: as many copies and then as many reads as
+// elements cost more than the deeper prefetch gives (d = 7166, 16384 rows: forward
+// 190 us with the ring, 121 without).
+template <int V_, bool LOOSE_, bool BLOCK_, int RING_>
 struct LnTag {
   static constexpr int V = V_, RING = RING_;
-  static constexpr bool BLOCK = BLOCK_;
+  static constexpr bool LOOSE = LOOSE_, BLOCK = BLOCK_;
 };
 template <typename T, typename F>
-void ln_pick(int v, int d, int per_sm, size_t row_bytes, F f) {
-  constexpr int VF = 16 / sizeof(T);
-  if (v == VF) {
-    if (d <= kWarpRowMax) return f(LnTag<VF, false, 0>(), (size_t)0);
+void ln_pick(LnMove v, int d, int per_sm, size_t row_bytes, F f) {
+  constexpr int VF = 16 / sizeof(T), VW = 4 / sizeof(T);
+  const bool warp = d <= kWarpRowMax;
+  if (v == LN_VECTORS) {
     const size_t share = 225 * 1024 / per_sm - 1024;
-    if (6 * row_bytes <= share) return f(LnTag<VF, true, 6>(), 6 * row_bytes);
-    return f(LnTag<VF, true, 3>(), 3 * row_bytes);
+    if (warp) f(LnTag<VF, false, false, 0>(), (size_t)0);
+    else if (6 * row_bytes <= share) f(LnTag<VF, false, true, 6>(), 6 * row_bytes);
+    else f(LnTag<VF, false, true, 3>(), 3 * row_bytes);
+  } else if (v == LN_WORDS) {
+    if (warp) f(LnTag<VW, false, false, 0>(), (size_t)0);
+    else f(LnTag<VW, false, true, 0>(), (size_t)0);
+  } else if constexpr (sizeof(T) == 2) {
+    if (warp) f(LnTag<2, true, false, 0>(), (size_t)0);
+    else f(LnTag<2, true, true, 0>(), (size_t)0);
   }
-  auto plain = [&](auto vc) {
-    constexpr int V = decltype(vc)::value;
-    if (d <= kWarpRowMax) f(LnTag<V, false, 0>(), (size_t)0);
-    else f(LnTag<V, true, 0>(), (size_t)0);
-  };
-  if (v == 1) return plain(std::integral_constant<int, 1>());
-  if constexpr (sizeof(T) == 2) plain(std::integral_constant<int, 2>());
 }
+
 }  // namespace
 
 }  // namespace moe
@@ -500,7 +558,7 @@ moe_status moe_layernorm_forward(int32_t dtype, int32_t wdtype, int64_t rows, in
   if (rows == 0) return MOE_OK;
   if (!elem_ok(x, es) || !elem_ok(y, es)) return MOE_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const int v = ln_vec(es, wes, d, bits(x) | bits(y) | (uintptr_t)(ldx * es) | (uintptr_t)(ldy * es),
+  const LnMove v = ln_move(es, d, bits(x) | bits(y) | (uintptr_t)(ldx * es) | (uintptr_t)(ldy * es),
                        bits(weight) | bits(bias));
   const int grid = ln_blocks(rows, d, kForwardThreads);
   return ops_status(ln_types(dtype, wdtype, [&](auto t, auto wt) {
@@ -516,7 +574,7 @@ moe_status moe_layernorm_forward(int32_t dtype, int32_t wdtype, int64_t rows, in
     else
       ln_pick<T>(v, d, ln_blocks_per_sm(d, kForwardThreads), d * sizeof(T), [&](auto tag, size_t smem) {
         using K = decltype(tag);
-        auto kern = ln_forward_kernel<T, W, K::V, K::BLOCK, K::RING>;
+        auto kern = ln_forward_kernel<T, W, K::V, K::LOOSE, K::BLOCK, K::RING>;
         static SmemAllowed allowed;
         e = allow_smem(kern, smem, allowed);
         if (e == cudaSuccess) e = launch_ops("layernorm_forward", kern, dim3(grid), dim3(K::BLOCK ? ln_block_threads(d) : 32 * kLnWarps), smem,
@@ -549,7 +607,7 @@ moe_status moe_layernorm_backward(int32_t dtype, int32_t wdtype, int64_t rows, i
     return MOE_ERR_INVALID_ARG;
   if (rows == 0 && !sums) return MOE_OK;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const int v = ln_vec(es, wes, d,
+  const LnMove v = ln_move(es, d,
                        bits(dy) | bits(x) | bits(dx) | bits(dadd) | (uintptr_t)(lddy * es) | (uintptr_t)(ldx * es) |
                            (uintptr_t)(lddx * es) | (uintptr_t)((dadd ? ldadd : 0) * es),
                        bits(weight));
@@ -569,7 +627,7 @@ moe_status moe_layernorm_backward(int32_t dtype, int32_t wdtype, int64_t rows, i
       else
         ln_pick<T>(v, d, ln_blocks_per_sm(d, kBackwardThreads), 2 * d * sizeof(T), [&](auto tag, size_t smem) {
           using K = decltype(tag);
-          auto kern = ln_backward_kernel<T, W, K::V, K::BLOCK, K::RING>;
+          auto kern = ln_backward_kernel<T, W, K::V, K::LOOSE, K::BLOCK, K::RING>;
           static SmemAllowed allowed;
           e = allow_smem(kern, smem, allowed);
           if (e == cudaSuccess) e = launch_ops("layernorm_backward", kern, dim3(grid), dim3(K::BLOCK ? ln_block_threads(d) : 32 * kLnWarps),
