@@ -62,15 +62,15 @@ struct Part : Words<T, V * N> {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           const int c = (i * nt + tid) * 2;
-          Base::w[i] = c < d ? p[c] : 0u;
-          high[i] = c + 1 < d ? p[c + 1] : 0u;
+          Base::w[i] = c < d ? gload(p + c) : 0u;
+          high[i] = c + 1 < d ? gload(p + c + 1) : 0u;
         }
       } else {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           const int c = (i * nt + tid) * 2;
-          if (c + 1 < d) Base::w[i] = *reinterpret_cast<const uint32_t*>(p + c);
-          else Base::w[i] = c < d ? p[c] : 0u;
+          if (c + 1 < d) Base::w[i] = gload(reinterpret_cast<const uint32_t*>(p + c));
+          else Base::w[i] = c < d ? gload(p + c) : 0u;
           high[i] = 0;
         }
       }
@@ -79,6 +79,17 @@ struct Part : Words<T, V * N> {
       for (int i = 0; i < N; ++i) {
         const int c = (i * nt + tid) * V;
         if (c < d) Base::template load<V>(i, row + c);
+        else Base::template zero<V>(i);
+      }
+    }
+  }
+  // The thread's own elements of a ring slot.
+  __device__ __forceinline__ void load_ring(const T* slot, int d, int tid, int nt) {
+    if constexpr (V * sizeof(T) == 16) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int c = (i * nt + tid) * V;
+        if (c < d) Base::load16_shared(i, slot + c);
         else Base::template zero<V>(i);
       }
     }
@@ -131,6 +142,13 @@ struct Weights : Words<W, V * N> {
     }
   }
 };
+
+// s / d, rounded once for s / d exact (a row of one value has that mean), with
+// inv = 1 / d: the IEEE division is a third of the forward's instructions.
+__device__ __forceinline__ float mean_of(float s, float d, float inv) {
+  const float q = s * inv;
+  return fmaf(fmaf(-q, d, s), inv, q);
+}
 
 // Copies of one thread's vectors of a row into its places of a ring slot.
 template <typename T, int V, int N>
@@ -185,11 +203,15 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
   for (int64_t r = first; r < rows; r += step) {
     if constexpr (RING > 0) {
       ring_wait<RING - 2>();
-      cur.load(ring + slot * d, d, tid, nt);
+      cur.load_ring(ring + slot * d, d, tid, nt);
     } else {
       cur = next;
       cur.join();
-      if (r + step < rows) next.load(x + (r + step) * ldx, d, tid, nt);
+      // without a branch (past the end this row again) a loose row's loads stay under way
+      // (147 us, not 208, for 16384 rows of 7167); whole words gain nothing by it (the
+      // compiler then waits for them at once: 197 us, not 122, for 7166)
+      if (LOOSE || sizeof(T) == 4) next.load(x + (r + step < rows ? r + step : r) * ldx, d, tid, nt);
+      else if (r + step < rows) next.load(x + (r + step) * ldx, d, tid, nt);
     }
     F2 v[kElems / 2], t(0.f, 0.f);
 #pragma unroll
@@ -203,7 +225,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
       copy_in(slot == 0 ? RING - 1 : slot - 1, r + (RING - 1) * step);
       if (++slot == RING) slot = 0;
     }
-    const float mu = s[0] / (float)d;
+    const float mu = mean_of(s[0], (float)d, inv_d);
     t = F2(0.f, 0.f);
     const F2 neg_mu(-mu, -mu);
 #pragma unroll
@@ -225,7 +247,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
     }
     s[0] = sum2(t);
     group_sum<BLOCK>(s, sh);
-    const float rs = 1.0f / sqrtf(s[0] * inv_d + eps);
+    const float rs = rsqrtf(fmaf(s[0], inv_d, eps));
     if (tid == 0 && mean != nullptr) {
       mean[r] = mu;
       rstd[r] = rs;
@@ -242,7 +264,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
 template <typename T, typename W, int V, bool LOOSE, bool BLOCK, int RING>
 __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
     ln_backward_kernel(const T* dy, int64_t lddy, const T* __restrict__ x, int64_t ldx, const W* __restrict__ w,
-                       const float* __restrict__ mean, const float* __restrict__ rstd, const T* dadd, int64_t ldadd,
+                       const float* mean, const float* rstd, const T* dadd, int64_t ldadd,
                        T* dx, int64_t lddx, float* __restrict__ part, int64_t rows, int d) {
   ops_begin();
   constexpr int N = kElems / V;
@@ -275,29 +297,29 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
     ny.load(dy + first * lddy, d, tid, nt);
   }
   if (first < rows) {
-    nmu = __ldg(mean + first);
-    nrs = __ldg(rstd + first);
+    nmu = gload(mean + first);
+    nrs = gload(rstd + first);
   }
   wv.load(w, 1.f, d, tid, nt);
   for (int64_t r = first; r < rows; r += step) {
     const float mu = nmu, rs = nrs;
-    if (r + step < rows) {
-      nmu = __ldg(mean + r + step);
-      nrs = __ldg(rstd + r + step);
-    }
+    // the next row's loads without a branch (past the end: this row again): behind one
+    // their values would be waited for where it joins (166 us, not 136, for 16384
+    // rows of 7168)
+    const int64_t rn = r + step < rows ? r + step : r;
+    nmu = gload(mean + rn);
+    nrs = gload(rstd + rn);
     if constexpr (RING > 0) {
       ring_wait<RING - 2>();
-      cx.load(ring + 2 * slot * d, d, tid, nt);
-      cy.load(ring + (2 * slot + 1) * d, d, tid, nt);
+      cx.load_ring(ring + 2 * slot * d, d, tid, nt);
+      cy.load_ring(ring + (2 * slot + 1) * d, d, tid, nt);
     } else {
       cx = nx;
       cy = ny;
       cx.join();
       cy.join();
-      if (r + step < rows) {
-        nx.load(x + (r + step) * ldx, d, tid, nt);
-        ny.load(dy + (r + step) * lddy, d, tid, nt);
-      }
+      nx.load(x + rn * ldx, d, tid, nt);
+      ny.load(dy + rn * lddy, d, tid, nt);
     }
     // elements past d: dy and so g are zero
     F2 xh[kElems / 2], g[kElems / 2], s1(0.f, 0.f), s2(0.f, 0.f);
@@ -387,12 +409,12 @@ __global__ void __launch_bounds__(kLoopThreads)
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
     const T* xr = x + r * ldx;
     float s[1] = {0.f};
-    for (int i = threadIdx.x; i < d; i += blockDim.x) s[0] += to_f32(xr[i]);
+    for (int i = threadIdx.x; i < d; i += blockDim.x) s[0] += gload_f32(xr + i);
     group_sum<true>(s, sh);
     const float mu = s[0] / (float)d;
     s[0] = 0.f;
     for (int i = threadIdx.x; i < d; i += blockDim.x) {
-      const float c = to_f32(xr[i]) - mu;
+      const float c = gload_f32(xr + i) - mu;
       s[0] = fmaf(c, c, s[0]);
     }
     group_sum<true>(s, sh);
@@ -402,7 +424,7 @@ __global__ void __launch_bounds__(kLoopThreads)
       rstd[r] = rs;
     }
     for (int i = threadIdx.x; i < d; i += blockDim.x)
-      y[r * ldy + i] = from_f32<T>(fmaf((to_f32(xr[i]) - mu) * rs, w ? to_f32(w[i]) : 1.f, b ? to_f32(b[i]) : 0.f));
+      y[r * ldy + i] = from_f32<T>(fmaf((gload_f32(xr + i) - mu) * rs, w ? gload_f32(w + i) : 1.f, b ? gload_f32(b + i) : 0.f));
   }
 }
 
@@ -416,11 +438,11 @@ __global__ void __launch_bounds__(kLoopThreads)
   float* mine = part ? part + (size_t)blockIdx.x * 2 * d : nullptr;
   bool begun = false;
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x, begun = true) {
-    const float mu = mean[r], rs = rstd[r];
+    const float mu = gload(mean + r), rs = gload(rstd + r);
     float s[2] = {0.f, 0.f};
     for (int i = threadIdx.x; i < d; i += blockDim.x) {
-      const float t = to_f32(dy[r * lddy + i]), g = t * (w ? to_f32(w[i]) : 1.f);
-      const float xh = (to_f32(x[r * ldx + i]) - mu) * rs;
+      const float t = gload_f32(dy + r * lddy + i), g = t * (w ? gload_f32(w + i) : 1.f);
+      const float xh = (gload_f32(x + r * ldx + i) - mu) * rs;
       s[0] += g;
       s[1] = fmaf(g, xh, s[1]);
       if (mine) {  // a column is one thread's
@@ -431,10 +453,10 @@ __global__ void __launch_bounds__(kLoopThreads)
     group_sum<true>(s, sh);
     const float m1 = s[0] / (float)d, m2 = s[1] / (float)d;
     for (int i = threadIdx.x; i < d; i += blockDim.x) {
-      const float g = to_f32(dy[r * lddy + i]) * (w ? to_f32(w[i]) : 1.f);
-      const float xh = (to_f32(x[r * ldx + i]) - mu) * rs;
+      const float g = gload_f32(dy + r * lddy + i) * (w ? gload_f32(w + i) : 1.f);
+      const float xh = (gload_f32(x + r * ldx + i) - mu) * rs;
       float v = rs * (g - m1 - xh * m2);
-      if (dadd) v += to_f32(dadd[r * ldadd + i]);
+      if (dadd) v += gload_f32(dadd + r * ldadd + i);
       dx[r * lddx + i] = from_f32<T>(v);
     }
   }
@@ -453,7 +475,7 @@ __global__ void __launch_bounds__(1024) ln_reduce_kernel(const float* __restrict
   float s = 0.f;
   if (c < 2 * d) {
 #pragma unroll 8
-    for (int p = warp * per; p < p1; ++p) s += __ldcg(part + (size_t)p * 2 * d + c);
+    for (int p = warp * per; p < p1; ++p) s += gload(part + (size_t)p * 2 * d + c);
   }
   sh[warp][lane] = s;
   __syncthreads();

@@ -86,35 +86,45 @@ __device__ __forceinline__ int warp_find_group(const int* __restrict__ off, int 
   if (off == nullptr) return 0;
   const int stride = (G + 31) >> 5;
   const int i = lane * stride;
-  const uint32_t b = __ballot_sync(0xffffffffu, i < G && __ldg(off + i) <= p);
+  const uint32_t b = __ballot_sync(0xffffffffu, i < G && gload(off + i) <= p);
   const int lo = (31 - __clz(b | 1u)) * stride;
-  const bool in = lane < stride && lo + lane < G && __ldg(off + lo + lane) <= p;
+  const bool in = lane < stride && lo + lane < G && gload(off + lo + lane) <= p;
   return lo + 31 - __clz(__ballot_sync(0xffffffffu, in) | 1u);
+}
+
+// The same for a row of each lane's own.
+__device__ __forceinline__ int lane_find_group(const int* off, int G, int p) {
+  if (off == nullptr) return 0;
+  int lo = 0, hi = G - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (gload(off + mid) <= p) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
 }
 
 // A block of 32 elements as loaded: 16 bytes at a time when V, else one by one.
 template <typename T, bool V>
 struct Block32 {
   static constexpr int W = V ? 16 / sizeof(T) : 1;
-  Vec<T, W> e[32 / W];
+  Words<T, 32> e;
   __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-    for (int i = 0; i < 32 / W; ++i) e[i] = load_vec<T, W>(p + i * W);
+    for (int i = 0; i < 32 / W; ++i) e.template load<W>(i, p + i * W);
   }
-  __device__ __forceinline__ float at(int i) const { return to_f32(e[i / W].e[i % W]); }
   // Bits of the largest magnitude as fp32 (of a NaN or infinity: 0x7F800000 or more).
   __device__ __forceinline__ uint32_t max_bits() const {
     uint32_t m = 0;
-    if constexpr (V && sizeof(T) == 2) {
+    if constexpr (sizeof(T) == 2) {
       // magnitudes order as their bits do: 16-bit integer maxima, two at a time
-      const uint32_t* u = reinterpret_cast<const uint32_t*>(e);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) m = __vmaxu2(m, u[i] & 0x7FFF7FFFu);
+      for (int i = 0; i < 16; ++i) m = __vmaxu2(m, e.w[i] & 0x7FFF7FFFu);
       const uint16_t h = (uint16_t)max(m & 0xFFFFu, m >> 16);
       return __float_as_uint(to_f32(*reinterpret_cast<const T*>(&h)));
     } else {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) m = max(m, __float_as_uint(at(i)) & 0x7FFFFFFFu);
+      for (int i = 0; i < 32; ++i) m = max(m, e.w[i] & 0x7FFFFFFFu);
       return m;
     }
   }
@@ -137,12 +147,12 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const T* __restrict__ x
   const int kb = (int)(i - p * nb);                // past the last row: beyond nb
   const bool in = kb * 32 < K;
   Block32<T, V> v;
-  if (in) v.load(x + (perm ? (int64_t)(__ldg(perm + p) / k) : p) * ldx + kb * 32);
+  if (in) v.load(x + (perm ? (int64_t)(gload(perm + p) / k) : p) * ldx + kb * 32);
   int g;
   if (first / nb == min(rows - 1, (first + 31) / nb)) g = warp_find_group(off, G, (int)p, lane);
-  else g = off ? find_expert(off, G, (int)p) : 0;
-  const int64_t o = off ? __ldg(off + g) : 0;
-  const bool live = kb < nb && (off == nullptr || p < __ldg(off + G));
+  else g = lane_find_group(off, G, (int)p);
+  const int64_t o = off ? gload(off + g) : 0;
+  const bool live = kb < nb && (off == nullptr || p < gload(off + G));
   uint32_t byte = 127;
   if (in && live) {
     const uint32_t m = v.max_bits();
@@ -154,7 +164,11 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const T* __restrict__ x
     for (int w = 0; w < 4; ++w) {
       float y[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = v.at(w * 8 + j) * f;
+      for (int j = 0; j < 4; ++j) {
+        const float2 t = mul2(v.e.pair(w * 4 + j), F2(f, f)).get();
+        y[2 * j] = t.x;
+        y[2 * j + 1] = t.y;
+      }
       c[w] = byte != 255u ? fp4_pack8(y) : 0u;
     }
     *reinterpret_cast<uint4*>(q + p * (K / 2) + kb * 16) = make_uint4(c[0], c[1], c[2], c[3]);
@@ -190,20 +204,20 @@ __global__ void __launch_bounds__(256) dequant_rows_kernel(const uint8_t* __rest
   const int64_t w = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5;
   const int64_t p = w / segs;
   const int pass0 = (int)(w % segs) * per;
-  if (p >= rows || (off != nullptr && p >= __ldg(off + G))) return;
+  if (p >= rows || (off != nullptr && p >= gload(off + G))) return;
   uint32_t code[kSegPasses];
 #pragma unroll
   for (int i = 0; i < kSegPasses; ++i) {
     const int c = (pass0 + i) * 256 + lane * 8;
-    code[i] = i < per && c < K ? *reinterpret_cast<const uint32_t*>(q + p * (K / 2) + c / 2) : 0u;
+    code[i] = i < per && c < K ? gload(reinterpret_cast<const uint32_t*>(q + p * (K / 2) + c / 2)) : 0u;
   }
   const int g = warp_find_group(off, G, (int)p, lane);
-  const int64_t o = off ? __ldg(off + g) : 0;
+  const int64_t o = off ? gload(off + g) : 0;
   uint32_t sb[kSegPasses];
 #pragma unroll
   for (int i = 0; i < kSegPasses; ++i) {
     const int c = (pass0 + i) * 256 + lane * 8;
-    sb[i] = i < per && c < K ? sc[fp4_row_scale_at(o, g, p - o, c / 32, KT)] : 0u;
+    sb[i] = i < per && c < K ? gload(sc + fp4_row_scale_at(o, g, p - o, c / 32, KT)) : 0u;
   }
 #pragma unroll
   for (int i = 0; i < kSegPasses; ++i) {
@@ -569,7 +583,7 @@ __global__ void __launch_bounds__(kThreads4, 1)
 
   // experts' rows and units
   // (offsets out of order or range give wrong rows, not accesses out of range)
-  for (int i = threadIdx.x; i <= p.G; i += blockDim.x) s_off[i] = p.off ? min(max(p.off[i], 0), p.rows) : (i ? p.rows : 0);
+  for (int i = threadIdx.x; i <= p.G; i += blockDim.x) s_off[i] = p.off ? min(max(gload(p.off + i), 0), p.rows) : (i ? p.rows : 0);
   __syncthreads();
   if (warp == 0) {
     int run = 0, most = 0;

@@ -27,15 +27,52 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { retu
 template <>
 __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
-// V consecutive elements of a row, loaded and stored as one access.
+// Loads of global memory that stay where they are written.  The kernels start before
+// the one that writes their inputs has ended and wait for it (ops_wait), so none of
+// their inputs is read-only for the whole kernel: a load that the compiler takes for
+// one (__ldg, const __restrict__ pointers) might be moved before the wait.
+__device__ __forceinline__ uint4 gload(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 gload(const uint2* p) {
+  uint2 v;
+  asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t gload(const uint32_t* p) {
+  uint32_t v;
+  asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t gload(const uint16_t* p) {
+  uint16_t v;
+  asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t gload(const uint8_t* p) {
+  uint32_t v;
+  asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ int gload(const int* p) { return (int)gload(reinterpret_cast<const uint32_t*>(p)); }
+__device__ __forceinline__ float gload(const float* p) {
+  return __uint_as_float(gload(reinterpret_cast<const uint32_t*>(p)));
+}
+__device__ __forceinline__ float gload_f32(const float* p) { return gload(p); }
+__device__ __forceinline__ float gload_f32(const __nv_bfloat16* p) {
+  return __uint_as_float(gload(reinterpret_cast<const uint16_t*>(p)) << 16);
+}
+__device__ __forceinline__ float gload_f32(const __half* p) {
+  return __half2float(__ushort_as_half((uint16_t)gload(reinterpret_cast<const uint16_t*>(p))));
+}
+
+// V consecutive elements of a row, stored as one access.
 template <typename T, int V>
 struct alignas(V * sizeof(T)) Vec {
   T e[V];
 };
-template <typename T, int V>
-__device__ __forceinline__ Vec<T, V> load_vec(const T* p) {
-  return *reinterpret_cast<const Vec<T, V>*>(p);
-}
 template <typename T, int V>
 __device__ __forceinline__ void store_vec(T* p, const Vec<T, V>& v) {
   *reinterpret_cast<Vec<T, V>*>(p) = v;
@@ -124,23 +161,30 @@ struct Words {
   __device__ __forceinline__ F2 pair(int k) const { return pair_f32<T>(w + k * (int)sizeof(T) / 2); }
   __device__ __forceinline__ void set(int k, F2 v) { pair_to<T>(w + k * (int)sizeof(T) / 2, v); }
   template <int V>
-  __device__ __forceinline__ void load(int i, const T* p) {
+  __device__ __forceinline__ void load(int i, const T* p) {  // from global memory
     if constexpr (V * sizeof(T) == 16) {
-      const uint4 u = *reinterpret_cast<const uint4*>(p);
+      const uint4 u = gload(reinterpret_cast<const uint4*>(p));
       w[4 * i] = u.x;
       w[4 * i + 1] = u.y;
       w[4 * i + 2] = u.z;
       w[4 * i + 3] = u.w;
     } else if constexpr (V * sizeof(T) == 8) {
-      const uint2 u = *reinterpret_cast<const uint2*>(p);
+      const uint2 u = gload(reinterpret_cast<const uint2*>(p));
       w[2 * i] = u.x;
       w[2 * i + 1] = u.y;
     } else if constexpr (V * sizeof(T) == 4) {
-      w[i] = *reinterpret_cast<const uint32_t*>(p);
+      w[i] = gload(reinterpret_cast<const uint32_t*>(p));
     } else {  // one 16-bit element
-      const uint32_t u = *reinterpret_cast<const uint16_t*>(p);
+      const uint32_t u = gload(reinterpret_cast<const uint16_t*>(p));
       w[i / 2] = i % 2 ? w[i / 2] | (u << 16) : u;
     }
+  }
+  __device__ __forceinline__ void load16_shared(int i, const T* p) {  // 16 bytes of shared memory
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    w[4 * i] = u.x;
+    w[4 * i + 1] = u.y;
+    w[4 * i + 2] = u.z;
+    w[4 * i + 3] = u.w;
   }
   __device__ __forceinline__ void clear() {
 #pragma unroll

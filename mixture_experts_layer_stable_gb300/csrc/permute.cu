@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(1024) sort_kernel(const int* __restrict__ ids,
 #pragma unroll
     for (int i = 0; i < kSortIters; ++i) {
       const int64_t r = w0 + i * 32 + lane;
-      e[i] = r < w1 ? bucket(__ldg(ids + r), E) : -1;
+      e[i] = r < w1 ? bucket(gload(ids + r), E) : -1;
     }
 #pragma unroll
     for (int i = 0; i < kSortIters; ++i) {
@@ -94,8 +94,8 @@ __global__ void __launch_bounds__(1024) sort_kernel(const int* __restrict__ ids,
         if (c < me) pre += v;
       }
     } else if (total != nullptr) {
-      all = __ldg(total + tid);
-      pre = __ldg(before + (size_t)blockIdx.x * nb + tid);
+      all = gload(total + tid);
+      pre = gload(before + (size_t)blockIdx.x * nb + tid);
     } else {
       all = tot[tid];
     }
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(1024) sort_kernel(const int* __restrict__ ids,
       const uint32_t me = cluster_ctarank(), a = smem_u32(tot + E);
       for (uint32_t c = 0; c < me; ++c) drop += ld_cluster(a, c);
     } else if (total != nullptr) {
-      drop = __ldg(before + (size_t)blockIdx.x * nb + E);
+      drop = gload(before + (size_t)blockIdx.x * nb + E);
     }
     start[E] = kept + drop;
     if (blockIdx.x == 0) offsets[E] = kept;
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(1024) sort_hist_kernel(const int* __restrict__
   __syncthreads();
   ops_begin();
   const int64_t r0 = blockIdx.x * (int64_t)kSortBlockRows, r1 = min(R, r0 + kSortBlockRows);
-  for (int64_t r = r0 + threadIdx.x; r < r1; r += blockDim.x) atomicAdd(&sh[bucket(__ldg(ids + r), E)], 1);
+  for (int64_t r = r0 + threadIdx.x; r < r1; r += blockDim.x) atomicAdd(&sh[bucket(gload(ids + r), E)], 1);
   __syncthreads();
   for (int e = threadIdx.x; e <= E; e += blockDim.x) hist[(size_t)blockIdx.x * (E + 1) + e] = sh[e];
 }
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(1024) sort_scan_kernel(int* __restrict__ hist,
   int sum = 0;
   if (e < nb) {
 #pragma unroll 8
-    for (int p = p0; p < p1; ++p) sum += __ldcg(hist + (size_t)p * nb + e);
+    for (int p = p0; p < p1; ++p) sum += gload(hist + (size_t)p * nb + e);
   }
   sh[warp][lane] = sum;
   __syncthreads();
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(1024) sort_scan_kernel(int* __restrict__ hist,
   for (int p = p0; p < p1; p += 8) {
     int c[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) c[u] = p + u < p1 ? __ldcg(hist + (size_t)(p + u) * nb + e) : 0;
+    for (int u = 0; u < 8; ++u) c[u] = p + u < p1 ? gload(hist + (size_t)(p + u) * nb + e) : 0;
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       if (p + u < p1) hist[(size_t)(p + u) * nb + e] = run;
@@ -222,14 +222,14 @@ __global__ void __launch_bounds__(256) permute_kernel(const T* __restrict__ x, i
   int64_t t;
   int c;
   if (!lay_at(lay, tokens, t, c)) return;
-  const int kept = __ldg(kept_p);
+  const int kept = gload(kept_p);
   Words<T, V> v, z;
   z.clear();
   v.template load<V>(0, x + t * ldx + c * V);
   const int* pi = inv + t * k;
 #pragma unroll 8
   for (int j = 0; j < k; ++j) {
-    const int p = __ldg(pi + j);
+    const int p = gload(pi + j);
     T* dst = xp + (int64_t)p * d + c * V;
     if (p < kept) v.template store<V>(0, dst);
     else z.template store<V>(0, dst);
@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(256) unpermute_kernel(const T* __restrict__ y,
   int64_t t;
   int c;
   if (!lay_at(lay, tokens, t, c)) return;
-  const int kept = __ldg(kept_p);
+  const int kept = gload(kept_p);
   F2 s[E / 2];
 #pragma unroll
   for (int q = 0; q < E / 2; ++q) s[q] = F2(0.f, 0.f);
@@ -263,12 +263,12 @@ __global__ void __launch_bounds__(256) unpermute_kernel(const T* __restrict__ y,
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const int j = j0 + u;
-      const int p = j < k ? __ldg(inv + t * k + j) : kept;
+      const int p = j < k ? gload(inv + t * k + j) : kept;
       v[u].clear();
       wj[u] = 0.f;
       if (p < kept) {
         v[u].template load<V>(0, y + (int64_t)p * d + c * V);
-        wj[u] = w ? __ldg(w + t * k + j) : 1.f;
+        wj[u] = w ? gload(w + t * k + j) : 1.f;
       }
     }
 #pragma unroll
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) unpermute_backward_kernel(
   ops_begin();
   const int64_t t = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, nw = nt >> 5;
-  const int kept = __ldg(kept_p), span = nt * V * kBwdVec;
+  const int kept = gload(kept_p), span = nt * V * kBwdVec;
   for (int c0 = 0; c0 < d; c0 += span) {
     Words<T, E> g[kBwdVec];
 #pragma unroll
@@ -311,9 +311,9 @@ __global__ void __launch_bounds__(kBwdThreads, 2) unpermute_backward_kernel(
     }
 #pragma unroll 2
     for (int j = 0; j < k; ++j) {
-      const int p = __ldg(inv + t * k + j);
+      const int p = gload(inv + t * k + j);
       const bool live = p < kept;
-      const float wr = live ? (w ? __ldg(w + t * k + j) : 1.f) : 0.f;
+      const float wr = live ? (w ? gload(w + t * k + j) : 1.f) : 0.f;
       const int64_t row = (int64_t)p * d;
       Words<T, E> v[kBwdVec];
       if (dw != nullptr && live) {
@@ -374,14 +374,14 @@ template <typename T, bool EDGE>
 __device__ __forceinline__ RawWord load_word(const T* p, bool whole, bool lo, bool hi) {
   RawWord r{0u, 0u};
   if constexpr (sizeof(T) == 4) {
-    if (!EDGE || lo) r.lo = *reinterpret_cast<const uint32_t*>(p);
+    if (!EDGE || lo) r.lo = gload(reinterpret_cast<const uint32_t*>(p));
   } else {
     const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
     if (EDGE || !whole) {
-      if (!EDGE || lo) r.lo = h[0];
-      if (!EDGE || hi) r.hi = h[1];
+      if (!EDGE || lo) r.lo = gload(h);
+      if (!EDGE || hi) r.hi = gload(h + 1);
     } else {
-      r.lo = *reinterpret_cast<const uint32_t*>(p);
+      r.lo = gload(reinterpret_cast<const uint32_t*>(p));
     }
   }
   return r;
@@ -403,10 +403,13 @@ __device__ __forceinline__ F2 word_f32(uint32_t w) {
 }
 template <typename T>
 __device__ __forceinline__ uint32_t f32_word(F2 v) {
-  if constexpr (sizeof(T) == 4) return __float_as_uint(v.get().x);
-  uint32_t w;
-  if constexpr (sizeof(T) == 2) pair_to<T>(&w, v);
-  return w;
+  if constexpr (sizeof(T) == 4) {
+    return __float_as_uint(v.get().x);
+  } else {
+    uint32_t w;
+    pair_to<T>(&w, v);
+    return w;
+  }
 }
 constexpr __host__ __device__ int words_of(int d, size_t es) { return es == 4 ? d : d / 2 + 1; }
 // Whether the row at p starts in the middle of a word.
@@ -420,11 +423,11 @@ struct Around {
   uint32_t even, odd;
   __device__ __forceinline__ void load(const T* row, int c, int d) {
     if constexpr (sizeof(T) == 4) {
-      even = odd = c < d ? *reinterpret_cast<const uint32_t*>(row + c) : 0u;
+      even = odd = c < d ? gload(reinterpret_cast<const uint32_t*>(row + c)) : 0u;
     } else {
       const uint16_t* h = reinterpret_cast<const uint16_t*>(row) + 2 * c;
-      const uint32_t m = c > 0 && 2 * c - 1 < d ? h[-1] : 0u;
-      const uint32_t a = 2 * c < d ? h[0] : 0u, b = 2 * c + 1 < d ? h[1] : 0u;
+      const uint32_t m = c > 0 && 2 * c - 1 < d ? gload(h - 1) : 0u;
+      const uint32_t a = 2 * c < d ? gload(h) : 0u, b = 2 * c + 1 < d ? gload(h + 1) : 0u;
       even = a | (b << 16);
       odd = m | (a << 16);
     }
@@ -450,7 +453,7 @@ __global__ void __launch_bounds__(256) permute_words_kernel(const T* __restrict_
   int64_t t;
   int c0;
   if (!lay_at(lay, tokens, t, c0)) return;
-  const int kept = __ldg(kept_p), n = words_of(d, sizeof(T));
+  const int kept = gload(kept_p), n = words_of(d, sizeof(T));
   const int* pi = inv + t * k;
   Around<T> v[kWordsEach];
 #pragma unroll
@@ -459,7 +462,7 @@ __global__ void __launch_bounds__(256) permute_words_kernel(const T* __restrict_
     constexpr bool EDGE = decltype(edge)::value;
 #pragma unroll 4
     for (int j = 0; j < k; ++j) {
-      const int p = __ldg(pi + j);
+      const int p = gload(pi + j);
       const bool live = p < kept;
       T* row = xp + (int64_t)p * d;
       const int a = half_word(row), e0 = c0 * E - a;
@@ -484,7 +487,7 @@ __global__ void __launch_bounds__(256) unpermute_words_kernel(const T* __restric
   int64_t t;
   int c0;
   if (!lay_at(lay, tokens, t, c0)) return;
-  const int kept = __ldg(kept_p), n = words_of(d, sizeof(T)), stride = lay.nv * E;
+  const int kept = gload(kept_p), n = words_of(d, sizeof(T)), stride = lay.nv * E;
   const int* pi = inv + t * k;
   const float* pw = w + t * k;
   T* row = out + t * ldout;
@@ -507,12 +510,12 @@ __global__ void __launch_bounds__(256) unpermute_words_kernel(const T* __restric
       float wj[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int p = j0 + q < k ? __ldg(pi + j0 + q) : kept;
+        const int p = j0 + q < k ? gload(pi + j0 + q) : kept;
         wj[q] = 0.f;
 #pragma unroll
         for (int u = 0; u < kWordsEach; ++u) v[q][u] = RawWord{0u, 0u};
         if (p < kept) {
-          wj[q] = w ? __ldg(pw + j0 + q) : 1.f;
+          wj[q] = w ? gload(pw + j0 + q) : 1.f;
           const T* src = y + (int64_t)p * d + e0;
           if (half_word(src)) {
 #pragma unroll
@@ -546,7 +549,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) unpermute_backward_words_kerne
   ops_begin();
   const int64_t t = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, nw = nt >> 5;
-  const int kept = __ldg(kept_p), n = words_of(d, sizeof(T)), stride = nt * E;
+  const int kept = gload(kept_p), n = words_of(d, sizeof(T)), stride = nt * E;
   const int* pi = inv + t * k;
   const float* pw = w + t * k;
   for (int b0 = 0; b0 < n; b0 += nt * kWordsEach) {
@@ -556,9 +559,9 @@ __global__ void __launch_bounds__(kBwdThreads, 2) unpermute_backward_words_kerne
     for (int u = 0; u < kWordsEach; ++u) g[u].load(dout + t * lddout, c0 + u * nt, d);
 #pragma unroll 2
     for (int j = 0; j < k; ++j) {
-      const int p = __ldg(pi + j);
+      const int p = gload(pi + j);
       const bool live = p < kept;
-      const float wr = live ? (w ? __ldg(pw + j) : 1.f) : 0.f;
+      const float wr = live ? (w ? gload(pw + j) : 1.f) : 0.f;
       const F2 w2(wr, wr);
       T* row = dy + (int64_t)p * d;
       const int a = half_word(row), e0 = c0 * E - a;
