@@ -313,16 +313,14 @@ __global__ void __launch_bounds__(kBwdThreads, 2) unpermute_backward_kernel(
     for (int j = 0; j < k; ++j) {
       const int p = gload(inv + t * k + j);
       const bool live = p < kept;
-      const float wr = live ? (w ? gload(w + t * k + j) : 1.f) : 0.f;
+      const float wj = w ? gload(w + t * k + j) : 1.f;
+      const float wr = live ? wj : 0.f;
       const int64_t row = (int64_t)p * d;
       Words<T, E> v[kBwdVec];
-      if (dw != nullptr && live) {
+      if (dw != nullptr) {  // (loads without branches: a dropped row's from row 0, past d of its last vector)
+        const T* src = y + (live ? row : 0);
 #pragma unroll
-        for (int i = 0; i < kBwdVec; ++i) {
-          const int c = c0 + (i * nt + tid) * V;
-          v[i].clear();
-          if (c < d) v[i].template load<V>(0, y + row + c);
-        }
+        for (int i = 0; i < kBwdVec; ++i) v[i].template load<V>(0, src + min(c0 + (i * nt + tid) * V, d - V));
       }
       const F2 w2(wr, wr);
 #pragma unroll
@@ -337,9 +335,11 @@ __global__ void __launch_bounds__(kBwdThreads, 2) unpermute_backward_kernel(
         F2 s(0.f, 0.f);
         if (live) {
 #pragma unroll
-          for (int i = 0; i < kBwdVec; ++i)
+          for (int i = 0; i < kBwdVec; ++i) {
+            if (c0 + (i * nt + tid) * V >= d) break;
 #pragma unroll
             for (int q = 0; q < E / 2; ++q) s = fma2(g[i].pair(q), v[i].pair(q), s);
+          }
         }
         const float r = warp_sum(sum2(s));
         if (lane == 0) sh[warp][j] = c0 ? sh[warp][j] + r : r;
