@@ -51,9 +51,8 @@ __device__ __forceinline__ float fp4_value(uint32_t c) {
 
 // Offset of the scale of row i of expert g (whose rows start at off), block kb:
 // off / 128 + g leaves every expert room for its rows rounded up to 128.
-__host__ __device__ inline size_t fp4_row_scale_at(int64_t off, int g, int64_t i, int kb, int KT) {
-  const int64_t run = off / 128 + g + i / 128;
-  const int r = (int)(i % 128);
+__device__ __forceinline__ size_t fp4_row_scale_at(uint32_t off, uint32_t g, uint32_t i, uint32_t kb, uint32_t KT) {
+  const uint32_t run = off / 128 + g + i / 128, r = i % 128;
   return ((size_t)run * KT + (kb >> 2)) * 512u + 16 * (r & 31) + 4 * (r >> 5) + (kb & 3);
 }
 __host__ __device__ inline size_t fp4_weight_scale_at(int64_t e, int n, int kb, int N, int KT) {
@@ -132,27 +131,24 @@ struct Block32 {
 
 // One lane a block (the blocks that pad a row's last scale tile included, scale 1):
 // the block's maximum needs no exchange, its codes leave as 16 bytes, and four lanes
-// join their scale bytes into a word of the tile.
+// join their scale bytes into a word of the tile.  A block of threads takes one row
+// (or 256 blocks of a wider one), or `rpb` short ones: it is bound by instruction
+// issue, and places from divisions of a flat index made up a third of that.
 template <typename T, bool V>
-__global__ void __launch_bounds__(256) quant_rows_kernel(const T* __restrict__ x, int64_t ldx, int64_t rows, int K,
-                                                         int G, const int* __restrict__ off,
-                                                         const int* __restrict__ perm, int k, uint8_t* __restrict__ q,
-                                                         uint8_t* __restrict__ sc) {
+__global__ void __launch_bounds__(256) quant_rows_kernel(const T* x, int64_t ldx, int rows, int K, int G,
+                                                         const int* off, const int* perm, int k, int rpb, uint8_t* q,
+                                                         uint8_t* sc) {
   ops_begin();
   const int lane = threadIdx.x & 31, KT = (K + 127) / 128, nb = KT * 4;
-  const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
-  const int64_t first = i - lane;                  // the warp's first block
-  if (first >= rows * nb) return;
-  const int64_t p = min(rows - 1, i / nb);
-  const int kb = (int)(i - p * nb);                // past the last row: beyond nb
-  const bool in = kb * 32 < K;
+  const int sub = rpb > 1 ? (int)threadIdx.x / nb : 0;
+  const int p_raw = (int)blockIdx.x * rpb + sub, p = min(p_raw, rows - 1);
+  const int kb = rpb > 1 ? (int)threadIdx.x - sub * nb : (int)(blockIdx.y * 256 + threadIdx.x);
+  const bool mine = p_raw < rows && sub < rpb && kb < nb, in = mine && kb * 32 < K;
   Block32<T, V> v;
-  if (in) v.load(x + (perm ? (int64_t)(gload(perm + p) / k) : p) * ldx + kb * 32);
-  int g;
-  if (first / nb == min(rows - 1, (first + 31) / nb)) g = warp_find_group(off, G, (int)p, lane);
-  else g = lane_find_group(off, G, (int)p);
-  const int64_t o = off ? gload(off + g) : 0;
-  const bool live = kb < nb && (off == nullptr || p < gload(off + G));
+  if (in) v.load(x + (int64_t)(perm ? gload(perm + p) / k : p) * ldx + kb * 32);
+  const int g = rpb > 1 ? lane_find_group(off, G, p) : warp_find_group(off, G, p, lane);
+  const int o = off ? gload(off + g) : 0;
+  const bool live = mine && (off == nullptr || p < gload(off + G));
   uint32_t byte = 127;
   if (in && live) {
     const uint32_t m = v.max_bits();
@@ -171,7 +167,7 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const T* __restrict__ x
       }
       c[w] = byte != 255u ? fp4_pack8(y) : 0u;
     }
-    *reinterpret_cast<uint4*>(q + p * (K / 2) + kb * 16) = make_uint4(c[0], c[1], c[2], c[3]);
+    *reinterpret_cast<uint4*>(q + (int64_t)p * (K / 2) + kb * 16) = make_uint4(c[0], c[1], c[2], c[3]);
   }
   byte <<= 8 * (lane & 3);
   byte |= __shfl_xor_sync(0xffffffffu, byte, 1);
@@ -217,7 +213,7 @@ __global__ void __launch_bounds__(256) dequant_rows_kernel(const uint8_t* __rest
 #pragma unroll
   for (int i = 0; i < kSegPasses; ++i) {
     const int c = (pass0 + i) * 256 + lane * 8;
-    sb[i] = i < per && c < K ? gload(sc + fp4_row_scale_at(o, g, p - o, c / 32, KT)) : 0u;
+    sb[i] = i < per && c < K ? gload(sc + fp4_row_scale_at((uint32_t)o, g, (uint32_t)(p - o), c / 32, KT)) : 0u;
   }
 #pragma unroll
   for (int i = 0; i < kSegPasses; ++i) {
@@ -977,9 +973,11 @@ moe_status moe_quantize_mxfp4_rows(int32_t dtype, int64_t rows, int32_t K, const
   return ops_status(with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
     auto kern = rows16(x, ldx, dtype) ? quant_rows_kernel<T, true> : quant_rows_kernel<T, false>;
-    const unsigned grid = (unsigned)((rows * ((K + 127) / 128) * 4 + 255) / 256);
-    return launch_ops("quantize_mxfp4_rows", kern, dim3(grid), dim3(256), 0, st, static_cast<const T*>(x), ldx, rows, K,
-                      G, offsets, perm, k, q, scales);
+    const int nb = (K + 127) / 128 * 4, rpb = nb < 64 ? 128 / nb : 1;
+    const int threads = nb > 256 ? 256 : (nb * rpb + 31) / 32 * 32;
+    return launch_ops("quantize_mxfp4_rows", kern, dim3((unsigned)((rows + rpb - 1) / rpb), (nb + 255) / 256),
+                      dim3(threads), 0, st, static_cast<const T*>(x), ldx, (int)rows, K, G, offsets, perm, k, rpb, q,
+                      scales);
   }));
 }
 
