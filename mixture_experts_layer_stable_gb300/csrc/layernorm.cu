@@ -27,21 +27,24 @@ constexpr int kBlockRowMax = 512 * kElems;  // a block up to this
 constexpr int kLnWarps = 8;      // warps (rows) of a block in the warp form
 constexpr int kLoopThreads = 512;
 
-// Sums of M values over the group's threads, the same in each.
-template <bool BLOCK, int M>
-__device__ __forceinline__ void group_sum(float (&v)[M], float (*sh)[M]) {
+// Sums of M values over the group's threads, the same in each.  ONE: with one barrier
+// instead of two -- sh is used in turns (`turn` counts the calls), and before a part is
+// written again every thread has passed the barrier of the call in between.
+template <bool BLOCK, bool ONE, int M>
+__device__ __forceinline__ void group_sum(float (&v)[M], float (*sh)[32][M], int& turn) {
 #pragma unroll
   for (int m = 0; m < M; ++m) v[m] = warp_sum(v[m]);
   if constexpr (BLOCK) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    __syncthreads();  // the last sums' values have been read
+    float(*to)[M] = ONE ? sh[turn++ & 1] : sh[0];
+    if (!ONE) __syncthreads();  // the last sums' values have been read
     if (lane == 0) {
 #pragma unroll
-      for (int m = 0; m < M; ++m) sh[warp][m] = v[m];
+      for (int m = 0; m < M; ++m) to[warp][m] = v[m];
     }
     __syncthreads();
 #pragma unroll
-    for (int m = 0; m < M; ++m) v[m] = warp_sum(lane < nw ? sh[lane][m] : 0.f);
+    for (int m = 0; m < M; ++m) v[m] = warp_sum(lane < nw ? to[lane][m] : 0.f);
   }
 }
 
@@ -179,7 +182,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
   ops_begin();
   constexpr int N = kElems / V;
   extern __shared__ __align__(16) uint8_t ring_mem[];
-  __shared__ float sh[32][1];
+  __shared__ float sh[2][32][2], sh1[2][32][1], sh_n[32];
   const int tid = BLOCK ? threadIdx.x : threadIdx.x & 31, nt = BLOCK ? blockDim.x : 32;
   const int64_t first = BLOCK ? blockIdx.x : blockIdx.x * (int64_t)kLnWarps + (threadIdx.x >> 5);
   const int64_t step = BLOCK ? gridDim.x : gridDim.x * (int64_t)kLnWarps;
@@ -187,7 +190,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
   T* ring = reinterpret_cast<T*>(ring_mem);
   Part<T, V, N, LOOSE> cur, next;
   Weights<W, V, N> wv, bv;
-  int slot = 0;
+  int slot = 0, turn = 0;
   auto copy_in = [&](int sl, int64_t r) {
     if (r < rows) ring_copy<T, V, N>(ring + sl * d, x + r * ldx, d, tid, nt);
     ring_commit();
@@ -197,6 +200,19 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
     for (int i = 0; i < RING - 1; ++i) copy_in(i, first + i * step);
   } else if (first < rows) {
     next.load(x + first * ldx, d, tid, nt);
+  }
+  // with a ring: the elements that this warp holds, and warp `lane`
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  float wn = 1.f, inv_wn = 1.f, ln = 0.f;
+  if constexpr (RING > 0) {
+    float mine = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) mine += (float)max(0, min(V, d - (i * nt + tid) * V));
+    wn = warp_sum(mine);
+    inv_wn = 1.0f / wn;
+    if (lane == 0) sh_n[warp] = wn;
+    __syncthreads();
+    ln = lane < nw ? sh_n[lane] : 0.f;
   }
   wv.load(w, 1.f, d, tid, nt);
   bv.load(b, 0.f, d, tid, nt);
@@ -219,15 +235,21 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
       v[k] = cur.pair(k);
       t = add2(t, v[k]);
     }
-    float s[1] = {sum2(t)};
-    group_sum<BLOCK>(s, sh);
+    // With a ring: the warp's mean and its squared distances from that, and the row's
+    // from the warps' (of distances only, so that a large mean costs nothing), in one
+    // exchange; else the row's mean, then the distances from it, in two.
+    float near;  // the mean that the distances are taken from
     if constexpr (RING > 0) {
+      near = mean_of(warp_sum(sum2(t)), wn, inv_wn);
       copy_in(slot == 0 ? RING - 1 : slot - 1, r + (RING - 1) * step);
       if (++slot == RING) slot = 0;
+    } else {
+      float s[1] = {sum2(t)};
+      group_sum<BLOCK, false>(s, sh1, turn);
+      near = mean_of(s[0], (float)d, inv_d);
     }
-    const float mu = mean_of(s[0], (float)d, inv_d);
     t = F2(0.f, 0.f);
-    const F2 neg_mu(-mu, -mu);
+    const F2 neg_mu(-near, -near);
 #pragma unroll
     for (int k = 0; k < kElems / 2; ++k) {
       const F2 c = add2(v[k], neg_mu);
@@ -245,16 +267,39 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
         t = fma2(c, c, t);
       }
     }
-    s[0] = sum2(t);
-    group_sum<BLOCK>(s, sh);
-    const float rs = rsqrtf(fmaf(s[0], inv_d, eps));
+    float mu = near, m2;
+    if constexpr (RING > 0) {
+      const float wm2 = warp_sum(sum2(t));
+      float(*to)[2] = sh[turn++ & 1];  // (in turns, as in group_sum)
+      if (lane == 0) {
+        to[warp][0] = near;
+        to[warp][1] = wm2;
+      }
+      __syncthreads();
+      const float lmu = lane < nw ? to[lane][0] : 0.f, lm2 = lane < nw ? to[lane][1] : 0.f;
+      mu = mean_of(warp_sum(ln * lmu), (float)d, inv_d);
+      const float dist = lmu - mu;
+      m2 = warp_sum(lane < nw ? fmaf(ln * dist, dist, lm2) : 0.f);
+    } else {
+      float s[1] = {sum2(t)};
+      group_sum<BLOCK, false>(s, sh1, turn);
+      m2 = s[0];
+    }
+    const float rs = rsqrtf(fmaf(m2, inv_d, eps));
     if (tid == 0 && mean != nullptr) {
       mean[r] = mu;
       rstd[r] = rs;
     }
     const F2 rs2(rs, rs);
+    if constexpr (RING > 0) {
+      const float shift = (near - mu) * rs;
+      const F2 shift2(shift, shift);
 #pragma unroll
-    for (int k = 0; k < kElems / 2; ++k) cur.set(k, fma2(mul2(v[k], rs2), wv.pair(k), bv.pair(k)));
+      for (int k = 0; k < kElems / 2; ++k) cur.set(k, fma2(fma2(v[k], rs2, shift2), wv.pair(k), bv.pair(k)));
+    } else {
+#pragma unroll
+      for (int k = 0; k < kElems / 2; ++k) cur.set(k, fma2(mul2(v[k], rs2), wv.pair(k), bv.pair(k)));
+    }
     cur.store(y + r * ldy, d, tid, nt);
   }
 }
@@ -269,7 +314,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
   ops_begin();
   constexpr int N = kElems / V;
   extern __shared__ __align__(16) uint8_t ring_mem[];
-  __shared__ float sh[32][2];
+  __shared__ float sh[2][32][2];
   const int tid = BLOCK ? threadIdx.x : threadIdx.x & 31, nt = BLOCK ? blockDim.x : 32;
   const int64_t first = BLOCK ? blockIdx.x : blockIdx.x * (int64_t)kLnWarps + (threadIdx.x >> 5);
   const int64_t step = BLOCK ? gridDim.x : gridDim.x * (int64_t)kLnWarps;
@@ -281,7 +326,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
   Part<T, V, N, LOOSE> cx, cy, nx, ny;
   Weights<W, V, N> wv;
   float nmu = 0.f, nrs = 0.f;
-  int slot = 0;
+  int slot = 0, turn = 0;
   auto copy_in = [&](int sl, int64_t r) {
     if (r < rows) {
       ring_copy<T, V, N>(ring + 2 * sl * d, x + r * ldx, d, tid, nt);
@@ -335,7 +380,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
       ab[k] = add2(ab[k], t);
     }
     float s[2] = {sum2(s1), sum2(s2)};
-    group_sum<BLOCK>(s, sh);
+    group_sum<BLOCK, (RING > 0)>(s, sh, turn);
     if constexpr (RING > 0) {
       copy_in(slot == 0 ? RING - 1 : slot - 1, r + (RING - 1) * step);
       if (++slot == RING) slot = 0;
@@ -404,20 +449,21 @@ template <typename T, typename W>
 __global__ void __launch_bounds__(kLoopThreads)
     ln_forward_loop_kernel(const T* x, int64_t ldx, const W* __restrict__ w, const W* __restrict__ b, float eps, T* y,
                            int64_t ldy, float* __restrict__ mean, float* __restrict__ rstd, int64_t rows, int d) {
-  __shared__ float sh[32][1];
+  __shared__ float sh[2][32][1];
+  int turn = 0;
   ops_begin();
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
     const T* xr = x + r * ldx;
     float s[1] = {0.f};
     for (int i = threadIdx.x; i < d; i += blockDim.x) s[0] += gload_f32(xr + i);
-    group_sum<true>(s, sh);
+    group_sum<true, false>(s, sh, turn);
     const float mu = s[0] / (float)d;
     s[0] = 0.f;
     for (int i = threadIdx.x; i < d; i += blockDim.x) {
       const float c = gload_f32(xr + i) - mu;
       s[0] = fmaf(c, c, s[0]);
     }
-    group_sum<true>(s, sh);
+    group_sum<true, false>(s, sh, turn);
     const float rs = 1.0f / sqrtf(s[0] / (float)d + eps);
     if (threadIdx.x == 0 && mean != nullptr) {
       mean[r] = mu;
@@ -433,7 +479,8 @@ __global__ void __launch_bounds__(kLoopThreads)
     ln_backward_loop_kernel(const T* dy, int64_t lddy, const T* __restrict__ x, int64_t ldx, const W* __restrict__ w,
                             const float* __restrict__ mean, const float* __restrict__ rstd, const T* dadd,
                             int64_t ldadd, T* dx, int64_t lddx, float* __restrict__ part, int64_t rows, int d) {
-  __shared__ float sh[32][2];
+  __shared__ float sh[2][32][2];
+  int turn = 0;
   ops_begin();
   float* mine = part ? part + (size_t)blockIdx.x * 2 * d : nullptr;
   bool begun = false;
@@ -450,7 +497,7 @@ __global__ void __launch_bounds__(kLoopThreads)
         mine[d + i] = (begun ? mine[d + i] : 0.f) + t;
       }
     }
-    group_sum<true>(s, sh);
+    group_sum<true, false>(s, sh, turn);
     const float m1 = s[0] / (float)d, m2 = s[1] / (float)d;
     for (int i = threadIdx.x; i < d; i += blockDim.x) {
       const float g = gload_f32(dy + r * lddy + i) * (w ? gload_f32(w + i) : 1.f);
@@ -532,8 +579,8 @@ int ln_blocks(int64_t rows, int d, int threads) {
 }
 
 // The kernel form for the way elements move and the row length, f(tag, ring bytes)
-// doing the launch.  Block rows of vectors go through a ring of six rows, three where
-// six would not fit into the block's share of shared memory (row_bytes: of all arrays
+// doing the launch.  Block rows of vectors go through a ring of four rows, three where
+// four would not fit into the block's share of shared memory (row_bytes: of all arrays
 // that a ring row holds).  Words do not: as many copies and then as many reads as
 // elements cost more than the deeper prefetch gives (d = 7166, 16384 rows: forward
 // 190 us with the ring, 121 without).
@@ -549,7 +596,7 @@ void ln_pick(LnMove v, int d, int per_sm, size_t row_bytes, F f) {
   if (v == LN_VECTORS) {
     const size_t share = 225 * 1024 / per_sm - 1024;
     if (warp) f(LnTag<VF, false, false, 0>(), (size_t)0);
-    else if (6 * row_bytes <= share) f(LnTag<VF, false, true, 6>(), 6 * row_bytes);
+    else if (4 * row_bytes <= share) f(LnTag<VF, false, true, 4>(), 4 * row_bytes);
     else f(LnTag<VF, false, true, 3>(), 3 * row_bytes);
   } else if (v == LN_WORDS) {
     if (warp) f(LnTag<VW, false, false, 0>(), (size_t)0);

@@ -6,7 +6,6 @@
 // with max |v| = m * 2^q, m in [0.5, 1), 6 * 2^s = 0.75 * 2^(s+3) gives
 // s = q - 3 for m <= 0.75 and q - 2 otherwise.
 #include "gemm_common.cuh"
-#include "mx.cuh"
 #include "ops_common.cuh"
 
 namespace moe {
@@ -133,7 +132,8 @@ struct Block32 {
 // the block's maximum needs no exchange, its codes leave as 16 bytes, and four lanes
 // join their scale bytes into a word of the tile.  A block of threads takes one row
 // (or 256 blocks of a wider one), or `rpb` short ones: it is bound by instruction
-// issue, and places from divisions of a flat index made up a third of that.
+// issue, and finding places by dividing a flat index cost a tenth of its time
+// (32768 x 7168: 104 us, now 95, 5.9 TB/s).
 template <typename T, bool V>
 __global__ void __launch_bounds__(256) quant_rows_kernel(const T* x, int64_t ldx, int rows, int K, int G,
                                                          const int* off, const int* perm, int k, int rpb, uint8_t* q,

@@ -36,11 +36,6 @@ __device__ __forceinline__ uint4 gload(const uint4* p) {
   asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }
-__device__ __forceinline__ uint2 gload(const uint2* p) {
-  uint2 v;
-  asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
-}
 __device__ __forceinline__ uint32_t gload(const uint32_t* p) {
   uint32_t v;
   asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p));
@@ -153,7 +148,7 @@ __device__ __forceinline__ void pair_to<__half>(uint32_t* w, F2 v) {
 }
 
 // E elements of T in registers, moved V at a time (V * sizeof(T) is 16, 4 or the
-// element's size; 8 for loads too): vector i of them from or to memory at p.
+// element's size): vector i of them from or to memory at p.
 template <typename T, int E>
 struct Words {
   static constexpr int kWords = E * (int)sizeof(T) / 4;
@@ -168,10 +163,6 @@ struct Words {
       w[4 * i + 1] = u.y;
       w[4 * i + 2] = u.z;
       w[4 * i + 3] = u.w;
-    } else if constexpr (V * sizeof(T) == 8) {
-      const uint2 u = gload(reinterpret_cast<const uint2*>(p));
-      w[2 * i] = u.x;
-      w[2 * i + 1] = u.y;
     } else if constexpr (V * sizeof(T) == 4) {
       w[i] = gload(reinterpret_cast<const uint32_t*>(p));
     } else {  // one 16-bit element
