@@ -51,8 +51,10 @@ __device__ __forceinline__ void group_sum(float (&v)[M], float (*sh)[32][M], int
 // The part of a row that one thread holds: N vectors of V elements, vector i at
 // (i * threads + thread) * V; elements past d read as zeros.  LOOSE (V = 2): rows of
 // 16-bit elements that may start in the middle of a 32-bit word or end with half of
-// one; in those that do the elements are moved one by one, and the loaded halves
-// joined by join(), before the first use, so that loads stay under way.
+// one: elements are loaded one by one and joined by join(), before the first use, so that
+// loads stay under way; they are stored as words in rows that start with one.  (Loads of
+// words in those rows: a branch, 382 us against 262 in the backward of 16384 rows of
+// 7167, 176 against 188 in the forward.)
 template <typename T, int V, int N, bool LOOSE>
 struct Part : Words<T, V * N> {
   using Base = Words<T, V * N>;
@@ -61,21 +63,10 @@ struct Part : Words<T, V * N> {
   __device__ __forceinline__ void load(const T* __restrict__ row, int d, int tid, int nt) {
     if constexpr (kLoose) {
       const uint16_t* p = reinterpret_cast<const uint16_t*>(row);
-      if (reinterpret_cast<uintptr_t>(row) & 2) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int c = (i * nt + tid) * 2;
-          Base::w[i] = c < d ? gload(p + c) : 0u;
-          high[i] = c + 1 < d ? gload(p + c + 1) : 0u;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int c = (i * nt + tid) * 2;
-          if (c + 1 < d) Base::w[i] = gload(reinterpret_cast<const uint32_t*>(p + c));
-          else Base::w[i] = c < d ? gload(p + c) : 0u;
-          high[i] = 0;
-        }
+      for (int i = 0; i < N; ++i) {
+        const int c = (i * nt + tid) * 2;
+        gload_pair(p + c, c < d, c + 1 < d, Base::w[i], high[i]);
       }
     } else {
 #pragma unroll
@@ -173,8 +164,8 @@ __device__ __forceinline__ void ring_wait() {
 }
 
 // RING: rows that the ring in shared memory holds (block form), or 0: the next row is
-// loaded into registers.  A slot is filled again after the first
-// barrier of the row that follows its own.
+// loaded into registers.  A slot is filled again during the row that follows its own,
+// by the threads that read it.
 template <typename T, typename W, int V, bool LOOSE, bool BLOCK, int RING>
 __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
     ln_forward_kernel(const T* x, int64_t ldx, const W* __restrict__ w, const W* __restrict__ b, float eps, T* y,
@@ -223,9 +214,10 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
     } else {
       cur = next;
       cur.join();
-      // without a branch (past the end this row again) a loose row's loads stay under way
-      // (147 us, not 208, for 16384 rows of 7167); whole words gain nothing by it (the
-      // compiler then waits for them at once: 197 us, not 122, for 7166)
+      // without a branch (past the end this row again) single elements' loads stay under
+      // way (147 us, not 208, for 16384 rows of 7168 with odd strides); whole words gain
+      // nothing by it (the compiler then waits for them at once: 197 us, not 117, for
+      // 7166)
       if (LOOSE || sizeof(T) == 4) next.load(x + (r + step < rows ? r + step : r) * ldx, d, tid, nt);
       else if (r + step < rows) next.load(x + (r + step) * ldx, d, tid, nt);
     }
@@ -349,8 +341,8 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
   for (int64_t r = first; r < rows; r += step) {
     const float mu = nmu, rs = nrs;
     // the next row's loads without a branch (past the end: this row again): behind one
-    // their values would be waited for where it joins (166 us, not 136, for 16384
-    // rows of 7168)
+    // their values would be waited for where it joins (16384 rows of 7168: 30 us more
+    // than the 129)
     const int64_t rn = r + step < rows ? r + step : r;
     nmu = gload(mean + rn);
     nrs = gload(rstd + rn);

@@ -63,21 +63,10 @@ __device__ __forceinline__ float gload_f32(const __half* p) {
   return __half2float(__ushort_as_half((uint16_t)gload(reinterpret_cast<const uint16_t*>(p))));
 }
 
-// Two 16-bit elements at p, to be joined as lo | hi << 16 at their use, without a branch:
-// a value loaded behind one is waited for where it joins.
-// One word where `whole` (p aligned to it), else the elements one by one.
-__device__ __forceinline__ void gload_word(const void* p, bool whole, uint32_t& lo, uint32_t& hi) {
-  asm volatile(
-      "{\n\t.reg .pred w;\n\t"
-      "setp.ne.b32 w, %3, 0;\n\t"
-      "mov.b32 %1, 0;\n\t"
-      "@w ld.global.u32 %0, [%2];\n\t"
-      "@!w ld.global.u16 %0, [%2];\n\t"
-      "@!w ld.global.u16 %1, [%2+2];\n\t}"
-      : "=&r"(lo), "=&r"(hi)
-      : "l"(p), "r"((int)whole));
-}
-// Element by element, each only where a / b says that it exists (else 0).
+// Two 16-bit elements at p, each only where a / b says that it exists (else 0), to be
+// joined as lo | hi << 16 at their use.  Without a branch: a value loaded behind one is
+// waited for where it joins.  (A third load, of both as a word into lo where p allows
+// it, costs more than it saves: it waits for the other that has the same target.)
 __device__ __forceinline__ void gload_pair(const void* p, bool a, bool b, uint32_t& lo, uint32_t& hi) {
   asm volatile(
       "{\n\t.reg .pred l, h;\n\t"

@@ -370,18 +370,18 @@ struct RawWord {
   __device__ __forceinline__ uint32_t join() const { return lo | (hi << 16); }
 };
 // The word at p; EDGE: only the elements that lo / hi say there are, the others 0.
-// `whole`: p is aligned to words.  PRED: all three loads under predicates, without a
-// branch.  Where rows differ in `whole` and stores lie between the loads (the gradient)
-// that took 289 us against 384 (4096 tokens, k = 8, d = 7166, 16 bit); the unpermute,
-// which has only loads, took 171 against 147, and branches.
-template <typename T, bool EDGE, bool PRED = false>
+// `whole`: p is aligned to words.  APART: 16-bit elements always one by one, without a
+// branch on `whole`.  Where rows differ in it and stores lie between the loads (the
+// gradient) that took 288 us against 384 (4096 tokens, k = 8, d = 7167, 16 bit; 288
+// against 388 at 7166); the unpermute, which has only loads, branches (147 us, not 171,
+// at 7166).
+template <typename T, bool EDGE, bool APART = false>
 __device__ __forceinline__ RawWord load_word(const T* p, bool whole, bool lo, bool hi) {
   RawWord r{0u, 0u};
   if constexpr (sizeof(T) == 4) {
     if (!EDGE || lo) r.lo = gload(reinterpret_cast<const uint32_t*>(p));
-  } else if constexpr (PRED) {
-    if constexpr (EDGE) gload_pair(p, lo, hi, r.lo, r.hi);
-    else gload_word(p, whole, r.lo, r.hi);
+  } else if constexpr (APART) {
+    gload_pair(p, !EDGE || lo, !EDGE || hi, r.lo, r.hi);
   } else {
     const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
     if (EDGE || !whole) {
