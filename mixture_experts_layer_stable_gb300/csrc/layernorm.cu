@@ -557,8 +557,10 @@ uintptr_t bits(const void* p) { return reinterpret_cast<uintptr_t>(p); }
 
 // Threads of a block that takes a row.
 int ln_block_threads(int d) { return ((d + kElems - 1) / kElems + 31) / 32 * 32; }
-// Threads an SM holds of each kernel, for the registers they need.
-constexpr int kForwardThreads = 1024, kBackwardThreads = 640;
+// Threads an SM holds of each kernel, for the registers they need: 64 a thread in the
+// forward of vectors, up to 128 in the others.
+constexpr int kForwardThreads = 1024, kBackwardThreads = 512;
+int ln_forward_threads(LnMove v) { return v == LN_VECTORS ? kForwardThreads : kBackwardThreads; }
 int ln_blocks_per_sm(int d, int threads) {
   const int t = d <= kWarpRowMax ? 32 * kLnWarps : d <= kBlockRowMax ? ln_block_threads(d) : kLoopThreads;
   return t > threads / 2 ? 1 : threads / t;
@@ -621,7 +623,7 @@ moe_status moe_layernorm_forward(int32_t dtype, int32_t wdtype, int64_t rows, in
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const LnMove v = ln_move(es, d, bits(x) | bits(y) | (uintptr_t)(ldx * es) | (uintptr_t)(ldy * es),
                        bits(weight) | bits(bias));
-  const int grid = ln_blocks(rows, d, kForwardThreads);
+  const int threads = ln_forward_threads(v), grid = ln_blocks(rows, d, threads);
   return ops_status(ln_types(dtype, wdtype, [&](auto t, auto wt) {
     using T = decltype(t);
     using W = decltype(wt);
@@ -633,7 +635,7 @@ moe_status moe_layernorm_forward(int32_t dtype, int32_t wdtype, int64_t rows, in
       e = launch_ops("layernorm_forward", ln_forward_loop_kernel<T, W>, dim3(grid), dim3(kLoopThreads), 0, st, xp, ldx, wp,
                      bp, eps, yp, ldy, mean, rstd, rows, d);
     else
-      ln_pick<T>(v, d, ln_blocks_per_sm(d, kForwardThreads), d * sizeof(T), [&](auto tag, size_t smem) {
+      ln_pick<T>(v, d, ln_blocks_per_sm(d, threads), d * sizeof(T), [&](auto tag, size_t smem) {
         using K = decltype(tag);
         auto kern = ln_forward_kernel<T, W, K::V, K::LOOSE, K::BLOCK, K::RING>;
         static SmemAllowed allowed;
