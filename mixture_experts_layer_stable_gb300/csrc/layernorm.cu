@@ -404,10 +404,19 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
     fb[2 * k + 1] = c.y;
   }
   if constexpr (BLOCK) {
+    constexpr int P = LOOSE ? 1 : V < 4 ? V : 4;  // floats at once (else d is a multiple of V)
 #pragma unroll
-    for (int k = 0; k < kElems; ++k) {
+    for (int k = 0; k < kElems; k += P) {
       const int c = (k / V * nt + tid) * V + k % V;
-      if (c < d) {
+      if constexpr (P > 1) {
+        Vec<float, P> pw, pb;
+#pragma unroll
+        for (int q = 0; q < P; ++q) pw.e[q] = fw[k + q], pb.e[q] = fb[k + q];
+        if (c < d) {
+          *reinterpret_cast<Vec<float, P>*>(mine + c) = pw;
+          *reinterpret_cast<Vec<float, P>*>(mine + d + c) = pb;
+        }
+      } else if (c < d) {
         mine[c] = fw[k];
         mine[d + c] = fb[k];
       }
