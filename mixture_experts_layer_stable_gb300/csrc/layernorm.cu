@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
     const float mu = nmu, rs = nrs;
     // the next row's loads without a branch (past the end: this row again): behind one
     // their values would be waited for where it joins (16384 rows of 7168: 30 us more
-    // than the 129)
+    // than the 124)
     const int64_t rn = r + step < rows ? r + step : r;
     nmu = gload(mean + rn);
     nrs = gload(rstd + rn);

@@ -372,9 +372,8 @@ struct RawWord {
 // The word at p; EDGE: only the elements that lo / hi say there are, the others 0.
 // `whole`: p is aligned to words.  APART: 16-bit elements always one by one, without a
 // branch on `whole`.  Where rows differ in it and stores lie between the loads (the
-// gradient) that took 288 us against 384 (4096 tokens, k = 8, d = 7167, 16 bit; 288
-// against 388 at 7166); the unpermute, which has only loads, branches (147 us, not 171,
-// at 7166).
+// gradient) that took 291 us against 388 (4096 tokens, k = 8, d = 7166 or 7167, 16
+// bit); the unpermute, which has only loads, branches (147 us, not 171, at 7166).
 template <typename T, bool EDGE, bool APART = false>
 __device__ __forceinline__ RawWord load_word(const T* p, bool whole, bool lo, bool hi) {
   RawWord r{0u, 0u};
