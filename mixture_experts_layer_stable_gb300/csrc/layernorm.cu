@@ -567,7 +567,9 @@ uintptr_t bits(const void* p) { return reinterpret_cast<uintptr_t>(p); }
 // Threads of a block that takes a row.
 int ln_block_threads(int d) { return ((d + kElems - 1) / kElems + 31) / 32 * 32; }
 // Threads an SM holds of each kernel, for the registers they need: 64 a thread in the
-// forward of vectors, up to 128 in the others.
+// forward of vectors, up to 128 in the others.  (More blocks than that leave a second
+// wave of them: 2048 rows of 2048, backward with 640 threads an SM 24.5 us, with 512
+// 20.4.)
 constexpr int kForwardThreads = 1024, kBackwardThreads = 512;
 int ln_forward_threads(LnMove v) { return v == LN_VECTORS ? kForwardThreads : kBackwardThreads; }
 int ln_blocks_per_sm(int d, int threads) {
@@ -586,7 +588,7 @@ int ln_blocks(int64_t rows, int d, int threads) {
 // four would not fit into the block's share of shared memory (row_bytes: of all arrays
 // that a ring row holds).  Words do not: as many copies and then as many reads as
 // elements cost more than the deeper prefetch gives (d = 7166, 16384 rows: forward
-// 190 us with the ring, 121 without).
+// 190 us with the ring, 117 without).
 template <int V_, bool LOOSE_, bool BLOCK_, int RING_>
 struct LnTag {
   static constexpr int V = V_, RING = RING_;
