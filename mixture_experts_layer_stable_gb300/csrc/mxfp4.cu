@@ -7,6 +7,7 @@
 // s = q - 3 for m <= 0.75 and q - 2 otherwise.
 #include "gemm_common.cuh"
 #include "ops_common.cuh"
+#include "row_tiles.h"
 
 namespace moe {
 
@@ -317,7 +318,6 @@ __global__ void __launch_bounds__(256) dequant_weights_kernel(const uint8_t* __r
 // instead of what its bytes take.
 constexpr int kEpiWarps4 = 8;          // two for each quarter of the TMEM lanes
 constexpr int kThreads4 = 64 + 32 * kEpiWarps4;
-constexpr int kMaxTok = 192;
 constexpr int kMaxStages = 12;
 constexpr int kSfCols = 24;             // TMEM columns of a stage's scales: features 2 x 4, rows 2 x 8
 constexpr int kWBytes = 128 * 128;      // weights of a stage
@@ -511,20 +511,6 @@ struct P4 {
   int rows, G, N, K, NT, KT, stages_k;
   int n_units;  // units along the features: NT, of a pair half as many
 };
-
-// Tiles of an expert's c rows: as few as kMaxTok allows, starting on multiples of
-// 64 (so a tile's scales lie in at most two 128-row tiles, from column 0 or 2 of
-// the first).
-MOE_DEV int tok_tiles(int c) { return (c + kMaxTok - 1) / kMaxTok; }
-MOE_DEV int tok_start(int c, int tiles, int t) { return t * ((c + 63) / 64) / tiles * 64; }
-// Rows of the largest of them (kMaxTok where there are many).
-MOE_DEV int tok_most(int c) {
-  const int tt = tok_tiles(c);
-  if (tt > 4) return kMaxTok;
-  int most = 0;
-  for (int t = 0; t < tt; ++t) most = max(most, (t + 1 < tt ? tok_start(c, tt, t + 1) : c) - tok_start(c, tt, t));
-  return most;
-}
 
 struct Unit4 {
   int e, n, row0, first, nt;  // expert, feature tile, first row of the expert, first row in it, rows
