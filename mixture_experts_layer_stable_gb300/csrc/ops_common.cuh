@@ -12,6 +12,7 @@
 
 #include "../../include/moe_ops.h"
 #include "moe_internal.h"
+#include "smem_limit.h"
 
 namespace moe {
 
@@ -244,24 +245,6 @@ cudaError_t launch_ops(const char* name, void (*kern)(P...), dim3 grid, dim3 blo
   cfg.numAttrs = 1;
   TraceScope ts(name, st);
   return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
-}
-
-// Lets `kern` use `bytes` of dynamic shared memory.  done: a flag for each device,
-// kept by the caller for each kernel, so that only its first call asks.
-struct SmemAllowed {
-  int bytes[64] = {0};
-};
-template <typename K>
-cudaError_t allow_smem(K kern, size_t bytes, SmemAllowed& done) {
-  if (bytes <= 40 * 1024) return cudaSuccess;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const bool known = dev >= 0 && dev < 64;
-  if (known && done.bytes[dev] >= (int)bytes) return cudaSuccess;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e == cudaSuccess && known) done.bytes[dev] = (int)bytes;
-  return e;
 }
 
 inline size_t dtype_bytes(int dt) { return dt == MOE_DT_F32 ? 4 : 2; }

@@ -2,6 +2,7 @@
 run on the CPU."""
 import ctypes
 import os
+import shutil
 import subprocess
 
 import numpy as np
@@ -54,3 +55,98 @@ def test_tiles_cover_an_expert_s_rows(tiles, counts):
         assert rows.max() == most if n <= 4 else rows.max() <= most, c
         # 128-row scale tiles that a tile touches: one where the largest tile has up to 128 rows, else two
         assert (s % 128 + rows).max() <= (128 if most <= 128 else 256), c
+
+
+# The CUDA runtime's calls as fakes.  Two threads ask for 60 and 120 KB and both come to the call that
+# sets the limit; the larger one's takes effect first and returns last (all waits end after half a second).
+LIMIT = """
+#include <chrono>
+#include <condition_variable>
+#include <initializer_list>
+#include <mutex>
+#include <stdio.h>
+#include <thread>
+#include "smem_limit.h"
+static std::mutex m;
+static std::condition_variable cv;
+static int device = 0, limit = 0, sets = 0, in_set = 0;
+static bool large_set = false, small_done = false;
+static thread_local int who = 0;  // 1: the smaller, 2: the larger
+template <typename P> static void until(std::unique_lock<std::mutex>& l, P p) {
+  cv.wait_for(l, std::chrono::milliseconds(500), p);
+}
+extern "C" cudaError_t cudaGetDevice(int* d) { *d = device; return cudaSuccess; }
+extern "C" cudaError_t cudaDeviceGetAttribute(int* v, cudaDeviceAttr a, int) {
+  if (a != cudaDevAttrMaxSharedMemoryPerBlockOptin) return cudaErrorInvalidValue;
+  *v = 232448;
+  return cudaSuccess;
+}
+extern "C" cudaError_t cudaFuncGetAttributes(cudaFuncAttributes* a, const void*) {
+  *a = cudaFuncAttributes();
+  a->sharedSizeBytes = 1000;
+  return cudaSuccess;
+}
+extern "C" cudaError_t cudaFuncSetAttribute(const void*, cudaFuncAttribute, int v) {
+  std::unique_lock<std::mutex> l(m);
+  if (v > 232448 - 1000) return cudaErrorInvalidValue;
+  ++sets;
+  if (who != 0) {
+    ++in_set;
+    cv.notify_all();
+    until(l, [] { return in_set == 2; });
+    if (who == 1) until(l, [] { return large_set; });
+  }
+  limit = v;
+  if (who == 2) {
+    large_set = true;
+    cv.notify_all();
+    until(l, [] { return small_done; });
+  }
+  return cudaSuccess;
+}
+static int fail(const char* what) { return printf("%s, limit %d\\n", what, limit), 1; }
+static void kernel(int) {}
+static moe::SmemAllowed allowed, other;
+int main() {
+  const size_t small = 60000, large = 120000;
+  cudaError_t es = cudaSuccess, el = cudaSuccess;
+  std::thread a([&] {
+    who = 1;
+    es = moe::allow_smem(kernel, small, allowed);
+    std::lock_guard<std::mutex> l(m);
+    small_done = true;
+    cv.notify_all();
+  });
+  std::thread b([&] { who = 2; el = moe::allow_smem(kernel, large, allowed); });
+  a.join();
+  b.join();
+  if (es != cudaSuccess || el != cudaSuccess) return fail("refused");
+  if (moe::allow_smem(kernel, large, allowed) != cudaSuccess || limit < (int)large)
+    return fail("lowered");
+  // once set, no more calls; sizes that need no limit make none
+  const int n = sets;
+  for (size_t bytes : {small, large, (size_t)200000})
+    if (moe::allow_smem(kernel, bytes, allowed) != cudaSuccess || limit < (int)bytes) return fail("later call");
+  if (sets != n) return fail("set again");
+  if (moe::allow_smem(kernel, 1000, other) != cudaSuccess || sets != n) return fail("small size");
+  // another device has a limit of its own; one past the table works too
+  for (int d : {1, 64}) {
+    device = d;
+    limit = 0;
+    if (moe::allow_smem(kernel, large, allowed) != cudaSuccess || limit < (int)large) return fail("other device");
+  }
+  return 0;
+}
+"""
+
+
+def test_two_threads_cannot_lower_a_kernel_s_shared_memory(tmp_path):
+    from mixture_experts_layer_stable_gb300 import build
+    nvcc = shutil.which(build._nvcc()) or build._nvcc()
+    include = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
+    src, exe = tmp_path / "t.cpp", tmp_path / "t"
+    src.write_text(LIMIT)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-pthread", "-I", CSRC, "-isystem", include, str(src),
+                    "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0, r.stdout
