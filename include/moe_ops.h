@@ -172,7 +172,8 @@ moe_status moe_dequantize_mxfp4_rows(int32_t dtype, int64_t rows, int32_t K, con
  *   dtype: of out (row stride ldo).  Rows from offsets[G] on are not written.
  *   0 <= rows <= 2^28, 1 <= G <= 1024, N >= 1, K a multiple of 32, K >= 32.
  *   ws: 128-byte aligned; moe_read_status(ws, stream) reports a wait that ran
- *   out. */
+ *   out in the last call that was given ws (each call, one without rows too,
+ *   clears what the one before left). */
 size_t moe_mxfp4_product_workspace_bytes(int64_t rows, int32_t N, int32_t K, int32_t G);
 moe_status moe_mxfp4_product(int32_t dtype, int64_t rows, int32_t N, int32_t K, int32_t G,
                              const int32_t* offsets, const uint8_t* xq, const uint8_t* xscales,

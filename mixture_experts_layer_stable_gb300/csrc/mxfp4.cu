@@ -896,6 +896,17 @@ bool fp4_weights(int64_t batch, int32_t K, int32_t N) {
 bool fp4_rows(int64_t rows, int32_t K, int32_t G) {
   return rows >= 0 && rows <= ((int64_t)1 << 28) && fp4_k(K) && G >= 1 && G <= kMaxE;
 }
+// The status of a call that launches no kernel.  (A ws that is not the device's memory
+// -- there may be no device -- has none to clear.)
+moe_status clear_status(void* ws, cudaStream_t st) {
+  cudaPointerAttributes a;
+  if (cudaPointerGetAttributes(&a, ws) != cudaSuccess) {
+    cudaGetLastError();
+    return MOE_OK;
+  }
+  if (a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged) return MOE_OK;
+  return ops_status(cudaMemsetAsync(ws, 0, 2 * sizeof(int), st));
+}
 bool aligned128(const void* p) { return p != nullptr && aligned_to(p, 128); }
 
 }  // namespace
@@ -998,7 +1009,7 @@ moe_status moe_mxfp4_product(int32_t dtype, int64_t rows, int32_t N, int32_t K, 
       ldo < (act == MOE_ACT_SWIGLU ? N / 2 : N) || !aligned128(ws))
     return MOE_ERR_INVALID_ARG;
   if (ws_bytes < moe_mxfp4_product_workspace_bytes(rows, N, K, G)) return MOE_ERR_WORKSPACE_TOO_SMALL;
-  if (rows == 0) return MOE_OK;
+  if (rows == 0) return clear_status(ws, reinterpret_cast<cudaStream_t>(stream));
   if (!aligned128(xq) || !aligned128(xscales) || !aligned128(wq) || !aligned128(wscales) ||
       !elem_ok(out, dtype_bytes(dtype)) || !elem_ok_or_null(offsets, 4))
     return MOE_ERR_INVALID_ARG;

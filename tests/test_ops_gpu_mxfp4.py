@@ -320,3 +320,20 @@ def test_other_stream():
     ops.moe_mxfp4_product(q2, s2, off, wq, ws, 1, b, w, stream=st)
     st.synchronize()
     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("N,act", [(64, 0), (64, 1)])
+def test_no_rows_clear_the_status(N, act):
+    """A call without rows launches no kernel, and its status is its own all the same: not what the
+    workspace held."""
+    K, G = 128, 3
+    off = torch.zeros(G + 1, dtype=torch.int32, device="cuda")
+    empty = torch.empty(0, dtype=torch.uint8, device="cuda")
+    wq, ws, _ = experts(gen(8), G, K, N, bool(act))
+    out = torch.empty(0, N // 2 if act else N, dtype=torch.bfloat16, device="cuda")
+    sc = torch.empty(ops.moe_mxfp4_row_scale_bytes(0, K, G), dtype=torch.uint8, device="cuda")
+    for stream in (None, torch.cuda.Stream()):
+        w = torch.full((ops.moe_mxfp4_product_workspace_bytes(0, N, K, G),), 255, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        ops.moe_mxfp4_product(empty, sc, off, wq, ws, act, out, w, stream=stream)
+        assert B.moe_read_status(w, stream) == 0
