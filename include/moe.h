@@ -159,7 +159,9 @@ moe_status moe_route(const moe_config* cfg, const moe_bf16* x, const moe_bf16* w
  *   dw_router[e, i] = sum_t dlogits[t, e] * x[t, i]
  * dlogits: device fp32 [T, E], rounded to bf16 for the tensor cores;
  * dx_router: device bf16 [T, d] output; dw_router: device bf16 [E, d] output.
- * Uses the workspace (not the schedule in it). */
+ * Uses the workspace (not the schedule in it: it may be a fresh one).  A status
+ * that a call since this workspace's schedule reported is kept; what memory
+ * without one held is cleared. */
 moe_status moe_router_backward(const moe_config* cfg, const moe_bf16* x, const moe_bf16* w_router,
                                const float* dlogits, moe_bf16* dx_router, moe_bf16* dw_router,
                                void* ws, size_t ws_bytes, moe_stream_t stream);

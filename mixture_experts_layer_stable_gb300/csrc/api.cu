@@ -196,7 +196,7 @@ moe_status moe_router_backward(const moe_config* cfg, const moe_bf16* x, const m
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int Epad = (c.E + 63) / 64 * 64;
   auto* dl16 = static_cast<__nv_bfloat16*>(w.at(w.L.dl16));
-  cudaError_t e = launch_to_bf16_padded(dlogits, c.T, c.E, Epad, dl16, st);
+  cudaError_t e = launch_to_bf16_padded(dlogits, c.T, c.E, Epad, dl16, w, st);
   if (e == cudaSuccess)
     e = router_bwd(c, w, dl16, Epad, reinterpret_cast<const __nv_bfloat16*>(x),
                    reinterpret_cast<const __nv_bfloat16*>(w_router),

@@ -692,8 +692,22 @@ cudaError_t launch_quant_cols(const __nv_bfloat16* src, int64_t max_rows, int K,
 }
 
 namespace {
+// The router's backward needs no schedule, so the workspace's status may be one that
+// a call on its schedule reported, or whatever the memory held.  The first is kept:
+// a code and a place that kernels report, and the totals of a schedule of R rows (or
+// none yet, where the schedule's own wait ran out).  Anything else is cleared.
+__device__ void keep_reported_status(int* hdr, int R, int Rp_max) {
+  const int code = hdr[kHdrStatus], where = hdr[kHdrWhere], rp = hdr[kHdrRpTotal], mt = hdr[kHdrMtTotal];
+  const bool reported = (code == kStatusTimeout || code == kStatusDeviceCheck) && where >= 100 && where < 2000;
+  const bool totals = rp == 0 ? mt == 0 : rp >= R && rp <= Rp_max && rp % kBM == 0 && mt == rp / kBM;
+  if (reported && totals) return;
+  hdr[kHdrStatus] = 0;
+  hdr[kHdrWhere] = 0;
+}
+
 __global__ void to_bf16_padded_kernel(const float* __restrict__ src, int T, int E, int Epad,
-                                      __nv_bfloat16* __restrict__ dst) {
+                                      __nv_bfloat16* __restrict__ dst, int* hdr, int R, int Rp_max) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) keep_reported_status(hdr, R, Rp_max);
   const size_t n = (size_t)T * Epad;
   for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (size_t)gridDim.x * blockDim.x) {
     const int t = (int)(i / Epad), e = (int)(i % Epad);
@@ -703,11 +717,11 @@ __global__ void to_bf16_padded_kernel(const float* __restrict__ src, int T, int 
 }  // namespace
 
 cudaError_t launch_to_bf16_padded(const float* src, int T, int E, int Epad, __nv_bfloat16* dst,
-                                  cudaStream_t st) {
+                                  const Ws& ws, cudaStream_t st) {
   const size_t n = (size_t)T * Epad;
   const int blocks = (int)((n + 255) / 256 < 4096 ? (n + 255) / 256 : 4096);
   TraceScope ts("router_dlogits_bf16", st);
-  to_bf16_padded_kernel<<<blocks, 256, 0, st>>>(src, T, E, Epad, dst);
+  to_bf16_padded_kernel<<<blocks, 256, 0, st>>>(src, T, E, Epad, dst, ws.hdr(), (int)ws.L.R, (int)ws.L.Rp_max);
   return cudaGetLastError();
 }
 

@@ -150,9 +150,10 @@ cudaError_t launch_schedule_from_logits(const moe_config& c, const float* logits
                                         const Ws& ws, cudaStream_t st);
 cudaError_t launch_schedule_tail(const moe_config& c, const moe_sched& s, const Ws& ws,
                                  cudaStream_t st);
-// dst [T, Epad] bf16 = src [T, E] fp32 rounded, zero in columns [E, Epad).
+// dst [T, Epad] bf16 = src [T, E] fp32 rounded, zero in columns [E, Epad).  Clears the
+// status of a workspace on which no call has reported one.
 cudaError_t launch_to_bf16_padded(const float* src, int T, int E, int Epad, __nv_bfloat16* dst,
-                                  cudaStream_t st);
+                                  const Ws& ws, cudaStream_t st);
 // The ring of windows a ring forward leaves behind: once it completed (header
 // word kHdrRingValid), slot w % slots still holds the rows of each of the
 // last `slots` windows w of `mb` padded rows (padding rows zero).

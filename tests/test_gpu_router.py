@@ -142,3 +142,50 @@ def test_route_and_router_backward_bitwise_deterministic_over_10_runs(T, d, E):
         for a, b in zip(ref, got):
             assert torch.equal(a, b)
     assert L.status() == 0
+
+
+def _words(ws):
+    return ws[:256].view(torch.int32)
+
+
+@pytest.mark.parametrize("poison", ["255", "5", "6"])
+@pytest.mark.parametrize("T,d,E", [(64, 128, 8), (129, 192, 300)])
+def test_router_backward_status_is_not_what_the_memory_held(T, d, E, poison):
+    """On a workspace without a schedule: bytes of 255, or integers that are status codes."""
+    cfg = with_config("tiny", T=T, d=d, f=64, E=E, k=2)
+    x, Wr = _router_inputs(T, d, E, seed=3)
+    dl = torch.randn(T, E, generator=torch.Generator().manual_seed(5)).cuda()
+    x, Wr, got = x.cuda(), Wr.cuda(), []
+    for how in ("0", poison):
+        L = Layer(cfg)
+        if how == "255":
+            L.ws.fill_(255)
+        else:
+            L.ws[:L.ws.numel() // 4 * 4].view(torch.int32).fill_(int(how))
+        dx = torch.empty(T, d, dtype=torch.bfloat16, device="cuda")
+        dW = torch.empty(E, d, dtype=torch.bfloat16, device="cuda")
+        B.moe_router_backward(L.c, x, Wr, dl, dx, dW, L.ws)
+        assert L.status() == 0
+        got.append((dx, dW))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+@pytest.mark.parametrize("code,where,scheduled", [(5, 203, True), (6, 150, True), (5, 950, False)])
+def test_router_backward_keeps_what_the_calls_before_it_reported(code, where, scheduled):
+    """Status words as a call on this workspace's schedule leaves them, or the schedule itself whose
+    wait ran out before its totals were written."""
+    cfg = with_config("tiny", T=300, d=128, f=64, E=8, k=2)
+    x, Wr = _router_inputs(300, 128, 8, seed=3)
+    dl = torch.randn(300, 8, generator=torch.Generator().manual_seed(5)).cuda()
+    L, _ = _route(cfg, x, Wr)
+    if not scheduled:
+        L.ws[:256].zero_()
+    _words(L.ws)[0] = code
+    _words(L.ws)[1] = where
+    dx = torch.empty(300, 128, dtype=torch.bfloat16, device="cuda")
+    dW = torch.empty(8, 128, dtype=torch.bfloat16, device="cuda")
+    B.moe_router_backward(L.c, x.cuda(), Wr.cuda(), dl, dx, dW, L.ws)
+    assert L.status() == code and int(_words(L.ws)[1]) == where
+    # the next schedule starts anew
+    B.moe_route(L.c, x.cuda(), Wr.cuda(), None, L.sched, L.ws)
+    assert L.status() == 0
