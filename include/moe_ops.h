@@ -169,6 +169,8 @@ moe_status moe_dequantize_mxfp4_rows(int32_t dtype, int64_t rows, int32_t K, con
  *   (offsets NULL: G = 1, all rows).  wq, wscales: moe_quantize_mxfp4.
  *   act MOE_ACT_NONE: out [rows, N].  MOE_ACT_SWIGLU (paired weights): out
  *   [rows, N/2], out[p, i] = silu(h[2i]) * h[2i+1] of the fp32 products h.
+ *   (silu to fp32 accuracy for fp32 results; for 16-bit ones to 2^-18, and 0
+ *   for gates below -87, where it is below 1e-36.)
  *   dtype: of out (row stride ldo).  Rows from offsets[G] on are not written.
  *   0 <= rows <= 2^28, 1 <= G <= 1024, N >= 1, K a multiple of 32, K >= 32.
  *   ws: 128-byte aligned; moe_read_status(ws, stream) reports a wait that ran

@@ -512,6 +512,24 @@ struct P4 {
   int n_units;  // units along the features: NT, of a pair half as many
 };
 
+// SiLU in the epilogue.  For results of 16 bits the layer's own: its hardware
+// exponential and reciprocal are off by less than 2^-18, a hundredth of a rounding to
+// bf16 or fp16.  For fp32 results accurate to fp32, from exp(-|g|), which cannot
+// overflow (exp(-g) would below -88, where the result has not vanished yet).  The
+// quotient n / d, d in [1, 2], is one from the hardware reciprocal with its residual's
+// added, one Newton step (64 experts' 256 rows of 2048 x 1536: 42 us, 57 with the IEEE
+// division, 39 with silu_f).
+template <typename T>
+MOE_DEV float silu_for(float g) {
+  if constexpr (sizeof(T) == 4) {
+    const float t = expf(-fabsf(g)), n = g < 0.f ? g * t : g, d = 1.0f + t;
+    const float r = __fdividef(1.0f, d), q = n * r;
+    return fabsf(q) < INFINITY ? fmaf(fmaf(-q, d, n), r, q) : q;
+  } else {
+    return silu_f(g);
+  }
+}
+
 struct Unit4 {
   int e, n, row0, first, nt;  // expert, feature tile, first row of the expert, first row in it, rows
 };
@@ -767,11 +785,13 @@ __global__ void __launch_bounds__(kThreads4, 1)
         if (SWIGLU) {
           // even lanes hold gates, odd lanes the matching up products: of each
           // pair of rows an even lane finishes the first (left in v[c]), an odd
-          // lane the second (left in v[c] too)
+          // lane the second (left in v[c] too).  The choice comes before silu: after
+          // it both sides are computed (fp32 results: 68 us, not 42)
 #pragma unroll
           for (int c = 0; c < 32; c += 2) {
             const float y = __shfl_xor_sync(0xffffffffu, odd ? v[c] : v[c + 1], 1);
-            v[c] = odd ? silu_f(y) * v[c + 1] : silu_f(v[c]) * y;
+            const float up = odd ? v[c + 1] : y;
+            v[c] = silu_for<T>(odd ? y : v[c]) * up;
           }
         }
         if (rows16 && n0 + 32 <= p.N) {

@@ -337,3 +337,59 @@ def test_no_rows_clear_the_status(N, act):
         torch.cuda.synchronize()
         ops.moe_mxfp4_product(empty, sc, off, wq, ws, act, out, w, stream=stream)
         assert B.moe_read_status(w, stream) == 0
+
+
+@pytest.mark.parametrize("n,K,N", [(40, 32, 512), (7, 96, 130), (160, 4096, 512)])
+def test_swiglu_in_fp32(n, K, N):
+    """Results of 32 bits have the precision of fp32 throughout.  One value a row meets one a
+    column, so that the products h are exact; of silu(g) u with g in [-72, 72] the exponential is off by
+    at most 2 units in the last place (2^-22) and the sum, the two products and the division by 2^-24
+    each: 2^-21 of the result."""
+    g = gen(9 + K)
+
+    def exact(count, low, high):  # +- 1 or 1.5 times a power of two: quantised without an error
+        m = 1 + 0.5 * torch.randint(0, 2, (count,), generator=g, device="cuda")
+        s = 1 - 2 * torch.randint(0, 2, (count,), generator=g, device="cuda")
+        return m * s * torch.exp2(torch.randint(low, high + 1, (count,), generator=g, device="cuda").float())
+
+    x, w = torch.zeros(n, K, device="cuda"), torch.zeros(1, K, N, device="cuda")
+    x[:, 0], w[0, 0] = exact(n, -2, 2), exact(N, -6, 3)
+    w[0, 0, N // 2:] = exact(N // 2, -3, 3)
+    off = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    q, sc, xv = rows_of(x, off)
+    assert torch.equal(xv, x.double())
+    wq = torch.empty(1, N, K // 2, dtype=torch.uint8, device="cuda")
+    ws = torch.empty(ops.moe_mxfp4_weight_scale_bytes(1, K, N), dtype=torch.uint8, device="cuda")
+    ops.moe_quantize_mxfp4(w, wq, ws, True)
+    h = x[:, :1].double() * w[0, :1].double()
+    want = h[:, :N // 2] * torch.sigmoid(h[:, :N // 2]) * h[:, N // 2:]
+    out = torch.empty(n, N // 2, device="cuda")
+    product(q, sc, off, wq, ws, 1, out)
+    close(out, want, "f32", 2.0 ** -21 * want.abs(), "out")
+
+
+def test_swiglu_in_fp32_of_large_gates():
+    """Gates far below zero met by large up products: exp(-g) would overflow, the result does not vanish."""
+    gate = torch.tensor([-64.0, -80.0, -84.0, -96.0, 96.0, 192.0], dtype=torch.float64, device="cuda")
+    up, K, n = 2.0 ** 100, 64, 4
+    N = 2 * gate.numel()
+    x, w = torch.zeros(n, K, device="cuda"), torch.zeros(1, K, N, device="cuda")
+    x[:, 0], x[:, 32] = 1.0, 1.0        # a block for the gates, one for the up products
+    # -80 and -84 as sums of two values that are exact in 4 bits
+    for i, v in enumerate(gate.tolist()):
+        a = {-80.0: -64.0, -84.0: -96.0}.get(v, v)
+        w[0, 0, i], w[0, 32, i] = a, v - a
+    w[0, 32, N // 2:] = up
+    off = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    q, sc, _ = rows_of(x, off)
+    wq = torch.empty(1, N, K // 2, dtype=torch.uint8, device="cuda")
+    ws = torch.empty(ops.moe_mxfp4_weight_scale_bytes(1, K, N), dtype=torch.uint8, device="cuda")
+    ops.moe_quantize_mxfp4(w, wq, ws, True)
+    v = torch.empty(1, K, N, device="cuda")
+    ops.moe_dequantize_mxfp4(wq, ws, v, True)
+    assert torch.equal(v, w)
+    want = (gate * torch.sigmoid(gate) * up).expand(n, -1)
+    out = torch.empty(n, N // 2, device="cuda")
+    product(q, sc, off, wq, ws, 1, out)
+    # exp(-96) = 2^-138.5 is a subnormal number in fp32, of steps of 2^-149: two of them are 2^-9.5 of it
+    close(out, want, "f32", (2.0 ** -21 + torch.where(gate < -87, 2.0 ** -9, 0.0)) * want.abs(), "out")
