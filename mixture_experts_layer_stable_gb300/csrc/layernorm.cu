@@ -360,11 +360,19 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
     }
     // elements past d: dy and so g are zero
     F2 xh[kElems / 2], g[kElems / 2], s1(0.f, 0.f), s2(0.f, 0.f);
-    const F2 rs2(rs, rs), off(-mu * rs, -mu * rs);
+    // (x - mean first: in one fma with -mean * rstd that product's rounding would count,
+    // which is large where the mean is many times the spread)
+    const F2 rs2(rs, rs), neg_mu(-mu, -mu);
+    // (loose rows: all of xh before the rest, 16384 rows of 7167 256 us, else 287; the
+    // others lose by it: 7168 139 us, not 124)
+    if constexpr (LOOSE) {
+#pragma unroll
+      for (int k = 0; k < kElems / 2; ++k) xh[k] = mul2(add2(cx.pair(k), neg_mu), rs2);
+    }
 #pragma unroll
     for (int k = 0; k < kElems / 2; ++k) {
       const F2 t = cy.pair(k);
-      xh[k] = fma2(cx.pair(k), rs2, off);
+      if constexpr (!LOOSE) xh[k] = mul2(add2(cx.pair(k), neg_mu), rs2);
       g[k] = mul2(t, wv.pair(k));
       s1 = add2(s1, g[k]);
       s2 = fma2(g[k], xh[k], s2);

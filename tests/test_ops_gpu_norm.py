@@ -214,3 +214,34 @@ def test_gradient_against_differences():
     assert abs(num - (got["dx"].double() * v.double()).sum()) <= 2e-3 * got["dx"].double().norm() * v.double().norm()
     num = (L(x, w + h * vw) - L(x, w - h * vw)) / (2 * h)
     assert abs(num - (got["dw"].double() * vw.double()).sum()) <= 2e-3 * got["dw"].double().norm() * vw.double().norm()
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("d,pad", [(96, 0), (97, 0), (500, 2), (512, 0), (2046, 0), (2047, 0), (2048, 0), (2048, 1), (7168, 0),
+                                   (12289, 0)])
+def test_backward_of_rows_far_from_zero(d, pad, dt):
+    """xh = (x - mean) rstd of the given statistics: the difference is exact here (neighbouring values of
+    the type), so xh is off by one rounding of the product, however large mean * rstd is.  The statistics
+    are chosen so that mean * rstd itself is not near an fp32 number."""
+    g = gen(d + pad)
+    n, at, step = 3, {"f32": 65536.0, "bf16": 256.0, "f16": 1024.0}[dt], {"f32": 1.0, "bf16": 2.0, "f16": 1.0}[dt]
+    x = strided(g, n, d, DT[dt], pad)
+    x.copy_(at + step * torch.randint(0, 3, (n, d), generator=g, device="cuda"))
+    mean = (at + step * (0.9 + 0.1 * torch.rand(n, generator=g, device="cuda"))).float()
+    tries = (0.9 + 0.2 * torch.rand(n, 1000, generator=g, device="cuda")) / step
+    off = ((mean[:, None] * tries).double() - mean[:, None].double() * tries.double()).abs()
+    rstd = tries.gather(1, off.argmax(1, keepdim=True))[:, 0].contiguous()
+    dy, w = strided(g, n, d, DT[dt], pad), randn(g, d, std=0.3, mean=1.0)
+    dx = empty_strided(n, d, DT[dt], pad)
+    dw, db = torch.empty(d, device="cuda"), torch.empty(d, device="cuda")
+    ws = torch.empty(ops.moe_layernorm_workspace_bytes(n, d), dtype=torch.uint8, device="cuda")
+    ops.moe_layernorm_backward(dy, x, w, mean, rstd, dx, dw, db, ws)
+    rs, t, e = rstd.double()[:, None], dy.double(), (32 + math.log2(d)) * 2.0 ** -24
+    xh, gg = (x.double() - mean.double()[:, None]) * rs, dy.double() * w.double()
+    exh = 2.0 ** -23 * xh.abs()
+    m1, m2 = gg.mean(1, keepdim=True), (gg * xh).mean(1, keepdim=True)
+    a1, a2 = gg.abs().mean(1, keepdim=True), (gg * xh).abs().mean(1, keepdim=True)
+    edx = rs * (e * (gg.abs() + a1 + 2 * xh.abs() * a2) + exh * a2 + xh.abs() * (gg.abs() * exh).mean(1, keepdim=True))
+    close(dw, (t * xh).sum(0), "f32", (t.abs() * (exh + (e + n * 2.0 ** -24) * xh.abs())).sum(0), "dw")
+    close(db, t.sum(0), "f32", (e + n * 2.0 ** -24) * t.abs().sum(0), "db")
+    close(dx, rs * (gg - m1 - xh * m2), dt, edx, "dx")
