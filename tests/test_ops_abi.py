@@ -156,3 +156,90 @@ def test_binding_refuses_tensors_that_do_not_fit(O):
     u8 = torch.zeros(4096, dtype=torch.uint8)
     with pytest.raises(MoeError):
         O.moe_mxfp4_product(u8, u8, None, torch.zeros(2, 4, 32, dtype=torch.uint8), u8, 0, torch.zeros(4, 4), u8, stream=0)
+
+
+def _calls(O, device):
+    """(function, its tensors) of a small valid call of every operator."""
+    def t(*shape, dtype=torch.float32):
+        return torch.zeros(*shape, dtype=dtype, device=device)
+
+    def i32(*shape):
+        return t(*shape, dtype=torch.int32)
+
+    def u8(n):
+        return t(n, dtype=torch.uint8)
+
+    x, v, w, ws = t(4, 32), t(4), t(32), u8(1 << 16)
+    inv, off, q, sc = i32(8), i32(3), u8(8 * 16), u8(O.moe_mxfp4_row_scale_bytes(8, 32, 2))
+    wq, wsc = t(2, 6, 16, dtype=torch.uint8), u8(O.moe_mxfp4_weight_scale_bytes(2, 32, 6))
+    return [
+        (lambda *a: O.moe_layernorm_forward(*a[:3], 1e-5, *a[3:], stream=0), [x, w, w.clone(), t(4, 32), v, v.clone()]),
+        (lambda *a: O.moe_layernorm_backward(*a[:9], dadd=a[9], stream=0),
+         [x, x.clone(), w, v, v.clone(), t(4, 32), t(32), t(32), ws, x.clone()]),
+        (lambda *a: O.moe_sort_rows(*a, stream=0), [i32(8), i32(2), off, i32(8), inv, ws]),
+        (lambda *a: O.moe_permute(a[0], 2, *a[1:], stream=0), [x, inv, off, t(8, 32)]),
+        (lambda *a: O.moe_unpermute(a[0], a[1], 2, *a[2:5], base=a[5], stream=0), [t(8, 32), t(8), inv, off, t(4, 32), x]),
+        (lambda *a: O.moe_unpermute_backward(*a[:3], 2, *a[3:], stream=0), [x, t(8, 32), t(8), inv, off, t(8, 32), t(8)]),
+        (lambda *a: O.moe_quantize_mxfp4(*a, stream=0), [t(2, 32, 6), wq, wsc]),
+        (lambda *a: O.moe_dequantize_mxfp4(*a, stream=0), [wq, wsc, t(2, 32, 6)]),
+        (lambda *a: O.moe_quantize_mxfp4_rows(*a, k=2, stream=0), [x, q, sc, off, i32(8)]),
+        (lambda *a: O.moe_dequantize_mxfp4_rows(a[0], a[1], a[2], a[3], stream=0), [q, sc, t(8, 32), off]),
+        (lambda *a: O.moe_mxfp4_product(*a[:5], 0, *a[5:], stream=0), [q, sc, off, wq, wsc, t(8, 6), ws]),
+    ]
+
+
+def test_binding_refuses_host_tensors(O):
+    """Refused as arguments, before the library sees their addresses."""
+    from mixture_experts_layer_stable_gb300.binding import MoeError
+    for f, tensors in _calls(O, "cpu"):
+        with pytest.raises(MoeError) as e:
+            f(*tensors)
+        assert e.value.code == INV
+
+
+@pytest.mark.gpu
+def test_binding_refuses_tensors_off_the_current_gpu(O, cuda_lib, monkeypatch):
+    from mixture_experts_layer_stable_gb300.binding import MoeError
+    calls = _calls(O, "cuda")
+    torch.cuda.synchronize()
+    for n, (f, tensors) in enumerate(calls):
+        f(*tensors)                               # all on the GPU: accepted
+        for i in range(len(tensors)):
+            mixed = list(tensors)
+            mixed[i] = tensors[i].cpu()
+            with pytest.raises(MoeError) as e:
+                f(*mixed)
+            assert e.value.code == INV, (n, i)
+    torch.cuda.synchronize()
+    # a workspace with gaps
+    strided = torch.zeros(1 << 12, 32, dtype=torch.uint8, device="cuda")[:, :16]
+    for n in (1, 2, 10):
+        f, tensors = calls[n]
+        at = next(i for i, t in enumerate(tensors) if t.numel() == 1 << 16)
+        with pytest.raises(MoeError) as e:
+            f(*[strided if i == at else t for i, t in enumerate(tensors)])
+        assert e.value.code == INV, n
+    # tensors on the GPU that do not fit together
+    x, u8 = torch.zeros(4, 8, device="cuda"), torch.zeros(4096, dtype=torch.uint8, device="cuda")
+
+    def i32(n):
+        return torch.zeros(n, dtype=torch.int32, device="cuda")
+
+    for f in (lambda: O.moe_layernorm_forward(x, None, None, 1e-5, torch.zeros(4, 7, device="cuda")),
+              lambda: O.moe_layernorm_forward(x.t(), None, None, 1e-5, torch.zeros(8, 4, device="cuda")),
+              lambda: O.moe_layernorm_forward(x.double(), None, None, 1e-5, x.double()),
+              lambda: O.moe_permute(x, 2, i32(7), i32(3), torch.zeros(8, 8, device="cuda")),
+              lambda: O.moe_sort_rows(torch.zeros(4, device="cuda"), i32(2), i32(3), i32(4), i32(4), u8),
+              lambda: O.moe_sort_rows(i32(4), i32(2), i32(3), i32(4), i32(3), u8),
+              lambda: O.moe_unpermute(torch.zeros(8, 8, device="cuda"), None, 2, i32(8), i32(3), x, base=x[:, :7]),
+              lambda: O.moe_mxfp4_product(u8, u8, None, torch.zeros(2, 4, 32, dtype=torch.uint8, device="cuda"), u8, 0,
+                                          torch.zeros(4, 4, device="cuda"), u8)):
+        with pytest.raises(MoeError) as e:
+            f()
+        assert e.value.code == INV
+    # another device is current
+    monkeypatch.setattr(O, "_current_device", lambda: 1)
+    for f, tensors in calls:
+        with pytest.raises(MoeError) as e:
+            f(*tensors)
+        assert e.value.code == INV
