@@ -29,8 +29,8 @@ def _bytes(n):
 
 
 class Block4Bit:
-    """norm_w, norm_b [d], w_router [E, d], W1 [E, d, 2f] and W2 [E, f, d] in bf16, for up to T tokens
-    of k experts each.  The experts' weights are quantised here, once."""
+    """norm_w, norm_b [d], w_router [E, d], W1 [E, d, 2f] and W2 [E, f, d] in bf16, for T tokens of
+    k experts each.  The experts' weights are quantised here, once."""
 
     def __init__(self, norm_w, norm_b, w_router, W1, W2, T, k):
         E, d, f2 = W1.shape
@@ -63,8 +63,9 @@ class Block4Bit:
 
 
 def cap_ids(ids, E, capacity):
-    """ids with the rows past the first `capacity` of each expert marked -1 (they are dropped)."""
-    one = torch.nn.functional.one_hot(ids.long(), E)
+    """ids with the rows past the first `capacity` of each expert marked -1 (they are dropped).
+    An id outside [0, E) is dropped already and stays."""
+    one = (ids[:, None] == torch.arange(E, device=ids.device)).int()
     rank = (one.cumsum(0) * one).sum(1) - 1
     return torch.where(rank < capacity, ids, torch.full_like(ids, -1))
 

@@ -1,12 +1,14 @@
 """Host-side arithmetic of the operators' kernels, compiled with the host compiler and
 run on the CPU."""
 import ctypes
+import importlib.util
 import os
 import shutil
 import subprocess
 
 import numpy as np
 import pytest
+import torch
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "mixture_experts_layer_stable_gb300", "csrc")
@@ -150,3 +152,26 @@ def test_two_threads_cannot_lower_a_kernel_s_shared_memory(tmp_path):
                     "-o", str(exe)], check=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
     assert r.returncode == 0, r.stdout
+
+
+@pytest.fixture(scope="module")
+def example():
+    spec = importlib.util.spec_from_file_location("prenorm_block", os.path.join(ROOT, "examples", "prenorm_block.py"))
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    return m
+
+
+@pytest.mark.parametrize("capacity", [0, 1, 2, 100])
+def test_example_caps_ids_that_have_no_expert(example, capacity):
+    """Rows that are dropped already (any id outside the experts) stay as they are and take no place."""
+    E, ids = 4, [2, -1, 2, 0, 7, 2, 3, -1, 0, 2, -2 ** 31]
+    seen, want = [0] * E, []
+    for i in ids:
+        if 0 <= i < E:
+            seen[i] += 1
+            want.append(i if seen[i] <= capacity else -1)
+        else:
+            want.append(i)
+    got = example.cap_ids(torch.tensor(ids, dtype=torch.int32), E, capacity)
+    assert got.dtype == torch.int32 and got.tolist() == want
