@@ -47,15 +47,20 @@ class Block4Bit:
         self.a, self.y = torch.empty(R, f2 // 2, **bf), torch.empty(R, d, **bf)
         self.xq, self.xs = _bytes(R * d // 2), _bytes(ops.moe_mxfp4_row_scale_bytes(R, d, E))
         self.aq, self.as_ = _bytes(R * f2 // 4), _bytes(ops.moe_mxfp4_row_scale_bytes(R, f2 // 2, E))
-        self.ws = _bytes(max(ops.moe_mxfp4_product_workspace_bytes(R, f2, d, E),
-                             ops.moe_mxfp4_product_workspace_bytes(R, d, f2 // 2, E)))
+        # a workspace for each product: its status is that of the last call that was given it
+        self.ws1 = _bytes(ops.moe_mxfp4_product_workspace_bytes(R, f2, d, E))
+        self.ws = _bytes(ops.moe_mxfp4_product_workspace_bytes(R, d, f2 // 2, E))
+
+    def status(self):
+        """The first error of the last call's bounded waits, 0 if there was none (synchronises)."""
+        return next((e for e in map(B.moe_read_status, (self.route_ws, self.ws1, self.ws)) if e), 0)
 
     def __call__(self, x):
         s, off = self.sched, self.sched["offsets"]
         ops.moe_layernorm_forward(x, self.norm_w, self.norm_b, EPS, self.xn)
         B.moe_route(self.cfg, self.xn, self.w_router, self.logits, s, self.route_ws)
         ops.moe_quantize_mxfp4_rows(self.xn, self.xq, self.xs, off, perm=s["perm"], k=self.k)
-        ops.moe_mxfp4_product(self.xq, self.xs, off, self.w1, self.s1, ops.MOE_ACT_SWIGLU, self.a, self.ws)
+        ops.moe_mxfp4_product(self.xq, self.xs, off, self.w1, self.s1, ops.MOE_ACT_SWIGLU, self.a, self.ws1)
         ops.moe_quantize_mxfp4_rows(self.a, self.aq, self.as_, off)
         ops.moe_mxfp4_product(self.aq, self.as_, off, self.w2, self.s2, ops.MOE_ACT_NONE, self.y, self.ws)
         ops.moe_unpermute(self.y, s["topk_w"], self.k, s["inv"], off, self.out, base=x)
@@ -112,6 +117,7 @@ def main():
                       randn(E, f, d, std=f ** -0.5), T, k)
     x = randn(T, d)
     out = block(x)
+    assert block.status() == 0, B.moe_status_string(block.status())
     print("4-bit block: out - x has rms %.3f" % (out.float() - x.float()).square().mean().sqrt().item())
 
     scale = randn(E, d)

@@ -120,3 +120,24 @@ def test_graph_capture(block):
     torch.cuda.synchronize()
     got = m.out.clone()
     assert torch.equal(m(x), got)
+
+
+def test_every_product_s_status_is_seen(block):
+    """An error that either product reported is not cleared by the other's call."""
+    g = gen(4)
+    bf = torch.bfloat16
+    T, d, f, E, k = 16, 256, 128, 4, 2
+    m = block.Block4Bit(randn(g, d, dtype=bf), randn(g, d, dtype=bf), randn(g, E, d, dtype=bf, std=d ** -0.5),
+                        randn(g, E, d, 2 * f, dtype=bf, std=d ** -0.5), randn(g, E, f, d, dtype=bf, std=f ** -0.5), T, k)
+    x = randn(g, T, d, dtype=bf)
+    m(x)
+    assert m.status() == 0
+    for ws in (m.ws1, m.ws, m.route_ws):
+        ws[:4].view(torch.int32).fill_(B.MOE_ERR_TIMEOUT)     # as a wait that ran out leaves it
+        assert m.status() == B.MOE_ERR_TIMEOUT
+        m(x)
+        assert m.status() == 0
+    # the second product alone does not touch the first one's
+    m.ws1[:4].view(torch.int32).fill_(B.MOE_ERR_TIMEOUT)
+    ops.moe_mxfp4_product(m.aq, m.as_, m.sched["offsets"], m.w2, m.s2, ops.MOE_ACT_NONE, m.y, m.ws)
+    assert m.status() == B.MOE_ERR_TIMEOUT
