@@ -370,17 +370,12 @@ struct RawWord {
   __device__ __forceinline__ uint32_t join() const { return lo | (hi << 16); }
 };
 // The word at p; EDGE: only the elements that lo / hi say there are, the others 0.
-// `whole`: p is aligned to words.  APART: 16-bit elements always one by one, without a
-// branch on `whole`.  Where rows differ in it and stores lie between the loads (the
-// gradient) that took 291 us against 388 (4096 tokens, k = 8, d = 7166 or 7167, 16
-// bit); the unpermute, which has only loads, branches (147 us, not 171, at 7166).
-template <typename T, bool EDGE, bool APART = false>
+// `whole`: p is aligned to words.
+template <typename T, bool EDGE>
 __device__ __forceinline__ RawWord load_word(const T* p, bool whole, bool lo, bool hi) {
   RawWord r{0u, 0u};
   if constexpr (sizeof(T) == 4) {
     if (!EDGE || lo) r.lo = gload(reinterpret_cast<const uint32_t*>(p));
-  } else if constexpr (APART) {
-    gload_pair(p, !EDGE || lo, !EDGE || hi, r.lo, r.hi);
   } else {
     const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
     if (EDGE || !whole) {
@@ -389,6 +384,20 @@ __device__ __forceinline__ RawWord load_word(const T* p, bool whole, bool lo, bo
     } else {
       r.lo = gload(reinterpret_cast<const uint32_t*>(p));
     }
+  }
+  return r;
+}
+// The same with 16-bit elements always one by one, without a branch on how p lies.
+// Where rows differ in it and stores lie between the loads (the gradient) that took
+// 291 us against 388 (4096 tokens, k = 8, d = 7166 or 7167, 16 bit); the unpermute,
+// which has only loads, branches (147 us, not 171, at 7166).
+template <typename T, bool EDGE>
+__device__ __forceinline__ RawWord load_apart(const T* p, bool lo, bool hi) {
+  RawWord r{0u, 0u};
+  if constexpr (sizeof(T) == 4) {
+    if (!EDGE || lo) r.lo = gload(reinterpret_cast<const uint32_t*>(p));
+  } else {
+    gload_pair(p, !EDGE || lo, !EDGE || hi, r.lo, r.hi);
   }
   return r;
 }
@@ -569,7 +578,6 @@ __global__ void __launch_bounds__(kBwdThreads, 2) unpermute_backward_words_kerne
       T* row = dy + (int64_t)p * d;
       const int a = half_word(row), e0 = c0 * E - a;
       const T* src = (live ? y + (int64_t)p * d : spare) + e0;
-      const bool aligned = !half_word(src);
       F2 s(0.f, 0.f);
       at_edges(c0, nt, n, sizeof(T), [&](auto edge) {
         constexpr bool EDGE = decltype(edge)::value;
@@ -580,7 +588,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) unpermute_backward_words_kerne
         for (int u = 0; u < kWordsEach; ++u) v[u] = RawWord{0u, 0u};
         if (dw != nullptr) {
 #pragma unroll
-          for (int u = 0; u < kWordsEach; ++u) v[u] = load_word<T, EDGE, true>(src + u * stride, aligned, lo(u), hi(u));
+          for (int u = 0; u < kWordsEach; ++u) v[u] = load_apart<T, EDGE>(src + u * stride, lo(u), hi(u));
         }
 #pragma unroll
         for (int u = 0; u < kWordsEach; ++u) {
