@@ -854,18 +854,19 @@ int grid_for(int64_t n) {
   const int64_t b = (n + 255) / 256;
   return (int)(b < 1 ? 1 : b < (1 << 20) ? b : (1 << 20));
 }
-// Clusters of two CTAs of kern that the GPU holds at once (cached by device).
+// Clusters of two CTAs of kern that the GPU holds at once.  resident: the answer for
+// each device (0: not asked yet), kept by the caller for its kernel; threads that ask
+// at the same time store the same value.
 template <typename K>
-int pair_clusters(K kern, const cudaLaunchConfig_t& cfg) {
-  static int resident[64] = {0};
+int pair_clusters(K kern, const cudaLaunchConfig_t& cfg, std::atomic<int> (&resident)[64]) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
-  if (resident[dev] == 0) {
-    int n = 0;
+  int n = resident[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
     if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) n = num_sms() / 2;
-    resident[dev] = n;
+    resident[dev].store(n, std::memory_order_relaxed);
   }
-  return resident[dev];
+  return n;
 }
 
 template <typename T, bool SWIGLU, bool PAIR>
@@ -894,7 +895,8 @@ cudaError_t launch_product(const CUtensorMap* tm, const P4& p, cudaStream_t st) 
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const int most = pair_clusters(kern, cfg);
+    static std::atomic<int> resident[64];
+    const int most = pair_clusters(kern, cfg, resident);
     cfg.numAttrs = 2;
     cfg.gridDim = dim3(2 * (unsigned)(units < most ? units : most));
     TraceScope ts("mxfp4_product", st);
