@@ -152,13 +152,14 @@ moe_status moe_dequantize_mxfp4(int32_t dtype, const uint8_t* q, const uint8_t* 
  *   G, offsets: the experts' segments; offsets NULL: one segment (G = 1).
  *   perm: NULL, or [rows] int32: row p is x row perm[p] / k (rows gathered
  *   into expert order on the way; moe_sort_rows' perm).  k >= 1.
- *   Rows from offsets[G] on are not written. */
+ *   Rows from offsets[G] on are not written, nor are those before offsets[0]
+ *   (the offsets of some of the experts, with all rows). */
 moe_status moe_quantize_mxfp4_rows(int32_t dtype, int64_t rows, int32_t K, const void* x,
                                    int64_t ldx, int32_t G, const int32_t* offsets,
                                    const int32_t* perm, int32_t k, uint8_t* q, uint8_t* scales,
                                    moe_stream_t stream);
-/* The values of quantised rows, y [rows, K] with row stride ldy; rows from
- * offsets[G] on are not written. */
+/* The values of quantised rows, y [rows, K] with row stride ldy; rows outside
+ * [offsets[0], offsets[G]) are not written. */
 moe_status moe_dequantize_mxfp4_rows(int32_t dtype, int64_t rows, int32_t K, const uint8_t* q,
                                      const uint8_t* scales, int32_t G, const int32_t* offsets,
                                      void* y, int64_t ldy, moe_stream_t stream);
@@ -171,7 +172,8 @@ moe_status moe_dequantize_mxfp4_rows(int32_t dtype, int64_t rows, int32_t K, con
  *   [rows, N/2], out[p, i] = silu(h[2i]) * h[2i+1] of the fp32 products h.
  *   (silu to fp32 accuracy for fp32 results; for 16-bit ones to 2^-18, and 0
  *   for gates below -87, where it is below 1e-36.)
- *   dtype: of out (row stride ldo).  Rows from offsets[G] on are not written.
+ *   dtype: of out (row stride ldo).  Rows outside [offsets[0], offsets[G]) are
+ *   not written.
  *   0 <= rows <= 2^28, 1 <= G <= 1024, N >= 1, K a multiple of 32, K >= 32.
  *   ws: 128-byte aligned; moe_read_status(ws, stream) reports a wait that ran
  *   out in the last call that was given ws (each call, one without rows too,

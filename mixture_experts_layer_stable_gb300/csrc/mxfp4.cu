@@ -149,7 +149,8 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const T* x, int64_t ldx
   if (in) v.load(x + (int64_t)(perm ? gload(perm + p) / k : p) * ldx + kb * 32);
   const int g = rpb > 1 ? lane_find_group(off, G, p) : warp_find_group(off, G, p, lane);
   const int o = off ? gload(off + g) : 0;
-  const bool live = mine && (off == nullptr || p < gload(off + G));
+  // (rows before the first segment are none's: their places would lie before the scales)
+  const bool live = mine && (off == nullptr || (p >= o && o >= 0 && p < gload(off + G)));
   uint32_t byte = 127;
   if (in && live) {
     const uint32_t m = v.max_bits();
@@ -210,6 +211,7 @@ __global__ void __launch_bounds__(256) dequant_rows_kernel(const uint8_t* __rest
   }
   const int g = warp_find_group(off, G, (int)p, lane);
   const int64_t o = off ? gload(off + g) : 0;
+  if (p < o || o < 0) return;  // a row before the first segment
   uint32_t sb[kSegPasses];
 #pragma unroll
   for (int i = 0; i < kSegPasses; ++i) {

@@ -393,3 +393,46 @@ def test_swiglu_in_fp32_of_large_gates():
     product(q, sc, off, wq, ws, 1, out)
     # exp(-96) = 2^-138.5 is a subnormal number in fp32, of steps of 2^-149: two of them are 2^-9.5 of it
     close(out, want, "f32", (2.0 ** -21 + torch.where(gate < -87, 2.0 ** -9, 0.0)) * want.abs(), "out")
+
+
+@pytest.mark.parametrize("K,n,bounds", [(128, 50, [10, 10, 31]), (96, 700, [1, 130, 258, 699]), (8224, 20, [5, 20])])
+def test_rows_before_the_first_expert_are_left_alone(K, n, bounds):
+    """The offsets of some of the experts: rows before theirs have no place among the scales."""
+    g = gen(K)
+    N, G = 72, len(bounds) - 1
+    a, b = bounds[0], bounds[-1]
+    off = torch.tensor(bounds, dtype=torch.int32, device="cuda")
+    x = randn(g, n, K, dtype=torch.bfloat16)
+    guard, size = 1 << 16, ops.moe_mxfp4_row_scale_bytes(n, K, G)
+    buf = torch.full((size + 2 * guard,), 77, dtype=torch.uint8, device="cuda")
+    sc = buf[guard:guard + size]
+    q = torch.full((n, K // 2), 255, dtype=torch.uint8, device="cuda")
+    ops.moe_quantize_mxfp4_rows(x, q, sc, off)
+    assert (q[:a] == 255).all() and (q[b:] == 255).all()
+    assert (buf[:guard] == 77).all() and (buf[guard + size:] == 77).all()
+    # the rows between as with offsets that begin at 0 for them alone
+    q0, s0, v0 = rows_of(x[a:b].contiguous(), off - a)
+    assert torch.equal(q[a:b], q0)
+    v = torch.full((n, K), 9.0, device="cuda")
+    ops.moe_dequantize_mxfp4_rows(q, sc, v, off)
+    assert torch.equal(v[a:b].double(), v0) and (v[:a] == 9.0).all() and (v[b:] == 9.0).all()
+    wq, ws, wv = experts(g, G, K, N)
+    out = torch.full((n, N), 5.0, dtype=torch.bfloat16, device="cuda")
+    product(q, sc, off, wq, ws, 0, out)
+    ref = torch.empty(b - a, N, dtype=torch.bfloat16, device="cuda")
+    product(q0, s0, off - a, wq, ws, 0, ref)
+    assert torch.equal(out[a:b], ref) and (out[:a] == 5.0).all() and (out[b:] == 5.0).all()
+
+
+def test_no_rows_in_a_graph():
+    """A call without rows is captured like any other."""
+    K, N = 64, 8
+    wq, ws, _ = experts(gen(10), 1, K, N)
+    empty, sc = torch.empty(0, dtype=torch.uint8, device="cuda"), torch.empty(512, dtype=torch.uint8, device="cuda")
+    out, w = torch.empty(0, N, device="cuda"), torch.full((128,), 255, dtype=torch.uint8, device="cuda")
+    off = torch.zeros(2, dtype=torch.int32, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ops.moe_mxfp4_product(empty, sc, off, wq, ws, 0, out, w)
+    graph.replay()
+    assert B.moe_read_status(w) == 0
