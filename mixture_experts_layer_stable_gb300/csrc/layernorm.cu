@@ -53,7 +53,7 @@ __device__ __forceinline__ void group_sum(float (&v)[M], float (*sh)[32][M], int
 // 16-bit elements that may start in the middle of a 32-bit word or end with half of
 // one: elements are loaded one by one and joined by join(), before the first use, so that
 // loads stay under way; they are stored as words in rows that start with one.  (Loads of
-// words in those rows: a branch, 382 us against 262 in the backward of 16384 rows of
+// words in those rows: a branch, 382 us against 256 in the backward of 16384 rows of
 // 7167, 176 against 188 in the forward.)
 template <typename T, int V, int N, bool LOOSE>
 struct Part : Words<T, V * N> {
@@ -388,6 +388,8 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
     // dx = rs g - rs m1 - xh rs m2
     const float m1 = -rs * (s[0] * inv_d), m2 = -rs * (s[1] * inv_d);
     const F2 m1s(m1, m1), m2s(m2, m2);
+    // (loaded behind the sums: 16384 rows of 7168 take 203 us with it, 138 for the bytes,
+    // and 127 without)
     if (dadd != nullptr) {
       cy.load(dadd + r * ldadd, d, tid, nt);
       cy.join();
@@ -453,7 +455,9 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 32 * kLnWarps)
 }
 
 // Rows too wide for a block's registers: three passes over the row (it stays in
-// L1 / L2), one element at a time.
+// L1 / L2), one element at a time.  Far from HBM's rate: 4096 rows of 12288 in bf16
+// take 225 us forward (30 for the bytes) and 580 backward (45), where each row also
+// reads and writes the block's sums of dw and db.
 template <typename T, typename W>
 __global__ void __launch_bounds__(kLoopThreads)
     ln_forward_loop_kernel(const T* x, int64_t ldx, const W* __restrict__ w, const W* __restrict__ b, float eps, T* y,
@@ -574,10 +578,15 @@ uintptr_t bits(const void* p) { return reinterpret_cast<uintptr_t>(p); }
 
 // Threads of a block that takes a row.
 int ln_block_threads(int d) { return ((d + kElems - 1) / kElems + 31) / 32 * 32; }
-// Threads an SM holds of each kernel, for the registers they need: 64 a thread in the
-// forward of vectors, up to 128 in the others.  (More blocks than that leave a second
-// wave of them: 2048 rows of 2048, backward with 640 threads an SM 24.5 us, with 512
-// 20.4.)
+// Threads launched for each SM.  They are what it holds of the block forms: 64 registers
+// a thread in the forward of vectors, up to 128 in the others.  (More blocks than that
+// leave a second wave of them: 2048 rows of 2048, backward with 640 threads an SM
+// 24.5 us, with 512 20.4.)  The warp forms (d <= 512) take more registers, and some leave
+// such a wave: of four blocks two or three fit in the forward of vectors (80 registers,
+// 88 in fp32; all four with fp16 weights, 64), of two one in the backward of fp32 rows
+// (150 to 165) and of loose ones (159 to 167).  The backward of loose block rows is cut
+// to 128 registers and spills: 48 bytes with fp32 weights, 236 with bf16 ones (16384
+// rows of 7167: 256 us and 550).
 constexpr int kForwardThreads = 1024, kBackwardThreads = 512;
 int ln_forward_threads(LnMove v) { return v == LN_VECTORS ? kForwardThreads : kBackwardThreads; }
 int ln_blocks_per_sm(int d, int threads) {
