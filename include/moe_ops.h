@@ -1,12 +1,14 @@
 /*
  * moe_ops.h -- C ABI of the operators around the expert layer of moe.h: layer
- * norm, rows sorted by expert and back, and the experts' product in
- * microscaled 4-bit floating point (MXFP4), for GB300 (sm_103a).
+ * norm, rows sorted by expert and back, the experts' products with their
+ * gradients, SwiGLU and activation checkpoints in 8 bits (MXINT8), and the
+ * experts' product in microscaled 4-bit floating point (MXFP4), for GB300
+ * (sm_103a).
  *
  * They are what a program needs that runs the layer's steps itself: the norm
  * in front of the layer, rows moved to an expert function of the program's own
- * and back with their gradients, and experts whose frozen weights are held in
- * 4 bits.
+ * and back with their gradients, that function's products and activation in
+ * training, and experts whose frozen weights are held in 4 bits.
  *
  * Conventions (those of moe.h, with two differences):
  *  - The caller owns every buffer; no call allocates or synchronises.  Every
@@ -114,6 +116,80 @@ moe_status moe_unpermute_backward(int32_t dtype, int64_t T, int32_t d, int32_t k
                                   const void* dout, int64_t lddout, const void* y, const float* w,
                                   const int32_t* inv, const int32_t* offsets, void* dy, float* dw,
                                   moe_stream_t stream);
+
+/* ------------------------------------------------- products by expert
+ * Every expert's rows times its weights, on rows as moe_permute lays them:
+ * expert g's are [offsets[g], offsets[g+1]), any number of them, none included.
+ *   out[p] = x[p] * w[g]     w [G, K, N]  (the layer's W1 and W2 layouts)
+ *   out[p] = x[p] * w[g]^T   w [G, N, K]  (transposed != 0)
+ * With w [G, K, N] the gradient of the rows of the first form is the second
+ * form on dy [rows, N] with K and N changed places; that of the weights is
+ * moe_grouped_product_dw.
+ *   dtype: of x and w; odtype: of out, dtype or MOE_DT_F32.  Products and sums
+ *   in fp32, each result rounded once.
+ *   x [rows, K], out [rows, N] with row strides ldx, ldo; w contiguous.
+ *   offsets [G+1], not decreasing; NULL: G = 1, all rows.  Rows outside
+ *   [offsets[0], offsets[G]) are neither used nor written.
+ *   0 <= rows <= 2^28, 1 <= G <= 1024, 1 <= K, N <= 2^22, no array of more than
+ *   2^40 elements.
+ *   16-bit operands run on the tensor cores: 16-byte aligned x, w and row
+ *   strides are the fast path.
+ *   ws: 128-byte aligned, of moe_grouped_product_workspace_bytes(rows, K, N, G)
+ *   bytes, which serve both calls and either form; calls that may overlap need
+ *   one each.  moe_read_status(ws, stream) reports a wait that ran out in the
+ *   last call that was given ws. */
+size_t moe_grouped_product_workspace_bytes(int64_t rows, int32_t K, int32_t N, int32_t G);
+moe_status moe_grouped_product(int32_t dtype, int32_t odtype, int64_t rows, int32_t K, int32_t N, int32_t G,
+                               const int32_t* offsets, const void* x, int64_t ldx, const void* w,
+                               int32_t transposed, void* out, int64_t ldo, void* ws, size_t ws_bytes,
+                               moe_stream_t stream);
+/* Gradient of the weights: dw[g] = sum over g's rows p of x[p]^T * dy[p], [G, K, N]
+ * contiguous; an expert without rows gets zeros.
+ *   wdtype: of dw, dtype or MOE_DT_F32.  accumulate != 0: added to dw (in fp32,
+ *   rounded once), which an expert without rows then keeps. */
+moe_status moe_grouped_product_dw(int32_t dtype, int32_t wdtype, int64_t rows, int32_t K, int32_t N, int32_t G,
+                                  const int32_t* offsets, const void* x, int64_t ldx, const void* dy,
+                                  int64_t lddy, void* dw, int32_t accumulate, void* ws, size_t ws_bytes,
+                                  moe_stream_t stream);
+
+/* ---------------------------------------------------------------- MXINT8
+ * Rows kept in 8 bits between a forward and its backward.  32 consecutive
+ * elements of a row (its last block may be shorter) share a UE8M0 scale 2^s and
+ * are whole numbers c in [-127, 127]; their values are c * 2^s.
+ * s is the smallest exponent with max |v| <= 127 * 2^s, at least -127; elements
+ * are rounded to the nearest, ties to even, so a value is off by at most
+ * 2^(s-1) <= max |v| / 127.  (A block that ends in the last 2^122 of fp32's
+ * range is cut to 63 * 2^122: finite values stay finite.)  A block with a NaN
+ * or an infinity gets the scale byte 255 (NaN) and comes back as NaN.
+ *   codes [rows, n] contiguous, scale bytes (s + 127) [rows, ceil(n / 32)]
+ *   contiguous.  Codes in 8-byte aligned rows take the fast path. */
+size_t moe_mxint8_scale_bytes(int64_t rows, int32_t n);
+moe_status moe_quantize_mxint8_rows(int32_t dtype, int64_t rows, int32_t n, const void* x, int64_t ldx,
+                                    int8_t* q, uint8_t* scales, moe_stream_t stream);
+/* The values, y [rows, n] with row stride ldy (in fp16 at most 65504). */
+moe_status moe_dequantize_mxint8_rows(int32_t dtype, int64_t rows, int32_t n, const int8_t* q,
+                                      const uint8_t* scales, void* y, int64_t ldy, moe_stream_t stream);
+
+/* ---------------------------------------------------------------- SwiGLU
+ * a = silu(g) * u of rows h = [g | u] of 2f elements, silu(g) = g / (1 + exp(-g)),
+ * in fp32, rounded once.  (16-bit types: silu to 2^-18, and 0 for gates below
+ * -87, where it is below 1e-36.)
+ *   q, scales: NULL, or a checkpoint of h for the backward: MXINT8 of the two
+ *   halves of each row, codes [rows, 2f] and scales [rows, 2 * ceil(f / 32)]
+ *   (moe_quantize_mxint8_rows of 2 * rows rows of f).
+ *   h [rows, 2f], a [rows, f] with row strides ldh, lda.
+ *   0 <= rows <= 2^30, 1 <= f <= 2^22 (n of the calls above too). */
+moe_status moe_swiglu_forward(int32_t dtype, int64_t rows, int32_t f, const void* h, int64_t ldh, void* a,
+                              int64_t lda, int8_t* q, uint8_t* scales, moe_stream_t stream);
+/* Backward for the gradient da [rows, f] of a: with s = 1 / (1 + exp(-g)),
+ *   dh = [da * u * s * (1 + g * (1 - s)) | da * g * s]
+ *   a  = g * s * u again (NULL: not wanted), the rows of the next weights'
+ *        gradient, which then need not be kept.
+ *   g, u: of h, or where h is NULL of the checkpoint q, scales.
+ *   dh may be h and a may be da (the same pointer and stride). */
+moe_status moe_swiglu_backward(int32_t dtype, int64_t rows, int32_t f, const void* da, int64_t ldda,
+                               const void* h, int64_t ldh, const int8_t* q, const uint8_t* scales, void* dh,
+                               int64_t lddh, void* a, int64_t lda, moe_stream_t stream);
 
 /* ---------------------------------------------------------------- MXFP4
  * OCP MX blocks: 32 consecutive elements along K share a UE8M0 scale 2^s and

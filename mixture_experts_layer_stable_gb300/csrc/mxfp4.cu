@@ -21,13 +21,6 @@ __device__ __forceinline__ int fp4_scale_exp(float amax) {
   const int s = (eb - 126) - ((b & 0x7FFFFFu) <= 0x400000u ? 3 : 2);
   return max(-127, s);       // at most 126: the largest finite value is below 6 * 2^126
 }
-// 2^-s for s in [-127, 126], exact.
-__device__ __forceinline__ float fp4_inv_scale(int s) { return __uint_as_float((uint32_t)(127 - s) << 23); }
-// 2^s of a scale byte; 255 is NaN.
-__device__ __forceinline__ float fp4_scale_of(uint32_t byte) {
-  return byte == 255 ? __uint_as_float(0x7FFFFFFFu) : byte == 0 ? __uint_as_float(0x400000u)
-                                                               : __uint_as_float(byte << 23);
-}
 // Eight values as 4-bit codes (lowest index in the lowest bits), to nearest, ties to even.
 __device__ __forceinline__ uint32_t fp4_pack8(const float* v) {
   uint32_t r;
@@ -69,7 +62,7 @@ __device__ __forceinline__ uint32_t fp4_quant_block(float* v, uint8_t* q) {
   uint32_t byte = 255;
   if (m < 0x7F800000u) {
     const int s = fp4_scale_exp(__uint_as_float(m));
-    const float f = fp4_inv_scale(s);
+    const float f = ue8m0_inverse(s);
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] *= f;
     code = make_uint4(fp4_pack8(v), fp4_pack8(v + 8), fp4_pack8(v + 16), fp4_pack8(v + 24));
@@ -155,7 +148,7 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const T* x, int64_t ldx
   if (in && live) {
     const uint32_t m = v.max_bits();
     const int s = m < 0x7F800000u ? fp4_scale_exp(__uint_as_float(m)) : 0;
-    const float f = fp4_inv_scale(s);
+    const float f = ue8m0_inverse(s);
     byte = m < 0x7F800000u ? (uint32_t)(s + 127) : 255u;
     uint32_t c[4];
 #pragma unroll
@@ -222,7 +215,7 @@ __global__ void __launch_bounds__(256) dequant_rows_kernel(const uint8_t* __rest
   for (int i = 0; i < kSegPasses; ++i) {
     const int c = (pass0 + i) * 256 + lane * 8;
     if (i >= per || c >= K) break;
-    const float s = fp4_scale_of(sb[i]);
+    const float s = ue8m0_value(sb[i]);
     constexpr int W = V ? 16 / sizeof(T) : 1;
     Vec<T, W> o8[8 / W];
 #pragma unroll
@@ -290,7 +283,7 @@ __global__ void __launch_bounds__(256) dequant_weights_kernel(const uint8_t* __r
   for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n_all; i += (int64_t)gridDim.x * blockDim.x) {
     const int n = (int)(i % N), c = (int)(i / N % (K / 2));
     const int64_t e = i / N / (K / 2);
-    const float s = fp4_scale_of(sc[fp4_weight_scale_at(e, n, c / 16, N, KT)]);
+    const float s = ue8m0_value(sc[fp4_weight_scale_at(e, n, c / 16, N, KT)]);
     const uint32_t b = q[(e * N + n) * (int64_t)(K / 2) + c];
     T* dst = w + (e * K + 2 * c) * (int64_t)N + fp4_column(n, N, paired);
     dst[0] = from_f32<T>(fp4_value(b & 15u) * s);
@@ -924,17 +917,6 @@ bool fp4_weights(int64_t batch, int32_t K, int32_t N) {
 }
 bool fp4_rows(int64_t rows, int32_t K, int32_t G) {
   return rows >= 0 && rows <= ((int64_t)1 << 28) && fp4_k(K) && G >= 1 && G <= kMaxE;
-}
-// The status of a call that launches no kernel.  (A ws that is not the device's memory
-// -- there may be no device -- has none to clear.)
-moe_status clear_status(void* ws, cudaStream_t st) {
-  cudaPointerAttributes a;
-  if (cudaPointerGetAttributes(&a, ws) != cudaSuccess) {
-    cudaGetLastError();
-    return MOE_OK;
-  }
-  if (a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged) return MOE_OK;
-  return ops_status(cudaMemsetAsync(ws, 0, 2 * sizeof(int), st));
 }
 bool aligned128(const void* p) { return p != nullptr && aligned_to(p, 128); }
 

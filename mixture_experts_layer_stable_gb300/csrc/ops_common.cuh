@@ -81,6 +81,14 @@ __device__ __forceinline__ void gload_pair(const void* p, bool a, bool b, uint32
       : "l"(p), "r"((int)a), "r"((int)b));
 }
 
+// Block scales 2^s: 2^-s for s in [-127, 126], exact.
+__device__ __forceinline__ float ue8m0_inverse(int s) { return __uint_as_float((uint32_t)(127 - s) << 23); }
+// 2^s of a scale byte s + 127; 255 is NaN.
+__device__ __forceinline__ float ue8m0_value(uint32_t byte) {
+  return byte == 255 ? __uint_as_float(0x7FFFFFFFu) : byte == 0 ? __uint_as_float(0x400000u)
+                                                               : __uint_as_float(byte << 23);
+}
+
 // V consecutive elements of a row, stored as one access.
 template <typename T, int V>
 struct alignas(V * sizeof(T)) Vec {
@@ -255,6 +263,17 @@ inline bool elem_ok(const void* p, size_t es) { return p != nullptr && aligned_t
 inline bool elem_ok_or_null(const void* p, size_t es) { return p == nullptr || aligned_to(p, es); }
 inline moe_status ops_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
+// The status of a call that launches no kernel.  (A ws that is not the device's memory
+// -- there may be no device -- has none to clear.)
+inline moe_status clear_status(void* ws, cudaStream_t st) {
+  cudaPointerAttributes a;
+  if (cudaPointerGetAttributes(&a, ws) != cudaSuccess) {
+    cudaGetLastError();
+    return MOE_OK;
+  }
+  if (a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged) return MOE_OK;
+  return ops_status(cudaMemsetAsync(ws, 0, 2 * sizeof(int), st));
+}
 // f(T{}) for the element type of dt.
 template <typename F>
 cudaError_t with_dtype(int dt, F f) {

@@ -1,6 +1,7 @@
 """ctypes binding of the operators of include/moe_ops.h in libmoe.so: layer
-norm, rows sorted by expert and back, and the experts' product in microscaled
-4-bit floating point (MXFP4).
+norm, rows sorted by expert and back, the experts' products with their
+gradients, SwiGLU and activation checkpoints in 8 bits (MXINT8), and the
+experts' product in microscaled 4-bit floating point (MXFP4).
 
 Argument marshalling only, as in binding.py: tensors are torch CUDA tensors
 whose sizes, strides and types are passed on; every step runs in the library's
@@ -34,6 +35,15 @@ _PROTOTYPES = {
     "moe_permute": (_i32, _i64, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _vp, _vp),
     "moe_unpermute": (_i32, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp),
     "moe_unpermute_backward": (_i32, _i64, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp),
+    "moe_grouped_product_workspace_bytes": (_i64, _i32, _i32, _i32),
+    "moe_grouped_product": (_i32, _i32, _i64, _i32, _i32, _i32, _vp, _vp, _i64, _vp, _i32, _vp, _i64, _vp, _sz, _vp),
+    "moe_grouped_product_dw": (_i32, _i32, _i64, _i32, _i32, _i32, _vp, _vp, _i64, _vp, _i64, _vp, _i32, _vp, _sz,
+                               _vp),
+    "moe_mxint8_scale_bytes": (_i64, _i32),
+    "moe_quantize_mxint8_rows": (_i32, _i64, _i32, _vp, _i64, _vp, _vp, _vp),
+    "moe_dequantize_mxint8_rows": (_i32, _i64, _i32, _vp, _vp, _vp, _i64, _vp),
+    "moe_swiglu_forward": (_i32, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _vp, _vp),
+    "moe_swiglu_backward": (_i32, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _vp),
     "moe_mxfp4_weight_scale_bytes": (_i64, _i32, _i32),
     "moe_mxfp4_row_scale_bytes": (_i64, _i32, _i32),
     "moe_quantize_mxfp4": (_i32, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _vp),
@@ -61,7 +71,7 @@ def lib():
     return _lib
 
 
-_f32t, _i32t, _u8 = torch.float32, torch.int32, torch.uint8
+_f32t, _i32t, _u8, _i8 = torch.float32, torch.int32, torch.uint8, torch.int8
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _current_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None) or
                    (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
@@ -236,6 +246,122 @@ def moe_unpermute_backward(dout, y, weights, k, inv, offsets, dy, dw, stream=Non
         _dt(gt, w), T, d, k, E, dout.data_ptr(), _ld(dout, T, d, w), _flat(y, T * k * d, gt, dev, w),
         _flat(weights, T * k, _f32t, dev, w), _flat(inv, T * k, _i32t, dev, w), off,
         _flat(dy, T * k * d, gt, dev, w), _flat(dw, T * k, _f32t, dev, w), st)
+    if rc:
+        raise MoeError(rc, w)
+
+
+# ---------------------------------------------------------------- products by expert
+def moe_grouped_product_workspace_bytes(rows, K, N, G=1):
+    return int(lib().moe_grouped_product_workspace_bytes(rows, K, N, G))
+
+
+def moe_grouped_product(x, weights, offsets, out, ws, transposed=False, stream=None):
+    """out[p] = x[p] times its expert's weights [G, K, N]; transposed: [G, N, K] and their transpose, the gradient of
+    x for out = dx and x = dy with the forward's weights."""
+    w = "moe_grouped_product"
+    dev = _gpu(x, w)
+    st = _current_stream(dev) if stream is None else _handle(stream)
+    G, off = _segments(offsets, dev, w)
+    rows, K = x.shape
+    n, N = out.shape
+    xt, ot = x.dtype, out.dtype
+    if n != rows or tuple(weights.shape) != ((G, N, K) if transposed else (G, K, N)):
+        raise MoeError(MOE_ERR_INVALID_ARG, w)
+    rc = (_lib or lib()).moe_grouped_product(
+        _dt(xt, w), _dt(ot, w), rows, K, N, G, off, x.data_ptr(), _ld(x, rows, K, w),
+        _flat(weights, G * K * N, xt, dev, w), int(transposed), out.data_ptr(), _rows(out, rows, N, ot, dev, w),
+        _ws(ws, dev, w), ws.nbytes, st)
+    if rc:
+        raise MoeError(rc, w)
+
+
+def moe_grouped_product_dw(x, dy, offsets, dweights, ws, accumulate=False, stream=None):
+    """dweights[g] = x^T dy over expert g's rows (accumulate: added to what is there)."""
+    w = "moe_grouped_product_dw"
+    dev = _gpu(x, w)
+    st = _current_stream(dev) if stream is None else _handle(stream)
+    G, off = _segments(offsets, dev, w)
+    rows, K = x.shape
+    N = dy.shape[1]
+    xt, wt = x.dtype, dweights.dtype
+    if tuple(dweights.shape) != (G, K, N):
+        raise MoeError(MOE_ERR_INVALID_ARG, w)
+    rc = (_lib or lib()).moe_grouped_product_dw(
+        _dt(xt, w), _dt(wt, w), rows, K, N, G, off, x.data_ptr(), _ld(x, rows, K, w), dy.data_ptr(),
+        _rows(dy, rows, N, xt, dev, w), _flat(dweights, G * K * N, wt, dev, w), int(accumulate), _ws(ws, dev, w),
+        ws.nbytes, st)
+    if rc:
+        raise MoeError(rc, w)
+
+
+# ---------------------------------------------------------------- MXINT8 and SwiGLU
+def moe_mxint8_scale_bytes(rows, n):
+    return int(lib().moe_mxint8_scale_bytes(rows, n))
+
+
+def _kept(q, scales, rows, n, dev, where):
+    """Pointers of a checkpoint: codes of rows * n elements and their scales; None stay None."""
+    if (q is None) != (scales is None):
+        raise MoeError(MOE_ERR_INVALID_ARG, where)
+    if q is None:
+        return None, None
+    return _flat(q, rows * n, _i8, dev, where), _bytes(scales, rows * ((n + 31) // 32), dev, where)
+
+
+def moe_quantize_mxint8_rows(x, q, scales, stream=None):
+    """Rows x [rows, n] -> codes q [rows, n] (int8) and scale bytes [rows, ceil(n / 32)]."""
+    w = "moe_quantize_mxint8_rows"
+    dev = _gpu(x, w)
+    st = _current_stream(dev) if stream is None else _handle(stream)
+    rows, n = x.shape
+    qp, sp = _kept(q, scales, rows, n, dev, w)
+    rc = (_lib or lib()).moe_quantize_mxint8_rows(
+        _dt(x.dtype, w), rows, n, x.data_ptr(), _ld(x, rows, n, w), qp, sp, st)
+    if rc:
+        raise MoeError(rc, w)
+
+
+def moe_dequantize_mxint8_rows(q, scales, y, stream=None):
+    """The values of rows in 8 bits, into y [rows, n]."""
+    w = "moe_dequantize_mxint8_rows"
+    dev = _gpu(y, w)
+    st = _current_stream(dev) if stream is None else _handle(stream)
+    rows, n = y.shape
+    qp, sp = _kept(q, scales, rows, n, dev, w)
+    rc = (_lib or lib()).moe_dequantize_mxint8_rows(
+        _dt(y.dtype, w), rows, n, qp, sp, y.data_ptr(), _ld(y, rows, n, w), st)
+    if rc:
+        raise MoeError(rc, w)
+
+
+def moe_swiglu_forward(h, a, q=None, scales=None, stream=None):
+    """a = silu(g) * u of the rows h = [g | u]; q [rows, 2f] and scales: h in 8 bits, kept for the backward."""
+    w = "moe_swiglu_forward"
+    dev = _gpu(a, w)
+    st = _current_stream(dev) if stream is None else _handle(stream)
+    rows, f = a.shape
+    at = a.dtype
+    qp, sp = _kept(q, scales, 2 * rows, f, dev, w)
+    rc = (_lib or lib()).moe_swiglu_forward(
+        _dt(at, w), rows, f, h.data_ptr(), _rows(h, rows, 2 * f, at, dev, w), a.data_ptr(), _ld(a, rows, f, w), qp, sp,
+        st)
+    if rc:
+        raise MoeError(rc, w)
+
+
+def moe_swiglu_backward(da, h, dh, a=None, q=None, scales=None, stream=None):
+    """dh [rows, 2f], and a again, from h or (h None) its checkpoint q, scales."""
+    w = "moe_swiglu_backward"
+    dev = _gpu(da, w)
+    st = _current_stream(dev) if stream is None else _handle(stream)
+    rows, f = da.shape
+    at = da.dtype
+    qp, sp = _kept(q, scales, 2 * rows, f, dev, w)
+    rc = (_lib or lib()).moe_swiglu_backward(
+        _dt(at, w), rows, f, da.data_ptr(), _ld(da, rows, f, w), None if h is None else h.data_ptr(),
+        0 if h is None else _rows(h, rows, 2 * f, at, dev, w), qp, sp, dh.data_ptr(),
+        _rows(dh, rows, 2 * f, at, dev, w), None if a is None else a.data_ptr(),
+        0 if a is None else _rows(a, rows, f, at, dev, w), st)
     if rc:
         raise MoeError(rc, w)
 
