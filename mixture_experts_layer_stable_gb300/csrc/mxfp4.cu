@@ -8,6 +8,7 @@
 #include "gemm_common.cuh"
 #include "ops_common.cuh"
 #include "row_tiles.h"
+#include "tc_roles.cuh"
 
 namespace moe {
 
@@ -326,8 +327,7 @@ constexpr int kStage4 = 1024;           // staging of an epilogue warp: 16 rows 
 
 // Shared-memory descriptors as their low words (address in units of 16 bytes and
 // the leading offset, so that adding moves the address); the high words are
-// constants: 128-byte swizzle with 1024 bytes between 8-row groups, or none with 128.
-constexpr uint32_t kDescSw128 = (1024 >> 4) | (1u << 14) | (2u << 29);
+// constants: kDescSw128, or no swizzle with 128 bytes between 8-row groups.
 constexpr uint32_t kDescPlain = (128 >> 4) | (1u << 14);
 MOE_DEV uint32_t desc_lo(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
 
@@ -377,73 +377,6 @@ MOE_DEV void tc_cp_scales(int on, uint32_t taddr, uint32_t lo) {
         "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], s;\n\t}" ::"r"(taddr), "r"(lo), "n"(kDescPlain), "r"(on)
         : "memory");
 }
-// One arrival on the barrier (of a pair: at this place in each CTA of mask) when what
-// was issued so far has completed.
-template <bool PAIR>
-MOE_DEV void tc_commit_on(int on, uint32_t bar, uint16_t mask = 3) {
-  if constexpr (PAIR)
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "setp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n\t}" ::
-            "r"(bar),
-        "r"(on), "h"(mask)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "setp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(on)
-        : "memory");
-}
-MOE_DEV void expect_tx_on(int on, uint32_t bar, uint32_t bytes) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "setp.ne.b32 q, %2, 0;\n\t"
-      "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes), "r"(on)
-      : "memory");
-}
-// (Of a pair: `bar` may be the other CTA's, by its shared::cluster address.)
-template <bool PAIR>
-MOE_DEV void tma_load_2d_on(int on, uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1) {
-  if constexpr (PAIR) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "setp.ne.b32 q, %5, 0;\n\t"
-        "@q cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(on)
-        : "memory");
-  } else {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "setp.ne.b32 q, %5, 0;\n\t"
-        "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(on)
-        : "memory");
-  }
-}
-template <bool PAIR>
-MOE_DEV void tma_load_3d_on(int on, uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2) {
-  if constexpr (PAIR) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "setp.ne.b32 q, %6, 0;\n\t"
-        "@q cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(on)
-        : "memory");
-  } else {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "setp.ne.b32 q, %6, 0;\n\t"
-        "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(on)
-        : "memory");
-  }
-}
 MOE_DEV void bulk_load_on(int on, uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile(
       "{\n\t.reg .pred q;\n\t"
@@ -452,53 +385,12 @@ MOE_DEV void bulk_load_on(int on, uint32_t dst, const void* src, uint32_t bytes,
       "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar), "r"(on)
       : "memory");
 }
-MOE_DEV bool try_wait(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-// The rest of a wait whose first try failed: gives up (false) on the abort flag
-// or after kWaitLimitNs, which it reports.
-__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status, int where) {
-  const uint64_t t0 = global_timer_ns();
-  for (uint32_t it = 1;; ++it) {
-    if (try_wait(bar, parity)) return true;
-    if ((it & 63u) == 0) {
-      if (*abort_flag) return false;
-      if (global_timer_ns() - t0 > kWaitLimitNs) {
-        *abort_flag = 1;
-        report_status(status, kStatusTimeout, where);
-        return false;
-      }
-    }
-  }
-}
 // Instruction descriptor: E2M1 A and B (K-major), UE8M0 scales taken from bytes
 // sf, sf + 1 of a 32-bit scale column (sf 0 or 2).
 MOE_DEV uint32_t idesc_mxf4(int M, int N, int sf) {
   return ((uint32_t)sf << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
          ((uint32_t)(M >> 4) << 24) | ((uint32_t)sf << 29);
 }
-
-// One lane of a converged warp.
-MOE_DEV bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(p));
-  return p != 0;
-}
-// A value that is the same in every lane, as one the compiler knows to be: a
-// warp reduction's result is warp-uniform (a shuffle's is not).
-MOE_DEV int uniform(int v) { return (int)__reduce_max_sync(0xffffffffu, (unsigned)v); }
 
 struct P4 {
   const int* off;      // [G+1] or NULL (one segment of `rows`)
@@ -854,21 +746,6 @@ int grid_for(int64_t n) {
   const int64_t b = (n + 255) / 256;
   return (int)(b < 1 ? 1 : b < (1 << 20) ? b : (1 << 20));
 }
-// Clusters of two CTAs of kern that the GPU holds at once.  resident: the answer for
-// each device (0: not asked yet), kept by the caller for its kernel; threads that ask
-// at the same time store the same value.
-template <typename K>
-int pair_clusters(K kern, const cudaLaunchConfig_t& cfg, std::atomic<int> (&resident)[64]) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
-  int n = resident[dev].load(std::memory_order_relaxed);
-  if (n == 0) {
-    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) n = num_sms() / 2;
-    resident[dev].store(n, std::memory_order_relaxed);
-  }
-  return n;
-}
-
 template <typename T, bool SWIGLU, bool PAIR>
 cudaError_t launch_product(const CUtensorMap* tm, const P4& p, cudaStream_t st) {
   auto kern = product_kernel<T, SWIGLU, PAIR>;

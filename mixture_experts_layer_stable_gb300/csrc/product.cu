@@ -7,54 +7,11 @@
 // All three forms are D = A * B per expert: A is the expert's rows (or their transpose),
 // B its weights (or rows), and the work is cut into units (expert, tile of D) that each
 // block numbers by itself from the offsets, so no call looks at them on the host.
-#include "gemm_common.cuh"
-#include "ops_common.cuh"
+#include "product.cuh"
 
 namespace moe {
 
 namespace {
-
-constexpr int kMaxG = 1024;
-
-struct ProdArgs {
-  const int* off;  // [G + 1], or NULL: one expert with all rows
-  const void* a;   // rows x
-  const void* b;   // weights, or rows dy
-  void* out;
-  int64_t lda, ldb, ldo;  // row strides (ldb: of dy, or of a weight matrix)
-  int* status;
-  int rows, G, K, N;
-  int accumulate;
-};
-
-// Rows and units of each expert, numbered by the block: s_off [G + 1] first rows, s_unit
-// [G + 1] first units; an expert has per units for each tile of `tile` rows, or `per`
-// whatever its rows (tile 0).  (Offsets out of order or range give wrong rows, not
-// accesses out of range.)  Ends with a barrier.
-__device__ __forceinline__ void number_units(const ProdArgs& p, int tile, int per, int* s_off, int* s_unit) {
-  for (int i = threadIdx.x; i <= p.G; i += blockDim.x)
-    s_off[i] = p.off ? min(max(gload(p.off + i), 0), p.rows) : (i ? p.rows : 0);
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    const int lane = threadIdx.x;
-    int run = 0;
-    for (int base = 0; base < p.G; base += 32) {
-      const int e = base + lane;
-      const int c = e < p.G ? max(0, s_off[e + 1] - s_off[e]) : 0;
-      const int mine = e < p.G ? (tile ? (c + tile - 1) / tile * per : per) : 0;
-      int inc = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
-      }
-      if (e < p.G) s_unit[e] = run + inc - mine;
-      run += __shfl_sync(0xffffffffu, inc, 31);
-    }
-    if (lane == 0) s_unit[p.G] = run;
-  }
-  __syncthreads();
-}
 
 // ------------------------------------------------------------------ fp32 units
 // Operands of any type and alignment: tiles of BM x 128 by 256 threads, 16 of the
@@ -229,8 +186,6 @@ __global__ void __launch_bounds__(kSimtThreads) simt_product_kernel(const ProdAr
 }
 
 // ------------------------------------------------------------------ host side
-enum ProdForm { PROD_ROWS, PROD_ROWS_T, PROD_DW };
-
 // (No array has more than 2^40 elements, so units are numbered in 32 bits.)
 bool prod_sizes(int64_t rows, int32_t K, int32_t N, int32_t G) {
   constexpr int64_t most = (int64_t)1 << 40;
@@ -260,6 +215,7 @@ cudaError_t launch_simt(const ProdArgs& p, cudaStream_t st) {
 }
 
 cudaError_t launch_product(ProdForm form, int dtype, int odtype, const ProdArgs& p, cudaStream_t st) {
+  if (dtype != MOE_DT_F32) return launch_product_tc(form, dtype, p, st);
   return prod_types(dtype, odtype, [&](auto t, auto o) {
     using T = decltype(t);
     using O = decltype(o);
@@ -309,6 +265,7 @@ moe_status moe_grouped_product(int32_t dtype, int32_t odtype, int64_t rows, int3
   p.G = G;
   p.K = K;
   p.N = N;
+  p.odt = odtype;
   return ops_status(launch_product(transposed ? PROD_ROWS_T : PROD_ROWS, dtype, odtype, p, st));
 }
 
@@ -337,6 +294,7 @@ moe_status moe_grouped_product_dw(int32_t dtype, int32_t wdtype, int64_t rows, i
   p.G = G;
   p.K = K;
   p.N = N;
+  p.odt = wdtype;
   p.accumulate = accumulate != 0;
   return ops_status(launch_product(PROD_DW, dtype, wdtype, p, st));
 }
