@@ -23,10 +23,12 @@ struct ProdArgs {
 };
 
 // Rows and units of each expert, numbered by the block: s_off [G + 1] first rows, s_unit
-// [G + 1] first units; an expert has per units for each tile of `tile` rows, or `per`
-// whatever its rows (tile 0).  (Offsets out of order or range give wrong rows, not
-// accesses out of range.)  Ends with a barrier.
-__device__ __forceinline__ void number_units(const ProdArgs& p, int tile, int per, int* s_off, int* s_unit) {
+// [G + 1] first units; an expert has `per` units for each tile of up to `tile` rows, or
+// `per` whatever its rows (tile 0).  (Offsets out of order or range give wrong rows, not
+// accesses out of range.)  Returns the rows of the expert with the most in the first
+// warp; ends with a barrier.
+__device__ __forceinline__ int number_units(const ProdArgs& p, int tile, int per, int* s_off, int* s_unit) {
+  int most = 0;
   for (int i = threadIdx.x; i <= p.G; i += blockDim.x)
     s_off[i] = p.off ? min(max(gload(p.off + i), 0), p.rows) : (i ? p.rows : 0);
   __syncthreads();
@@ -36,6 +38,7 @@ __device__ __forceinline__ void number_units(const ProdArgs& p, int tile, int pe
     for (int base = 0; base < p.G; base += 32) {
       const int e = base + lane;
       const int c = e < p.G ? max(0, s_off[e + 1] - s_off[e]) : 0;
+      most = max(most, c);
       const int mine = e < p.G ? (tile ? (c + tile - 1) / tile * per : per) : 0;
       int inc = mine;
 #pragma unroll
@@ -47,15 +50,22 @@ __device__ __forceinline__ void number_units(const ProdArgs& p, int tile, int pe
       run += __shfl_sync(0xffffffffu, inc, 31);
     }
     if (lane == 0) s_unit[p.G] = run;
+    most = __reduce_max_sync(0xffffffffu, most);
   }
   __syncthreads();
+  return most;
 }
 
-// Units of a call at most, for D tiles of bm x bn.
-inline int64_t most_units(ProdForm form, const ProdArgs& p, int bm, int bn) {
-  const int64_t nt = (p.N + bn - 1) / bn;
-  if (form == PROD_DW) return nt * ((p.K + bm - 1) / bm) * p.G;
-  return nt * ((int64_t)p.rows / bm + (p.G < p.rows ? p.G : p.rows));
+// Expert of unit u: e with s_unit[e] <= u < s_unit[e + 1]; `at` is a first guess.
+__device__ __forceinline__ int expert_of(const int* s_unit, int G, int u, int at) {
+  if (u >= s_unit[at] && u < s_unit[at + 1]) return at;
+  int lo = 0, hi = G - 1;  // the last e with s_unit[e] <= u (experts without units have none)
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (s_unit[mid] <= u) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
 }
 
 // 16-bit operands on the tensor cores (product_tc.cu).

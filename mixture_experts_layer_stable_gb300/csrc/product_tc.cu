@@ -3,27 +3,43 @@
 //
 // Warp-specialised and persistent, one CTA per SM: warp 0 issues the copies (or eight
 // more warps load the operands themselves), one thread of warp 1 the tensor-core
-// instructions, warps 2..9 the epilogue.  A unit is (expert, tile of D): A is the M side
-// (128 rows of x; for the weights' gradient 128 columns of x), B the N side (256 columns
-// of the weights or of dy), and a stage of the ring holds 64 of the contraction:
-//   A 128 x 64 (16 KB), B 256 x 64 (32 KB).
+// instructions, warps 2..9 the epilogue.
+//
+// The MMA's M side are the output's columns (the weights; for the weights' gradient dy's
+// columns), 128 a CTA, and its N side the output's rows: up to 256 rows of an expert, or
+// 256 columns of x.  So the MMA's time goes with the rows there are, rounded up to 32,
+// and an expert with a few rows costs its weight stream and little else; and a TMEM lane
+// holds one output column, so a warp stores 32 neighbours of a row with one instruction,
+// whatever the row's alignment.
+//
+// A unit is (expert, 128 or 256 output columns, tile of output rows); a stage of the ring
+// holds 64 of the contraction: 16 KB of the M side and 128 bytes for every output row.
 // What is contiguous along the contraction lies in rows of 128 bytes (x and transposed
 // weights), the rest in blocks of 64 columns x 64 rows of 128 bytes; both 128-byte
 // swizzled, so in shared memory every operand is rows of 64 elements that were
-// contiguous in memory.
-// TMEM: two accumulators of 256 columns, so that a unit's epilogue runs beside the next
-// unit's products.
+// contiguous in memory.  The ring has as many stages as the largest tile there is leaves
+// room for.  TMEM: two accumulators of 256 columns, so that a unit's epilogue runs beside
+// the next unit's products.
 //
-// PAIR: two CTAs (a cluster) share each MMA of M = 256 rows, 128 in each, and each holds
-// half of B's columns: 32 KB a stage and SM instead of 48 for the same products.  The even
-// CTA's barriers count both CTAs' copies, its one thread issues for both, and its commits
-// arrive in both.
+// PAIR: two CTAs (a cluster) share each MMA of M = 256 columns, 128 in each, and each
+// holds half of the rows: 32 KB a stage and SM instead of 48 for the same products.  The
+// even CTA's barriers count both CTAs' copies, its one thread issues for both, and its
+// commits arrive in both.
 //
-// Ragged edges.  Rows of x behind an expert's last are other experts': they fill rows of D
-// that are not stored.  The contraction over an expert's rows (the weights' gradient) may
-// end inside a stage: the instructions past its end are not issued, and the up to 15 rows
-// of both operands that the last one still takes are overwritten with zeros first (one of
-// them would not do: what lies there may be NaN).
+// Order.  Units are numbered expert by expert, and a CTA's k-th unit is taken from the
+// front and the back of that order in turns, so that experts with many rows (bound by the
+// tensor cores) run beside experts with few (bound by their weights' way from HBM).
+//
+// Ragged edges.  Rows behind an expert's last are other experts': they fill accumulator
+// columns that are not stored.  The contraction over an expert's rows (the weights'
+// gradient) may end inside a stage: the instructions past its end are not issued, and the
+// up to 15 rows of both operands that the last one still takes are overwritten with zeros
+// first (one of them would not do: what lies there may be NaN).
+//
+// Sums.  The tensor cores add to their fp32 accumulators by truncation, which a long
+// contraction shows in results of 32 bits (4096 rows into a weight gradient: 1e-5 of it).
+// For those an accumulator takes 256 of the contraction and the epilogue adds the
+// accumulators up in registers, rounding to nearest.
 #include "gemm_common.cuh"
 #include "product.cuh"
 #include "tc_roles.cuh"
@@ -34,16 +50,19 @@ namespace {
 
 enum TcMode { TC_COPY, TC_PAIR, TC_LOAD };  // tensor copies, the same by CTA pairs, plain loads
 
-constexpr int kBlkM = 128, kBlkN = 256, kBlkK = 64;
+constexpr int kBlkM = 128, kAccCols = 256, kBlkK = 64;
 constexpr int kEpiWarpsP = 8;   // two for each quarter of the TMEM lanes
 constexpr int kLoadWarps = 8;   // of TC_LOAD
 constexpr int kABytes = kBlkM * kBlkK * 2;
 constexpr int kBoxBytes = 64 * 128;  // 64 rows of 64 elements
-constexpr int kRingBytes = 192 * 1024;
-constexpr int kStagesCopy = 4, kStagesPair = 6;
-constexpr int kStageRow = 17;        // floats between the rows of an epilogue warp's staging: 32 x 16
-constexpr int kStagingP = 32 * kStageRow * 4;
-constexpr int kSmemP = 1024 + kRingBytes + kEpiWarpsP * kStagingP;
+constexpr int kStagesP = 12;         // at most
+constexpr int kTablesP = 8704;       // static shared memory: the experts' rows and units, barriers
+constexpr int kSmemP = 232448 - kTablesP;
+constexpr int kSumSteps = 4;         // stages that a 32-bit result's accumulator takes
+
+// Output rows of a tile at most.  (With loading warps an SM's registers hold the sums of
+// half as many.)
+constexpr int tile_most(TcMode mode, bool f32) { return mode == TC_LOAD && f32 ? 128 : 256; }
 
 // D (+)= A B, 16-bit operands, K = 16; a and b are descriptors' low words.
 template <bool PAIR>
@@ -83,8 +102,9 @@ MOE_DEV bool try_wait_cluster(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// Two 16-bit elements of a row in one register, the second behind the first; only those
-// below n exist.  WORD: the row starts with a 32-bit word.
+// Elements i and i + 1 of a row of n (may be negative), each 0 if it does not exist, to be
+// joined as lo | hi << 16.  WORD: the row starts with a 32-bit word and i is even; then as
+// lo | hi.
 template <bool WORD>
 MOE_DEV void load_two(const uint16_t* p, int i, int n, uint32_t& lo, uint32_t& hi) {
   if constexpr (WORD) {
@@ -103,42 +123,53 @@ MOE_DEV void load_two(const uint16_t* p, int i, int n, uint32_t& lo, uint32_t& h
   }
 }
 
+// One result, or its sum with what is there.
+template <typename T>
+MOE_DEV void put(void* out, int64_t at, float v, bool add) {
+  T* q = static_cast<T*>(out) + at;
+  *q = from_f32<T>(add ? v + to_f32(*q) : v);
+}
+
 struct TcUnit {
-  int e, row0, count, m0, n0;
+  int e, row0, count;  // the expert and its rows
+  int n0;              // first output column (of a pair: of both CTAs)
+  int r0, nt;          // first output row of the tile, in the expert, and rows
 };
 
-template <ProdForm FORM, TcMode MODE>
+// F32: results of 32 bits.
+template <ProdForm FORM, TcMode MODE, bool F32>
 __global__ void __launch_bounds__(64 + 32 * (kEpiWarpsP + (MODE == TC_LOAD ? kLoadWarps : 0)), 1)
-    tc_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_a128,
-                      const __grid_constant__ CUtensorMap tm_b, const ProdArgs p, const uint32_t formats) {
-  constexpr bool PAIR = MODE == TC_PAIR, DW = FORM == PROD_DW, B_MN = FORM != PROD_ROWS_T;
-  constexpr int S = PAIR ? kStagesPair : kStagesCopy;
-  constexpr uint32_t kStage = kRingBytes / S;
-  constexpr int kTileM = PAIR ? 2 * kBlkM : kBlkM;
+    tc_product_kernel(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ CUtensorMap tm_n,
+                      const __grid_constant__ CUtensorMap tm_n128, const ProdArgs p, const uint32_t formats) {
+  constexpr bool PAIR = MODE == TC_PAIR, DW = FORM == PROD_DW;
+  constexpr bool M_MN = FORM != PROD_ROWS_T, N_MN = DW;  // operands whose contraction is not contiguous
+  constexpr int kCols = PAIR ? 2 * kBlkM : kBlkM;        // output columns of a unit
+  constexpr int kTileRows = tile_most(MODE, F32);
+  constexpr int kBoxRows = DW ? 64 : 32;                 // output rows of a box of the N side
+  constexpr uint32_t kNBox = kBoxRows * 128;
   extern __shared__ uint8_t smem_raw[];
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   __shared__ int s_off[kMaxG + 1], s_unit[kMaxG + 1];
-  __shared__ alignas(8) uint64_t full[S], empty[S], tfull[2], tempty[2], drain, tail_full, tail_ready;
+  __shared__ alignas(8) uint64_t full[kStagesP], empty[kStagesP], ready[kStagesP], tfull[2], tempty[2], drain;
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort;
+  __shared__ int s_abort, s_most;
   if (warp == 0 && lane == 0) {
-    for (int i = 0; i < S; ++i) {
+    for (int i = 0; i < kStagesP; ++i) {
       mbar_init(&full[i], MODE == TC_LOAD ? kLoadWarps : 1);
       mbar_init(&empty[i], 1);
+      mbar_init(&ready[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull[i], 1);
       mbar_init(&tempty[i], (PAIR ? 2 : 1) * kEpiWarpsP);
     }
     mbar_init(&drain, 1);
-    mbar_init(&tail_full, 1);
-    mbar_init(&tail_ready, 1);
     s_abort = 0;
     fence_mbar_init();
     if (MODE != TC_LOAD) {
-      tma_prefetch_desc(&tm_a);
-      tma_prefetch_desc(&tm_a128);
-      tma_prefetch_desc(&tm_b);
+      tma_prefetch_desc(&tm_m);
+      tma_prefetch_desc(&tm_n);
+      tma_prefetch_desc(&tm_n128);
     }
   }
   if (warp == 1) {
@@ -152,8 +183,9 @@ __global__ void __launch_bounds__(64 + 32 * (kEpiWarpsP + (MODE == TC_LOAD ? kLo
   }
   ops_wait();
   if (blockIdx.x == 0 && threadIdx.x < 2) p.status[threadIdx.x] = 0;
-  const int nts = (p.N + kBlkN - 1) / kBlkN, mts_dw = (p.K + kTileM - 1) / kTileM;
-  number_units(p, DW ? 0 : kTileM, DW ? mts_dw * nts : nts, s_off, s_unit);
+  const int col_tiles = (p.N + kCols - 1) / kCols, dw_tiles = (p.K + kTileRows - 1) / kTileRows;
+  const int most = number_units(p, DW ? 0 : kTileRows, DW ? dw_tiles * col_tiles : col_tiles, s_off, s_unit);
+  if (threadIdx.x == 0) s_most = DW ? p.K : most;
   tc_fence_before();
   __syncthreads();
   if constexpr (PAIR) cluster_sync();  // the other CTA's barriers exist before their use
@@ -161,26 +193,37 @@ __global__ void __launch_bounds__(64 + 32 * (kEpiWarpsP + (MODE == TC_LOAD ? kLo
   const uint32_t tmem = (uint32_t)uniform((int)s_tmem);
   const int total = uniform(s_unit[p.G]);
   volatile int* abort_flag = &s_abort;
-  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const int rank = PAIR ? uniform((int)cluster_ctarank()) : 0;
   const int unit0 = PAIR ? blockIdx.x / 2 : blockIdx.x, unit_step = PAIR ? gridDim.x / 2 : gridDim.x;
 
-  // Unit u; each role walks its units upwards and keeps its place in the experts.
+  // An output's c rows in tiles as even as multiples of 32 allow; the longest.
+  auto tile_rows = [](int c, int tiles) { return ((c + tiles - 1) / tiles + 31) & ~31; };
+  // this CTA's rows of a tile of nt, and its share of shared memory for them
+  auto mine_of = [&](int nt) { return PAIR ? ((nt + 31) & ~31) / 2 : nt; };
+  // Stage layout for the largest tile there is.
+  const int cap = uniform(s_most > kTileRows ? kTileRows : max(32, (s_most + 31) & ~31));
+  const int cap_n = (mine_of(cap) + kBoxRows - 1) / kBoxRows * kBoxRows;
+  const uint32_t stage_bytes = (uint32_t)(kABytes + cap_n * 128);
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const int S = min(kStagesP, (int)((kSmemP - (base - smem_u32(smem_raw))) / stage_bytes));
+
+  // The L-th unit in the order they are taken; each role keeps its place in the experts.
   int at_e = 0;
-  auto unit_at = [&](int u) {
-    while (u >= uniform(s_unit[at_e + 1])) ++at_e;
+  auto unit_at = [&](int L) {
+    const int u = L & 1 ? total - 1 - (L >> 1) : L >> 1;
+    at_e = uniform(expert_of(s_unit, p.G, u, at_e));
     TcUnit t;
     t.e = at_e;
     t.row0 = uniform(s_off[at_e]);
     t.count = max(0, uniform(s_off[at_e + 1]) - t.row0);
-    const int mts = DW ? mts_dw : (t.count + kTileM - 1) / kTileM, r = u - uniform(s_unit[at_e]);
-    const int n = r / mts;
-    t.n0 = n * kBlkN;
-    t.m0 = (r - n * mts) * kTileM;
+    const int r = u - uniform(s_unit[at_e]), c = DW ? p.K : t.count;
+    const int tiles = DW ? dw_tiles : (c + kTileRows - 1) / kTileRows, n = tiles == 1 ? r : r / tiles;
+    t.n0 = n * kCols;
+    const int sz = tile_rows(c, tiles);
+    t.r0 = (r - n * tiles) * sz;
+    t.nt = min(sz, c - t.r0);  // (sz <= kTileRows, so every tile has a row)
     return t;
   };
-  // columns of the MMA, and of this CTA's B
-  auto mma_n = [&](const TcUnit& t) { return min(kBlkN, (p.N - t.n0 + 31) & ~31); };
   auto steps_of = [&](const TcUnit& t) { return ((DW ? t.count : p.K) + kBlkK - 1) / kBlkK; };
   const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty);
   // All lanes wait; the result is the same in each.
@@ -188,12 +231,11 @@ __global__ void __launch_bounds__(64 + 32 * (kEpiWarpsP + (MODE == TC_LOAD ? kLo
     if (__all_sync(0xffffffffu, try_wait(bar, parity))) return true;
     return __all_sync(0xffffffffu, wait_on(bar, parity, abort_flag, p.status, where)) != 0;
   };
-  // Zeros in rows [from, to) of every block of 64 rows of a stage (MN-major operands),
-  // visible to the tensor cores.
+  // Zeros in rows [from, to) of every block of 64 rows of a stage (neither operand's
+  // contraction contiguous), visible to the tensor cores.
   auto zero_rows = [&](uint32_t stage, int from, int to) {
-    constexpr int kBlocks = (int)(kStage / kBoxBytes);
-    const int n = (to - from) * 8;
-    for (int i = lane; i < kBlocks * n; i += 32) {
+    const int n = (to - from) * 8, blocks = (int)(stage_bytes / kBoxBytes);
+    for (int i = lane; i < blocks * n; i += 32) {
       const int b = i / n, r = i - b * n;
       st_shared_v4(stage + (uint32_t)(b * kBoxBytes + (from + (r >> 3)) * 128 + (r & 7) * 16), 0, 0, 0, 0);
     }
@@ -204,32 +246,36 @@ __global__ void __launch_bounds__(64 + 32 * (kEpiWarpsP + (MODE == TC_LOAD ? kLo
   if (warp == 0 && MODE != TC_LOAD) {
     const int leader = elect_one();
     int s = 0;
-    uint32_t ph = 0, used = 0, last = 0, apart_n = 0;
+    uint32_t ph = 0, used = 0, last = 0, apart_used = 0, apart_ph = 0;
     for (int u = unit0; u < total; u += unit_step) {
       const TcUnit t = unit_at(u);
-      const int hw = PAIR ? mma_n(t) / 2 : mma_n(t), steps = steps_of(t);
-      // boxes of CTA r's A (32 rows, or 64 columns) and B (64)
-      auto a_boxes = [&](int r) {
-        if (DW) return max(0, min(2, (p.K - t.m0 - r * kBlkM + 63) / 64));
-        return max(0, min(4, (t.count - t.m0 - r * kBlkM + 31) / 32));
+      const int mine = mine_of(t.nt), steps = steps_of(t);
+      // boxes of CTA r's M side (64 columns, or all 128); of its N side
+      auto m_boxes = [&](int r) {
+        const int left = p.N - t.n0 - r * kBlkM;
+        return M_MN ? max(0, min(2, (left + 63) / 64)) : left > 0 ? 1 : 0;
       };
-      const int ab = a_boxes(rank), bb = (hw + 63) / 64;
-      const uint32_t bytes = (uint32_t)(ab * (DW ? kBoxBytes : kBoxBytes / 2) + bb * kBoxBytes);
-      const uint32_t others = PAIR ? (uint32_t)(a_boxes(1) * (DW ? kBoxBytes : kBoxBytes / 2) + bb * kBoxBytes) : 0u;
-      const int am = t.m0 + rank * kBlkM, bn = t.n0 + rank * hw;
+      constexpr uint32_t kMBox = M_MN ? kBoxBytes : kABytes;
+      const int mb = m_boxes(rank), nb = (mine + kBoxRows - 1) / kBoxRows;
+      const uint32_t n_bytes = (uint32_t)nb * kNBox, bytes = (uint32_t)mb * kMBox + n_bytes;
+      const uint32_t others = PAIR ? (uint32_t)m_boxes(1) * kMBox + n_bytes : 0u;
+      const int col = t.n0 + rank * kBlkM, row = t.r0 + rank * mine;
+      const int big = DW ? 0 : nb / 4;  // boxes of 128 rows
       for (int kb = 0; kb < steps; ++kb) {
         if (!wait_all(empty0 + 8u * s, ph ^ 1u, 2000 + s)) goto produced;
-        const uint32_t sa = base + (uint32_t)s * kStage, sb = sa + kABytes;
+        const uint32_t sa = base + (uint32_t)s * stage_bytes, sb = sa + kABytes;
         const int k0 = kb * kBlkK;
         // of a pair, the odd CTA zeroes the end of the contraction in its own shared memory
-        // and waits for its own copies first
+        // and waits for its own copies first, on its own barrier of the stage (which has no
+        // other use)
         const bool apart = PAIR && DW && kb == steps - 1 && (t.count & 15) != 0;
         uint32_t fb = full0 + 8u * s;
         if constexpr (PAIR) {
           if (apart && rank == 1) {
-            fb = mapa_shared(smem_u32(&tail_full), 1);
-            expect_tx_on(leader, smem_u32(&tail_full), bytes);
-            ++apart_n;
+            expect_tx_on(leader, fb, bytes);
+            fb = mapa_shared(fb, 1);
+            apart_used |= 1u << s;
+            apart_ph ^= 1u << s;  // the parity of this stage's next use
           } else {
             fb = mapa_shared(fb, 0);
             expect_tx_on(leader && rank == 0, full0 + 8u * s, bytes + (apart ? 0u : others));
@@ -237,19 +283,20 @@ __global__ void __launch_bounds__(64 + 32 * (kEpiWarpsP + (MODE == TC_LOAD ? kLo
         } else {
           expect_tx_on(leader, fb, bytes);
         }
-        if constexpr (DW) {
-          for (int i = 0; i < ab; ++i)
-            tma_load_2d_on<PAIR>(leader, sa + i * kBoxBytes, &tm_a, fb, am + i * 64, t.row0 + k0);
-        } else {
-          tma_load_2d_on<PAIR>(leader && ab == 4, sa, &tm_a128, fb, k0, t.row0 + am);
-          for (int i = ab == 4 ? 4 : 0; i < ab; ++i)
-            tma_load_2d_on<PAIR>(leader, sa + i * (kBoxBytes / 2), &tm_a, fb, k0, t.row0 + am + i * 32);
+        for (int i = 0; i < mb; ++i) {
+          const uint32_t dst = sa + i * kMBox;
+          if constexpr (DW) tma_load_2d_on<PAIR>(leader, dst, &tm_m, fb, col + i * 64, t.row0 + k0);
+          else if constexpr (M_MN) tma_load_3d_on<PAIR>(leader, dst, &tm_m, fb, col + i * 64, k0, t.e);
+          else tma_load_3d_on<PAIR>(leader, dst, &tm_m, fb, k0, col, t.e);
         }
-        for (int i = 0; i < bb; ++i) {
-          const uint32_t dst = sb + i * kBoxBytes;
-          if constexpr (DW) tma_load_2d_on<PAIR>(leader, dst, &tm_b, fb, bn + i * 64, t.row0 + k0);
-          else if constexpr (B_MN) tma_load_3d_on<PAIR>(leader, dst, &tm_b, fb, bn + i * 64, k0, t.e);
-          else tma_load_3d_on<PAIR>(leader, dst, &tm_b, fb, k0, bn + i * 64, t.e);
+        if constexpr (DW) {
+          for (int i = 0; i < nb; ++i)
+            tma_load_2d_on<PAIR>(leader, sb + i * kNBox, &tm_n, fb, row + i * 64, t.row0 + k0);
+        } else {
+          for (int i = 0; i < big; ++i)
+            tma_load_2d_on<PAIR>(leader, sb + i * 4 * kNBox, &tm_n128, fb, k0, t.row0 + row + i * 128);
+          for (int i = 4 * big; i < nb; ++i)
+            tma_load_2d_on<PAIR>(leader, sb + i * kNBox, &tm_n, fb, k0, t.row0 + row + i * 32);
         }
         used |= 1u << s;
         last = (last & ~(1u << s)) | (ph << s);
@@ -262,53 +309,55 @@ __global__ void __launch_bounds__(64 + 32 * (kEpiWarpsP + (MODE == TC_LOAD ? kLo
   produced:
     // every issued copy has landed before the CTA can exit (of a pair the even CTA's
     // barriers count both CTAs'), and of a pair every commit has arrived
-    for (int i = 0; i < S; ++i) {
+    for (int i = 0; i < kStagesP; ++i) {
       if (((used >> i) & 1u) == 0) continue;
       if (rank == 0 && !mbar_wait_drain(&full[i], (last >> i) & 1u)) break;
       if (PAIR && !mbar_wait_drain(&empty[i], (last >> i) & 1u)) break;
     }
-    if (apart_n > 0) mbar_wait_drain(&tail_full, (apart_n - 1) & 1u);
+    for (int i = 0; i < kStagesP; ++i)
+      if (((apart_used >> i) & 1u) != 0 && !mbar_wait_drain(&full[i], ((apart_ph >> i) & 1u) ^ 1u)) break;
   } else if (warp == 1 && rank == 0) {
     const int leader = elect_one();
     int s = 0, acc = 0;
     uint32_t ph = 0, aph = 0, tph = 0;
     constexpr uint32_t kMN = 512u << 16, kKM = 1u << 16;  // leading offsets: 8 KB between blocks of 64 columns
-    const uint32_t da0 = (base >> 4) | (DW ? kMN : kKM), db0 = ((base + kABytes) >> 4) | (B_MN ? kMN : kKM);
-    constexpr uint32_t ka = DW ? 128u : 2u, kb_ = B_MN ? 128u : 2u;  // 16 of the contraction, in units of 16 bytes
+    const uint32_t da0 = (base >> 4) | (M_MN ? kMN : kKM), db0 = ((base + kABytes) >> 4) | (N_MN ? kMN : kKM);
+    constexpr uint32_t ka = M_MN ? 128u : 2u, kn = N_MN ? 128u : 2u;  // 16 of the contraction, in units of 16 bytes
     for (int u = unit0; u < total; u += unit_step) {
       const TcUnit t = unit_at(u);
       const int steps = steps_of(t);
-      if (steps == 0) continue;
-      const uint32_t id = (1u << 4) | formats | ((DW ? 1u : 0u) << 15) | ((B_MN ? 1u : 0u) << 16) |
-                          ((uint32_t)(mma_n(t) >> 3) << 17) | ((uint32_t)((PAIR ? 256 : 128) >> 4) << 24);
-      const uint32_t d = tmem + (uint32_t)(acc * kBlkN);
-      if (!wait_all(smem_u32(&tempty[acc]), aph ^ 1u, 2100 + acc)) goto issued;
-      tc_fence_after();
+      const int mma_n = PAIR ? (t.nt + 31) & ~31 : (t.nt + 15) & ~15;
+      const uint32_t id = (1u << 4) | formats | ((M_MN ? 1u : 0u) << 15) | ((N_MN ? 1u : 0u) << 16) |
+                          ((uint32_t)(mma_n >> 3) << 17) | ((uint32_t)((PAIR ? 256 : 128) >> 4) << 24);
       int left = DW ? t.count : p.K;
       uint32_t more = 0;
       for (int kb = 0; kb < steps; ++kb) {
+        const uint32_t d = tmem + (uint32_t)(acc * kAccCols);
+        if (!more) {
+          if (!wait_all(smem_u32(&tempty[acc]), aph ^ 1u, 2100 + acc)) goto issued;
+        }
         if (!wait_all(full0 + 8u * s, ph, 2200 + s)) goto issued;
         if constexpr (DW && MODE != TC_LOAD) {
           if (left < kBlkK && (left & 15) != 0) {
-            zero_rows(base + (uint32_t)s * kStage, left, (left + 15) & ~15);
+            zero_rows(base + (uint32_t)s * stage_bytes, left, (left + 15) & ~15);
             if constexpr (PAIR) {
-              const uint32_t bar = smem_u32(&tail_ready);
-              bool ok = __all_sync(0xffffffffu, try_wait_cluster(bar, tph));
+              const uint32_t bar = smem_u32(&ready[s]), par = (tph >> s) & 1u;
+              bool ok = __all_sync(0xffffffffu, try_wait_cluster(bar, par));
               if (!ok) {
-                ok = __all_sync(0xffffffffu, wait_on(bar, tph, abort_flag, p.status, 2300));
-                ok = ok && __all_sync(0xffffffffu, try_wait_cluster(bar, tph));
+                ok = __all_sync(0xffffffffu, wait_on(bar, par, abort_flag, p.status, 2300));
+                ok = ok && __all_sync(0xffffffffu, try_wait_cluster(bar, par));
               }
               if (!ok) goto issued;
-              tph ^= 1u;
+              tph ^= 1u << s;
             }
           }
         }
         tc_fence_after();
-        const uint32_t da = da0 + (uint32_t)s * (kStage / 16u), db = db0 + (uint32_t)s * (kStage / 16u);
+        const uint32_t da = da0 + (uint32_t)s * (stage_bytes / 16u), db = db0 + (uint32_t)s * (stage_bytes / 16u);
         tc_mma_f16_on<PAIR>(leader, d, da, db, id, more);
-        tc_mma_f16_on<PAIR>(leader && left > 16, d, da + ka, db + kb_, id, 1u);
-        tc_mma_f16_on<PAIR>(leader && left > 32, d, da + 2 * ka, db + 2 * kb_, id, 1u);
-        tc_mma_f16_on<PAIR>(leader && left > 48, d, da + 3 * ka, db + 3 * kb_, id, 1u);
+        tc_mma_f16_on<PAIR>(leader && left > 16, d, da + ka, db + kn, id, 1u);
+        tc_mma_f16_on<PAIR>(leader && left > 32, d, da + 2 * ka, db + 2 * kn, id, 1u);
+        tc_mma_f16_on<PAIR>(leader && left > 48, d, da + 3 * ka, db + 3 * kn, id, 1u);
         tc_commit_on<PAIR>(leader, empty0 + 8u * s);
         left -= kBlkK;
         more = 1u;
@@ -316,18 +365,23 @@ __global__ void __launch_bounds__(64 + 32 * (kEpiWarpsP + (MODE == TC_LOAD ? kLo
           s = 0;
           ph ^= 1u;
         }
-      }
-      tc_commit_on<PAIR>(leader, smem_u32(&tfull[acc]));
-      if (++acc == 2) {
-        acc = 0;
-        aph ^= 1u;
+        if (kb == steps - 1 || (F32 && (kb + 1) % kSumSteps == 0)) {
+          tc_commit_on<PAIR>(leader, smem_u32(&tfull[acc]));
+          more = 0;
+          if (++acc == 2) {
+            acc = 0;
+            aph ^= 1u;
+          }
+        }
       }
     }
   issued:
     tc_commit_on<PAIR>(leader, smem_u32(&drain), 1);
     mbar_wait_drain(&drain, 0);
   } else if (PAIR && DW && warp == 1) {
-    // the odd CTA's part of the contraction's end
+    // the odd CTA's part of the contraction's end.  (Barriers of each stage's own: the copies
+    // of several units' ends can be under way, but a stage is not filled again before its
+    // products are done.)
     int s = 0;
     uint32_t tph = 0;
     for (int u = unit0; u < total; u += unit_step) {
@@ -336,11 +390,11 @@ __global__ void __launch_bounds__(64 + 32 * (kEpiWarpsP + (MODE == TC_LOAD ? kLo
       if (steps == 0) continue;
       s = (s + steps - 1) % S;
       if ((t.count & 15) != 0) {
-        if (!wait_all(smem_u32(&tail_full), tph, 2400)) break;
-        tph ^= 1u;
+        if (!wait_all(full0 + 8u * s, (tph >> s) & 1u, 2400)) break;
+        tph ^= 1u << s;
         const int left = t.count - (steps - 1) * kBlkK;
-        zero_rows(base + (uint32_t)s * kStage, left, (left + 15) & ~15);
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tail_ready), 0));
+        zero_rows(base + (uint32_t)s * stage_bytes, left, (left + 15) & ~15);
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&ready[s]), 0));
       }
       if (++s == S) s = 0;
     }
@@ -350,7 +404,7 @@ __global__ void __launch_bounds__(64 + 32 * (kEpiWarpsP + (MODE == TC_LOAD ? kLo
     int s = 0;
     uint32_t ph = 0;
     const uint16_t *A = static_cast<const uint16_t*>(p.a), *B = static_cast<const uint16_t*>(p.b);
-    // rows [w, n) of shared memory from `to`: row r is row_at(r, pointer) elements of memory
+    // n rows of shared memory from `to`: row r is as many elements at src as row_at(r, src) says
     auto fill = [&](uint32_t to, int n, auto word, auto row_at) {
       constexpr int U = 8;
       for (int r0 = w; r0 < n; r0 += kLoadWarps * U) {
@@ -381,34 +435,34 @@ __global__ void __launch_bounds__(64 + 32 * (kEpiWarpsP + (MODE == TC_LOAD ? kLo
     const bool b_words = ((reinterpret_cast<uintptr_t>(B) | (uintptr_t)p.ldb * 2 | (DW ? 0 : (uintptr_t)p.K * p.N * 2)) & 3) == 0;
     for (int u = unit0; u < total; u += unit_step) {
       const TcUnit t = unit_at(u);
-      const int nn = mma_n(t), steps = steps_of(t), kk = DW ? t.count : p.K;
+      const int steps = steps_of(t), kk = DW ? t.count : p.K;
       const uint16_t* we = DW ? B + (int64_t)t.row0 * p.ldb : B + (int64_t)t.e * p.K * p.N;
       for (int kb = 0; kb < steps; ++kb) {
         if (!wait_all(empty0 + 8u * s, ph ^ 1u, 2000 + s)) goto loaded;
-        const uint32_t sa = base + (uint32_t)s * kStage, sb = sa + kABytes;
+        const uint32_t sa = base + (uint32_t)s * stage_bytes, sb = sa + kABytes;
         const int k0 = kb * kBlkK;
-        // contraction along the row (K-major): row c of D's side, `have` elements from k0;
-        // else row r % 64 of the contraction, 64 columns from 64 * (r / 64)
-        if constexpr (DW)
-          fill_any(sa, kBlkM, a_words, [&](int r, const uint16_t*& src) {
-            const int k = k0 + (r & 63), c = t.m0 + (r & ~63);
-            src = A + (int64_t)(t.row0 + k) * p.lda + c;
-            return k < kk ? p.K - c : 0;
-          });
-        else
-          fill_any(sa, min(kBlkM, t.count - t.m0), a_words, [&](int r, const uint16_t*& src) {
-            src = A + (int64_t)(t.row0 + t.m0 + r) * p.lda + k0;
-            return kk - k0;
-          });
-        if constexpr (B_MN)
-          fill_any(sb, (nn + 63) & ~63, b_words, [&](int r, const uint16_t*& src) {
+        // contraction along the row: row r of the operand, its elements from k0 on; else
+        // row r % 64 of the contraction, 64 columns from 64 * (r / 64) on
+        if constexpr (M_MN)
+          fill_any(sa, kBlkM, b_words, [&](int r, const uint16_t*& src) {
             const int k = k0 + (r & 63), c = t.n0 + (r & ~63);
             src = we + (int64_t)k * p.ldb + c;
             return k < kk ? p.N - c : 0;
           });
         else
-          fill_any(sb, min(nn, p.N - t.n0), b_words, [&](int r, const uint16_t*& src) {
+          fill_any(sa, min(kBlkM, p.N - t.n0), b_words, [&](int r, const uint16_t*& src) {
             src = we + (int64_t)(t.n0 + r) * p.ldb + k0;
+            return kk - k0;
+          });
+        if constexpr (N_MN)
+          fill_any(sb, (t.nt + 63) & ~63, a_words, [&](int r, const uint16_t*& src) {
+            const int k = k0 + (r & 63), c = t.r0 + (r & ~63);
+            src = A + (int64_t)(t.row0 + k) * p.lda + c;
+            return k < kk ? p.K - c : 0;
+          });
+        else
+          fill_any(sb, t.nt, a_words, [&](int r, const uint16_t*& src) {
+            src = A + (int64_t)(t.row0 + t.r0 + r) * p.lda + k0;
             return kk - k0;
           });
         fence_proxy_async_smem();
@@ -422,108 +476,13 @@ __global__ void __launch_bounds__(64 + 32 * (kEpiWarpsP + (MODE == TC_LOAD ? kLo
     }
   loaded:;
   } else if (warp > 1 && warp < 2 + kEpiWarpsP) {
-    // A lane holds a row of D; a warp takes every other 32 columns of its quarter's 32 rows.
-    // Rows that are 16-byte aligned are stored from the lanes, others through the warp's
-    // staging, 16 columns at a time, so that neighbouring lanes store neighbouring elements.
-    const int q = warp & 3;  // TMEM lane quarter of this warp
-    const uint32_t stg = base + kRingBytes + (uint32_t)(warp - 2) * kStagingP;
+    // A lane holds an output column; a warp takes every other 32 rows of its quarter's 32
+    // columns.
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16) + 32u * half;
     int acc = 0;
     uint32_t aph = 0;
-    const int osz = p.odt == MOE_DT_F32 ? 4 : 2;
-    uint8_t* out = static_cast<uint8_t*>(p.out);
-    const bool rows16 = ((reinterpret_cast<uintptr_t>(out) | (uintptr_t)p.ldo * osz) & 15) == 0;
-    for (int u = unit0; u < total; u += unit_step) {
-      const TcUnit t = unit_at(u);
-      const bool some = steps_of(t) > 0;
-      if (!some && p.accumulate) continue;
-      if (some) {
-        if (!wait_all(smem_u32(&tfull[acc]), aph, 2500 + acc)) break;
-        tc_fence_after();
-      }
-      const int m0 = t.m0 + rank * kBlkM + q * 32, left = (DW ? p.K : t.count) - m0;  // rows of this warp
-      const int64_t row = DW ? (int64_t)t.e * p.K + m0 : (int64_t)t.row0 + m0;
-      const int nend = min(kBlkN, p.N - t.n0);
-      for (int c0 = 32 * ((warp - 2) >> 2); c0 < nend && left > 0; c0 += 64) {
-        float v[32];
-        if (some) {
-          tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kBlkN + c0), v);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0.f;
-        }
-        uint8_t* dst = out + ((row + lane) * p.ldo + t.n0 + c0) * osz;
-        if (rows16 && c0 + 32 <= nend) {
-          if (lane < left) {
-            if (osz == 4) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                float4* d4 = reinterpret_cast<float4*>(dst) + i;
-                float4 w = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                if (DW && p.accumulate) {
-                  const float4 o = *d4;
-                  w.x += o.x;
-                  w.y += o.y;
-                  w.z += o.z;
-                  w.w += o.w;
-                }
-                *d4 = w;
-              }
-            } else {
-              const bool bf = p.odt == MOE_DT_BF16;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint4* d4 = reinterpret_cast<uint4*>(dst) + i;
-                uint32_t w[4];
-                if (DW && p.accumulate) {
-                  const uint4 o = *d4;
-                  w[0] = o.x;
-                  w[1] = o.y;
-                  w[2] = o.z;
-                  w[3] = o.w;
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  F2 r(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
-                  if (DW && p.accumulate) r = add2(r, bf ? pair_f32<__nv_bfloat16>(w + j) : pair_f32<__half>(w + j));
-                  if (bf) pair_to<__nv_bfloat16>(w + j, r);
-                  else pair_to<__half>(w + j, r);
-                }
-                *d4 = make_uint4(w[0], w[1], w[2], w[3]);
-              }
-            }
-          }
-        } else {
-#pragma unroll
-          for (int h = 0; h < 32; h += 16) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              asm volatile("st.shared.f32 [%0], %1;" ::"r"(stg + (uint32_t)(lane * kStageRow + i) * 4u), "f"(v[h + i]) : "memory");
-            __syncwarp();
-            const int col = lane & 15;
-#pragma unroll 4
-            for (int i = 0; i < 16; ++i) {
-              const int r = 2 * i + (lane >> 4);
-              float x;
-              asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(stg + (uint32_t)(r * kStageRow + col) * 4u));
-              if (r < left && c0 + h + col < nend) {
-                const int64_t at = (row + r) * p.ldo + t.n0 + c0 + h + col;
-                if (osz == 4) {
-                  float* f = reinterpret_cast<float*>(out) + at;
-                  *f = DW && p.accumulate ? x + *f : x;
-                } else if (p.odt == MOE_DT_BF16) {
-                  __nv_bfloat16* f = reinterpret_cast<__nv_bfloat16*>(out) + at;
-                  *f = from_f32<__nv_bfloat16>(DW && p.accumulate ? x + to_f32(*f) : x);
-                } else {
-                  __half* f = reinterpret_cast<__half*>(out) + at;
-                  *f = from_f32<__half>(DW && p.accumulate ? x + to_f32(*f) : x);
-                }
-              }
-            }
-            __syncwarp();
-          }
-        }
-      }
-      if (!some) continue;
+    auto done = [&]() {  // this accumulator may be filled again
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -534,7 +493,69 @@ __global__ void __launch_bounds__(64 + 32 * (kEpiWarpsP + (MODE == TC_LOAD ? kLo
         acc = 0;
         aph ^= 1u;
       }
+    };
+    for (int u = unit0; u < total; u += unit_step) {
+      const TcUnit t = unit_at(u);
+      const int steps = steps_of(t);
+      if (steps == 0 && p.accumulate) continue;
+      const int n = t.n0 + rank * kBlkM + q * 32 + lane;
+      const int64_t row = (DW ? (int64_t)t.e * p.K : (int64_t)t.row0) + t.r0;
+      const bool add = DW && p.accumulate;
+      // 32 rows from c0 on
+      auto store = [&](int c0, const float (&v)[32]) {
+        if (n >= p.N) return;
+        const int64_t at = (row + c0) * p.ldo + n;
+        const int rows = t.nt - c0;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          if (j < rows) {
+            if constexpr (F32) put<float>(p.out, at + j * p.ldo, v[j], add);
+            else if (p.odt == MOE_DT_BF16) put<__nv_bfloat16>(p.out, at + j * p.ldo, v[j], add);
+            else put<__half>(p.out, at + j * p.ldo, v[j], add);
+          }
+        }
+      };
+      if constexpr (F32) {
+        constexpr int kParts = kTileRows / 64;
+        float sum[kParts][32];
+#pragma unroll
+        for (int i = 0; i < kParts; ++i)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) sum[i][j] = 0.f;
+        for (int k = 0; k < steps; k += kSumSteps) {
+          if (!wait_all(smem_u32(&tfull[acc]), aph, 2500 + acc)) goto stored;
+          tc_fence_after();
+#pragma unroll
+          for (int i = 0; i < kParts; ++i) {
+            if (32 * half + 64 * i < t.nt) {
+              float v[32];
+              tmem_ld32(tq + (uint32_t)(acc * kAccCols + 64 * i), v);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) sum[i][j] += v[j];
+            }
+          }
+          done();
+        }
+#pragma unroll
+        for (int i = 0; i < kParts; ++i)
+          if (32 * half + 64 * i < t.nt) store(32 * half + 64 * i, sum[i]);
+      } else if (steps == 0) {
+        float v[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = 0.f;
+        for (int c0 = 32 * half; c0 < t.nt; c0 += 64) store(c0, v);
+      } else {
+        if (!wait_all(smem_u32(&tfull[acc]), aph, 2500 + acc)) goto stored;
+        tc_fence_after();
+        for (int c0 = 32 * half; c0 < t.nt; c0 += 64) {
+          float v[32];
+          tmem_ld32(tq + (uint32_t)(acc * kAccCols + c0 - 32 * half), v);
+          store(c0, v);
+        }
+        done();
+      }
     }
+  stored:;
   }
   ops_let_next();
   tc_fence_before();
@@ -564,14 +585,18 @@ bool tc_map(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <ProdForm FORM, TcMode MODE>
+template <ProdForm FORM, TcMode MODE, bool F32>
 cudaError_t launch_tc(const CUtensorMap* tm, const ProdArgs& p, uint32_t formats, cudaStream_t st) {
-  auto kern = tc_product_kernel<FORM, MODE>;
+  auto kern = tc_product_kernel<FORM, MODE, F32>;
   static SmemAllowed allowed;
   const cudaError_t e = allow_smem(kern, kSmemP, allowed);
   if (e != cudaSuccess) return e;
   const char* name = FORM == PROD_DW ? "grouped_product_dw" : "grouped_product";
-  const int64_t units = most_units(FORM, p, MODE == TC_PAIR ? 2 * kBlkM : kBlkM, kBlkN);
+  // units at most
+  constexpr int kTileRows = tile_most(MODE, F32), cols = MODE == TC_PAIR ? 2 * kBlkM : kBlkM;
+  const int64_t tiles = FORM == PROD_DW ? (int64_t)((p.K + kTileRows - 1) / kTileRows) * p.G
+                                        : (int64_t)p.rows / kTileRows + (p.G < p.rows ? p.G : p.rows);
+  const int64_t units = tiles * ((p.N + cols - 1) / cols);
   const dim3 block(64 + 32 * (kEpiWarpsP + (MODE == TC_LOAD ? kLoadWarps : 0)));
   if constexpr (MODE != TC_PAIR) {
     const int grid = units < num_sms() ? (int)units : num_sms();
@@ -599,7 +624,7 @@ cudaError_t launch_tc(const CUtensorMap* tm, const ProdArgs& p, uint32_t formats
   }
 }
 
-template <ProdForm FORM>
+template <ProdForm FORM, bool F32>
 cudaError_t launch_form(int dtype, const ProdArgs& p, cudaStream_t st) {
   const uint32_t fmt = dtype == MOE_DT_BF16 ? 1u : 0u, formats = (fmt << 7) | (fmt << 10);
   // tensor copies: every row starts on 16 bytes (and there are rows)
@@ -607,29 +632,31 @@ cudaError_t launch_form(int dtype, const ProdArgs& p, cudaStream_t st) {
   CUtensorMap tm[3];
   if (!copy) {
     memset(tm, 0, sizeof(tm));
-    return launch_tc<FORM, TC_LOAD>(tm, p, formats, st);
+    return launch_tc<FORM, TC_LOAD, F32>(tm, p, formats, st);
   }
-  const bool pair = FORM != PROD_DW && p.rows >= 128 * (int64_t)p.G;
+  const bool pair = p.N > kBlkM && p.rows >= 64 * (int64_t)p.G;
   const uint64_t R = (uint64_t)p.rows, K = (uint64_t)p.K, N = (uint64_t)p.N, G = (uint64_t)p.G;
   bool ok;
   if (FORM == PROD_DW) {
-    ok = tc_map(&tm[0], p.a, K, R, p.lda, 0, 0, 64, 64) && tc_map(&tm[2], p.b, N, R, p.ldb, 0, 0, 64, 64);
-    tm[1] = tm[0];
+    ok = tc_map(&tm[0], p.b, N, R, p.ldb, 0, 0, 64, 64) && tc_map(&tm[1], p.a, K, R, p.lda, 0, 0, 64, 64);
+    tm[2] = tm[1];
   } else {
-    ok = tc_map(&tm[0], p.a, K, R, p.lda, 0, 0, 64, 32) && tc_map(&tm[1], p.a, K, R, p.lda, 0, 0, 64, 128) &&
-         (FORM == PROD_ROWS ? tc_map(&tm[2], p.b, N, K, N, G, K * N, 64, 64) : tc_map(&tm[2], p.b, K, N, K, G, K * N, 64, 64));
+    ok = (FORM == PROD_ROWS ? tc_map(&tm[0], p.b, N, K, N, G, K * N, 64, 64) : tc_map(&tm[0], p.b, K, N, K, G, K * N, 64, 128)) &&
+         tc_map(&tm[1], p.a, K, R, p.lda, 0, 0, 64, 32) && tc_map(&tm[2], p.a, K, R, p.lda, 0, 0, 64, 128);
   }
   if (!ok) return cudaErrorInvalidValue;
-  return pair ? launch_tc<FORM, TC_PAIR>(tm, p, formats, st) : launch_tc<FORM, TC_COPY>(tm, p, formats, st);
+  return pair ? launch_tc<FORM, TC_PAIR, F32>(tm, p, formats, st) : launch_tc<FORM, TC_COPY, F32>(tm, p, formats, st);
 }
 
 }  // namespace
 
 cudaError_t launch_product_tc(ProdForm form, int dtype, const ProdArgs& p, cudaStream_t st) {
+  const bool f32 = p.odt == MOE_DT_F32;
   switch (form) {
-    case PROD_ROWS: return launch_form<PROD_ROWS>(dtype, p, st);
-    case PROD_ROWS_T: return launch_form<PROD_ROWS_T>(dtype, p, st);
-    default: return launch_form<PROD_DW>(dtype, p, st);
+    case PROD_ROWS: return f32 ? launch_form<PROD_ROWS, true>(dtype, p, st) : launch_form<PROD_ROWS, false>(dtype, p, st);
+    case PROD_ROWS_T:
+      return f32 ? launch_form<PROD_ROWS_T, true>(dtype, p, st) : launch_form<PROD_ROWS_T, false>(dtype, p, st);
+    default: return f32 ? launch_form<PROD_DW, true>(dtype, p, st) : launch_form<PROD_DW, false>(dtype, p, st);
   }
 }
 

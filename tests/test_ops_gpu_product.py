@@ -122,6 +122,13 @@ def test_many_experts(dt):
     run_all(dt, dt, counts, 24, 40)
 
 
+@pytest.mark.parametrize("odt", ["bf16", "f32"])
+@pytest.mark.parametrize("counts,K,N", [([1000, 40, 24], 16, 40_000), ([500, 7, 0, 9], 264, 10_000)])
+def test_many_units_of_one_stage(odt, counts, K, N):
+    """Contractions that end inside their only stage, several units of them under way in a block."""
+    run_all("bf16", odt, counts, K, N)
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f16"])
 def test_one_segment_and_long_contractions(dt):
     """offsets None, K long; and one expert's many rows into its weights' gradient."""
