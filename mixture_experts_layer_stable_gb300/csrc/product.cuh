@@ -25,20 +25,21 @@ struct ProdArgs {
 // Rows and units of each expert, numbered by the block: s_off [G + 1] first rows, s_unit
 // [G + 1] first units; an expert has `per` units for each tile of up to `tile` rows, or
 // `per` whatever its rows (tile 0).  (Offsets out of order or range give wrong rows, not
-// accesses out of range.)  Returns the rows of the expert with the most in the first
-// warp; ends with a barrier.
-__device__ __forceinline__ int number_units(const ProdArgs& p, int tile, int per, int* s_off, int* s_unit) {
-  int most = 0;
+// accesses out of range.)  Returns, in the first warp, the rows of the expert with the
+// most and the average of those that have some; ends with a barrier.
+__device__ __forceinline__ int2 number_units(const ProdArgs& p, int tile, int per, int* s_off, int* s_unit) {
+  int most = 0, average = 0;
   for (int i = threadIdx.x; i <= p.G; i += blockDim.x)
     s_off[i] = p.off ? min(max(gload(p.off + i), 0), p.rows) : (i ? p.rows : 0);
   __syncthreads();
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
-    int run = 0;
+    int run = 0, with = 0;
     for (int base = 0; base < p.G; base += 32) {
       const int e = base + lane;
       const int c = e < p.G ? max(0, s_off[e + 1] - s_off[e]) : 0;
       most = max(most, c);
+      with += __popc(__ballot_sync(0xffffffffu, c > 0));
       const int mine = e < p.G ? (tile ? (c + tile - 1) / tile * per : per) : 0;
       int inc = mine;
 #pragma unroll
@@ -51,9 +52,10 @@ __device__ __forceinline__ int number_units(const ProdArgs& p, int tile, int per
     }
     if (lane == 0) s_unit[p.G] = run;
     most = __reduce_max_sync(0xffffffffu, most);
+    average = with ? max(0, s_off[p.G] - s_off[0]) / with : 0;
   }
   __syncthreads();
-  return most;
+  return make_int2(most, average);
 }
 
 // Expert of unit u: e with s_unit[e] <= u < s_unit[e + 1]; `at` is a first guess.

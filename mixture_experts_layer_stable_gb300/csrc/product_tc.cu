@@ -26,9 +26,12 @@
 // even CTA's barriers count both CTAs' copies, its one thread issues for both, and its
 // commits arrive in both.
 //
-// Order.  Units are numbered expert by expert, and a CTA's k-th unit is taken from the
-// front and the back of that order in turns, so that experts with many rows (bound by the
-// tensor cores) run beside experts with few (bound by their weights' way from HBM).
+// Order.  Units are numbered expert by expert, so that those that share operands run side
+// by side.  Where experts' rows differ much they are taken from the front and the back of
+// that order in turns: experts with many rows (bound by the tensor cores) then run beside
+// experts with few (bound by their weights' way from HBM).  32768 rows skewed over 256
+// experts, 7168 x 4096: 1815 us, 1985 in one order; 16384 rows of four experts, where two
+// experts' operands at a time do not fit into L2: 543 us in turns, 512 in one order.
 //
 // Ragged edges.  Rows behind an expert's last are other experts': they fill accumulator
 // columns that are not stored.  The contraction over an expert's rows (the weights'
@@ -37,9 +40,10 @@
 // first (one of them would not do: what lies there may be NaN).
 //
 // Sums.  The tensor cores add to their fp32 accumulators by truncation, which a long
-// contraction shows in results of 32 bits (4096 rows into a weight gradient: 1e-5 of it).
-// For those an accumulator takes 256 of the contraction and the epilogue adds the
-// accumulators up in registers, rounding to nearest.
+// contraction shows in results of 32 bits (4e-6 of a weight gradient of 4096 rows).  For
+// those an accumulator takes 512 of the contraction and the epilogue adds the accumulators
+// up in registers, rounding to nearest (5e-7; 598 us instead of 580 for 16384 rows of four
+// experts into 7168 x 4096; with 256 of the contraction 2.4e-7 and 780 us).
 #include "gemm_common.cuh"
 #include "product.cuh"
 #include "tc_roles.cuh"
@@ -51,15 +55,16 @@ namespace {
 enum TcMode { TC_COPY, TC_PAIR, TC_LOAD };  // tensor copies, the same by CTA pairs, plain loads
 
 constexpr int kBlkM = 128, kAccCols = 256, kBlkK = 64;
-constexpr int kEpiWarpsP = 8;   // two for each quarter of the TMEM lanes
+constexpr int kEpi = 8;        // warps of the epilogue, two for each quarter of the TMEM lanes
 constexpr int kLoadWarps = 8;   // of TC_LOAD
 constexpr int kABytes = kBlkM * kBlkK * 2;
 constexpr int kBoxBytes = 64 * 128;  // 64 rows of 64 elements
 constexpr int kStagesP = 12;         // at most
 constexpr int kTablesP = 8704;       // static shared memory: the experts' rows and units, barriers
 constexpr int kSmemP = 232448 - kTablesP;
-constexpr int kSumSteps = 4;         // stages that a 32-bit result's accumulator takes
+constexpr int kSumSteps = 8;         // stages that a 32-bit result's accumulator takes
 
+constexpr int threads_of(TcMode mode) { return 64 + 32 * (kEpi + (mode == TC_LOAD ? kLoadWarps : 0)); }
 // Output rows of a tile at most.  (With loading warps an SM's registers hold the sums of
 // half as many.)
 constexpr int tile_most(TcMode mode, bool f32) { return mode == TC_LOAD && f32 ? 128 : 256; }
@@ -123,11 +128,29 @@ MOE_DEV void load_two(const uint16_t* p, int i, int n, uint32_t& lo, uint32_t& h
   }
 }
 
-// One result, or its sum with what is there.
-template <typename T>
-MOE_DEV void put(void* out, int64_t at, float v, bool add) {
-  T* q = static_cast<T*>(out) + at;
-  *q = from_f32<T>(add ? v + to_f32(*q) : v);
+// 32 results of a column to rows q, q + ld, ..., of which `rows` exist; ADD: their sums with
+// what is there.
+template <typename T, bool ADD>
+MOE_DEV void put_rows(T* q, int64_t ld, int rows, const float (&v)[32]) {
+  if (rows >= 32) {
+    float old[ADD ? 32 : 1];
+    if constexpr (ADD) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) old[j] = to_f32(q[j * ld]);
+    }
+#pragma unroll
+    for (int j = 0; j < 32; ++j, q += ld) *q = from_f32<T>(ADD ? v[j] + old[ADD ? j : 0] : v[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j, q += ld)
+      if (j < rows) *q = from_f32<T>(ADD ? v[j] + to_f32(*q) : v[j]);
+  }
+}
+template <typename T, bool DW>
+MOE_DEV void put_tile(const ProdArgs& p, int64_t at, int rows, const float (&v)[32]) {
+  T* q = static_cast<T*>(p.out) + at;
+  if (DW && p.accumulate) put_rows<T, DW>(q, p.ldo, rows, v);
+  else put_rows<T, false>(q, p.ldo, rows, v);
 }
 
 struct TcUnit {
@@ -138,7 +161,7 @@ struct TcUnit {
 
 // F32: results of 32 bits.
 template <ProdForm FORM, TcMode MODE, bool F32>
-__global__ void __launch_bounds__(64 + 32 * (kEpiWarpsP + (MODE == TC_LOAD ? kLoadWarps : 0)), 1)
+__global__ void __launch_bounds__(threads_of(MODE), 1)
     tc_product_kernel(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ CUtensorMap tm_n,
                       const __grid_constant__ CUtensorMap tm_n128, const ProdArgs p, const uint32_t formats) {
   constexpr bool PAIR = MODE == TC_PAIR, DW = FORM == PROD_DW;
@@ -152,7 +175,7 @@ __global__ void __launch_bounds__(64 + 32 * (kEpiWarpsP + (MODE == TC_LOAD ? kLo
   __shared__ int s_off[kMaxG + 1], s_unit[kMaxG + 1];
   __shared__ alignas(8) uint64_t full[kStagesP], empty[kStagesP], ready[kStagesP], tfull[2], tempty[2], drain;
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort, s_most;
+  __shared__ int s_abort, s_most, s_turns;
   if (warp == 0 && lane == 0) {
     for (int i = 0; i < kStagesP; ++i) {
       mbar_init(&full[i], MODE == TC_LOAD ? kLoadWarps : 1);
@@ -161,7 +184,7 @@ __global__ void __launch_bounds__(64 + 32 * (kEpiWarpsP + (MODE == TC_LOAD ? kLo
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull[i], 1);
-      mbar_init(&tempty[i], (PAIR ? 2 : 1) * kEpiWarpsP);
+      mbar_init(&tempty[i], (PAIR ? 2 : 1) * kEpi);
     }
     mbar_init(&drain, 1);
     s_abort = 0;
@@ -184,14 +207,17 @@ __global__ void __launch_bounds__(64 + 32 * (kEpiWarpsP + (MODE == TC_LOAD ? kLo
   ops_wait();
   if (blockIdx.x == 0 && threadIdx.x < 2) p.status[threadIdx.x] = 0;
   const int col_tiles = (p.N + kCols - 1) / kCols, dw_tiles = (p.K + kTileRows - 1) / kTileRows;
-  const int most = number_units(p, DW ? 0 : kTileRows, DW ? dw_tiles * col_tiles : col_tiles, s_off, s_unit);
-  if (threadIdx.x == 0) s_most = DW ? p.K : most;
+  const int2 most = number_units(p, DW ? 0 : kTileRows, DW ? dw_tiles * col_tiles : col_tiles, s_off, s_unit);
+  // in turns: an expert has four times the average of those that have rows
+  if (threadIdx.x == 0) s_most = DW ? p.K : most.x;
+  if (threadIdx.x == 0) s_turns = most.x > 4 * most.y;
   tc_fence_before();
   __syncthreads();
   if constexpr (PAIR) cluster_sync();  // the other CTA's barriers exist before their use
   tc_fence_after();
   const uint32_t tmem = (uint32_t)uniform((int)s_tmem);
   const int total = uniform(s_unit[p.G]);
+  const bool turns = uniform(s_turns) != 0;
   volatile int* abort_flag = &s_abort;
   const int rank = PAIR ? uniform((int)cluster_ctarank()) : 0;
   const int unit0 = PAIR ? blockIdx.x / 2 : blockIdx.x, unit_step = PAIR ? gridDim.x / 2 : gridDim.x;
@@ -210,7 +236,7 @@ __global__ void __launch_bounds__(64 + 32 * (kEpiWarpsP + (MODE == TC_LOAD ? kLo
   // The L-th unit in the order they are taken; each role keeps its place in the experts.
   int at_e = 0;
   auto unit_at = [&](int L) {
-    const int u = L & 1 ? total - 1 - (L >> 1) : L >> 1;
+    const int u = !turns ? L : L & 1 ? total - 1 - (L >> 1) : L >> 1;
     at_e = uniform(expert_of(s_unit, p.G, u, at_e));
     TcUnit t;
     t.e = at_e;
@@ -398,9 +424,9 @@ __global__ void __launch_bounds__(64 + 32 * (kEpiWarpsP + (MODE == TC_LOAD ? kLo
       }
       if (++s == S) s = 0;
     }
-  } else if (MODE == TC_LOAD && warp >= 2 + kEpiWarpsP) {
+  } else if (MODE == TC_LOAD && warp >= 2 + kEpi) {
     // Rows of 64 elements, a lane two of each.  Eight rows of loads are under way in a warp.
-    const int w = warp - 2 - kEpiWarpsP;
+    const int w = warp - 2 - kEpi;
     int s = 0;
     uint32_t ph = 0;
     const uint16_t *A = static_cast<const uint16_t*>(p.a), *B = static_cast<const uint16_t*>(p.b);
@@ -475,11 +501,13 @@ __global__ void __launch_bounds__(64 + 32 * (kEpiWarpsP + (MODE == TC_LOAD ? kLo
       }
     }
   loaded:;
-  } else if (warp > 1 && warp < 2 + kEpiWarpsP) {
-    // A lane holds an output column; a warp takes every other 32 rows of its quarter's 32
-    // columns.
-    const int q = warp & 3, half = (warp - 2) >> 2;
-    const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16) + 32u * half;
+  } else if (warp > 1 && warp < 2 + kEpi) {
+    // A lane holds an output column; a warp takes 32 rows in kStep of its quarter's 32 columns.
+    // (Sixteen warps, half of the sums each, are slower: 16384 rows of four experts into
+    // 7168 x 4096 711 us, not 653.)
+    constexpr int kStep = 8 * kEpi;
+    const int q = warp & 3, c_first = 32 * ((warp - 2) >> 2);
+    const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16);
     int acc = 0;
     uint32_t aph = 0;
     auto done = [&]() {  // this accumulator may be filled again
@@ -500,23 +528,16 @@ __global__ void __launch_bounds__(64 + 32 * (kEpiWarpsP + (MODE == TC_LOAD ? kLo
       if (steps == 0 && p.accumulate) continue;
       const int n = t.n0 + rank * kBlkM + q * 32 + lane;
       const int64_t row = (DW ? (int64_t)t.e * p.K : (int64_t)t.row0) + t.r0;
-      const bool add = DW && p.accumulate;
       // 32 rows from c0 on
       auto store = [&](int c0, const float (&v)[32]) {
         if (n >= p.N) return;
         const int64_t at = (row + c0) * p.ldo + n;
-        const int rows = t.nt - c0;
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          if (j < rows) {
-            if constexpr (F32) put<float>(p.out, at + j * p.ldo, v[j], add);
-            else if (p.odt == MOE_DT_BF16) put<__nv_bfloat16>(p.out, at + j * p.ldo, v[j], add);
-            else put<__half>(p.out, at + j * p.ldo, v[j], add);
-          }
-        }
+        if constexpr (F32) put_tile<float, DW>(p, at, t.nt - c0, v);
+        else if (p.odt == MOE_DT_BF16) put_tile<__nv_bfloat16, DW>(p, at, t.nt - c0, v);
+        else put_tile<__half, DW>(p, at, t.nt - c0, v);
       };
       if constexpr (F32) {
-        constexpr int kParts = kTileRows / 64;
+        constexpr int kParts = kTileRows / kStep;
         float sum[kParts][32];
 #pragma unroll
         for (int i = 0; i < kParts; ++i)
@@ -527,9 +548,9 @@ __global__ void __launch_bounds__(64 + 32 * (kEpiWarpsP + (MODE == TC_LOAD ? kLo
           tc_fence_after();
 #pragma unroll
           for (int i = 0; i < kParts; ++i) {
-            if (32 * half + 64 * i < t.nt) {
+            if (c_first + kStep * i < t.nt) {
               float v[32];
-              tmem_ld32(tq + (uint32_t)(acc * kAccCols + 64 * i), v);
+              tmem_ld32(tq + (uint32_t)(acc * kAccCols + c_first + kStep * i), v);
 #pragma unroll
               for (int j = 0; j < 32; ++j) sum[i][j] += v[j];
             }
@@ -538,18 +559,18 @@ __global__ void __launch_bounds__(64 + 32 * (kEpiWarpsP + (MODE == TC_LOAD ? kLo
         }
 #pragma unroll
         for (int i = 0; i < kParts; ++i)
-          if (32 * half + 64 * i < t.nt) store(32 * half + 64 * i, sum[i]);
+          if (c_first + kStep * i < t.nt) store(c_first + kStep * i, sum[i]);
       } else if (steps == 0) {
         float v[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = 0.f;
-        for (int c0 = 32 * half; c0 < t.nt; c0 += 64) store(c0, v);
+        for (int c0 = c_first; c0 < t.nt; c0 += kStep) store(c0, v);
       } else {
         if (!wait_all(smem_u32(&tfull[acc]), aph, 2500 + acc)) goto stored;
         tc_fence_after();
-        for (int c0 = 32 * half; c0 < t.nt; c0 += 64) {
+        for (int c0 = c_first; c0 < t.nt; c0 += kStep) {
           float v[32];
-          tmem_ld32(tq + (uint32_t)(acc * kAccCols + c0 - 32 * half), v);
+          tmem_ld32(tq + (uint32_t)(acc * kAccCols + c0), v);
           store(c0, v);
         }
         done();
@@ -597,7 +618,7 @@ cudaError_t launch_tc(const CUtensorMap* tm, const ProdArgs& p, uint32_t formats
   const int64_t tiles = FORM == PROD_DW ? (int64_t)((p.K + kTileRows - 1) / kTileRows) * p.G
                                         : (int64_t)p.rows / kTileRows + (p.G < p.rows ? p.G : p.rows);
   const int64_t units = tiles * ((p.N + cols - 1) / cols);
-  const dim3 block(64 + 32 * (kEpiWarpsP + (MODE == TC_LOAD ? kLoadWarps : 0)));
+  const dim3 block(threads_of(MODE));
   if constexpr (MODE != TC_PAIR) {
     const int grid = units < num_sms() ? (int)units : num_sms();
     return launch_ops(name, kern, dim3(grid), block, kSmemP, st, tm[0], tm[1], tm[2], p, formats);
