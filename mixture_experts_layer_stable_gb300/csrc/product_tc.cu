@@ -1,7 +1,7 @@
 // product_tc.cu -- the experts' products of 16-bit operands on the tensor cores
 // (tcgen05 kind::f16; product.cu has the formulas and the calls).
 //
-// Warp-specialised and persistent, one CTA per SM: warp 0 issues the copies (or eight
+// Warp-specialised and persistent, one CTA per SM: warp 0 issues the copies (or sixteen
 // more warps load the operands themselves), one thread of warp 1 the tensor-core
 // instructions, warps 2..9 the epilogue.
 //
@@ -44,6 +44,8 @@
 // those an accumulator takes 512 of the contraction and the epilogue adds the accumulators
 // up in registers, rounding to nearest (5e-7; 598 us instead of 580 for 16384 rows of four
 // experts into 7168 x 4096; with 256 of the contraction 2.4e-7 and 780 us).
+#include <limits.h>
+
 #include "gemm_common.cuh"
 #include "product.cuh"
 #include "tc_roles.cuh"
@@ -56,7 +58,7 @@ enum TcMode { TC_COPY, TC_PAIR, TC_LOAD };  // tensor copies, the same by CTA pa
 
 constexpr int kBlkM = 128, kAccCols = 256, kBlkK = 64;
 constexpr int kEpi = 8;        // warps of the epilogue, two for each quarter of the TMEM lanes
-constexpr int kLoadWarps = 8;   // of TC_LOAD
+constexpr int kLoadWarps = 16;  // of TC_LOAD
 constexpr int kABytes = kBlkM * kBlkK * 2;
 constexpr int kBoxBytes = 64 * 128;  // 64 rows of 64 elements
 constexpr int kStagesP = 12;         // at most
@@ -425,37 +427,70 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
       if (++s == S) s = 0;
     }
   } else if (MODE == TC_LOAD && warp >= 2 + kEpi) {
-    // Rows of 64 elements, a lane two of each.  Eight rows of loads are under way in a warp.
+    // Rows of 64 elements, a lane two of each, a warp every 16th row: all of a warp's rows
+    // then lie alike to the swizzle, and their addresses are constant steps apart.  Eight
+    // rows of loads are under way in a warp.
+    constexpr int W = kLoadWarps;
+    static_assert(W % 8 == 0 && 64 % W == 0, "a warp's rows have one swizzle, and blocks whole numbers of them");
     const int w = warp - 2 - kEpi;
     int s = 0;
     uint32_t ph = 0;
     const uint16_t *A = static_cast<const uint16_t*>(p.a), *B = static_cast<const uint16_t*>(p.b);
-    // n rows of shared memory from `to`: row r is as many elements at src as row_at(r, src) says
-    auto fill = [&](uint32_t to, int n, auto word, auto row_at) {
-      constexpr int U = 8;
-      for (int r0 = w; r0 < n; r0 += kLoadWarps * U) {
-        uint32_t lo[U], hi[U];
+    const uint32_t lane_at = (uint32_t)(w * 128 + (((lane >> 2) ^ (w & 7)) << 4) + (lane & 3) * 4);
+    auto put_word = [&](uint32_t at, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(v) : "memory"); };
+    // Eight rows j of a warp, row j from src_of(j) to at_of(j); have_of(j): its elements
+    // (<= 0: zeros).  full: all have 64.
+    auto eight = [&](bool full, auto word, auto src_of, auto at_of, auto have_of) {
+      constexpr bool WORD = decltype(word)::value;
+      uint32_t lo[8], hi[8];
+      if (full) {
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-          const int r = r0 + i * kLoadWarps;
-          const uint16_t* src = A;
-          const int have = r < n ? row_at(r, src) : 0;
-          load_two<decltype(word)::value>(src, 2 * lane, have, lo[i], hi[i]);
+        for (int j = 0; j < 8; ++j) {
+          const uint16_t* q = src_of(j) + 2 * lane;
+          if constexpr (WORD) {
+            lo[j] = gload(reinterpret_cast<const uint32_t*>(q));
+          } else {
+            lo[j] = gload(q);
+            hi[j] = gload(q + 1);
+          }
         }
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-          const int r = r0 + i * kLoadWarps;
-          const uint32_t v = decltype(word)::value ? lo[i] | hi[i] : lo[i] | hi[i] << 16;
-          if (r < n)
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + (uint32_t)(r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4)),
-                         "r"(v)
-                         : "memory");
-        }
+        for (int j = 0; j < 8; ++j) put_word(at_of(j), WORD ? lo[j] : __byte_perm(lo[j], hi[j], 0x5410));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) load_two<WORD>(src_of(j), 2 * lane, have_of(j), lo[j], hi[j]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (have_of(j) > INT_MIN) put_word(at_of(j), WORD ? lo[j] | hi[j] : __byte_perm(lo[j], hi[j], 0x5410));
       }
     };
-    auto fill_any = [&](uint32_t to, int n, bool words, auto row_at) {
-      if (words) fill(to, n, std::true_type(), row_at);
-      else fill(to, n, std::false_type(), row_at);
+    // n rows, row r at src + r * ld, of `have` elements each.
+    auto fill_rows = [&](uint32_t to, const uint16_t* src, int64_t ld, int n, int have, bool words) {
+      const uint16_t* q = src + w * ld;
+      for (int r0 = w; r0 < n; r0 += 8 * W, q += 8 * W * ld, to += 8 * W * 128) {
+        const bool full = have >= 64 && r0 + 7 * W < n;
+        auto src_of = [&](int j) { return q + j * (W * ld); };
+        auto at_of = [&](int j) { return to + lane_at + (uint32_t)(j * W * 128); };
+        auto have_of = [&](int j) { return r0 + j * W < n ? have : INT_MIN; };
+        if (words) eight(full, std::true_type(), src_of, at_of, have_of);
+        else eight(full, std::false_type(), src_of, at_of, have_of);
+      }
+    };
+    // Blocks of 64 columns x 64 rows: row r of block b at src + 64 b + r * ld; there are
+    // `cols` columns and `rows` rows, the rest is zeros.
+    auto fill_blocks = [&](uint32_t to, const uint16_t* src, int64_t ld, int blocks, int cols, int rows, bool words) {
+      constexpr int kEach = 64 / W, kTwo = 8 / kEach;  // a warp's rows of a block; blocks at a time
+      const uint16_t* q = src + w * ld;
+      for (int b = 0; b < blocks; b += kTwo, q += 64 * kTwo, to += kTwo * kBoxBytes) {
+        const bool full = rows >= 64 && b + kTwo <= blocks && cols >= 64 * (b + kTwo);
+        auto src_of = [&](int j) { return q + j / kEach * 64 + (j % kEach) * (W * ld); };
+        auto at_of = [&](int j) { return to + lane_at + (uint32_t)(j / kEach * kBoxBytes + (j % kEach) * (W * 128)); };
+        auto have_of = [&](int j) {
+          return b + j / kEach >= blocks ? INT_MIN : w + (j % kEach) * W < rows ? cols - 64 * (b + j / kEach) : 0;
+        };
+        if (words) eight(full, std::true_type(), src_of, at_of, have_of);
+        else eight(full, std::false_type(), src_of, at_of, have_of);
+      }
     };
     const bool a_words = ((reinterpret_cast<uintptr_t>(A) | (uintptr_t)p.lda * 2) & 3) == 0;
     const bool b_words = ((reinterpret_cast<uintptr_t>(B) | (uintptr_t)p.ldb * 2 | (DW ? 0 : (uintptr_t)p.K * p.N * 2)) & 3) == 0;
@@ -467,30 +502,15 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
         if (!wait_all(empty0 + 8u * s, ph ^ 1u, 2000 + s)) goto loaded;
         const uint32_t sa = base + (uint32_t)s * stage_bytes, sb = sa + kABytes;
         const int k0 = kb * kBlkK;
-        // contraction along the row: row r of the operand, its elements from k0 on; else
-        // row r % 64 of the contraction, 64 columns from 64 * (r / 64) on
+        // what is contiguous along the contraction as rows, the rest as blocks
         if constexpr (M_MN)
-          fill_any(sa, kBlkM, b_words, [&](int r, const uint16_t*& src) {
-            const int k = k0 + (r & 63), c = t.n0 + (r & ~63);
-            src = we + (int64_t)k * p.ldb + c;
-            return k < kk ? p.N - c : 0;
-          });
+          fill_blocks(sa, we + (int64_t)k0 * p.ldb + t.n0, p.ldb, kBlkM / 64, p.N - t.n0, kk - k0, b_words);
         else
-          fill_any(sa, min(kBlkM, p.N - t.n0), b_words, [&](int r, const uint16_t*& src) {
-            src = we + (int64_t)(t.n0 + r) * p.ldb + k0;
-            return kk - k0;
-          });
+          fill_rows(sa, we + (int64_t)t.n0 * p.ldb + k0, p.ldb, min(kBlkM, p.N - t.n0), kk - k0, b_words);
         if constexpr (N_MN)
-          fill_any(sb, (t.nt + 63) & ~63, a_words, [&](int r, const uint16_t*& src) {
-            const int k = k0 + (r & 63), c = t.r0 + (r & ~63);
-            src = A + (int64_t)(t.row0 + k) * p.lda + c;
-            return k < kk ? p.K - c : 0;
-          });
+          fill_blocks(sb, A + (int64_t)(t.row0 + k0) * p.lda + t.r0, p.lda, (t.nt + 63) / 64, p.K - t.r0, kk - k0, a_words);
         else
-          fill_any(sb, t.nt, a_words, [&](int r, const uint16_t*& src) {
-            src = A + (int64_t)(t.row0 + t.r0 + r) * p.lda + k0;
-            return kk - k0;
-          });
+          fill_rows(sb, A + (int64_t)(t.row0 + t.r0) * p.lda + k0, p.lda, t.nt, kk - k0, a_words);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[s]);
