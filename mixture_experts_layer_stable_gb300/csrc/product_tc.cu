@@ -44,8 +44,6 @@
 // those an accumulator takes 512 of the contraction and the epilogue adds the accumulators
 // up in registers, rounding to nearest (5e-7; 598 us instead of 580 for 16384 rows of four
 // experts into 7168 x 4096; with 256 of the contraction 2.4e-7 and 780 us).
-#include <limits.h>
-
 #include "gemm_common.cuh"
 #include "product.cuh"
 #include "tc_roles.cuh"
@@ -64,6 +62,7 @@ constexpr int kBoxBytes = 64 * 128;  // 64 rows of 64 elements
 constexpr int kStagesP = 12;         // at most
 constexpr int kTablesP = 8704;       // static shared memory: the experts' rows and units, barriers
 constexpr int kSmemP = 232448 - kTablesP;
+constexpr int kRawRow = 144;         // TC_LOAD: 64 elements from anywhere in a 16-byte block
 constexpr int kSumSteps = 8;         // stages that a 32-bit result's accumulator takes
 
 constexpr int threads_of(TcMode mode) { return 64 + 32 * (kEpi + (mode == TC_LOAD ? kLoadWarps : 0)); }
@@ -107,27 +106,6 @@ MOE_DEV bool try_wait_cluster(uint32_t bar, uint32_t parity) {
       : "r"(bar), "r"(parity)
       : "memory");
   return ok != 0;
-}
-
-// Elements i and i + 1 of a row of n (may be negative), each 0 if it does not exist, to be
-// joined as lo | hi << 16.  WORD: the row starts with a 32-bit word and i is even; then as
-// lo | hi.
-template <bool WORD>
-MOE_DEV void load_two(const uint16_t* p, int i, int n, uint32_t& lo, uint32_t& hi) {
-  if constexpr (WORD) {
-    asm volatile(
-        "{\n\t.reg .pred l, h;\n\t"
-        "setp.ne.b32 l, %3, 0;\n\t"
-        "setp.ne.b32 h, %4, 0;\n\t"
-        "mov.b32 %0, 0;\n\t"
-        "mov.b32 %1, 0;\n\t"
-        "@h ld.global.u32 %0, [%2];\n\t"
-        "@l ld.global.u16 %1, [%2];\n\t}"
-        : "=&r"(lo), "=&r"(hi)
-        : "l"(p + i), "r"((int)(i + 1 == n)), "r"((int)(i + 1 < n)));
-  } else {
-    gload_pair(p + i, i < n, i + 1 < n, lo, hi);
-  }
 }
 
 // 32 results of a column to rows q, q + ld, ..., of which `rows` exist; ADD: their sums with
@@ -233,7 +211,9 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
   const int cap_n = (mine_of(cap) + kBoxRows - 1) / kBoxRows * kBoxRows;
   const uint32_t stage_bytes = (uint32_t)(kABytes + cap_n * 128);
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const int S = min(kStagesP, (int)((kSmemP - (base - smem_u32(smem_raw))) / stage_bytes));
+  // (loading warps: two stages' rows as they lie in memory, 144 bytes each, behind the ring)
+  const uint32_t raw_bytes = MODE == TC_LOAD ? 2u * (uint32_t)(kBlkM + cap_n) * kRawRow : 0u;
+  const int S = min(kStagesP, (int)((kSmemP - raw_bytes - (base - smem_u32(smem_raw))) / stage_bytes));
 
   // The L-th unit in the order they are taken; each role keeps its place in the experts.
   int at_e = 0;
@@ -427,100 +407,174 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
       if (++s == S) s = 0;
     }
   } else if (MODE == TC_LOAD && warp >= 2 + kEpi) {
-    // Rows of 64 elements, a lane two of each, a warp every 16th row: all of a warp's rows
-    // then lie alike to the swizzle, and their addresses are constant steps apart.  Eight
-    // rows of loads are under way in a warp.
-    constexpr int W = kLoadWarps;
-    static_assert(W % 8 == 0 && 64 % W == 0, "a warp's rows have one swizzle, and blocks whole numbers of them");
-    const int w = warp - 2 - kEpi;
-    int s = 0;
-    uint32_t ph = 0;
-    const uint16_t *A = static_cast<const uint16_t*>(p.a), *B = static_cast<const uint16_t*>(p.b);
-    const uint32_t lane_at = (uint32_t)(w * 128 + (((lane >> 2) ^ (w & 7)) << 4) + (lane & 3) * 4);
-    auto put_word = [&](uint32_t at, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(v) : "memory"); };
-    // Eight rows j of a warp, row j from src_of(j) to at_of(j); have_of(j): its elements
-    // (<= 0: zeros).  full: all have 64.
-    auto eight = [&](bool full, auto word, auto src_of, auto at_of, auto have_of) {
-      constexpr bool WORD = decltype(word)::value;
-      uint32_t lo[8], hi[8];
-      if (full) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint16_t* q = src_of(j) + 2 * lane;
-          if constexpr (WORD) {
-            lo[j] = gload(reinterpret_cast<const uint32_t*>(q));
-          } else {
-            lo[j] = gload(q);
-            hi[j] = gload(q + 1);
+    // The operands lie in rows of 64 elements (128 bytes) that start at any element.  Eight
+    // warps load the M side, eight the N side, each every eighth row: all of a warp's rows lie
+    // alike to 16 bytes and to the swizzle.  The 16-byte blocks that hold a row are copied to
+    // shared memory as they are (cp.async, the next stage's while one is worked on: loads into
+    // registers left a stage at the latency of two, 8192 rows of 16 experts, 2047 x 1535, 231
+    // us), and from there 16 bytes at a time go to the stage by shifts that are the same in all
+    // lanes.  (A stage that is not wholly inside the operand's array in such blocks is loaded
+    // element by element.)
+    const int w7 = (warp - 2 - kEpi) & 7, chunk = lane & 7;
+    auto run_side = [&](auto m_side) {
+      constexpr bool MS = decltype(m_side)::value, BLK = MS ? M_MN : N_MN;
+      const uint16_t* arr = static_cast<const uint16_t*>(MS ? p.b : p.a);
+      const int64_t ld = MS ? p.ldb : p.lda;
+      const uintptr_t lo = reinterpret_cast<uintptr_t>(arr);
+      const uintptr_t hi = reinterpret_cast<uintptr_t>(MS ? (DW ? arr + (int64_t)(p.rows - 1) * ld + p.N : arr + (int64_t)p.G * p.K * p.N)
+                                                          : arr + (int64_t)(p.rows - 1) * ld + p.K);
+      const int row = w7 + 8 * (lane >> 3);  // group i has row + 32 (i % 2) of block i / 2, or 64 (i / 2) rows on
+      const uint32_t off = (uint32_t)((lane >> 3) * 16 * ld + 16 * chunk), half = (uint32_t)(64 * ld);
+      const uint32_t apart = BLK ? 128u : (uint32_t)(128 * ld);
+      const uint32_t lane_dst = (MS ? 0u : (uint32_t)kABytes) + (uint32_t)(row * 128 + ((chunk ^ w7) << 4));
+      // the warp's rows as they lie in memory: group i's four at 4 i, two buffers
+      const uint32_t raw_size = (uint32_t)((MS ? kBlkM : cap_n) / 8 * kRawRow);
+      const uint32_t raw = base + (uint32_t)S * stage_bytes + (MS ? 0u : 2u * kBlkM * kRawRow) + 2u * raw_size * (uint32_t)w7;
+      const uint32_t raw_lane = (uint32_t)((lane >> 3) * kRawRow + 16 * chunk);
+      const bool near = ld < (1 << 22);  // a tile's offsets have 32 bits
+      auto copy16 = [](uint32_t to, const uint8_t* q) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(q) : "memory");
+      };
+      struct Stage {
+        const uint16_t* src;        // its row 0
+        int left, have, put, sh;    // of the contraction; rows or columns that exist, that are stored
+        bool fast;
+      };
+      // where the next stage is
+      int u = unit0, kb = 0, steps = 0;
+      Stage at = {};
+      bool more = true;
+      auto find_unit = [&]() {  // from unit u on, the first with a contraction
+        for (; u < total; u += unit_step) {
+          const TcUnit t = unit_at(u);
+          steps = steps_of(t);
+          if (steps == 0) continue;
+          at.left = DW ? t.count : p.K;
+          at.have = MS ? min(kBlkM, p.N - t.n0) : DW ? min((t.nt + 63) & ~63, p.K - t.r0) : t.nt;
+          at.put = MS ? kBlkM : DW ? (t.nt + 63) & ~63 : t.nt;
+          at.src = arr + (MS ? (DW ? t.row0 * ld : (int64_t)t.e * p.K * p.N) : t.row0 * ld);
+          at.src += MS ? (BLK ? (int64_t)t.n0 : t.n0 * ld) : BLK ? (int64_t)t.r0 : t.r0 * ld;
+          at.sh = (int)(reinterpret_cast<uintptr_t>(at.src + w7 * ld) & 15);
+          return;
+        }
+        more = false;
+      };
+      auto issue = [&](uint32_t to) {
+        const int len = min(at.left, kBlkK);
+        const int64_t span = BLK ? (len - 1) * ld + at.have : (at.have - 1) * ld + len;  // elements of the stage
+        const uintptr_t f = reinterpret_cast<uintptr_t>(at.src);
+        at.fast = near && (f & ~(uintptr_t)15) >= lo && ((f + 2 * span + 15) & ~(uintptr_t)15) <= hi;
+        if (at.fast) {
+          const uint8_t* q = reinterpret_cast<const uint8_t*>(at.src + w7 * ld) - at.sh;
+          // a row's blocks; those that hold none of the elements that exist are left out
+          const int rows = BLK ? len : at.have, bytes = 2 * (BLK ? at.have : len) + at.sh;
+          for (int i = 0; 32 * i < at.put; ++i) {
+            const int r = row + 32 * (i & 1) + (BLK ? 0 : 64 * (i >> 1)), b = BLK ? 128 * (i >> 1) : 0;
+            const uint8_t* e = q + (off + (i & 1) * half + (i >> 1) * apart);
+            if (r < rows && b + 16 * chunk < bytes) copy16(to + raw_lane + (uint32_t)(4 * i * kRawRow), e);
+            if (chunk == 7 && at.sh != 0 && r < rows && b + 128 < bytes) copy16(to + raw_lane + (uint32_t)(4 * i * kRawRow) + 16, e + 16);
           }
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        const Stage now = at;
+        at.src += BLK ? kBlkK * ld : kBlkK;
+        at.left -= kBlkK;
+        if (++kb == steps) {
+          kb = 0;
+          u += unit_step;
+          find_unit();
+        }
+        return now;
+      };
+      // 16 bytes of shared memory from byte 2 * halves of two blocks
+      auto shifted = [](auto halves, uint32_t from, uint32_t (&v)[4]) {
+        constexpr int H = decltype(halves)::value, W = H / 2;
+        constexpr uint32_t sel = H % 2 ? 0x5432 : 0x3210;
+        uint32_t w[8];
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(from));
+        if constexpr (H > 0)
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7]) : "r"(from + 16));
+        else
+          w[4] = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) put_word(at_of(j), WORD ? lo[j] : __byte_perm(lo[j], hi[j], 0x5410));
-      } else {
+        for (int k = 0; k < 4; ++k) v[k] = __byte_perm(w[W + k], w[W + k + 1], sel);
+      };
+      auto store = [&](const Stage& x, uint32_t from, uint32_t to) {
+        // (not unrolled further than its two rows' groups: the eight shifts' copies are long)
+        auto by = [&](auto halves) {
+#pragma unroll 2
+          for (int i = 0; 32 * i < x.put; ++i) {
+            const int r = row + 32 * (i & 1) + (BLK ? 0 : 64 * (i >> 1));
+            uint32_t v[4];
+            shifted(halves, from + raw_lane + (uint32_t)(4 * i * kRawRow), v);
+            if (x.left < kBlkK) {  // zeros past the end of the contraction
+              const int n = BLK ? (r < x.left ? 8 : 0) : x.left - 8 * chunk;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) load_two<WORD>(src_of(j), 2 * lane, have_of(j), lo[j], hi[j]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (have_of(j) > INT_MIN) put_word(at_of(j), WORD ? lo[j] | hi[j] : __byte_perm(lo[j], hi[j], 0x5410));
-      }
-    };
-    // n rows, row r at src + r * ld, of `have` elements each.
-    auto fill_rows = [&](uint32_t to, const uint16_t* src, int64_t ld, int n, int have, bool words) {
-      const uint16_t* q = src + w * ld;
-      for (int r0 = w; r0 < n; r0 += 8 * W, q += 8 * W * ld, to += 8 * W * 128) {
-        const bool full = have >= 64 && r0 + 7 * W < n;
-        auto src_of = [&](int j) { return q + j * (W * ld); };
-        auto at_of = [&](int j) { return to + lane_at + (uint32_t)(j * W * 128); };
-        auto have_of = [&](int j) { return r0 + j * W < n ? have : INT_MIN; };
-        if (words) eight(full, std::true_type(), src_of, at_of, have_of);
-        else eight(full, std::false_type(), src_of, at_of, have_of);
-      }
-    };
-    // Blocks of 64 columns x 64 rows: row r of block b at src + 64 b + r * ld; there are
-    // `cols` columns and `rows` rows, the rest is zeros.
-    auto fill_blocks = [&](uint32_t to, const uint16_t* src, int64_t ld, int blocks, int cols, int rows, bool words) {
-      constexpr int kEach = 64 / W, kTwo = 8 / kEach;  // a warp's rows of a block; blocks at a time
-      const uint16_t* q = src + w * ld;
-      for (int b = 0; b < blocks; b += kTwo, q += 64 * kTwo, to += kTwo * kBoxBytes) {
-        const bool full = rows >= 64 && b + kTwo <= blocks && cols >= 64 * (b + kTwo);
-        auto src_of = [&](int j) { return q + j / kEach * 64 + (j % kEach) * (W * ld); };
-        auto at_of = [&](int j) { return to + lane_at + (uint32_t)(j / kEach * kBoxBytes + (j % kEach) * (W * 128)); };
-        auto have_of = [&](int j) {
-          return b + j / kEach >= blocks ? INT_MIN : w + (j % kEach) * W < rows ? cols - 64 * (b + j / kEach) : 0;
+              for (int k = 0; k < 4; ++k) v[k] &= (2 * k < n ? 0xFFFFu : 0u) | (2 * k + 1 < n ? 0xFFFF0000u : 0u);
+            }
+            if (BLK || r < x.put) st_shared_v4(to + (uint32_t)((i & 1) * 4096 + (i >> 1) * kBoxBytes), v[0], v[1], v[2], v[3]);
+          }
         };
-        if (words) eight(full, std::true_type(), src_of, at_of, have_of);
-        else eight(full, std::false_type(), src_of, at_of, have_of);
-      }
-    };
-    const bool a_words = ((reinterpret_cast<uintptr_t>(A) | (uintptr_t)p.lda * 2) & 3) == 0;
-    const bool b_words = ((reinterpret_cast<uintptr_t>(B) | (uintptr_t)p.ldb * 2 | (DW ? 0 : (uintptr_t)p.K * p.N * 2)) & 3) == 0;
-    for (int u = unit0; u < total; u += unit_step) {
-      const TcUnit t = unit_at(u);
-      const int steps = steps_of(t), kk = DW ? t.count : p.K;
-      const uint16_t* we = DW ? B + (int64_t)t.row0 * p.ldb : B + (int64_t)t.e * p.K * p.N;
-      for (int kb = 0; kb < steps; ++kb) {
-        if (!wait_all(empty0 + 8u * s, ph ^ 1u, 2000 + s)) goto loaded;
-        const uint32_t sa = base + (uint32_t)s * stage_bytes, sb = sa + kABytes;
-        const int k0 = kb * kBlkK;
-        // what is contiguous along the contraction as rows, the rest as blocks
-        if constexpr (M_MN)
-          fill_blocks(sa, we + (int64_t)k0 * p.ldb + t.n0, p.ldb, kBlkM / 64, p.N - t.n0, kk - k0, b_words);
-        else
-          fill_rows(sa, we + (int64_t)t.n0 * p.ldb + k0, p.ldb, min(kBlkM, p.N - t.n0), kk - k0, b_words);
-        if constexpr (N_MN)
-          fill_blocks(sb, A + (int64_t)(t.row0 + k0) * p.lda + t.r0, p.lda, (t.nt + 63) / 64, p.K - t.r0, kk - k0, a_words);
-        else
-          fill_rows(sb, A + (int64_t)(t.row0 + t.r0) * p.lda + k0, p.lda, t.nt, kk - k0, a_words);
-        fence_proxy_async_smem();
+        switch (x.sh >> 1) {
+          case 0: by(std::integral_constant<int, 0>()); break;
+          case 1: by(std::integral_constant<int, 1>()); break;
+          case 2: by(std::integral_constant<int, 2>()); break;
+          case 3: by(std::integral_constant<int, 3>()); break;
+          case 4: by(std::integral_constant<int, 4>()); break;
+          case 5: by(std::integral_constant<int, 5>()); break;
+          case 6: by(std::integral_constant<int, 6>()); break;
+          default: by(std::integral_constant<int, 7>());
+        }
+      };
+      // element by element
+      auto store_slow = [&](const Stage& x, uint32_t to) {
+#pragma unroll 1
+        for (int i = 0; 32 * i < x.put; ++i) {
+          const int b = BLK ? i >> 1 : 0, r = row + 32 * (i & 1) + (BLK ? 0 : 64 * (i >> 1));
+          const uint16_t* q = x.src + r * ld + 64 * b + 8 * chunk;
+          // elements that exist
+          const int n = r < (BLK ? x.left : x.have) ? (BLK ? x.have : x.left) - 64 * b - 8 * chunk : 0;
+          uint32_t v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            v[k] = (2 * k < n ? gload(q + 2 * k) : 0u) | (2 * k + 1 < n ? gload(q + 2 * k + 1) << 16 : 0u);
+          if (BLK || r < x.put) st_shared_v4(to + (uint32_t)((i & 1) * 4096 + (i >> 1) * kBoxBytes), v[0], v[1], v[2], v[3]);
+        }
+      };
+      find_unit();
+      if (!more) return;
+      int s = 0;
+      uint32_t ph = 0, buf = 0;
+      Stage now = issue(raw);
+      for (;;) {
+        Stage next = now;
+        const bool go_on = more;
+        if (go_on) {
+          next = issue(raw + raw_size - buf);
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
+        } else {
+          asm volatile("cp.async.wait_group 0;" ::: "memory");
+        }
         __syncwarp();
+        if (!wait_all(empty0 + 8u * s, ph ^ 1u, 2000 + s)) break;
+        const uint32_t to = base + (uint32_t)s * stage_bytes + lane_dst;
+        if (now.fast) store(now, raw + buf, to);
+        else store_slow(now, to);
+        fence_proxy_async_smem();
+        __syncwarp();  // (also: this buffer has been read)
         if (lane == 0) mbar_arrive(&full[s]);
         if (++s == S) {
           s = 0;
           ph ^= 1u;
         }
+        if (!go_on) break;
+        now = next;
+        buf = raw_size - buf;
       }
-    }
-  loaded:;
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    };
+    if (warp < 2 + kEpi + 8) run_side(std::true_type());
+    else run_side(std::false_type());
   } else if (warp > 1 && warp < 2 + kEpi) {
     // A lane holds an output column; a warp takes 32 rows in kStep of its quarter's 32 columns.
     // (Sixteen warps, half of the sums each, are slower: 16384 rows of four experts into
