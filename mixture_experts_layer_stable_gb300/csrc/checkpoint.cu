@@ -9,10 +9,10 @@
 // Scales are powers of two, so v * 2^-s is exact, codes do not depend on the order or
 // precision of any arithmetic, and a code times its scale is exact in fp32.
 //
-// Every call is bound by HBM.  A thread holds V elements of a block (16 bytes of a row;
-// one element of rows that are not 16-byte aligned), the 32 / V threads of a block are
-// neighbours in a warp and take its maximum by shuffles, and everything a thread reads
-// is loaded before anything is computed.
+// Every call is bound by HBM.  A thread holds V elements of a block (16 bytes of a row, 8
+// where rows allow no more, or four elements one by one in rows that start anywhere), the
+// 32 / V threads of a block are neighbours in a warp and take its maximum by shuffles, and
+// everything a thread reads is loaded before anything is computed.
 #include "gemm_common.cuh"
 #include "ops_common.cuh"
 
@@ -21,6 +21,9 @@ namespace moe {
 namespace {
 
 constexpr int kThreadsCk = 256;
+// Pieces of a thread: 16384 rows of 4096 bf16 to 8 bits 80 us with one, 68 with two, 66 with
+// four, back 76, 64, 66.
+constexpr int kPieces = 2;
 
 // Which part of which row a thread has: rpb rows a block, or several blocks (y) a row.
 struct CkLay {
@@ -45,117 +48,156 @@ __device__ __forceinline__ uint32_t pack_bytes(float a, float b, float c, float 
   return __byte_perm(lo, hi, 0x5410);
 }
 
-// V elements of a row in fp32 as pairs (V = 1: one element, the pair's first).
-template <typename T, int V>
-struct Piece {
-  Words<T, V == 1 ? 2 : V> w;
-  float one;
-  __device__ __forceinline__ void load(const T* p, bool there) {
-    if constexpr (V == 1) {
-      one = there ? gload_f32(p) : 0.f;
-    } else {
-      if (there) w.template load<V>(0, p);
-      else w.clear();
-    }
-  }
-  __device__ __forceinline__ F2 pair(int k) const {
-    if constexpr (V == 1) return F2(one, 0.f);
-    else return w.pair(k);
-  }
-};
-template <typename T, int V>
-__device__ __forceinline__ void store_pairs(T* p, const F2 (&v)[(V + 1) / 2]) {
-  if constexpr (V == 1) {
-    *p = from_f32<T>(v[0].get().x);
-  } else {
-    Words<T, V> w;
-#pragma unroll
-    for (int k = 0; k < V / 2; ++k) w.set(k, v[k]);
-    w.template store<V>(0, p);
-  }
+// One element where it exists, else 0, without a branch (behind one it would be waited for).
+__device__ __forceinline__ uint32_t gload_if(const uint32_t* p, bool there) {
+  uint32_t v;
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\tmov.b32 %0, 0;\n\t@q ld.global.u32 %0, [%1];\n\t}"
+               : "=&r"(v) : "l"(p), "r"((int)there));
+  return v;
+}
+__device__ __forceinline__ uint32_t gload_if(const uint16_t* p, bool there) {
+  uint32_t v;
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\tmov.b32 %0, 0;\n\t@q ld.global.u16 %0, [%1];\n\t}"
+               : "=&r"(v) : "l"(p), "r"((int)there));
+  return v;
+}
+__device__ __forceinline__ uint32_t gload_if(const uint8_t* p, bool there) {
+  uint32_t v;
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\tmov.b32 %0, 0;\n\t@q ld.global.u8 %0, [%1];\n\t}"
+               : "=&r"(v) : "l"(p), "r"((int)there));
+  return v;
 }
 
-// The block's codes and scale from its threads' elements; the warp calls it together.
-// there: whether this thread's elements exist (else they are zeros), sub: its place in
-// the block.
-template <int V>
-__device__ __forceinline__ void int8_store(const F2 (&v)[(V + 1) / 2], int8_t* codes, uint8_t* scale, bool there,
-                                           int sub) {
-  uint32_t m = 0;
+// V elements of a row, of which n exist (the others are zeros).  LOOSE: one by one, else as
+// one access (all of them or none exist).
+template <typename T, int V, bool LOOSE>
+struct Piece {
+  Words<T, V> w;
+  uint32_t one[LOOSE ? V : 1];
+  // the elements, before their first use
+  __device__ __forceinline__ void join() {
+    if constexpr (LOOSE) {
 #pragma unroll
-  for (int k = 0; k < (V + 1) / 2; ++k) {
-    const float2 f = v[k].get();
-    m = max(m, max(__float_as_uint(f.x) & 0x7FFFFFFFu, __float_as_uint(f.y) & 0x7FFFFFFFu));
+      for (int j = 0; j < V; ++j) {
+        if constexpr (sizeof(T) == 4) w.w[j] = one[j];
+        else w.w[j / 2] = j % 2 ? w.w[j / 2] | one[j] << 16 : one[j];
+      }
+    }
   }
+  __device__ __forceinline__ void load(const T* p, int n) {
+    if constexpr (LOOSE) {
+      using E = std::conditional_t<sizeof(T) == 4, uint32_t, uint16_t>;
+#pragma unroll
+      for (int j = 0; j < V; ++j) one[j] = gload_if(reinterpret_cast<const E*>(p + j), j < n);
+    } else if (n <= 0) {
+      w.clear();
+    } else if constexpr (V * sizeof(T) == 8) {
+      asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(w.w[0]), "=r"(w.w[1]) : "l"(p));
+    } else {
+      w.template load<V>(0, p);
+    }
+  }
+  __device__ __forceinline__ void store(T* p, int n) const {
+    if constexpr (LOOSE) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        if constexpr (sizeof(T) == 4) {
+          if (j < n) *reinterpret_cast<uint32_t*>(p + j) = w.w[j];
+        } else {
+          if (j < n) *reinterpret_cast<uint16_t*>(p + j) = (uint16_t)(w.w[j / 2] >> (16 * (j % 2)));
+        }
+      }
+    } else if (n > 0) {
+      if constexpr (V * sizeof(T) == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w.w[0], w.w[1]);
+      else w.template store<V>(0, p);
+    }
+  }
+  // the bits of max |v| in fp32
+  __device__ __forceinline__ uint32_t top() const {
+    if constexpr (sizeof(T) == 4) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < V; ++j) m = max(m, w.w[j] & 0x7FFFFFFFu);
+      return m;
+    } else {  // two at a time: magnitudes are ordered as their bits are
+      uint32_t m = w.w[0] & 0x7FFF7FFFu;
+#pragma unroll
+      for (int j = 1; j < V / 2; ++j) m = __vmaxu2(m, w.w[j] & 0x7FFF7FFFu);
+      const uint32_t one = max(m >> 16, m & 0xFFFFu);
+      if constexpr (std::is_same<T, __half>::value) return __float_as_uint(__half2float(__ushort_as_half((uint16_t)one)));
+      else return one << 16;
+    }
+  }
+};
+
+// The block's codes and scale from its threads' elements (n of V exist here, this thread's
+// place in the block is sub); the warp calls it together.
+template <typename T, int V, bool LOOSE>
+__device__ __forceinline__ void int8_store(const Piece<T, V, LOOSE>& x, int8_t* codes, uint8_t* scale, int n, int sub) {
+  uint32_t m = x.top();
 #pragma unroll
   for (int o = 16 / V; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
   const bool finite = m < 0x7F800000u;
   const int s = finite ? int8_scale_exp(m) : 0;
-  const float inv = finite ? ue8m0_inverse(s) : 0.f;
-  if (!there) return;
+  const float inv = ue8m0_inverse(s);
+  if (n <= 0) return;
   if (sub == 0) *scale = finite ? (uint8_t)(s + 127) : (uint8_t)255;
-  const float lim = s >= 122 ? 63.f : 127.f;  // 64 * 2^122 is past fp32's range
-  float r[2 * ((V + 1) / 2)];
+  const F2 inv2(inv, inv), magic(12582912.f, 12582912.f);
+  float r[V];
 #pragma unroll
-  for (int k = 0; k < (V + 1) / 2; ++k) {
-    const float2 f = v[k].get();
+  for (int k = 0; k < V / 2; ++k) {
     // one rounding, to a whole number: the sum is in [2^23, 2^24)
-    r[2 * k] = finite ? fmaf(f.x, inv, 12582912.f) : 0.f;
-    r[2 * k + 1] = finite ? fmaf(f.y, inv, 12582912.f) : 0.f;
-    if (s >= 122) {
-      r[2 * k] = fminf(fmaxf(r[2 * k], 12582912.f - lim), 12582912.f + lim);
-      r[2 * k + 1] = fminf(fmaxf(r[2 * k + 1], 12582912.f - lim), 12582912.f + lim);
-    }
+    const float2 f = fma2(x.w.pair(k), inv2, magic).get();
+    r[2 * k] = f.x;
+    r[2 * k + 1] = f.y;
   }
-  if constexpr (V == 1) {
-    *codes = (int8_t)__float_as_uint(r[0]);
+  if (finite && s >= 122) {  // 64 * 2^122 is past fp32's range
+#pragma unroll
+    for (int k = 0; k < V; ++k) r[k] = fminf(fmaxf(r[k], 12582912.f - 63.f), 12582912.f + 63.f);
+  }
+  uint32_t w[V / 4];
+#pragma unroll
+  for (int k = 0; k < V / 4; ++k)
+    w[k] = finite ? pack_bytes(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]) : 0u;
+  if constexpr (LOOSE) {
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (j < n) codes[j] = (int8_t)(w[j / 4] >> (8 * (j % 4)));
   } else if constexpr (V == 4) {
-    *reinterpret_cast<uint32_t*>(codes) = pack_bytes(r[0], r[1], r[2], r[3]);
+    *reinterpret_cast<uint32_t*>(codes) = w[0];
   } else {
-    uint2 w;
-    w.x = pack_bytes(r[0], r[1], r[2], r[3]);
-    w.y = pack_bytes(r[4], r[5], r[6], r[7]);
-    *reinterpret_cast<uint2*>(codes) = w;
+    *reinterpret_cast<uint2*>(codes) = make_uint2(w[0], w[1]);
   }
 }
 
 // V codes and their scale byte, as loaded, and their values.
-template <int V>
+template <int V, bool LOOSE>
 struct Kept {
-  uint32_t w[(V + 3) / 4], byte;
-  __device__ __forceinline__ void load(const int8_t* codes, const uint8_t* scale, bool there) {
-    byte = 127;
+  uint32_t w[V / 4], byte, one[LOOSE ? V : 1];
+  __device__ __forceinline__ void load(const int8_t* codes, const uint8_t* scale, int n) {
+    byte = gload_if(scale, n > 0);
+    if constexpr (LOOSE) {
 #pragma unroll
-    for (int i = 0; i < (V + 3) / 4; ++i) w[i] = 0;
-    if (there) {
-      byte = gload(scale);
-      if constexpr (V == 1) {
-        w[0] = gload(reinterpret_cast<const uint8_t*>(codes));
-      } else {
-#pragma unroll
-        for (int i = 0; i < V / 4; ++i) w[i] = 0;
-        if constexpr (V == 8) {
-          asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(codes));
-        } else {
-          w[0] = gload(reinterpret_cast<const uint32_t*>(codes));
-        }
-      }
+      for (int j = 0; j < V; ++j) one[j] = gload_if(reinterpret_cast<const uint8_t*>(codes + j), j < n);
+    } else if (n > 0) {
+      if constexpr (V == 8) asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(codes));
+      else w[0] = gload(reinterpret_cast<const uint32_t*>(codes));
     }
   }
-  __device__ __forceinline__ void values(F2 (&v)[(V + 1) / 2]) const {
-    const float s = ue8m0_value(byte);
-    if constexpr (V == 1) {
-      v[0] = F2((float)(int8_t)w[0] * s, 0.f);
-    } else {
-      // code + 128 as the low byte of 2^23, from which 2^23 + 128 is taken
-      const F2 s2(s, s), off(-8388736.f, -8388736.f);
+  __device__ __forceinline__ void values(F2 (&v)[V / 2]) {
+    if constexpr (LOOSE) {
 #pragma unroll
-      for (int k = 0; k < V / 2; ++k) {
-        const uint32_t u = w[k / 2] ^ 0x80808080u;
-        const F2 f(__uint_as_float(__byte_perm(u, 0x4B000000u, k % 2 ? 0x7542 : 0x7540)),
-                   __uint_as_float(__byte_perm(u, 0x4B000000u, k % 2 ? 0x7543 : 0x7541)));
-        v[k] = mul2(add2(f, off), s2);
-      }
+      for (int i = 0; i < V / 4; ++i) w[i] = one[4 * i] | one[4 * i + 1] << 8 | one[4 * i + 2] << 16 | one[4 * i + 3] << 24;
+    }
+    // code + 128 as the low byte of 2^23, from which 2^23 + 128 is taken
+    const float s = ue8m0_value(byte);
+    const F2 s2(s, s), off(-8388736.f, -8388736.f);
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) {
+      const uint32_t u = w[k / 2] ^ 0x80808080u;
+      const F2 f(__uint_as_float(__byte_perm(u, 0x4B000000u, k % 2 ? 0x7542 : 0x7540)),
+                 __uint_as_float(__byte_perm(u, 0x4B000000u, k % 2 ? 0x7543 : 0x7541)));
+      v[k] = mul2(add2(f, off), s2);
     }
   }
 };
@@ -188,51 +230,50 @@ __device__ __forceinline__ F2 in_range(F2 v) {
   }
 }
 
-template <typename T, int V, int U>
+template <typename T, int V, bool LOOSE>
 __global__ void __launch_bounds__(kThreadsCk)
     int8_quantize_kernel(const T* x, int64_t ldx, int64_t rows, int n, CkLay l, int8_t* q, uint8_t* scales) {
   ops_begin();
   constexpr int L = 32 / V;
   const CkAt at = ck_at(l, rows);
   const int nb = (n + 31) / 32, sub = at.t % L;
-  Piece<T, V> p[U];
+  Piece<T, V, LOOSE> p[kPieces];
 #pragma unroll
-  for (int i = 0; i < U; ++i) {
+  for (int i = 0; i < kPieces; ++i) {
     const int b = at.t / L + i * l.nq, c = b * 32 + sub * V;
-    p[i].load(x + at.row * ldx + c, at.there && c < n);
+    p[i].load(x + at.row * ldx + c, at.there ? n - c : 0);
   }
 #pragma unroll
-  for (int i = 0; i < U; ++i) {
+  for (int i = 0; i < kPieces; ++i) {
     const int b = at.t / L + i * l.nq, c = b * 32 + sub * V;
-    F2 v[(V + 1) / 2];
-#pragma unroll
-    for (int k = 0; k < (V + 1) / 2; ++k) v[k] = p[i].pair(k);
-    int8_store<V>(v, q + at.row * n + c, scales + at.row * nb + b, at.there && c < n, sub);
+    p[i].join();
+    int8_store(p[i], q + at.row * n + c, scales + at.row * nb + b, at.there ? n - c : 0, sub);
   }
 }
 
-template <typename T, int V, int U>
+template <typename T, int V, bool LOOSE>
 __global__ void __launch_bounds__(kThreadsCk)
     int8_dequantize_kernel(const int8_t* q, const uint8_t* scales, int64_t rows, int n, CkLay l, T* y, int64_t ldy) {
   ops_begin();
   constexpr int L = 32 / V;
   const CkAt at = ck_at(l, rows);
   const int nb = (n + 31) / 32, sub = at.t % L;
-  Kept<V> p[U];
+  Kept<V, LOOSE> p[kPieces];
 #pragma unroll
-  for (int i = 0; i < U; ++i) {
+  for (int i = 0; i < kPieces; ++i) {
     const int b = at.t / L + i * l.nq, c = b * 32 + sub * V;
-    p[i].load(q + at.row * n + c, scales + at.row * nb + b, at.there && c < n);
+    p[i].load(q + at.row * n + c, scales + at.row * nb + b, at.there ? n - c : 0);
   }
 #pragma unroll
-  for (int i = 0; i < U; ++i) {
+  for (int i = 0; i < kPieces; ++i) {
     const int b = at.t / L + i * l.nq, c = b * 32 + sub * V;
     if (!(at.there && c < n)) continue;
-    F2 v[(V + 1) / 2];
+    F2 v[V / 2];
+    Piece<T, V, LOOSE> o;
     p[i].values(v);
 #pragma unroll
-    for (int k = 0; k < (V + 1) / 2; ++k) v[k] = in_range<T>(v[k]);
-    store_pairs<T, V>(y + at.row * ldy + c, v);
+    for (int k = 0; k < V / 2; ++k) o.w.set(k, in_range<T>(v[k]));
+    o.store(y + at.row * ldy + c, n - c);
   }
 }
 
@@ -251,101 +292,105 @@ __device__ __forceinline__ void sigmoids(float g, float& s, float& c) {
   }
 }
 
-template <typename T, int V, int U, bool KEEP>
+template <typename T, int V, bool LOOSE, bool KEEP>
 __global__ void __launch_bounds__(kThreadsCk)
     swiglu_forward_kernel(const T* h, int64_t ldh, int64_t rows, int f, CkLay l, T* a, int64_t lda, int8_t* q,
                           uint8_t* scales) {
   ops_begin();
-  constexpr int L = 32 / V, P = (V + 1) / 2;
+  constexpr int L = 32 / V, P = V / 2;
   const CkAt at = ck_at(l, rows);
   const int nb = (f + 31) / 32, sub = at.t % L;
-  Piece<T, V> pg[U], pu[U];
+  Piece<T, V, LOOSE> pg[kPieces], pu[kPieces];
 #pragma unroll
-  for (int i = 0; i < U; ++i) {
+  for (int i = 0; i < kPieces; ++i) {
     const int b = at.t / L + i * l.nq, c = b * 32 + sub * V;
-    pg[i].load(h + at.row * ldh + c, at.there && c < f);
-    pu[i].load(h + at.row * ldh + f + c, at.there && c < f);
+    const int n = at.there ? f - c : 0;
+    pg[i].load(h + at.row * ldh + c, n);
+    pu[i].load(h + at.row * ldh + f + c, n);
   }
 #pragma unroll
-  for (int i = 0; i < U; ++i) {
+  for (int i = 0; i < kPieces; ++i) {
     const int b = at.t / L + i * l.nq, c = b * 32 + sub * V;
-    const bool there = at.there && c < f;
-    F2 g[P], u[P];
-#pragma unroll
-    for (int k = 0; k < P; ++k) {
-      g[k] = pg[i].pair(k);
-      u[k] = pu[i].pair(k);
-    }
+    const int n = at.there ? f - c : 0;
+    pg[i].join();
+    pu[i].join();
     if constexpr (KEEP) {
-      int8_store<V>(g, q + at.row * 2 * f + c, scales + at.row * 2 * nb + b, there, sub);
-      int8_store<V>(u, q + at.row * 2 * f + f + c, scales + at.row * 2 * nb + nb + b, there, sub);
+      int8_store(pg[i], q + at.row * 2 * f + c, scales + at.row * 2 * nb + b, n, sub);
+      int8_store(pu[i], q + at.row * 2 * f + f + c, scales + at.row * 2 * nb + nb + b, n, sub);
     }
-    if (!there) continue;
+    if (n <= 0) continue;
+    Piece<T, V, LOOSE> o;
 #pragma unroll
     for (int k = 0; k < P; ++k) {
-      const float2 gf = g[k].get();
+      const F2 g = pg[i].w.pair(k);
+      const float2 gf = g.get();
       float s0, s1, c0;
       sigmoids<T>(gf.x, s0, c0);
       sigmoids<T>(gf.y, s1, c0);
-      g[k] = mul2(mul2(g[k], F2(s0, s1)), u[k]);
+      o.w.set(k, mul2(mul2(g, F2(s0, s1)), pu[i].w.pair(k)));
     }
-    store_pairs<T, V>(a + at.row * lda + c, g);
+    o.store(a + at.row * lda + c, n);
   }
 }
 
-template <typename T, int V, int U, bool KEPT>
+template <typename T, int V, bool LOOSE, bool KEPT>
 __global__ void __launch_bounds__(kThreadsCk)
     swiglu_backward_kernel(const T* da, int64_t ldda, const T* h, int64_t ldh, const int8_t* q, const uint8_t* scales,
                            int64_t rows, int f, CkLay l, T* dh, int64_t lddh, T* a, int64_t lda) {
   ops_begin();
-  constexpr int L = 32 / V, P = (V + 1) / 2;
+  constexpr int L = 32 / V, P = V / 2;
   const CkAt at = ck_at(l, rows);
   const int nb = (f + 31) / 32, sub = at.t % L;
-  Piece<T, V> pd[U], pg[U], pu[U];
-  Kept<V> kg[U], ku[U];
+  Piece<T, V, LOOSE> pd[kPieces], pg[kPieces], pu[kPieces];
+  Kept<V, LOOSE> kg[kPieces], ku[kPieces];
 #pragma unroll
-  for (int i = 0; i < U; ++i) {
+  for (int i = 0; i < kPieces; ++i) {
     const int b = at.t / L + i * l.nq, c = b * 32 + sub * V;
-    const bool there = at.there && c < f;
+    const int n = at.there ? f - c : 0;
     if constexpr (KEPT) {
-      kg[i].load(q + at.row * 2 * f + c, scales + at.row * 2 * nb + b, there);
-      ku[i].load(q + at.row * 2 * f + f + c, scales + at.row * 2 * nb + nb + b, there);
+      kg[i].load(q + at.row * 2 * f + c, scales + at.row * 2 * nb + b, n);
+      ku[i].load(q + at.row * 2 * f + f + c, scales + at.row * 2 * nb + nb + b, n);
     } else {
-      pg[i].load(h + at.row * ldh + c, there);
-      pu[i].load(h + at.row * ldh + f + c, there);
+      pg[i].load(h + at.row * ldh + c, n);
+      pu[i].load(h + at.row * ldh + f + c, n);
     }
-    pd[i].load(da + at.row * ldda + c, there);
+    pd[i].load(da + at.row * ldda + c, n);
   }
 #pragma unroll
-  for (int i = 0; i < U; ++i) {
+  for (int i = 0; i < kPieces; ++i) {
     const int b = at.t / L + i * l.nq, c = b * 32 + sub * V;
     if (!(at.there && c < f)) continue;
-    F2 g[P], u[P], d[P], again[P];
+    F2 g[P], u[P];
+    Piece<T, V, LOOSE> og, ou, oa;
+    pd[i].join();
     if constexpr (KEPT) {
       kg[i].values(g);
       ku[i].values(u);
+    } else {
+      pg[i].join();
+      pu[i].join();
     }
 #pragma unroll
     for (int k = 0; k < P; ++k) {
       if constexpr (!KEPT) {
-        g[k] = pg[i].pair(k);
-        u[k] = pu[i].pair(k);
+        g[k] = pg[i].w.pair(k);
+        u[k] = pu[i].w.pair(k);
       }
-      d[k] = pd[i].pair(k);
+      const F2 d = pd[i].w.pair(k);
       const float2 gf = g[k].get();
       float s0, s1, c0, c1;
       sigmoids<T>(gf.x, s0, c0);
       sigmoids<T>(gf.y, s1, c1);
       const F2 s(s0, s1), gs = mul2(g[k], s);
-      again[k] = mul2(gs, u[k]);
+      oa.w.set(k, mul2(gs, u[k]));
       // sg * (1 + g * (1 - sg)) = sg + (g sg)(1 - sg)
       const F2 slope = fma2(gs, F2(c0, c1), s);
-      g[k] = mul2(mul2(d[k], u[k]), slope);
-      u[k] = mul2(d[k], gs);
+      og.w.set(k, mul2(mul2(d, u[k]), slope));
+      ou.w.set(k, mul2(d, gs));
     }
-    store_pairs<T, V>(dh + at.row * lddh + c, g);
-    store_pairs<T, V>(dh + at.row * lddh + f + c, u);
-    if (a != nullptr) store_pairs<T, V>(a + at.row * lda + c, again);
+    og.store(dh + at.row * lddh + c, f - c);
+    ou.store(dh + at.row * lddh + f + c, f - c);
+    if (a != nullptr) oa.store(a + at.row * lda + c, f - c);
   }
 }
 
@@ -355,20 +400,23 @@ bool ck_args(int32_t dtype, int64_t rows, int32_t n) {
 }
 uintptr_t bits(const void* p) { return reinterpret_cast<uintptr_t>(p); }
 
-// Whether rows of n elements move as 16-byte vectors: `a` the or of the rows' addresses
-// and strides in bytes; the codes of a vector (es * 8 bytes' worth) lie aligned too.
-bool ck_vec(size_t es, int n, uintptr_t a, const void* q) {
-  return ((a | (uintptr_t)n * es) & 15) == 0 && (bits(q) & (16 / es - 1)) == 0;
+// Bytes that a thread moves at once of rows of n elements: 16 or 8 (of 16-bit types)
+// where every row allows it, else 0, one by one.  `a`: the or of the rows' addresses and
+// strides in bytes; the codes of a vector lie aligned too.
+int ck_bytes(size_t es, int n, uintptr_t a, const void* q) {
+  a |= (uintptr_t)n * es;
+  if (((a & 15) | (bits(q) & (16 / es - 1))) == 0) return 16;
+  return es == 2 && ((a & 7) | (bits(q) & 3)) == 0 ? 8 : 0;
 }
 
 struct CkLaunch {
   CkLay lay;
   dim3 grid, block;
 };
-CkLaunch ck_lay(int64_t rows, int n, int V, int U) {
+CkLaunch ck_lay(int64_t rows, int n, int V) {
   CkLaunch l;
   const int nb = (n + 31) / 32;
-  l.lay.nq = (nb + U - 1) / U;
+  l.lay.nq = (nb + kPieces - 1) / kPieces;
   l.lay.per_row = l.lay.nq * (32 / V);
   l.lay.rpb = l.lay.per_row < kThreadsCk ? kThreadsCk / l.lay.per_row : 1;
   if (l.lay.rpb > rows) l.lay.rpb = (int)rows;
@@ -380,16 +428,22 @@ CkLaunch ck_lay(int64_t rows, int n, int V, int U) {
   return l;
 }
 
-// Blocks of 32 that a thread of loose rows takes part in.
-constexpr int kLooseU = 4;
-
-// f(T{}, V, U) for the element type and the way rows move.
+template <typename T_, int V_, bool LOOSE_>
+struct CkTag {
+  using T = T_;
+  static constexpr int V = V_;
+  static constexpr bool LOOSE = LOOSE_;
+};
+// f(tag) for the element type and the way rows move.
 template <typename F>
-cudaError_t ck_pick(int dtype, bool vec, F f) {
+cudaError_t ck_pick(int dtype, int bytes, F f) {
   return with_dtype(dtype, [&](auto t) {
-    constexpr int V = 16 / (int)sizeof(t);
-    return vec ? f(t, std::integral_constant<int, V>(), std::integral_constant<int, 1>())
-               : f(t, std::integral_constant<int, 1>(), std::integral_constant<int, kLooseU>());
+    using T = decltype(t);
+    if (bytes == 16) return f(CkTag<T, 16 / (int)sizeof(T), false>());
+    if constexpr (sizeof(T) == 2) {
+      if (bytes == 8) return f(CkTag<T, 4, false>());
+    }
+    return f(CkTag<T, 4, true>());
   });
 }
 
@@ -413,11 +467,11 @@ moe_status moe_quantize_mxint8_rows(int32_t dtype, int64_t rows, int32_t n, cons
   const size_t es = dtype_bytes(dtype);
   if (!elem_ok(x, es) || q == nullptr || scales == nullptr) return MOE_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return ops_status(ck_pick(dtype, ck_vec(es, n, bits(x) | (uintptr_t)(ldx * es), q), [&](auto t, auto v, auto u) {
-    using T = decltype(t);
-    constexpr int V = decltype(v)::value, U = decltype(u)::value;
-    const CkLaunch l = ck_lay(rows, n, V, U);
-    return launch_ops("quantize_mxint8_rows", int8_quantize_kernel<T, V, U>, l.grid, l.block, 0, st,
+  return ops_status(ck_pick(dtype, ck_bytes(es, n, bits(x) | (uintptr_t)(ldx * es), q), [&](auto tag) {
+    using K = decltype(tag);
+    using T = typename K::T;
+    const CkLaunch l = ck_lay(rows, n, K::V);
+    return launch_ops("quantize_mxint8_rows", int8_quantize_kernel<T, K::V, K::LOOSE>, l.grid, l.block, 0, st,
                       static_cast<const T*>(x), ldx, rows, n, l.lay, q, scales);
   }));
 }
@@ -429,11 +483,11 @@ moe_status moe_dequantize_mxint8_rows(int32_t dtype, int64_t rows, int32_t n, co
   const size_t es = dtype_bytes(dtype);
   if (!elem_ok(y, es) || q == nullptr || scales == nullptr) return MOE_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return ops_status(ck_pick(dtype, ck_vec(es, n, bits(y) | (uintptr_t)(ldy * es), q), [&](auto t, auto v, auto u) {
-    using T = decltype(t);
-    constexpr int V = decltype(v)::value, U = decltype(u)::value;
-    const CkLaunch l = ck_lay(rows, n, V, U);
-    return launch_ops("dequantize_mxint8_rows", int8_dequantize_kernel<T, V, U>, l.grid, l.block, 0, st, q, scales,
+  return ops_status(ck_pick(dtype, ck_bytes(es, n, bits(y) | (uintptr_t)(ldy * es), q), [&](auto tag) {
+    using K = decltype(tag);
+    using T = typename K::T;
+    const CkLaunch l = ck_lay(rows, n, K::V);
+    return launch_ops("dequantize_mxint8_rows", int8_dequantize_kernel<T, K::V, K::LOOSE>, l.grid, l.block, 0, st, q, scales,
                       rows, n, l.lay, static_cast<T*>(y), ldy);
   }));
 }
@@ -446,12 +500,12 @@ moe_status moe_swiglu_forward(int32_t dtype, int64_t rows, int32_t f, const void
   const size_t es = dtype_bytes(dtype);
   if (!elem_ok(h, es) || !elem_ok(a, es)) return MOE_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const bool vec = ck_vec(es, f, bits(h) | bits(a) | (uintptr_t)(ldh * es) | (uintptr_t)(lda * es), q);
-  return ops_status(ck_pick(dtype, vec, [&](auto t, auto v, auto u) {
-    using T = decltype(t);
-    constexpr int V = decltype(v)::value, U = decltype(u)::value;
-    const CkLaunch l = ck_lay(rows, f, V, U);
-    auto kern = q ? swiglu_forward_kernel<T, V, U, true> : swiglu_forward_kernel<T, V, U, false>;
+  const int bytes = ck_bytes(es, f, bits(h) | bits(a) | (uintptr_t)(ldh * es) | (uintptr_t)(lda * es), q);
+  return ops_status(ck_pick(dtype, bytes, [&](auto tag) {
+    using K = decltype(tag);
+    using T = typename K::T;
+    const CkLaunch l = ck_lay(rows, f, K::V);
+    auto kern = q ? swiglu_forward_kernel<T, K::V, K::LOOSE, true> : swiglu_forward_kernel<T, K::V, K::LOOSE, false>;
     return launch_ops("swiglu_forward", kern, l.grid, l.block, 0, st, static_cast<const T*>(h), ldh, rows, f, l.lay,
                       static_cast<T*>(a), lda, q, scales);
   }));
@@ -471,11 +525,11 @@ moe_status moe_swiglu_backward(int32_t dtype, int64_t rows, int32_t f, const voi
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const uintptr_t rows_at = bits(da) | bits(dh) | bits(a) | bits(h) | (uintptr_t)(ldda * es) | (uintptr_t)(lddh * es) |
                             (uintptr_t)((a ? lda : 0) * es) | (uintptr_t)((h ? ldh : 0) * es);
-  return ops_status(ck_pick(dtype, ck_vec(es, f, rows_at, h ? nullptr : q), [&](auto t, auto v, auto u) {
-    using T = decltype(t);
-    constexpr int V = decltype(v)::value, U = decltype(u)::value;
-    const CkLaunch l = ck_lay(rows, f, V, U);
-    auto kern = h ? swiglu_backward_kernel<T, V, U, false> : swiglu_backward_kernel<T, V, U, true>;
+  return ops_status(ck_pick(dtype, ck_bytes(es, f, rows_at, h ? nullptr : q), [&](auto tag) {
+    using K = decltype(tag);
+    using T = typename K::T;
+    const CkLaunch l = ck_lay(rows, f, K::V);
+    auto kern = h ? swiglu_backward_kernel<T, K::V, K::LOOSE, false> : swiglu_backward_kernel<T, K::V, K::LOOSE, true>;
     return launch_ops("swiglu_backward", kern, l.grid, l.block, 0, st, static_cast<const T*>(da), ldda,
                       static_cast<const T*>(h), ldh, q, scales, rows, f, l.lay, static_cast<T*>(dh), lddh,
                       static_cast<T*>(a), lda);
