@@ -1,5 +1,5 @@
-// product_tc.cu -- the experts' products of 16-bit operands on the tensor cores
-// (tcgen05 kind::f16; product.cu has the formulas and the calls).
+// product_tc.cu -- the experts' products on the tensor cores (tcgen05 kind::f16;
+// product.cu has the formulas and the calls).
 //
 // Warp-specialised and persistent, one CTA per SM: warp 0 issues the copies (or sixteen
 // more warps load the operands themselves), one thread of warp 1 the tensor-core
@@ -44,6 +44,13 @@
 // those an accumulator takes 512 of the contraction and the epilogue adds the accumulators
 // up in registers, rounding to nearest (5e-7; 598 us instead of 580 for 16384 rows of four
 // experts into 7168 x 4096; with 256 of the contraction 2.4e-7 and 780 us).
+// fp32 operands.  A value is the sum of three of bf16, x = h + m + l exactly (h nearest to x,
+// m to x - h, l the rest: 8 bits of its 24 each), and
+//   x w = h h' + (h m' + m h' + m m' + h l' + l h') + r,  |r| <= 2^-24 |x w|,
+// so six products on the tensor cores give fp32's precision.  The loading warps split the
+// values into three images of each operand; the first product and the other five have an
+// accumulator each, so that the small ones lose nothing to the large one's truncation.  A
+// stage takes 24 MMAs of 128 x 128 x 16; 128 rows a tile.
 #include "gemm_common.cuh"
 #include "product.cuh"
 #include "tc_roles.cuh"
@@ -52,7 +59,9 @@ namespace moe {
 
 namespace {
 
-enum TcMode { TC_COPY, TC_PAIR, TC_LOAD };  // tensor copies, the same by CTA pairs, plain loads
+// tensor copies, the same by CTA pairs, plain loads, plain loads of fp32 operands
+enum TcMode { TC_COPY, TC_PAIR, TC_LOAD, TC_SPLIT };
+constexpr bool loads(TcMode mode) { return mode == TC_LOAD || mode == TC_SPLIT; }
 
 constexpr int kBlkM = 128, kAccCols = 256, kBlkK = 64;
 constexpr int kEpi = 8;        // warps of the epilogue, two for each quarter of the TMEM lanes
@@ -63,12 +72,13 @@ constexpr int kStagesP = 12;         // at most
 constexpr int kTablesP = 8704;       // static shared memory: the experts' rows and units, barriers
 constexpr int kSmemP = 232448 - kTablesP;
 constexpr int kRawRow = 144;         // TC_LOAD: 64 elements from anywhere in a 16-byte block
-constexpr int kSumSteps = 8;         // stages that a 32-bit result's accumulator takes
+// Stages that a 32-bit result's accumulator takes.
+constexpr int sum_steps(TcMode mode) { return mode == TC_SPLIT ? 4 : 8; }
 
-constexpr int threads_of(TcMode mode) { return 64 + 32 * (kEpi + (mode == TC_LOAD ? kLoadWarps : 0)); }
+constexpr int threads_of(TcMode mode) { return 64 + 32 * (kEpi + (loads(mode) ? kLoadWarps : 0)); }
 // Output rows of a tile at most.  (With loading warps an SM's registers hold the sums of
 // half as many.)
-constexpr int tile_most(TcMode mode, bool f32) { return mode == TC_LOAD && f32 ? 128 : 256; }
+constexpr int tile_most(TcMode mode, bool f32) { return loads(mode) && f32 ? 128 : 256; }
 
 // D (+)= A B, 16-bit operands, K = 16; a and b are descriptors' low words.
 template <bool PAIR>
@@ -94,6 +104,21 @@ MOE_DEV void tc_mma_f16_on(int on, uint32_t d, uint32_t a, uint32_t b, uint32_t 
         "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescSw128), "r"(on)
         : "memory");
   }
+}
+// 16 consecutive fp32 columns of this thread's TMEM lane, added to v.
+MOE_DEV void tmem_add16(uint32_t taddr, float* v) {
+  uint32_t r[16];
+  asm volatile(
+      "{\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n\t}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(r[i]);
 }
 // A wait for an arrival from the other CTA that orders what that one wrote.
 MOE_DEV bool try_wait_cluster(uint32_t bar, uint32_t parity) {
@@ -147,7 +172,8 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
   constexpr bool PAIR = MODE == TC_PAIR, DW = FORM == PROD_DW;
   constexpr bool M_MN = FORM != PROD_ROWS_T, N_MN = DW;  // operands whose contraction is not contiguous
   constexpr int kCols = PAIR ? 2 * kBlkM : kBlkM;        // output columns of a unit
-  constexpr int kTileRows = tile_most(MODE, F32);
+  constexpr int kTileRows = tile_most(MODE, F32), kSumSteps = sum_steps(MODE);
+  constexpr int kImages = MODE == TC_SPLIT ? 3 : 1;  // of each operand in a stage
   constexpr int kBoxRows = DW ? 64 : 32;                 // output rows of a box of the N side
   constexpr uint32_t kNBox = kBoxRows * 128;
   extern __shared__ uint8_t smem_raw[];
@@ -158,7 +184,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
   __shared__ int s_abort, s_most, s_turns;
   if (warp == 0 && lane == 0) {
     for (int i = 0; i < kStagesP; ++i) {
-      mbar_init(&full[i], MODE == TC_LOAD ? kLoadWarps : 1);
+      mbar_init(&full[i], loads(MODE) ? kLoadWarps : 1);
       mbar_init(&empty[i], 1);
       mbar_init(&ready[i], 1);
     }
@@ -169,7 +195,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
     mbar_init(&drain, 1);
     s_abort = 0;
     fence_mbar_init();
-    if (MODE != TC_LOAD) {
+    if (!loads(MODE)) {
       tma_prefetch_desc(&tm_m);
       tma_prefetch_desc(&tm_n);
       tma_prefetch_desc(&tm_n128);
@@ -209,7 +235,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
   // Stage layout for the largest tile there is.
   const int cap = uniform(s_most > kTileRows ? kTileRows : max(32, (s_most + 31) & ~31));
   const int cap_n = (mine_of(cap) + kBoxRows - 1) / kBoxRows * kBoxRows;
-  const uint32_t stage_bytes = (uint32_t)(kABytes + cap_n * 128);
+  const uint32_t n_image = (uint32_t)cap_n * 128u, n_at = kImages * kABytes, stage_bytes = n_at + kImages * n_image;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   // (loading warps: two stages' rows as they lie in memory, 144 bytes each, behind the ring)
   const uint32_t raw_bytes = MODE == TC_LOAD ? 2u * (uint32_t)(kBlkM + cap_n) * kRawRow : 0u;
@@ -251,7 +277,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
     __syncwarp();
   };
 
-  if (warp == 0 && MODE != TC_LOAD) {
+  if (warp == 0 && !loads(MODE)) {
     const int leader = elect_one();
     int s = 0;
     uint32_t ph = 0, used = 0, last = 0, apart_used = 0, apart_ph = 0;
@@ -329,7 +355,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
     int s = 0, acc = 0;
     uint32_t ph = 0, aph = 0, tph = 0;
     constexpr uint32_t kMN = 512u << 16, kKM = 1u << 16;  // leading offsets: 8 KB between blocks of 64 columns
-    const uint32_t da0 = (base >> 4) | (M_MN ? kMN : kKM), db0 = ((base + kABytes) >> 4) | (N_MN ? kMN : kKM);
+    const uint32_t da0 = (base >> 4) | (M_MN ? kMN : kKM), db0 = ((base + n_at) >> 4) | (N_MN ? kMN : kKM);
     constexpr uint32_t ka = M_MN ? 128u : 2u, kn = N_MN ? 128u : 2u;  // 16 of the contraction, in units of 16 bytes
     for (int u = unit0; u < total; u += unit_step) {
       const TcUnit t = unit_at(u);
@@ -345,7 +371,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
           if (!wait_all(smem_u32(&tempty[acc]), aph ^ 1u, 2100 + acc)) goto issued;
         }
         if (!wait_all(full0 + 8u * s, ph, 2200 + s)) goto issued;
-        if constexpr (DW && MODE != TC_LOAD) {
+        if constexpr (DW && !loads(MODE)) {
           if (left < kBlkK && (left & 15) != 0) {
             zero_rows(base + (uint32_t)s * stage_bytes, left, (left + 15) & ~15);
             if constexpr (PAIR) {
@@ -362,10 +388,23 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
         }
         tc_fence_after();
         const uint32_t da = da0 + (uint32_t)s * (stage_bytes / 16u), db = db0 + (uint32_t)s * (stage_bytes / 16u);
-        tc_mma_f16_on<PAIR>(leader, d, da, db, id, more);
-        tc_mma_f16_on<PAIR>(leader && left > 16, d, da + ka, db + kn, id, 1u);
-        tc_mma_f16_on<PAIR>(leader && left > 32, d, da + 2 * ka, db + 2 * kn, id, 1u);
-        tc_mma_f16_on<PAIR>(leader && left > 48, d, da + 3 * ka, db + 3 * kn, id, 1u);
+        // 64 of the contraction: image i of the M side by image j of the N side
+        auto products = [&](uint32_t to, int i, int j, uint32_t onto) {
+          const uint32_t a = da + (uint32_t)(i * (kABytes / 16)), b = db + (uint32_t)j * (n_image / 16u);
+          tc_mma_f16_on<PAIR>(leader, to, a, b, id, onto);
+          tc_mma_f16_on<PAIR>(leader && left > 16, to, a + ka, b + kn, id, 1u);
+          tc_mma_f16_on<PAIR>(leader && left > 32, to, a + 2 * ka, b + 2 * kn, id, 1u);
+          tc_mma_f16_on<PAIR>(leader && left > 48, to, a + 3 * ka, b + 3 * kn, id, 1u);
+        };
+        products(d, 0, 0, more);
+        if constexpr (MODE == TC_SPLIT) {
+          const uint32_t small = d + kTileRows;
+          products(small, 0, 2, more);
+          products(small, 2, 0, 1u);
+          products(small, 1, 1, 1u);
+          products(small, 0, 1, 1u);
+          products(small, 1, 0, 1u);
+        }
         tc_commit_on<PAIR>(leader, empty0 + 8u * s);
         left -= kBlkK;
         more = 1u;
@@ -575,6 +614,146 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
     };
     if (warp < 2 + kEpi + 8) run_side(std::true_type());
     else run_side(std::false_type());
+  } else if (MODE == TC_SPLIT && warp >= 2 + kEpi) {
+    // Eight warps load and split the M side, eight the N side, each every eighth row of 64
+    // values.  Eight lanes have a row, four rows are a group (row + 32 (i % 2) of block i / 2,
+    // or 64 (i / 2) rows on); two groups' loads are under way while two are split.
+    const int w7 = (warp - 2 - kEpi) & 7, chunk = lane & 7;
+    auto run_side = [&](auto m_side, auto vectors) {
+      constexpr bool MS = decltype(m_side)::value, VEC = decltype(vectors)::value, BLK = MS ? M_MN : N_MN;
+      const float* arr = static_cast<const float*>(MS ? p.b : p.a);
+      const int64_t ld = MS ? p.ldb : p.lda;
+      const int row = w7 + 8 * (lane >> 3);
+      const uint32_t lane_dst = (MS ? 0u : n_at) + (uint32_t)(row * 128 + ((chunk ^ w7) << 4));
+      const uint32_t image = MS ? (uint32_t)kABytes : n_image;
+      // where the next half stage (two groups) is
+      int u = unit0, kb = 0, steps = 0, h = 0, left = 0, have = 0, put = 0;
+      const float* src = nullptr;  // the stage's row 0
+      bool more = true;
+      auto find_unit = [&]() {  // from unit u on, the first with a contraction
+        for (; u < total; u += unit_step) {
+          const TcUnit t = unit_at(u);
+          steps = steps_of(t);
+          if (steps == 0) continue;
+          left = DW ? t.count : p.K;
+          have = MS ? min(kBlkM, p.N - t.n0) : DW ? min((t.nt + 63) & ~63, p.K - t.r0) : t.nt;
+          put = MS ? kBlkM : DW ? (t.nt + 63) & ~63 : t.nt;
+          src = arr + (MS ? (DW ? t.row0 * ld : (int64_t)t.e * p.K * p.N) : t.row0 * ld);
+          src += MS ? (BLK ? (int64_t)t.n0 : t.n0 * ld) : BLK ? (int64_t)t.r0 : t.r0 * ld;
+          return;
+        }
+        more = false;
+      };
+      struct Half {
+        uint32_t v[2][8];
+        int h;
+        bool put[2], first, last;  // of its stage
+      };
+      auto load = [&](Half& x) {
+        x.h = h;
+        x.first = h == 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = row + 32 * i + (BLK ? 0 : 64 * h), c = BLK ? 64 * h + 8 * chunk : 8 * chunk;
+          const float* q = src + r * ld + c;
+          // elements that exist: of a row `have` or what is left of the contraction
+          const int n = r < (BLK ? min(left, kBlkK) : have) ? (BLK ? have : left) - c : 0;
+          x.put[i] = BLK || r < put;
+          if constexpr (VEC) {
+            asm volatile(
+                "{\n\t.reg .pred p, q;\n\t"
+                "setp.gt.s32 p, %9, 0;\n\t"
+                "setp.gt.s32 q, %9, 4;\n\t"
+                "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+                "mov.b32 %4, 0;\n\tmov.b32 %5, 0;\n\tmov.b32 %6, 0;\n\tmov.b32 %7, 0;\n\t"
+                "@p ld.global.v4.u32 {%0, %1, %2, %3}, [%8];\n\t"
+                "@q ld.global.v4.u32 {%4, %5, %6, %7}, [%8+16];\n\t}"
+                : "=&r"(x.v[i][0]), "=&r"(x.v[i][1]), "=&r"(x.v[i][2]), "=&r"(x.v[i][3]), "=&r"(x.v[i][4]),
+                  "=&r"(x.v[i][5]), "=&r"(x.v[i][6]), "=&r"(x.v[i][7])
+                : "l"(q), "r"(n));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              asm volatile("{\n\t.reg .pred p;\n\tsetp.gt.s32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t@p ld.global.u32 %0, [%1];\n\t}"
+                           : "=&r"(x.v[i][j])
+                           : "l"(q + j), "r"(n - j));
+          }
+        }
+        // on to the next
+        x.last = 64 * (h + 1) >= put;
+        ++h;
+        if (x.last) {
+          h = 0;
+          src += BLK ? kBlkK * ld : kBlkK;
+          left -= kBlkK;
+          if (++kb == steps) {
+            kb = 0;
+            u += unit_step;
+            find_unit();
+          }
+        }
+      };
+      int s = 0;
+      uint32_t ph = 0;
+      auto split = [&](const Half& x) {
+        if (x.first && !wait_all(empty0 + 8u * s, ph ^ 1u, 2000 + s)) return false;
+        const uint32_t to = base + (uint32_t)s * stage_bytes + lane_dst + (uint32_t)(x.h * kBoxBytes);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t w[3][4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            // (the largest values would round to an infinity)
+            constexpr float kMax = 3.3895313892515355e38f;
+            float a = __uint_as_float(x.v[i][2 * k]), b = __uint_as_float(x.v[i][2 * k + 1]);
+            w[0][k] = pack_bf16x2(fminf(fmaxf(a, -kMax), kMax), fminf(fmaxf(b, -kMax), kMax));
+            a -= __uint_as_float(w[0][k] << 16);
+            b -= __uint_as_float(w[0][k] & 0xFFFF0000u);
+            w[1][k] = pack_bf16x2(a, b);
+            a -= __uint_as_float(w[1][k] << 16);
+            b -= __uint_as_float(w[1][k] & 0xFFFF0000u);
+            w[2][k] = pack_bf16x2(a, b);
+          }
+          if (x.put[i]) {
+#pragma unroll
+            for (int j = 0; j < 3; ++j)
+              st_shared_v4(to + (uint32_t)(i * 4096) + (uint32_t)j * image, w[j][0], w[j][1], w[j][2], w[j][3]);
+          }
+        }
+        if (x.last) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[s]);
+          if (++s == S) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        return true;
+      };
+      find_unit();
+      if (!more) return;
+      Half x, y;
+      load(x);
+      for (;;) {
+        const bool in_y = more;
+        if (in_y) load(y);
+        if (!split(x) || !in_y) break;
+        const bool in_x = more;
+        if (in_x) load(x);
+        if (!split(y) || !in_x) break;
+      }
+    };
+    // 16 bytes at a time where every row starts on them and is a whole number of them
+    const bool vec = ((reinterpret_cast<uintptr_t>(p.a) | reinterpret_cast<uintptr_t>(p.b) |
+                       (uintptr_t)(p.lda | p.ldb | p.K | p.N) * 4) & 15) == 0;
+    if (warp < 2 + kEpi + 8) {
+      if (vec) run_side(std::true_type(), std::true_type());
+      else run_side(std::true_type(), std::false_type());
+    } else {
+      if (vec) run_side(std::false_type(), std::true_type());
+      else run_side(std::false_type(), std::false_type());
+    }
   } else if (warp > 1 && warp < 2 + kEpi) {
     // A lane holds an output column; a warp takes 32 rows in kStep of its quarter's 32 columns.
     // (Sixteen warps, half of the sums each, are slower: 16384 rows of four experts into
@@ -623,10 +802,21 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
 #pragma unroll
           for (int i = 0; i < kParts; ++i) {
             if (c_first + kStep * i < t.nt) {
-              float v[32];
-              tmem_ld32(tq + (uint32_t)(acc * kAccCols + c_first + kStep * i), v);
+              // (16 at a time where loading warps leave a thread 72 registers)
+              const uint32_t from = tq + (uint32_t)(acc * kAccCols + c_first + kStep * i);
+              if constexpr (loads(MODE)) {
+                if constexpr (MODE == TC_SPLIT) {
+                  tmem_add16(from + kTileRows, sum[i]);
+                  tmem_add16(from + kTileRows + 16, sum[i] + 16);
+                }
+                tmem_add16(from, sum[i]);
+                tmem_add16(from + 16, sum[i] + 16);
+              } else {
+                float v[32];
+                tmem_ld32(from, v);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) sum[i][j] += v[j];
+                for (int j = 0; j < 32; ++j) sum[i][j] += v[j];
+              }
             }
           }
           done();
@@ -723,10 +913,13 @@ template <ProdForm FORM, bool F32>
 cudaError_t launch_form(int dtype, const ProdArgs& p, cudaStream_t st) {
   const uint32_t fmt = dtype == MOE_DT_BF16 ? 1u : 0u, formats = (fmt << 7) | (fmt << 10);
   // tensor copies: every row starts on 16 bytes (and there are rows)
-  const bool copy = p.rows > 0 && ((bits(p.a) | bits(p.b) | (uintptr_t)p.lda * 2 | (uintptr_t)p.ldb * 2) & 15) == 0;
+  const bool copy = dtype != MOE_DT_F32 && p.rows > 0 && ((bits(p.a) | bits(p.b) | (uintptr_t)p.lda * 2 | (uintptr_t)p.ldb * 2) & 15) == 0;
   CUtensorMap tm[3];
   if (!copy) {
     memset(tm, 0, sizeof(tm));
+    if constexpr (F32) {
+      if (dtype == MOE_DT_F32) return launch_tc<FORM, TC_SPLIT, true>(tm, p, (1u << 7) | (1u << 10), st);
+    }
     return launch_tc<FORM, TC_LOAD, F32>(tm, p, formats, st);
   }
   const bool pair = p.N > kBlkM && p.rows >= 64 * (int64_t)p.G;
