@@ -1,5 +1,5 @@
-// product.cuh -- what the two kernels of the experts' products share: the call's
-// arguments and the numbering of its units of work.
+// product.cuh -- the experts' products: a call's arguments, the numbering of its units of
+// work, and the launch of the kernel (product_tc.cu).
 #pragma once
 
 #include "ops_common.cuh"
@@ -70,7 +70,6 @@ __device__ __forceinline__ int expert_of(const int* s_unit, int G, int u, int at
   return lo;
 }
 
-// 16-bit operands on the tensor cores (product_tc.cu).
 cudaError_t launch_product_tc(ProdForm form, int dtype, const ProdArgs& p, cudaStream_t st);
 
 }  // namespace moe
