@@ -120,6 +120,12 @@ MOE_DEV void tmem_add16(uint32_t taddr, float* v) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(r[i]);
 }
+// An arrival in the even CTA's barrier that orders nothing but this thread's TMEM reads,
+// which have ended: a release over the cluster would wait for the thread's stores to memory
+// (16384 rows into 64 weight gradients of 2048 x 1536: 151 us with it, DWNEW without).
+MOE_DEV void mbar_arrive_even(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(bar, 0)) : "memory");
+}
 // A wait for an arrival from the other CTA that orders what that one wrote.
 MOE_DEV bool try_wait_cluster(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -767,7 +773,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        if constexpr (PAIR) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
+        if constexpr (PAIR) mbar_arrive_even(smem_u32(&tempty[acc]));
         else mbar_arrive(&tempty[acc]);
       }
       if (++acc == 2) {
