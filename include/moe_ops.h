@@ -126,14 +126,17 @@ moe_status moe_unpermute_backward(int32_t dtype, int64_t T, int32_t d, int32_t k
  * form on dy [rows, N] with K and N changed places; that of the weights is
  * moe_grouped_product_dw.
  *   dtype: of x and w; odtype: of out, dtype or MOE_DT_F32.  Products and sums
- *   in fp32, each result rounded once.
+ *   in fp32, each result rounded once.  (All run on the tensor cores, whose sums
+ *   truncate: fp32 results are off by at most n 2^-23 of the sum of their n terms'
+ *   magnitudes, about 3e-7 of a result in practice.  fp32 values are split into
+ *   three parts of 8 bits: below 2^-102 they are held to 2^-126, and a sum with
+ *   an infinity in it may be NaN instead.)
  *   x [rows, K], out [rows, N] with row strides ldx, ldo; w contiguous.
  *   offsets [G+1], not decreasing; NULL: G = 1, all rows.  Rows outside
  *   [offsets[0], offsets[G]) are neither used nor written.
  *   0 <= rows <= 2^28, 1 <= G <= 1024, 1 <= K, N <= 2^22, no array of more than
  *   2^40 elements.
- *   16-bit operands run on the tensor cores: 16-byte aligned x, w and row
- *   strides are the fast path.
+ *   16-byte aligned x, w and row strides are the fast path.
  *   ws: 128-byte aligned, of moe_grouped_product_workspace_bytes(rows, K, N, G)
  *   bytes, which serve both calls and either form; calls that may overlap need
  *   one each.  moe_read_status(ws, stream) reports a wait that ran out in the

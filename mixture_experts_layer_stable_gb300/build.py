@@ -16,7 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 OBJDIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe.so")
 SOURCES = ["api.cu", "sched.cu", "gather_merge.cu", "gemm.cu", "ring.cu", "noalloc.cu",
-           "layernorm.cu", "permute.cu", "mxfp4.cu", "product.cu", "product_tc.cu", "checkpoint.cu"]
+           "layernorm.cu", "permute.cu", "mxfp4.cu", "product.cu", "product_rows.cu",
+           "product_rows_t.cu", "product_dw.cu", "checkpoint.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xcompiler", "-Wall", "-DNDEBUG"]

@@ -456,7 +456,7 @@ using namespace moe;
 extern "C" {
 
 size_t moe_mxint8_scale_bytes(int64_t rows, int32_t n) {
-  if (rows > ((int64_t)1 << 31) || !ck_args(MOE_DT_F32, rows / 2, n)) return 0;
+  if (rows < 0 || rows > ((int64_t)1 << 31) || !ck_args(MOE_DT_F32, 0, n)) return 0;  // (two a row of SwiGLU's)
   return (size_t)rows * ((n + 31) / 32);
 }
 

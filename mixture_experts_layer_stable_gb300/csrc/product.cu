@@ -1,6 +1,6 @@
 // product.cu -- the calls of the experts' products and their weights' gradients
 // (include/moe_ops.h, moe_grouped_product, moe_grouped_product_dw; the kernel is in
-// product_tc.cu).
+// product_tc.cuh).
 //
 //   out[p] = x[p] * w[g]      p in [offsets[g], offsets[g + 1])
 //   dw[g]  = sum over g's rows p of x[p]^T * dy[p]
@@ -21,6 +21,17 @@ bool prod_sizes(int64_t rows, int32_t K, int32_t N, int32_t G) {
          G <= kMaxG && (int64_t)K * N <= most / G && rows <= most / (K > N ? K : N);
 }
 
+// Bytes of partial sums that a call can need.
+size_t partial_bytes(ProdForm form, int64_t rows, int K, int N, int G) {
+  int splits = 1;
+  for (const TcMode mode : {TC_COPY, TC_PAIR, TC_LOAD}) {  // (fp32 operands' tiles are TC_LOAD's)
+    if (mode == TC_PAIR && !takes_pairs(rows, N, G)) continue;
+    const int s = splits_of(form, mode, rows, K, N, G);
+    splits = s > splits ? s : splits;
+  }
+  return splits > 1 ? (size_t)splits * results_of(form, rows, K, N, G) * sizeof(float) : 0;
+}
+
 }  // namespace
 
 }  // namespace moe
@@ -31,7 +42,14 @@ extern "C" {
 
 size_t moe_grouped_product_workspace_bytes(int64_t rows, int32_t K, int32_t N, int32_t G) {
   if (!prod_sizes(rows, K, N, G)) return 0;
-  return 128;
+  // every form, K and N also in each other's place: both orders need the same
+  size_t most = 0;
+  for (const ProdForm form : {PROD_ROWS, PROD_ROWS_T, PROD_DW}) {
+    const size_t a = partial_bytes(form, rows, K, N, G), b = partial_bytes(form, rows, N, K, G);
+    most = most < a ? a : most;
+    most = most < b ? b : most;
+  }
+  return 128 + (most + 127) / 128 * 128;
 }
 
 moe_status moe_grouped_product(int32_t dtype, int32_t odtype, int64_t rows, int32_t K, int32_t N, int32_t G,
@@ -55,12 +73,14 @@ moe_status moe_grouped_product(int32_t dtype, int32_t odtype, int64_t rows, int3
   p.ldb = transposed ? K : N;
   p.ldo = ldo;
   p.status = static_cast<int*>(ws);
+  p.ws = static_cast<char*>(ws) + 128;
+  p.splits = 1;
   p.rows = (int)rows;
   p.G = G;
   p.K = K;
   p.N = N;
   p.odt = odtype;
-  return ops_status(launch_product_tc(transposed ? PROD_ROWS_T : PROD_ROWS, dtype, p, st));
+  return ops_status(transposed ? launch_product_rows_t(dtype, p, st) : launch_product_rows(dtype, p, st));
 }
 
 moe_status moe_grouped_product_dw(int32_t dtype, int32_t wdtype, int64_t rows, int32_t K, int32_t N, int32_t G,
@@ -84,13 +104,15 @@ moe_status moe_grouped_product_dw(int32_t dtype, int32_t wdtype, int64_t rows, i
   p.ldb = lddy;
   p.ldo = N;
   p.status = static_cast<int*>(ws);
+  p.ws = static_cast<char*>(ws) + 128;
+  p.splits = 1;
   p.rows = (int)rows;
   p.G = G;
   p.K = K;
   p.N = N;
   p.odt = wdtype;
   p.accumulate = accumulate != 0;
-  return ops_status(launch_product_tc(PROD_DW, dtype, p, st));
+  return ops_status(launch_product_dw(dtype, p, st));
 }
 
 }  // extern "C"

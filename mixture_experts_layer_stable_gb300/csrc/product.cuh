@@ -1,5 +1,5 @@
 // product.cuh -- the experts' products: a call's arguments, the numbering of its units of
-// work, and the launch of the kernel (product_tc.cu).
+// work, and the choice of the kernel (product_tc.cuh).
 #pragma once
 
 #include "ops_common.cuh"
@@ -20,6 +20,9 @@ struct ProdArgs {
   int rows, G, K, N;
   int odt;         // type of out
   int accumulate;
+  void* ws;        // partial sums
+  int splits;      // parts of the contraction, 1: out is the result; else partial sums of
+  int64_t split_stride;  // this many floats each
 };
 
 // Rows and units of each expert, numbered by the block: s_off [G + 1] first rows, s_unit
@@ -70,6 +73,40 @@ __device__ __forceinline__ int expert_of(const int* s_unit, int G, int u, int at
   return lo;
 }
 
-cudaError_t launch_product_tc(ProdForm form, int dtype, const ProdArgs& p, cudaStream_t st);
+// How a call runs: tensor copies, the same by CTA pairs, plain loads, plain loads of fp32 operands
+enum TcMode { TC_COPY, TC_PAIR, TC_LOAD, TC_SPLIT };
+constexpr bool loads(TcMode mode) { return mode == TC_LOAD || mode == TC_SPLIT; }
+constexpr int kBlkM = 128, kBlkK = 64;  // output columns of a CTA's tile, contraction of a stage
+// Output rows of a tile at most.  (With loading warps an SM's registers hold the sums of
+// half as many.)
+constexpr int tile_most(TcMode mode, bool f32) { return loads(mode) && f32 ? 128 : 256; }
+
+inline bool takes_pairs(int64_t rows, int N, int G) { return N > kBlkM && rows >= 64 * (int64_t)G; }
+
+// Units of a call at most.
+inline int64_t units_of(ProdForm form, TcMode mode, bool f32, int64_t rows, int K, int N, int G) {
+  const int tile = tile_most(mode, f32), cols = mode == TC_PAIR ? 2 * kBlkM : kBlkM;
+  const int64_t tiles = form == PROD_DW ? (int64_t)((K + tile - 1) / tile) * G : rows / tile + (G < rows ? G : rows);
+  return tiles * ((N + cols - 1) / cols);
+}
+
+// Parts that the contraction is cut into, their sums joined by a second kernel: as many as
+// leave every worker a unit where there are at most half as many units as workers, of four
+// stages at least.  (8 bf16 rows, 7168 to 256, two tiles: 29 us whole, 16 in parts; 3636
+// rows' gradient of 84 columns through 6373, 15 tiles of unaligned rows: 47 us in parts.)
+inline int splits_of(ProdForm form, TcMode mode, int64_t rows, int K, int N, int G) {
+  const int64_t units = units_of(form, mode, true, rows, K, N, G), workers = mode == TC_PAIR ? num_sms() / 2 : num_sms();
+  const int64_t stages = ((form == PROD_DW ? rows / G : K) + kBlkK - 1) / kBlkK;
+  if (units < 1 || 2 * units > workers || stages < 16) return 1;
+  const int64_t most = stages / 4, want = workers / units;
+  return (int)(want < most ? want : most);
+}
+inline int64_t results_of(ProdForm form, int64_t rows, int K, int N, int G) {
+  return form == PROD_DW ? (int64_t)G * K * N : rows * N;
+}
+
+cudaError_t launch_product_rows(int dtype, const ProdArgs& p, cudaStream_t st);
+cudaError_t launch_product_rows_t(int dtype, const ProdArgs& p, cudaStream_t st);
+cudaError_t launch_product_dw(int dtype, const ProdArgs& p, cudaStream_t st);
 
 }  // namespace moe

@@ -1,5 +1,5 @@
-// product_tc.cu -- the experts' products on the tensor cores (tcgen05 kind::f16;
-// product.cu has the formulas and the calls).
+// product_tc.cuh -- the experts' products on the tensor cores (tcgen05 kind::f16;
+// product.cu has the formulas and the calls; each form is compiled in a file of its own).
 //
 // Warp-specialised and persistent, one CTA per SM: warp 0 issues the copies (or sixteen
 // more warps load the operands themselves), one thread of warp 1 the tensor-core
@@ -51,6 +51,8 @@
 // values into three images of each operand; the first product and the other five have an
 // accumulator each, so that the small ones lose nothing to the large one's truncation.  A
 // stage takes 24 MMAs of 128 x 128 x 16; 128 rows a tile.
+#pragma once
+
 #include "gemm_common.cuh"
 #include "product.cuh"
 #include "tc_roles.cuh"
@@ -59,11 +61,8 @@ namespace moe {
 
 namespace {
 
-// tensor copies, the same by CTA pairs, plain loads, plain loads of fp32 operands
-enum TcMode { TC_COPY, TC_PAIR, TC_LOAD, TC_SPLIT };
-constexpr bool loads(TcMode mode) { return mode == TC_LOAD || mode == TC_SPLIT; }
 
-constexpr int kBlkM = 128, kAccCols = 256, kBlkK = 64;
+constexpr int kAccCols = 256;
 constexpr int kEpi = 8;        // warps of the epilogue, two for each quarter of the TMEM lanes
 constexpr int kLoadWarps = 16;  // of TC_LOAD
 constexpr int kABytes = kBlkM * kBlkK * 2;
@@ -76,10 +75,6 @@ constexpr int kRawRow = 144;         // TC_LOAD: 64 elements from anywhere in a 
 constexpr int sum_steps(TcMode mode) { return mode == TC_SPLIT ? 4 : 8; }
 
 constexpr int threads_of(TcMode mode) { return 64 + 32 * (kEpi + (loads(mode) ? kLoadWarps : 0)); }
-// Output rows of a tile at most.  (With loading warps an SM's registers hold the sums of
-// half as many.)
-constexpr int tile_most(TcMode mode, bool f32) { return loads(mode) && f32 ? 128 : 256; }
-
 // D (+)= A B, 16-bit operands, K = 16; a and b are descriptors' low words.
 template <bool PAIR>
 MOE_DEV void tc_mma_f16_on(int on, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
@@ -122,7 +117,7 @@ MOE_DEV void tmem_add16(uint32_t taddr, float* v) {
 }
 // An arrival in the even CTA's barrier that orders nothing but this thread's TMEM reads,
 // which have ended: a release over the cluster would wait for the thread's stores to memory
-// (16384 rows into 64 weight gradients of 2048 x 1536: 151 us with it, DWNEW without).
+// (16384 rows into 64 weight gradients of 2048 x 1536: 151 us with it, 125 without).
 MOE_DEV void mbar_arrive_even(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(bar, 0)) : "memory");
 }
@@ -168,10 +163,14 @@ struct TcUnit {
   int e, row0, count;  // the expert and its rows
   int n0;              // first output column (of a pair: of both CTAs)
   int r0, nt;          // first output row of the tile, in the expert, and rows
+  int part, kb0, steps;  // part of the contraction: its first stage and how many
+  bool end;              // whether the contraction ends with it
 };
 
-// F32: results of 32 bits.
-template <ProdForm FORM, TcMode MODE, bool F32>
+// F32: results of 32 bits.  PARTS: of parts of the contraction (F32; its own kernel, since
+// what it adds to a unit costs the others registers: 4096 fp32 rows of 8 experts, 1024 x
+// 1024, 86 us instead of 74).
+template <ProdForm FORM, TcMode MODE, bool F32, bool PARTS>
 __global__ void __launch_bounds__(threads_of(MODE), 1)
     tc_product_kernel(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ CUtensorMap tm_n,
                       const __grid_constant__ CUtensorMap tm_n128, const ProdArgs p, const uint32_t formats) {
@@ -219,7 +218,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
   ops_wait();
   if (blockIdx.x == 0 && threadIdx.x < 2) p.status[threadIdx.x] = 0;
   const int col_tiles = (p.N + kCols - 1) / kCols, dw_tiles = (p.K + kTileRows - 1) / kTileRows;
-  const int2 most = number_units(p, DW ? 0 : kTileRows, DW ? dw_tiles * col_tiles : col_tiles, s_off, s_unit);
+  const int2 most = number_units(p, DW ? 0 : kTileRows, (DW ? dw_tiles * col_tiles : col_tiles) * p.splits, s_off, s_unit);
   // in turns: an expert has four times the average of those that have rows
   if (threadIdx.x == 0) s_most = DW ? p.K : most.x;
   if (threadIdx.x == 0) s_turns = most.x > 4 * most.y;
@@ -256,7 +255,18 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
     t.e = at_e;
     t.row0 = uniform(s_off[at_e]);
     t.count = max(0, uniform(s_off[at_e + 1]) - t.row0);
-    const int r = u - uniform(s_unit[at_e]), c = DW ? p.K : t.count;
+    int r = u - uniform(s_unit[at_e]);
+    const int c = DW ? p.K : t.count, stages = ((DW ? t.count : p.K) + kBlkK - 1) / kBlkK;
+    t.part = t.kb0 = 0;
+    t.steps = stages;
+    if constexpr (PARTS) {
+      const int each = (stages + p.splits - 1) / p.splits;
+      t.part = r % p.splits;
+      r /= p.splits;
+      t.kb0 = min(stages, t.part * each);
+      t.steps = min(stages - t.kb0, each);
+    }
+    t.end = t.kb0 + t.steps == stages;
     const int tiles = DW ? dw_tiles : (c + kTileRows - 1) / kTileRows, n = tiles == 1 ? r : r / tiles;
     t.n0 = n * kCols;
     const int sz = tile_rows(c, tiles);
@@ -264,7 +274,8 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
     t.nt = min(sz, c - t.r0);  // (sz <= kTileRows, so every tile has a row)
     return t;
   };
-  auto steps_of = [&](const TcUnit& t) { return ((DW ? t.count : p.K) + kBlkK - 1) / kBlkK; };
+  // what is left of the contraction where the unit begins
+  auto left_of = [&](const TcUnit& t) { return (DW ? t.count : p.K) - t.kb0 * kBlkK; };
   const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty);
   // All lanes wait; the result is the same in each.
   auto wait_all = [&](uint32_t bar, uint32_t parity, int where) {
@@ -289,7 +300,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
     uint32_t ph = 0, used = 0, last = 0, apart_used = 0, apart_ph = 0;
     for (int u = unit0; u < total; u += unit_step) {
       const TcUnit t = unit_at(u);
-      const int mine = mine_of(t.nt), steps = steps_of(t);
+      const int mine = mine_of(t.nt), steps = t.steps;
       // boxes of CTA r's M side (64 columns, or all 128); of its N side
       auto m_boxes = [&](int r) {
         const int left = p.N - t.n0 - r * kBlkM;
@@ -304,11 +315,11 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
       for (int kb = 0; kb < steps; ++kb) {
         if (!wait_all(empty0 + 8u * s, ph ^ 1u, 2000 + s)) goto produced;
         const uint32_t sa = base + (uint32_t)s * stage_bytes, sb = sa + kABytes;
-        const int k0 = kb * kBlkK;
+        const int k0 = (t.kb0 + kb) * kBlkK;
         // of a pair, the odd CTA zeroes the end of the contraction in its own shared memory
         // and waits for its own copies first, on its own barrier of the stage (which has no
         // other use)
-        const bool apart = PAIR && DW && kb == steps - 1 && (t.count & 15) != 0;
+        const bool apart = PAIR && DW && kb == steps - 1 && t.end && (t.count & 15) != 0;
         uint32_t fb = full0 + 8u * s;
         if constexpr (PAIR) {
           if (apart && rank == 1) {
@@ -365,11 +376,11 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
     constexpr uint32_t ka = M_MN ? 128u : 2u, kn = N_MN ? 128u : 2u;  // 16 of the contraction, in units of 16 bytes
     for (int u = unit0; u < total; u += unit_step) {
       const TcUnit t = unit_at(u);
-      const int steps = steps_of(t);
+      const int steps = t.steps;
       const int mma_n = PAIR ? (t.nt + 31) & ~31 : (t.nt + 15) & ~15;
       const uint32_t id = (1u << 4) | formats | ((M_MN ? 1u : 0u) << 15) | ((N_MN ? 1u : 0u) << 16) |
                           ((uint32_t)(mma_n >> 3) << 17) | ((uint32_t)((PAIR ? 256 : 128) >> 4) << 24);
-      int left = DW ? t.count : p.K;
+      int left = left_of(t);
       uint32_t more = 0;
       for (int kb = 0; kb < steps; ++kb) {
         const uint32_t d = tmem + (uint32_t)(acc * kAccCols);
@@ -439,13 +450,13 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
     uint32_t tph = 0;
     for (int u = unit0; u < total; u += unit_step) {
       const TcUnit t = unit_at(u);
-      const int steps = steps_of(t);
+      const int steps = t.steps;
       if (steps == 0) continue;
       s = (s + steps - 1) % S;
-      if ((t.count & 15) != 0) {
+      if (t.end && (t.count & 15) != 0) {
         if (!wait_all(full0 + 8u * s, (tph >> s) & 1u, 2400)) break;
         tph ^= 1u << s;
-        const int left = t.count - (steps - 1) * kBlkK;
+        const int left = left_of(t) - (steps - 1) * kBlkK;
         zero_rows(base + (uint32_t)s * stage_bytes, left, (left + 15) & ~15);
         if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&ready[s]), 0));
       }
@@ -492,13 +503,13 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
       auto find_unit = [&]() {  // from unit u on, the first with a contraction
         for (; u < total; u += unit_step) {
           const TcUnit t = unit_at(u);
-          steps = steps_of(t);
+          steps = t.steps;
           if (steps == 0) continue;
-          at.left = DW ? t.count : p.K;
+          at.left = left_of(t);
           at.have = MS ? min(kBlkM, p.N - t.n0) : DW ? min((t.nt + 63) & ~63, p.K - t.r0) : t.nt;
           at.put = MS ? kBlkM : DW ? (t.nt + 63) & ~63 : t.nt;
           at.src = arr + (MS ? (DW ? t.row0 * ld : (int64_t)t.e * p.K * p.N) : t.row0 * ld);
-          at.src += MS ? (BLK ? (int64_t)t.n0 : t.n0 * ld) : BLK ? (int64_t)t.r0 : t.r0 * ld;
+          at.src += (MS ? (BLK ? (int64_t)t.n0 : t.n0 * ld) : BLK ? (int64_t)t.r0 : t.r0 * ld) + t.kb0 * (BLK ? kBlkK * ld : kBlkK);
           at.sh = (int)(reinterpret_cast<uintptr_t>(at.src + w7 * ld) & 15);
           return;
         }
@@ -639,32 +650,30 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
       auto find_unit = [&]() {  // from unit u on, the first with a contraction
         for (; u < total; u += unit_step) {
           const TcUnit t = unit_at(u);
-          steps = steps_of(t);
+          steps = t.steps;
           if (steps == 0) continue;
-          left = DW ? t.count : p.K;
+          left = left_of(t);
           have = MS ? min(kBlkM, p.N - t.n0) : DW ? min((t.nt + 63) & ~63, p.K - t.r0) : t.nt;
           put = MS ? kBlkM : DW ? (t.nt + 63) & ~63 : t.nt;
           src = arr + (MS ? (DW ? t.row0 * ld : (int64_t)t.e * p.K * p.N) : t.row0 * ld);
-          src += MS ? (BLK ? (int64_t)t.n0 : t.n0 * ld) : BLK ? (int64_t)t.r0 : t.r0 * ld;
+          src += (MS ? (BLK ? (int64_t)t.n0 : t.n0 * ld) : BLK ? (int64_t)t.r0 : t.r0 * ld) + t.kb0 * (BLK ? kBlkK * ld : kBlkK);
           return;
         }
         more = false;
       };
       struct Half {
         uint32_t v[2][8];
-        int h;
-        bool put[2], first, last;  // of its stage
+        int h, put;  // of its stage the first (0) or second; rows or columns that are stored
       };
       auto load = [&](Half& x) {
         x.h = h;
-        x.first = h == 0;
+        x.put = put;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int r = row + 32 * i + (BLK ? 0 : 64 * h), c = BLK ? 64 * h + 8 * chunk : 8 * chunk;
           const float* q = src + r * ld + c;
           // elements that exist: of a row `have` or what is left of the contraction
           const int n = r < (BLK ? min(left, kBlkK) : have) ? (BLK ? have : left) - c : 0;
-          x.put[i] = BLK || r < put;
           if constexpr (VEC) {
             asm volatile(
                 "{\n\t.reg .pred p, q;\n\t"
@@ -686,9 +695,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
           }
         }
         // on to the next
-        x.last = 64 * (h + 1) >= put;
-        ++h;
-        if (x.last) {
+        if (64 * ++h >= put) {
           h = 0;
           src += BLK ? kBlkK * ld : kBlkK;
           left -= kBlkK;
@@ -702,7 +709,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
       int s = 0;
       uint32_t ph = 0;
       auto split = [&](const Half& x) {
-        if (x.first && !wait_all(empty0 + 8u * s, ph ^ 1u, 2000 + s)) return false;
+        if (x.h == 0 && !wait_all(empty0 + 8u * s, ph ^ 1u, 2000 + s)) return false;
         const uint32_t to = base + (uint32_t)s * stage_bytes + lane_dst + (uint32_t)(x.h * kBoxBytes);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -720,13 +727,13 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
             b -= __uint_as_float(w[1][k] & 0xFFFF0000u);
             w[2][k] = pack_bf16x2(a, b);
           }
-          if (x.put[i]) {
+          if (BLK || row + 32 * i + 64 * x.h < x.put) {
 #pragma unroll
             for (int j = 0; j < 3; ++j)
               st_shared_v4(to + (uint32_t)(i * 4096) + (uint32_t)j * image, w[j][0], w[j][1], w[j][2], w[j][3]);
           }
         }
-        if (x.last) {
+        if (64 * (x.h + 1) >= x.put) {
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&full[s]);
@@ -783,17 +790,20 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
     };
     for (int u = unit0; u < total; u += unit_step) {
       const TcUnit t = unit_at(u);
-      const int steps = steps_of(t);
+      const int steps = t.steps;
       if (steps == 0 && p.accumulate) continue;
       const int n = t.n0 + rank * kBlkM + q * 32 + lane;
-      const int64_t row = (DW ? (int64_t)t.e * p.K : (int64_t)t.row0) + t.r0;
+      const bool there = n < p.N;
+      // the lane's column of the tile's first row
+      const int64_t first = ((DW ? (int64_t)t.e * p.K : (int64_t)t.row0) + t.r0) * p.ldo + n + (PARTS ? t.part * p.split_stride : 0);
+      const int nt = t.nt;
       // 32 rows from c0 on
       auto store = [&](int c0, const float (&v)[32]) {
-        if (n >= p.N) return;
-        const int64_t at = (row + c0) * p.ldo + n;
-        if constexpr (F32) put_tile<float, DW>(p, at, t.nt - c0, v);
-        else if (p.odt == MOE_DT_BF16) put_tile<__nv_bfloat16, DW>(p, at, t.nt - c0, v);
-        else put_tile<__half, DW>(p, at, t.nt - c0, v);
+        if (!there) return;
+        const int64_t at = first + c0 * p.ldo;
+        if constexpr (F32) put_tile<float, DW>(p, at, nt - c0, v);
+        else if (p.odt == MOE_DT_BF16) put_tile<__nv_bfloat16, DW>(p, at, nt - c0, v);
+        else put_tile<__half, DW>(p, at, nt - c0, v);
       };
       if constexpr (F32) {
         constexpr int kParts = kTileRows / kStep;
@@ -807,7 +817,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
           tc_fence_after();
 #pragma unroll
           for (int i = 0; i < kParts; ++i) {
-            if (c_first + kStep * i < t.nt) {
+            if (c_first + kStep * i < nt) {
               // (16 at a time where loading warps leave a thread 72 registers)
               const uint32_t from = tq + (uint32_t)(acc * kAccCols + c_first + kStep * i);
               if constexpr (loads(MODE)) {
@@ -829,16 +839,16 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
         }
 #pragma unroll
         for (int i = 0; i < kParts; ++i)
-          if (c_first + kStep * i < t.nt) store(c_first + kStep * i, sum[i]);
+          if (c_first + kStep * i < nt) store(c_first + kStep * i, sum[i]);
       } else if (steps == 0) {
         float v[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = 0.f;
-        for (int c0 = c_first; c0 < t.nt; c0 += kStep) store(c0, v);
+        for (int c0 = c_first; c0 < nt; c0 += kStep) store(c0, v);
       } else {
         if (!wait_all(smem_u32(&tfull[acc]), aph, 2500 + acc)) goto stored;
         tc_fence_after();
-        for (int c0 = c_first; c0 < t.nt; c0 += kStep) {
+        for (int c0 = c_first; c0 < nt; c0 += kStep) {
           float v[32];
           tmem_ld32(tq + (uint32_t)(acc * kAccCols + c0), v);
           store(c0, v);
@@ -859,6 +869,27 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
   }
 }
 
+// Results from their partial sums, added in order: n columns of rows first..last (of experts
+// [offsets[0], offsets[G]); NULL: of all).
+template <typename T>
+__global__ void __launch_bounds__(256)
+    sum_parts_kernel(const float* __restrict__ part, int splits, int64_t stride, const int* off, int G, int64_t rows, int n,
+                     T* out, int64_t ldo, bool add) {
+  ops_begin();
+  const int64_t first = off ? min((int64_t)max(gload(off), 0), rows) : 0, last = off ? min((int64_t)max(gload(off + G), 0), rows) : rows;
+  // (at most 76 tiles of 256 x 256: 32 bits)
+  const int total = last > first ? (int)((last - first) * n) : 0;
+  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < total; i += gridDim.x * blockDim.x) {
+    const int64_t r = first + i / n, c = i % n;
+    const float* q = part + r * n + c;
+    T* o = out + r * ldo + c;
+    float s = add ? to_f32(*o) : 0.f;
+#pragma unroll 8
+    for (int k = 0; k < splits; ++k) s += gload(q + k * stride);
+    *o = from_f32<T>(s);
+  }
+}
+
 // ------------------------------------------------------------------ host side
 uintptr_t bits(const void* p) { return reinterpret_cast<uintptr_t>(p); }
 
@@ -876,18 +907,14 @@ bool tc_map(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <ProdForm FORM, TcMode MODE, bool F32>
+template <ProdForm FORM, TcMode MODE, bool F32, bool PARTS>
 cudaError_t launch_tc(const CUtensorMap* tm, const ProdArgs& p, uint32_t formats, cudaStream_t st) {
-  auto kern = tc_product_kernel<FORM, MODE, F32>;
+  auto kern = tc_product_kernel<FORM, MODE, F32, PARTS>;
   static SmemAllowed allowed;
   const cudaError_t e = allow_smem(kern, kSmemP, allowed);
   if (e != cudaSuccess) return e;
   const char* name = FORM == PROD_DW ? "grouped_product_dw" : "grouped_product";
-  // units at most
-  constexpr int kTileRows = tile_most(MODE, F32), cols = MODE == TC_PAIR ? 2 * kBlkM : kBlkM;
-  const int64_t tiles = FORM == PROD_DW ? (int64_t)((p.K + kTileRows - 1) / kTileRows) * p.G
-                                        : (int64_t)p.rows / kTileRows + (p.G < p.rows ? p.G : p.rows);
-  const int64_t units = tiles * ((p.N + cols - 1) / cols);
+  const int64_t units = units_of(FORM, MODE, F32, p.rows, p.K, p.N, p.G) * p.splits;
   const dim3 block(threads_of(MODE));
   if constexpr (MODE != TC_PAIR) {
     const int grid = units < num_sms() ? (int)units : num_sms();
@@ -915,6 +942,31 @@ cudaError_t launch_tc(const CUtensorMap* tm, const ProdArgs& p, uint32_t formats
   }
 }
 
+// The kernel in mode MODE, with its contraction in parts if that pays.
+template <ProdForm FORM, TcMode MODE, bool F32>
+cudaError_t launch_parts(const CUtensorMap* tm, const ProdArgs& p, uint32_t formats, cudaStream_t st) {
+  const int splits = splits_of(FORM, MODE, p.rows, p.K, p.N, p.G);
+  if (splits <= 1) return launch_tc<FORM, MODE, F32, false>(tm, p, formats, st);
+  ProdArgs q = p;
+  const int64_t n = results_of(FORM, p.rows, p.K, p.N, p.G);
+  q.out = p.ws;
+  q.ldo = p.N;
+  q.odt = MOE_DT_F32;
+  q.accumulate = 0;
+  q.splits = splits;
+  q.split_stride = n;
+  cudaError_t e = launch_tc<FORM, MODE, true, true>(tm, q, formats, st);
+  if (e != cudaSuccess) return e;
+  const int64_t blocks = (n + 255) / 256, most = (int64_t)num_sms() * 8;
+  return with_dtype(p.odt, [&](auto t) {
+    using T = decltype(t);
+    const bool dw = FORM == PROD_DW;
+    return launch_ops("grouped_product_sum", sum_parts_kernel<T>, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0,
+                      st, static_cast<const float*>(p.ws), splits, n, dw ? (const int*)nullptr : p.off, p.G,
+                      dw ? (int64_t)p.G * p.K : (int64_t)p.rows, p.N, static_cast<T*>(p.out), p.ldo, p.accumulate != 0);
+  });
+}
+
 template <ProdForm FORM, bool F32>
 cudaError_t launch_form(int dtype, const ProdArgs& p, cudaStream_t st) {
   const uint32_t fmt = dtype == MOE_DT_BF16 ? 1u : 0u, formats = (fmt << 7) | (fmt << 10);
@@ -924,11 +976,11 @@ cudaError_t launch_form(int dtype, const ProdArgs& p, cudaStream_t st) {
   if (!copy) {
     memset(tm, 0, sizeof(tm));
     if constexpr (F32) {
-      if (dtype == MOE_DT_F32) return launch_tc<FORM, TC_SPLIT, true>(tm, p, (1u << 7) | (1u << 10), st);
+      if (dtype == MOE_DT_F32) return launch_parts<FORM, TC_SPLIT, true>(tm, p, (1u << 7) | (1u << 10), st);
     }
-    return launch_tc<FORM, TC_LOAD, F32>(tm, p, formats, st);
+    return launch_parts<FORM, TC_LOAD, F32>(tm, p, formats, st);
   }
-  const bool pair = p.N > kBlkM && p.rows >= 64 * (int64_t)p.G;
+  const bool pair = takes_pairs(p.rows, p.N, p.G);
   const uint64_t R = (uint64_t)p.rows, K = (uint64_t)p.K, N = (uint64_t)p.N, G = (uint64_t)p.G;
   bool ok;
   if (FORM == PROD_DW) {
@@ -939,19 +991,9 @@ cudaError_t launch_form(int dtype, const ProdArgs& p, cudaStream_t st) {
          tc_map(&tm[1], p.a, K, R, p.lda, 0, 0, 64, 32) && tc_map(&tm[2], p.a, K, R, p.lda, 0, 0, 64, 128);
   }
   if (!ok) return cudaErrorInvalidValue;
-  return pair ? launch_tc<FORM, TC_PAIR, F32>(tm, p, formats, st) : launch_tc<FORM, TC_COPY, F32>(tm, p, formats, st);
+  return pair ? launch_parts<FORM, TC_PAIR, F32>(tm, p, formats, st) : launch_parts<FORM, TC_COPY, F32>(tm, p, formats, st);
 }
 
 }  // namespace
-
-cudaError_t launch_product_tc(ProdForm form, int dtype, const ProdArgs& p, cudaStream_t st) {
-  const bool f32 = p.odt == MOE_DT_F32;
-  switch (form) {
-    case PROD_ROWS: return f32 ? launch_form<PROD_ROWS, true>(dtype, p, st) : launch_form<PROD_ROWS, false>(dtype, p, st);
-    case PROD_ROWS_T:
-      return f32 ? launch_form<PROD_ROWS_T, true>(dtype, p, st) : launch_form<PROD_ROWS_T, false>(dtype, p, st);
-    default: return f32 ? launch_form<PROD_DW, true>(dtype, p, st) : launch_form<PROD_DW, false>(dtype, p, st);
-  }
-}
 
 }  // namespace moe

@@ -1,5 +1,5 @@
 // tc_roles.cuh -- what the warp-specialised product kernels of the operators (mxfp4.cu,
-// product_tc.cu) share: copies, commits and waits predicated on an elected lane, for
+// product_tc.cuh) share: copies, commits and waits predicated on an elected lane, for
 // loops that whole warps run without branches, and the clusters a kernel can have.
 #pragma once
 

@@ -107,6 +107,15 @@ def test_strides_and_alignment(dt, odt, counts, K, N, pad, shift):
     run_all(dt, odt, counts, K, N, pad, shift)
 
 
+@pytest.mark.parametrize("dt,odt", TYPES)
+@pytest.mark.parametrize("counts,K,N,first,behind", [
+    ([8], 4096, 24, 0, 0), ([40, 3], 2048, 130, 7, 90), ([3000], 24, 136, 0, 0), ([1, 0, 2500, 17], 96, 40, 3, 1),
+    ([130], 1100, 260, 0, 0), ([5], 1025, 1023, 2, 3), ([2049], 65, 33, 0, 0)])
+def test_long_contractions_of_few_tiles(dt, odt, counts, K, N, first, behind):
+    """Contractions cut into parts, those of experts that are shorter than the others too."""
+    run_all(dt, odt, counts, K, N, first=first, behind=behind)
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("K,N", [(64, 128), (61, 45)])
 def test_rows_of_some_of_the_experts(dt, K, N):
