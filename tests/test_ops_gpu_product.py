@@ -1,7 +1,7 @@
 """Products by expert and their gradients on the GPU, against 64 bits.
 
-Bounds: a product of two 16-bit values is exact in fp32, one of fp32 values enters its sum
-with one rounding; a sum of n of them in fp32, whatever the order and even if every addition
+Bounds: a product of two 16-bit values is exact in fp32; one of fp32 values, in three parts of 8
+bits each, misses terms of less than 2^-24 of it; a sum of n of them in fp32, whatever the order and even if every addition
 truncates, is off by at most n 2^-23 of the sum of magnitudes (n + 1 with an initial value);
 then one rounding (u |want|)."""
 import pytest
@@ -180,6 +180,29 @@ def test_non_finite_values_stay_in_their_rows(dt):
     assert bool(bad[0, 3].all()) and bool(bad[1, 5].all())
     bad[0, 3] = bad[1, 5] = False
     assert not bool(bad.any())
+
+
+def test_fp32_values_over_their_range():
+    """Rows and weights of very different sizes, the largest values (which the nearest 16-bit value is past)
+    and an infinity, which stays in its row."""
+    g = gen(9)
+    K, N, n = 70, 50, 40
+    x, w = randn(g, n, K), randn(g, 1, K, N)
+    x *= torch.exp2(torch.randint(-60, 61, (n, K), generator=g, device="cuda").float())
+    w *= torch.exp2(torch.randint(-30, 31, (1, K, N), generator=g, device="cuda").float())
+    x[0] = torch.finfo(torch.float32).max
+    x[1] = -torch.finfo(torch.float32).max
+    w[0, 0] *= 2.0 ** -40
+    x[0:2, 1:] = 0
+    out, ws = torch.empty(n, N, device="cuda"), workspace(n, K, N, 1)
+    off = torch.tensor([0, n])
+    ops.moe_grouped_product(x, w, None, out, ws)
+    check_rows(x, w, off, out, "f32", False)
+    x[3, 4] = float("inf")
+    ops.moe_grouped_product(x, w, None, out, ws)
+    assert not bool(torch.isfinite(out[3]).any())
+    out[3], x[3] = 0, 0
+    check_rows(x, w, off, out, "f32", False)
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
