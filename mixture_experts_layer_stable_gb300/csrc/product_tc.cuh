@@ -988,7 +988,10 @@ cudaError_t launch_form(int dtype, const ProdArgs& p, cudaStream_t st) {
     tm[2] = tm[1];
   } else {
     ok = (FORM == PROD_ROWS ? tc_map(&tm[0], p.b, N, K, N, G, K * N, 64, 64) : tc_map(&tm[0], p.b, K, N, K, G, K * N, 64, 128)) &&
-         tc_map(&tm[1], p.a, K, R, p.lda, 0, 0, 64, 32) && tc_map(&tm[2], p.a, K, R, p.lda, 0, 0, 64, 128);
+         tc_map(&tm[1], p.a, K, R, p.lda, 0, 0, 64, 32);
+    // (boxes of 128 rows: of no use to fewer, and a map takes the host a while)
+    if (p.rows < 97) tm[2] = tm[1];
+    else ok = ok && tc_map(&tm[2], p.a, K, R, p.lda, 0, 0, 64, 128);
   }
   if (!ok) return cudaErrorInvalidValue;
   return pair ? launch_parts<FORM, TC_PAIR, F32>(tm, p, formats, st) : launch_parts<FORM, TC_COPY, F32>(tm, p, formats, st);

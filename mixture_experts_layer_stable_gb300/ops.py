@@ -265,12 +265,18 @@ def moe_grouped_product(x, weights, offsets, out, ws, transposed=False, stream=N
     rows, K = x.shape
     n, N = out.shape
     xt, ot = x.dtype, out.dtype
-    if n != rows or tuple(weights.shape) != ((G, N, K) if transposed else (G, K, N)):
+    ldx, x1 = x.stride()
+    ldo, o1 = out.stride()
+    # (one condition: a call of a few rows waits for its checks)
+    if (n != rows or weights.shape != ((G, N, K) if transposed else (G, K, N)) or weights.dtype is not xt or
+            not weights.is_contiguous() or weights.get_device() != dev or out.get_device() != dev or
+            ws.get_device() != dev or not ws.is_contiguous() or (x1 != 1 and K != 1) or (o1 != 1 and N != 1)):
         raise MoeError(MOE_ERR_INVALID_ARG, w)
-    rc = (_lib or lib()).moe_grouped_product(
-        _dt(xt, w), _dt(ot, w), rows, K, N, G, off, x.data_ptr(), _ld(x, rows, K, w),
-        _flat(weights, G * K * N, xt, dev, w), int(transposed), out.data_ptr(), _rows(out, rows, N, ot, dev, w),
-        _ws(ws, dev, w), ws.nbytes, st)
+    if rows <= 1:
+        ldx, ldo = max(ldx, K), max(ldo, N)
+    rc = (_lib or lib()).moe_grouped_product(_dt(xt, w), _dt(ot, w), rows, K, N, G, off, x.data_ptr(), ldx,
+                                             weights.data_ptr(), 1 if transposed else 0, out.data_ptr(), ldo,
+                                             ws.data_ptr(), ws.nbytes, st)
     if rc:
         raise MoeError(rc, w)
 
@@ -282,14 +288,19 @@ def moe_grouped_product_dw(x, dy, offsets, dweights, ws, accumulate=False, strea
     st = _current_stream(dev) if stream is None else _handle(stream)
     G, off = _segments(offsets, dev, w)
     rows, K = x.shape
-    N = dy.shape[1]
-    xt, wt = x.dtype, dweights.dtype
-    if tuple(dweights.shape) != (G, K, N):
+    n, N = dy.shape
+    xt = x.dtype
+    ldx, x1 = x.stride()
+    lddy, y1 = dy.stride()
+    if (n != rows or dweights.shape != (G, K, N) or dy.dtype is not xt or not dweights.is_contiguous() or
+            dweights.get_device() != dev or dy.get_device() != dev or ws.get_device() != dev or not ws.is_contiguous() or
+            (x1 != 1 and K != 1) or (y1 != 1 and N != 1)):
         raise MoeError(MOE_ERR_INVALID_ARG, w)
-    rc = (_lib or lib()).moe_grouped_product_dw(
-        _dt(xt, w), _dt(wt, w), rows, K, N, G, off, x.data_ptr(), _ld(x, rows, K, w), dy.data_ptr(),
-        _rows(dy, rows, N, xt, dev, w), _flat(dweights, G * K * N, wt, dev, w), int(accumulate), _ws(ws, dev, w),
-        ws.nbytes, st)
+    if rows <= 1:
+        ldx, lddy = max(ldx, K), max(lddy, N)
+    rc = (_lib or lib()).moe_grouped_product_dw(_dt(xt, w), _dt(dweights.dtype, w), rows, K, N, G, off, x.data_ptr(), ldx,
+                                                dy.data_ptr(), lddy, dweights.data_ptr(), 1 if accumulate else 0,
+                                                ws.data_ptr(), ws.nbytes, st)
     if rc:
         raise MoeError(rc, w)
 
