@@ -633,15 +633,17 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
     else run_side(std::false_type());
   } else if (MODE == TC_SPLIT && warp >= 2 + kEpi) {
     // Eight warps load and split the M side, eight the N side, each every eighth row of 64
-    // values.  Eight lanes have a row, four rows are a group (row + 32 (i % 2) of block i / 2,
-    // or 64 (i / 2) rows on); two groups' loads are under way while two are split.
+    // values.  Where rows are whole 16-byte vectors eight lanes have a row, four rows are a
+    // group (row + 32 (i % 2) of block i / 2, or 64 (i / 2) rows on), and two groups' loads are
+    // under way while two are split; else a lane has two values of each of eight rows.
     const int w7 = (warp - 2 - kEpi) & 7, chunk = lane & 7;
     auto run_side = [&](auto m_side, auto vectors) {
       constexpr bool MS = decltype(m_side)::value, VEC = decltype(vectors)::value, BLK = MS ? M_MN : N_MN;
       const float* arr = static_cast<const float*>(MS ? p.b : p.a);
       const int64_t ld = MS ? p.ldb : p.lda;
       const int row = w7 + 8 * (lane >> 3);
-      const uint32_t lane_dst = (MS ? 0u : n_at) + (uint32_t)(row * 128 + ((chunk ^ w7) << 4));
+      const uint32_t lane_dst = (MS ? 0u : n_at) + (VEC ? (uint32_t)(row * 128 + ((chunk ^ w7) << 4))
+                                                        : (uint32_t)(w7 * 128 + (((lane >> 2) ^ w7) << 4) + (lane & 3) * 4));
       const uint32_t image = MS ? (uint32_t)kABytes : n_image;
       // where the next half stage (two groups) is
       int u = unit0, kb = 0, steps = 0, h = 0, left = 0, have = 0, put = 0;
@@ -662,19 +664,25 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
         more = false;
       };
       struct Half {
-        uint32_t v[2][8];
+        uint32_t v[16];
         int h, put;  // of its stage the first (0) or second; rows or columns that are stored
       };
       auto load = [&](Half& x) {
         x.h = h;
         x.put = put;
+        // row r and its values from c on; n: those that exist (of a row `have` or what is
+        // left of the contraction)
+        auto at = [&](int r, int c, int& n) {
+          n = r < (BLK ? min(left, kBlkK) : have) ? (BLK ? have : left) - c : 0;
+          return src + r * ld + c;
+        };
+        const int c0 = BLK ? 64 * h : 0, r0 = BLK ? 0 : 64 * h;
+        if constexpr (VEC) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = row + 32 * i + (BLK ? 0 : 64 * h), c = BLK ? 64 * h + 8 * chunk : 8 * chunk;
-          const float* q = src + r * ld + c;
-          // elements that exist: of a row `have` or what is left of the contraction
-          const int n = r < (BLK ? min(left, kBlkK) : have) ? (BLK ? have : left) - c : 0;
-          if constexpr (VEC) {
+          for (int i = 0; i < 2; ++i) {
+            int n;
+            const float* q = at(r0 + row + 32 * i, c0 + 8 * chunk, n);
+            uint32_t* v = x.v + 8 * i;
             asm volatile(
                 "{\n\t.reg .pred p, q;\n\t"
                 "setp.gt.s32 p, %9, 0;\n\t"
@@ -683,15 +691,23 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
                 "mov.b32 %4, 0;\n\tmov.b32 %5, 0;\n\tmov.b32 %6, 0;\n\tmov.b32 %7, 0;\n\t"
                 "@p ld.global.v4.u32 {%0, %1, %2, %3}, [%8];\n\t"
                 "@q ld.global.v4.u32 {%4, %5, %6, %7}, [%8+16];\n\t}"
-                : "=&r"(x.v[i][0]), "=&r"(x.v[i][1]), "=&r"(x.v[i][2]), "=&r"(x.v[i][3]), "=&r"(x.v[i][4]),
-                  "=&r"(x.v[i][5]), "=&r"(x.v[i][6]), "=&r"(x.v[i][7])
+                : "=&r"(v[0]), "=&r"(v[1]), "=&r"(v[2]), "=&r"(v[3]), "=&r"(v[4]), "=&r"(v[5]), "=&r"(v[6]), "=&r"(v[7])
                 : "l"(q), "r"(n));
-          } else {
+          }
+        } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              asm volatile("{\n\t.reg .pred p;\n\tsetp.gt.s32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t@p ld.global.u32 %0, [%1];\n\t}"
-                           : "=&r"(x.v[i][j])
-                           : "l"(q + j), "r"(n - j));
+          for (int j = 0; j < 8; ++j) {
+            int n;
+            const float* q = at(r0 + w7 + 8 * j, c0 + 2 * lane, n);
+            asm volatile(
+                "{\n\t.reg .pred p, q;\n\t"
+                "setp.gt.s32 p, %3, 0;\n\t"
+                "setp.gt.s32 q, %3, 1;\n\t"
+                "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
+                "@p ld.global.u32 %0, [%2];\n\t"
+                "@q ld.global.u32 %1, [%2+4];\n\t}"
+                : "=&r"(x.v[2 * j]), "=&r"(x.v[2 * j + 1])
+                : "l"(q), "r"(n));
           }
         }
         // on to the next
@@ -711,26 +727,40 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
       auto split = [&](const Half& x) {
         if (x.h == 0 && !wait_all(empty0 + 8u * s, ph ^ 1u, 2000 + s)) return false;
         const uint32_t to = base + (uint32_t)s * stage_bytes + lane_dst + (uint32_t)(x.h * kBoxBytes);
+        // two values' parts
+        auto parts = [](const uint32_t* v, uint32_t& h2, uint32_t& m2, uint32_t& l2) {
+          constexpr float kMax = 3.3895313892515355e38f;  // (larger ones would round to an infinity)
+          float a = __uint_as_float(v[0]), b = __uint_as_float(v[1]);
+          h2 = pack_bf16x2(fminf(fmaxf(a, -kMax), kMax), fminf(fmaxf(b, -kMax), kMax));
+          a -= __uint_as_float(h2 << 16);
+          b -= __uint_as_float(h2 & 0xFFFF0000u);
+          m2 = pack_bf16x2(a, b);
+          a -= __uint_as_float(m2 << 16);
+          b -= __uint_as_float(m2 & 0xFFFF0000u);
+          l2 = pack_bf16x2(a, b);
+        };
+        if constexpr (VEC) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t w[3][4];
+          for (int i = 0; i < 2; ++i) {
+            uint32_t w[3][4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            // (the largest values would round to an infinity)
-            constexpr float kMax = 3.3895313892515355e38f;
-            float a = __uint_as_float(x.v[i][2 * k]), b = __uint_as_float(x.v[i][2 * k + 1]);
-            w[0][k] = pack_bf16x2(fminf(fmaxf(a, -kMax), kMax), fminf(fmaxf(b, -kMax), kMax));
-            a -= __uint_as_float(w[0][k] << 16);
-            b -= __uint_as_float(w[0][k] & 0xFFFF0000u);
-            w[1][k] = pack_bf16x2(a, b);
-            a -= __uint_as_float(w[1][k] << 16);
-            b -= __uint_as_float(w[1][k] & 0xFFFF0000u);
-            w[2][k] = pack_bf16x2(a, b);
+            for (int k = 0; k < 4; ++k) parts(x.v + 8 * i + 2 * k, w[0][k], w[1][k], w[2][k]);
+            if (BLK || row + 32 * i + 64 * x.h < x.put) {
+#pragma unroll
+              for (int j = 0; j < 3; ++j)
+                st_shared_v4(to + (uint32_t)(i * 4096) + (uint32_t)j * image, w[j][0], w[j][1], w[j][2], w[j][3]);
+            }
           }
-          if (BLK || row + 32 * i + 64 * x.h < x.put) {
+        } else {
 #pragma unroll
-            for (int j = 0; j < 3; ++j)
-              st_shared_v4(to + (uint32_t)(i * 4096) + (uint32_t)j * image, w[j][0], w[j][1], w[j][2], w[j][3]);
+          for (int j = 0; j < 8; ++j) {
+            uint32_t w[3];
+            parts(x.v + 2 * j, w[0], w[1], w[2]);
+            if (BLK || w7 + 8 * j + 64 * x.h < x.put) {
+#pragma unroll
+              for (int i = 0; i < 3; ++i)
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + (uint32_t)(j * 1024) + (uint32_t)i * image), "r"(w[i]) : "memory");
+            }
           }
         }
         if (64 * (x.h + 1) >= x.put) {
