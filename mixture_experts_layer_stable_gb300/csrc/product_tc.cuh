@@ -243,7 +243,9 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
   const uint32_t n_image = (uint32_t)cap_n * 128u, n_at = kImages * kABytes, stage_bytes = n_at + kImages * n_image;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   // (loading warps: two stages' rows as they lie in memory, 144 bytes each, behind the ring)
-  const uint32_t raw_bytes = MODE == TC_LOAD ? 2u * (uint32_t)(kBlkM + cap_n) * kRawRow : 0u;
+  // (of groups in pairs, 64 rows)
+  const int raw_n = (cap_n + 63) & ~63;
+  const uint32_t raw_bytes = MODE == TC_LOAD ? 2u * (uint32_t)(kBlkM + raw_n) * kRawRow : 0u;
   const int S = min(kStagesP, (int)((kSmemP - raw_bytes - (base - smem_u32(smem_raw))) / stage_bytes));
 
   // The L-th unit in the order they are taken; each role keeps its place in the experts.
@@ -484,22 +486,41 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
       const uint32_t apart = BLK ? 128u : (uint32_t)(128 * ld);
       const uint32_t lane_dst = (MS ? 0u : (uint32_t)kABytes) + (uint32_t)(row * 128 + ((chunk ^ w7) << 4));
       // the warp's rows as they lie in memory: group i's four at 4 i, two buffers
-      const uint32_t raw_size = (uint32_t)((MS ? kBlkM : cap_n) / 8 * kRawRow);
+      const uint32_t raw_size = (uint32_t)((MS ? kBlkM : raw_n) / 8 * kRawRow);
       const uint32_t raw = base + (uint32_t)S * stage_bytes + (MS ? 0u : 2u * kBlkM * kRawRow) + 2u * raw_size * (uint32_t)w7;
       const uint32_t raw_lane = (uint32_t)((lane >> 3) * kRawRow + 16 * chunk);
       const bool near = ld < (1 << 22);  // a tile's offsets have 32 bits
-      auto copy16 = [](uint32_t to, const uint8_t* q) {
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(q) : "memory");
-      };
       struct Stage {
-        const uint16_t* src;        // its row 0
-        int left, have, put, sh;    // of the contraction; rows or columns that exist, that are stored
+        const uint16_t* src;      // its row 0
+        int left, have, put, sh;  // of the contraction; rows or columns that exist, that are stored
         bool fast;
       };
-      // where the next stage is
-      int u = unit0, kb = 0, steps = 0;
+      // Where the next stage is.  What is the same for all of a unit's whole stages is worked
+      // out once: a warp's instructions, one after the other, are what a stage takes.
+      int u = unit0, kb = 0, steps = 0, fast0 = 0, fast1 = 0;
+      uint32_t copies = 0;           // bit i: the lane's block of group i, bit 8 + i: the row's ninth
+      const uint8_t* blk = nullptr;  // the lane's block of the stage's group 0
       Stage at = {};
       bool more = true;
+      // which blocks hold some of `rows` rows' (or their first `bytes` bytes')
+      auto copies_of = [&](int rows, int bytes) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = row + 32 * (i & 1) + (BLK ? 0 : 64 * (i >> 1)), b = BLK ? 128 * (i >> 1) : 0;
+          if (32 * i < at.put && r < rows) {
+            if (b + 16 * chunk < bytes) m |= 1u << i;
+            if (chunk == 7 && at.sh != 0 && b + 128 < bytes) m |= 256u << i;
+          }
+        }
+        return m;
+      };
+      // whether a stage of `len` at `src` lies in the array's whole blocks
+      auto inside = [&](const uint16_t* src, int len) {
+        const int64_t span = BLK ? (len - 1) * ld + at.have : (at.have - 1) * ld + len;
+        const uintptr_t f = reinterpret_cast<uintptr_t>(src);
+        return near && (f & ~(uintptr_t)15) >= lo && ((f + 2 * span + 15) & ~(uintptr_t)15) <= hi;
+      };
       auto find_unit = [&]() {  // from unit u on, the first with a contraction
         for (; u < total; u += unit_step) {
           const TcUnit t = unit_at(u);
@@ -511,29 +532,50 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
           at.src = arr + (MS ? (DW ? t.row0 * ld : (int64_t)t.e * p.K * p.N) : t.row0 * ld);
           at.src += (MS ? (BLK ? (int64_t)t.n0 : t.n0 * ld) : BLK ? (int64_t)t.r0 : t.r0 * ld) + t.kb0 * (BLK ? kBlkK * ld : kBlkK);
           at.sh = (int)(reinterpret_cast<uintptr_t>(at.src + w7 * ld) & 15);
+          blk = reinterpret_cast<const uint8_t*>(at.src + w7 * ld) - at.sh + off;
+          copies = copies_of(BLK ? kBlkK : at.have, 2 * (BLK ? at.have : kBlkK) + at.sh);
+          // (only the first stage can begin before the array's first whole block, only the last
+          // whole one, and what is left, end behind its last)
+          const int whole = min(steps, at.left / kBlkK);
+          const int64_t next = BLK ? kBlkK * ld : kBlkK;
+          fast0 = whole > 0 && inside(at.src, kBlkK) ? 0 : 1;
+          fast1 = whole == 0 ? 0 : inside(at.src + (whole - 1) * next, kBlkK) ? whole : whole - 1;
           return;
         }
         more = false;
       };
       auto issue = [&](uint32_t to) {
-        const int len = min(at.left, kBlkK);
-        const int64_t span = BLK ? (len - 1) * ld + at.have : (at.have - 1) * ld + len;  // elements of the stage
-        const uintptr_t f = reinterpret_cast<uintptr_t>(at.src);
-        at.fast = near && (f & ~(uintptr_t)15) >= lo && ((f + 2 * span + 15) & ~(uintptr_t)15) <= hi;
-        if (at.fast) {
-          const uint8_t* q = reinterpret_cast<const uint8_t*>(at.src + w7 * ld) - at.sh;
-          // a row's blocks; those that hold none of the elements that exist are left out
-          const int rows = BLK ? len : at.have, bytes = 2 * (BLK ? at.have : len) + at.sh;
-          for (int i = 0; 32 * i < at.put; ++i) {
-            const int r = row + 32 * (i & 1) + (BLK ? 0 : 64 * (i >> 1)), b = BLK ? 128 * (i >> 1) : 0;
-            const uint8_t* e = q + (off + (i & 1) * half + (i >> 1) * apart);
-            if (r < rows && b + 16 * chunk < bytes) copy16(to + raw_lane + (uint32_t)(4 * i * kRawRow), e);
-            if (chunk == 7 && at.sh != 0 && r < rows && b + 128 < bytes) copy16(to + raw_lane + (uint32_t)(4 * i * kRawRow) + 16, e + 16);
-          }
+        at.fast = kb >= fast0 && kb < fast1;
+        uint32_t m = copies;
+        if (!at.fast) {
+          const int len = min(at.left, kBlkK);
+          at.fast = inside(at.src, len);
+          m = at.fast ? copies_of(BLK ? len : at.have, 2 * (BLK ? at.have : len) + at.sh) : 0u;
+        }
+        // (loops of two groups: the warps' roles share the instruction caches, and whole
+        // unrolling made the rows' gradient of that product 375 us, not 182)
+        to += raw_lane;
+        uint32_t o = 0;
+#pragma unroll 1
+        for (int i = 0; 32 * i < at.put; i += 2, m >>= 2, o += apart, to += 8 * kRawRow) {
+          const uint8_t *e = blk + o, *e1 = blk + (o + half);
+          asm volatile(
+              "{\n\t.reg .pred p, q, r, s;\n\t.reg .b32 t;\n\t"
+              "and.b32 t, %3, 1;\n\tsetp.ne.b32 p, t, 0;\n\t"
+              "and.b32 t, %3, 256;\n\tsetp.ne.b32 q, t, 0;\n\t"
+              "and.b32 t, %3, 2;\n\tsetp.ne.b32 r, t, 0;\n\t"
+              "and.b32 t, %3, 512;\n\tsetp.ne.b32 s, t, 0;\n\t"
+              "@p cp.async.cg.shared.global [%0], [%1], 16;\n\t"
+              "@r cp.async.cg.shared.global [%0+576], [%2], 16;\n\t"
+              "@q cp.async.cg.shared.global [%0+16], [%1+16], 16;\n\t"
+              "@s cp.async.cg.shared.global [%0+592], [%2+16], 16;\n\t}" ::"r"(to),
+              "l"(e), "l"(e1), "r"(m)
+              : "memory");
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
         const Stage now = at;
         at.src += BLK ? kBlkK * ld : kBlkK;
+        blk += BLK ? 2 * kBlkK * ld : 2 * kBlkK;
         at.left -= kBlkK;
         if (++kb == steps) {
           kb = 0;
@@ -542,44 +584,46 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
         }
         return now;
       };
-      // 16 bytes of shared memory from byte 2 * halves of two blocks
-      auto shifted = [](auto halves, uint32_t from, uint32_t (&v)[4]) {
-        constexpr int H = decltype(halves)::value, W = H / 2;
-        constexpr uint32_t sel = H % 2 ? 0x5432 : 0x3210;
-        uint32_t w[8];
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(from));
-        if constexpr (H > 0)
-          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7]) : "r"(from + 16));
-        else
-          w[4] = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = __byte_perm(w[W + k], w[W + k + 1], sel);
-      };
+      // two groups' 16 bytes from word W, and half of one if `sel` says so, of their two blocks
       auto store = [&](const Stage& x, uint32_t from, uint32_t to) {
-        // (not unrolled further than its two rows' groups: the eight shifts' copies are long)
-        auto by = [&](auto halves) {
-#pragma unroll 2
-          for (int i = 0; 32 * i < x.put; ++i) {
-            const int r = row + 32 * (i & 1) + (BLK ? 0 : 64 * (i >> 1));
-            uint32_t v[4];
-            shifted(halves, from + raw_lane + (uint32_t)(4 * i * kRawRow), v);
-            if (x.left < kBlkK) {  // zeros past the end of the contraction
-              const int n = BLK ? (r < x.left ? 8 : 0) : x.left - 8 * chunk;
+        from += raw_lane;
+        const uint32_t sel = x.sh & 2 ? 0x5432 : 0x3210;
+        const bool end = x.left < kBlkK;
+        auto by = [&](auto words) {
+          constexpr int W = decltype(words)::value;
+          int r = row;  // of group i
+#pragma unroll 1
+          for (int i = 0; 32 * i < x.put; i += 2, from += 8 * kRawRow, to += kBoxBytes) {
+            uint32_t v[2][4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) v[k] &= (2 * k < n ? 0xFFFFu : 0u) | (2 * k + 1 < n ? 0xFFFF0000u : 0u);
+            for (int j = 0; j < 2; ++j) {
+              uint32_t w[8];
+              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(from + j * 4 * kRawRow));
+              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7]) : "r"(from + j * 4 * kRawRow + 16));
+#pragma unroll
+              for (int k = 0; k < 4; ++k) v[j][k] = __byte_perm(w[W + k], w[W + k + 1], sel);
             }
-            if (BLK || r < x.put) st_shared_v4(to + (uint32_t)((i & 1) * 4096 + (i >> 1) * kBoxBytes), v[0], v[1], v[2], v[3]);
+            if (end) {  // zeros past the end of the contraction
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const int n = BLK ? (row + 32 * j < x.left ? 8 : 0) : x.left - 8 * chunk;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[j][k] &= (2 * k < n ? 0xFFFFu : 0u) | (2 * k + 1 < n ? 0xFFFF0000u : 0u);
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              if (MS || BLK || r + 32 * j < x.put) st_shared_v4(to + (uint32_t)(j * 4096), v[j][0], v[j][1], v[j][2], v[j][3]);
+            r += 64;
           }
         };
-        switch (x.sh >> 1) {
+        switch (x.sh >> 2) {
           case 0: by(std::integral_constant<int, 0>()); break;
           case 1: by(std::integral_constant<int, 1>()); break;
           case 2: by(std::integral_constant<int, 2>()); break;
-          case 3: by(std::integral_constant<int, 3>()); break;
-          case 4: by(std::integral_constant<int, 4>()); break;
-          case 5: by(std::integral_constant<int, 5>()); break;
-          case 6: by(std::integral_constant<int, 6>()); break;
-          default: by(std::integral_constant<int, 7>());
+          default: by(std::integral_constant<int, 3>());
         }
       };
       // element by element
