@@ -9,10 +9,11 @@
 // Scales are powers of two, so v * 2^-s is exact, codes do not depend on the order or
 // precision of any arithmetic, and a code times its scale is exact in fp32.
 //
-// Every call is bound by HBM.  A thread holds V elements of a block (16 bytes of a row, 8
-// where rows allow no more, or four elements one by one in rows that start anywhere), the
-// 32 / V threads of a block are neighbours in a warp and take its maximum by shuffles, and
-// everything a thread reads is loaded before anything is computed.
+// Every call is bound by HBM.  A thread holds V elements of a block: 16 bytes of a row as
+// one access, 8 where rows allow no more, eight elements in four words, or four elements
+// one by one in rows that start anywhere.  The 32 / V threads of a block are neighbours in
+// a warp and take its maximum by shuffles, and everything a thread reads is loaded before
+// anything is computed.
 #include "gemm_common.cuh"
 #include "ops_common.cuh"
 
@@ -68,15 +69,15 @@ __device__ __forceinline__ uint32_t gload_if(const uint8_t* p, bool there) {
   return v;
 }
 
-// V elements of a row, of which n exist (the others are zeros).  LOOSE: one by one, else as
-// one access (all of them or none exist).
-template <typename T, int V, bool LOOSE>
+// V elements of a row, of which n exist (the others are zeros), as one access (all of them or
+// none exist).  LOOSE 1: one by one; 2: 16-bit elements two by two (n is even).
+template <typename T, int V, int LOOSE>
 struct Piece {
   Words<T, V> w;
-  uint32_t one[LOOSE ? V : 1];
+  uint32_t one[LOOSE == 1 ? V : 1];
   // the elements, before their first use
   __device__ __forceinline__ void join() {
-    if constexpr (LOOSE) {
+    if constexpr (LOOSE == 1) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         if constexpr (sizeof(T) == 4) w.w[j] = one[j];
@@ -85,7 +86,10 @@ struct Piece {
     }
   }
   __device__ __forceinline__ void load(const T* p, int n) {
-    if constexpr (LOOSE) {
+    if constexpr (LOOSE == 2) {
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) w.w[j] = gload_if(reinterpret_cast<const uint32_t*>(p + 2 * j), 2 * j < n);
+    } else if constexpr (LOOSE == 1) {
       using E = std::conditional_t<sizeof(T) == 4, uint32_t, uint16_t>;
 #pragma unroll
       for (int j = 0; j < V; ++j) one[j] = gload_if(reinterpret_cast<const E*>(p + j), j < n);
@@ -98,7 +102,11 @@ struct Piece {
     }
   }
   __device__ __forceinline__ void store(T* p, int n) const {
-    if constexpr (LOOSE) {
+    if constexpr (LOOSE == 2) {
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j)
+        if (2 * j < n) *reinterpret_cast<uint32_t*>(p + 2 * j) = w.w[j];
+    } else if constexpr (LOOSE == 1) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         if constexpr (sizeof(T) == 4) {
@@ -132,7 +140,7 @@ struct Piece {
 
 // The block's codes and scale from its threads' elements (n of V exist here, this thread's
 // place in the block is sub); the warp calls it together.
-template <typename T, int V, bool LOOSE>
+template <typename T, int V, int LOOSE>
 __device__ __forceinline__ void int8_store(const Piece<T, V, LOOSE>& x, int8_t* codes, uint8_t* scale, int n, int sub) {
   uint32_t m = x.top();
 #pragma unroll
@@ -159,7 +167,11 @@ __device__ __forceinline__ void int8_store(const Piece<T, V, LOOSE>& x, int8_t* 
 #pragma unroll
   for (int k = 0; k < V / 4; ++k)
     w[k] = finite ? pack_bytes(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]) : 0u;
-  if constexpr (LOOSE) {
+  if constexpr (LOOSE == 2) {
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j)
+      if (2 * j < n) *reinterpret_cast<uint16_t*>(codes + 2 * j) = (uint16_t)(w[j / 2] >> (16 * (j % 2)));
+  } else if constexpr (LOOSE == 1) {
 #pragma unroll
     for (int j = 0; j < V; ++j)
       if (j < n) codes[j] = (int8_t)(w[j / 4] >> (8 * (j % 4)));
@@ -171,12 +183,15 @@ __device__ __forceinline__ void int8_store(const Piece<T, V, LOOSE>& x, int8_t* 
 }
 
 // V codes and their scale byte, as loaded, and their values.
-template <int V, bool LOOSE>
+template <int V, int LOOSE>
 struct Kept {
-  uint32_t w[V / 4], byte, one[LOOSE ? V : 1];
+  uint32_t w[V / 4], byte, one[LOOSE == 1 ? V : LOOSE == 2 ? V / 2 : 1];
   __device__ __forceinline__ void load(const int8_t* codes, const uint8_t* scale, int n) {
     byte = gload_if(scale, n > 0);
-    if constexpr (LOOSE) {
+    if constexpr (LOOSE == 2) {
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) one[j] = gload_if(reinterpret_cast<const uint16_t*>(codes + 2 * j), 2 * j < n);
+    } else if constexpr (LOOSE == 1) {
 #pragma unroll
       for (int j = 0; j < V; ++j) one[j] = gload_if(reinterpret_cast<const uint8_t*>(codes + j), j < n);
     } else if (n > 0) {
@@ -185,7 +200,10 @@ struct Kept {
     }
   }
   __device__ __forceinline__ void values(F2 (&v)[V / 2]) {
-    if constexpr (LOOSE) {
+    if constexpr (LOOSE == 2) {
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) w[i] = one[2 * i] | one[2 * i + 1] << 16;
+    } else if constexpr (LOOSE == 1) {
 #pragma unroll
       for (int i = 0; i < V / 4; ++i) w[i] = one[4 * i] | one[4 * i + 1] << 8 | one[4 * i + 2] << 16 | one[4 * i + 3] << 24;
     }
@@ -230,7 +248,7 @@ __device__ __forceinline__ F2 in_range(F2 v) {
   }
 }
 
-template <typename T, int V, bool LOOSE>
+template <typename T, int V, int LOOSE>
 __global__ void __launch_bounds__(kThreadsCk)
     int8_quantize_kernel(const T* x, int64_t ldx, int64_t rows, int n, CkLay l, int8_t* q, uint8_t* scales) {
   ops_begin();
@@ -251,7 +269,7 @@ __global__ void __launch_bounds__(kThreadsCk)
   }
 }
 
-template <typename T, int V, bool LOOSE>
+template <typename T, int V, int LOOSE>
 __global__ void __launch_bounds__(kThreadsCk)
     int8_dequantize_kernel(const int8_t* q, const uint8_t* scales, int64_t rows, int n, CkLay l, T* y, int64_t ldy) {
   ops_begin();
@@ -292,7 +310,7 @@ __device__ __forceinline__ void sigmoids(float g, float& s, float& c) {
   }
 }
 
-template <typename T, int V, bool LOOSE, bool KEEP>
+template <typename T, int V, int LOOSE, bool KEEP>
 __global__ void __launch_bounds__(kThreadsCk)
     swiglu_forward_kernel(const T* h, int64_t ldh, int64_t rows, int f, CkLay l, T* a, int64_t lda, int8_t* q,
                           uint8_t* scales) {
@@ -333,7 +351,7 @@ __global__ void __launch_bounds__(kThreadsCk)
   }
 }
 
-template <typename T, int V, bool LOOSE, bool KEPT>
+template <typename T, int V, int LOOSE, bool KEPT>
 __global__ void __launch_bounds__(kThreadsCk)
     swiglu_backward_kernel(const T* da, int64_t ldda, const T* h, int64_t ldh, const int8_t* q, const uint8_t* scales,
                            int64_t rows, int f, CkLay l, T* dh, int64_t lddh, T* a, int64_t lda) {
@@ -400,13 +418,16 @@ bool ck_args(int32_t dtype, int64_t rows, int32_t n) {
 }
 uintptr_t bits(const void* p) { return reinterpret_cast<uintptr_t>(p); }
 
-// Bytes that a thread moves at once of rows of n elements: 16 or 8 (of 16-bit types)
-// where every row allows it, else 0, one by one.  `a`: the or of the rows' addresses and
+// Bytes that a thread moves at once of rows of n elements: 16, 8 or 4 (of 16-bit types)
+// where every row allows it, else 0, one by one.  (12793 rows of 2 x 4690 bf16, in words:
+// forward with its checkpoint 119 us, backward 131, one by one 367 together; 71 and 89 for
+// the bytes.  5331 rows of 2 x 1333 fp16, one by one: 25 and 31; 8 and 10 for the bytes.)  `a`: the or of the rows' addresses and
 // strides in bytes; the codes of a vector lie aligned too.
 int ck_bytes(size_t es, int n, uintptr_t a, const void* q) {
   a |= (uintptr_t)n * es;
   if (((a & 15) | (bits(q) & (16 / es - 1))) == 0) return 16;
-  return es == 2 && ((a & 7) | (bits(q) & 3)) == 0 ? 8 : 0;
+  if (es == 2 && ((a & 7) | (bits(q) & 3)) == 0) return 8;
+  return es == 2 && ((a & 3) | (bits(q) & 1)) == 0 ? 4 : 0;
 }
 
 struct CkLaunch {
@@ -428,22 +449,23 @@ CkLaunch ck_lay(int64_t rows, int n, int V) {
   return l;
 }
 
-template <typename T_, int V_, bool LOOSE_>
+template <typename T_, int V_, int LOOSE_>
 struct CkTag {
   using T = T_;
   static constexpr int V = V_;
-  static constexpr bool LOOSE = LOOSE_;
+  static constexpr int LOOSE = LOOSE_;
 };
 // f(tag) for the element type and the way rows move.
 template <typename F>
 cudaError_t ck_pick(int dtype, int bytes, F f) {
   return with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
-    if (bytes == 16) return f(CkTag<T, 16 / (int)sizeof(T), false>());
+    if (bytes == 16) return f(CkTag<T, 16 / (int)sizeof(T), 0>());
     if constexpr (sizeof(T) == 2) {
-      if (bytes == 8) return f(CkTag<T, 4, false>());
+      if (bytes == 8) return f(CkTag<T, 4, 0>());
+      if (bytes == 4) return f(CkTag<T, 8, 2>());
     }
-    return f(CkTag<T, 4, true>());
+    return f(CkTag<T, 4, 1>());
   });
 }
 
