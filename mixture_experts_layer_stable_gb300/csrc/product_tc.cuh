@@ -691,7 +691,8 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
       const uint32_t image = MS ? (uint32_t)kABytes : n_image;
       // where the next half stage (two groups) is
       int u = unit0, kb = 0, steps = 0, h = 0, left = 0, have = 0, put = 0;
-      const float* src = nullptr;  // the stage's row 0
+      const float* src = nullptr;  // the half's first value of this lane
+      const int64_t ld8 = 8 * ld, ld32 = 32 * ld, to_half = BLK ? 64 : 64 * ld, to_stage = BLK ? kBlkK * ld : kBlkK;
       bool more = true;
       auto find_unit = [&]() {  // from unit u on, the first with a contraction
         for (; u < total; u += unit_step) {
@@ -702,7 +703,8 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
           have = MS ? min(kBlkM, p.N - t.n0) : DW ? min((t.nt + 63) & ~63, p.K - t.r0) : t.nt;
           put = MS ? kBlkM : DW ? (t.nt + 63) & ~63 : t.nt;
           src = arr + (MS ? (DW ? t.row0 * ld : (int64_t)t.e * p.K * p.N) : t.row0 * ld);
-          src += (MS ? (BLK ? (int64_t)t.n0 : t.n0 * ld) : BLK ? (int64_t)t.r0 : t.r0 * ld) + t.kb0 * (BLK ? kBlkK * ld : kBlkK);
+          src += (MS ? (BLK ? (int64_t)t.n0 : t.n0 * ld) : BLK ? (int64_t)t.r0 : t.r0 * ld) + t.kb0 * to_stage;
+          src += VEC ? row * ld + 8 * chunk : w7 * ld + 2 * lane;
           return;
         }
         more = false;
@@ -714,18 +716,13 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
       auto load = [&](Half& x) {
         x.h = h;
         x.put = put;
-        // row r and its values from c on; n: those that exist (of a row `have` or what is
-        // left of the contraction)
-        auto at = [&](int r, int c, int& n) {
-          n = r < (BLK ? min(left, kBlkK) : have) ? (BLK ? have : left) - c : 0;
-          return src + r * ld + c;
-        };
-        const int c0 = BLK ? 64 * h : 0, r0 = BLK ? 0 : 64 * h;
+        // the half's rows that exist, and of a row's values those that do from this lane's on
+        const int rows = BLK ? left : have - 64 * h, values = (BLK ? have - 64 * h : left) - (VEC ? 8 * chunk : 2 * lane);
+        const float* q = src;
         if constexpr (VEC) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            int n;
-            const float* q = at(r0 + row + 32 * i, c0 + 8 * chunk, n);
+            const int n = row + 32 * i < rows ? values : 0;
             uint32_t* v = x.v + 8 * i;
             asm volatile(
                 "{\n\t.reg .pred p, q;\n\t"
@@ -737,12 +734,12 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
                 "@q ld.global.v4.u32 {%4, %5, %6, %7}, [%8+16];\n\t}"
                 : "=&r"(v[0]), "=&r"(v[1]), "=&r"(v[2]), "=&r"(v[3]), "=&r"(v[4]), "=&r"(v[5]), "=&r"(v[6]), "=&r"(v[7])
                 : "l"(q), "r"(n));
+            q += ld32;
           }
         } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            int n;
-            const float* q = at(r0 + w7 + 8 * j, c0 + 2 * lane, n);
+            const int n = w7 + 8 * j < rows ? values : 0;
             asm volatile(
                 "{\n\t.reg .pred p, q;\n\t"
                 "setp.gt.s32 p, %3, 0;\n\t"
@@ -752,12 +749,14 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
                 "@q ld.global.u32 %1, [%2+4];\n\t}"
                 : "=&r"(x.v[2 * j]), "=&r"(x.v[2 * j + 1])
                 : "l"(q), "r"(n));
+            q += ld8;
           }
         }
         // on to the next
+        src += to_half;
         if (64 * ++h >= put) {
+          src += to_stage - h * to_half;
           h = 0;
-          src += BLK ? kBlkK * ld : kBlkK;
           left -= kBlkK;
           if (++kb == steps) {
             kb = 0;
@@ -773,15 +772,12 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
         const uint32_t to = base + (uint32_t)s * stage_bytes + lane_dst + (uint32_t)(x.h * kBoxBytes);
         // two values' parts
         auto parts = [](const uint32_t* v, uint32_t& h2, uint32_t& m2, uint32_t& l2) {
-          constexpr float kMax = 3.3895313892515355e38f;  // (larger ones would round to an infinity)
-          float a = __uint_as_float(v[0]), b = __uint_as_float(v[1]);
-          h2 = pack_bf16x2(fminf(fmaxf(a, -kMax), kMax), fminf(fmaxf(b, -kMax), kMax));
-          a -= __uint_as_float(h2 << 16);
-          b -= __uint_as_float(h2 & 0xFFFF0000u);
-          m2 = pack_bf16x2(a, b);
-          a -= __uint_as_float(m2 << 16);
-          b -= __uint_as_float(m2 & 0xFFFF0000u);
-          l2 = pack_bf16x2(a, b);
+          auto top = [](uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); };
+          const float2 r = sub2(F2(__uint_as_float(v[0]), __uint_as_float(v[1])), F2(top(v[0]), top(v[1]))).get();
+          m2 = pack_bf16x2(r.x, r.y);
+          const float2 t = sub2(F2(r.x, r.y), F2(__uint_as_float(m2 << 16), top(m2))).get();
+          h2 = __byte_perm(v[0], v[1], 0x7632);
+          l2 = __byte_perm(__float_as_uint(t.x), __float_as_uint(t.y), 0x7632);
         };
         if constexpr (VEC) {
 #pragma unroll
