@@ -713,6 +713,19 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
         uint32_t v[16];
         int h, put;  // of its stage the first (0) or second; rows or columns that are stored
       };
+      auto advance = [&]() {  // (in front of the loads: behind them it would wait for them)
+        src += to_half;
+        if (64 * ++h >= put) {
+          src += to_stage - h * to_half;
+          h = 0;
+          left -= kBlkK;
+          if (++kb == steps) {
+            kb = 0;
+            u += unit_step;
+            find_unit();
+          }
+        }
+      };
       auto load = [&](Half& x) {
         x.h = h;
         x.put = put;
@@ -750,18 +763,6 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
                 : "=&r"(x.v[2 * j]), "=&r"(x.v[2 * j + 1])
                 : "l"(q), "r"(n));
             q += ld8;
-          }
-        }
-        // on to the next
-        src += to_half;
-        if (64 * ++h >= put) {
-          src += to_stage - h * to_half;
-          h = 0;
-          left -= kBlkK;
-          if (++kb == steps) {
-            kb = 0;
-            u += unit_step;
-            find_unit();
           }
         }
       };
@@ -819,12 +820,20 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
       Half x, y;
       load(x);
       for (;;) {
-        const bool in_y = more;
-        if (in_y) load(y);
-        if (!split(x) || !in_y) break;
-        const bool in_x = more;
-        if (in_x) load(x);
-        if (!split(y) || !in_x) break;
+        advance();
+        if (!more) {
+          split(x);
+          break;
+        }
+        load(y);
+        if (!split(x)) break;
+        advance();
+        if (!more) {
+          split(y);
+          break;
+        }
+        load(x);
+        if (!split(y)) break;
       }
     };
     // 16 bytes at a time where every row starts on them and is a whole number of them
