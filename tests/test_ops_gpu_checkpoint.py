@@ -55,7 +55,8 @@ def kept(rows, n, shift=0):
 
 
 SHAPES = [(1, 1, 0, 0), (3, 31, 0, 0), (2, 32, 0, 0), (5, 33, 1, 1), (64, 96, 8, 0), (17, 1000, 0, 0), (9, 1003, 0, 0),
-          (300, 768, 0, 0), (40, 2048, 16, 8), (7, 2048, 3, 0), (33, 8200, 0, 0), (4, 20000, 8, 8), (6, 4099, 5, 3)]
+          (300, 768, 0, 0), (40, 2048, 16, 8), (7, 2048, 3, 0), (33, 8200, 0, 0), (4, 20000, 8, 8), (6, 4099, 5, 3),
+          (3, 2, 0, 0), (21, 34, 2, 2), (50, 1002, 0, 0), (5, 4690, 4, 2)]
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
