@@ -30,8 +30,8 @@
 // by side.  Where experts' rows differ much they are taken from the front and the back of
 // that order in turns: experts with many rows (bound by the tensor cores) then run beside
 // experts with few (bound by their weights' way from HBM).  32768 rows skewed over 256
-// experts, 7168 x 4096: 1815 us, 1985 in one order; 16384 rows of four experts, where two
-// experts' operands at a time do not fit into L2: 543 us in turns, 512 in one order.
+// experts, 7168 x 4096: 1849 us, 1996 in one order; 16384 rows of four experts, where two
+// experts' operands at a time do not fit into L2: 541 us in turns, 514 in one order.
 //
 // Ragged edges.  Rows behind an expert's last are other experts': they fill accumulator
 // columns that are not stored.  The contraction over an expert's rows (the weights'
@@ -42,11 +42,12 @@
 // Sums.  The tensor cores add to their fp32 accumulators by truncation, which a long
 // contraction shows in results of 32 bits (4e-6 of a weight gradient of 4096 rows).  For
 // those an accumulator takes 512 of the contraction and the epilogue adds the accumulators
-// up in registers, rounding to nearest (5e-7; 598 us instead of 580 for 16384 rows of four
-// experts into 7168 x 4096; with 256 of the contraction 2.4e-7 and 780 us).
+// up in registers, rounding to nearest (5e-7; 16384 rows of four experts into 7168 x 4096
+// 576 us, as without; with 256 of the contraction 2.4e-7 and 589 us).
+//
 // fp32 operands.  A value is the sum of three of bf16, x = h + m + l exactly (h nearest to x,
-// m to x - h, l the rest: 8 bits of its 24 each), and
-//   x w = h h' + (h m' + m h' + m m' + h l' + l h') + r,  |r| <= 2^-24 |x w|,
+// m to x - h, l the rest: |m| <= 2^-8 |x|, |l| <= 2^-17 |x|), and
+//   x w = h h' + (h m' + m h' + m m' + h l' + l h') + r,  |r| <= (2^-24 + 2^-34) |x w|,
 // so six products on the tensor cores give fp32's precision.  The loading warps split the
 // values into three images of each operand; the first product and the other five have an
 // accumulator each, so that the small ones lose nothing to the large one's truncation.  A
@@ -774,10 +775,11 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
         // two values' parts
         auto parts = [](const uint32_t* v, uint32_t& h2, uint32_t& m2, uint32_t& l2) {
           auto top = [](uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); };
-          const float2 r = sub2(F2(__uint_as_float(v[0]), __uint_as_float(v[1])), F2(top(v[0]), top(v[1]))).get();
+          // (rounded, values over the largest bf16 would be infinities)
+          asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(h2) : "f"(__uint_as_float(v[1])), "f"(__uint_as_float(v[0])));
+          const float2 r = sub2(F2(__uint_as_float(v[0]), __uint_as_float(v[1])), F2(__uint_as_float(h2 << 16), top(h2))).get();
           m2 = pack_bf16x2(r.x, r.y);
           const float2 t = sub2(F2(r.x, r.y), F2(__uint_as_float(m2 << 16), top(m2))).get();
-          h2 = __byte_perm(v[0], v[1], 0x7632);
           l2 = __byte_perm(__float_as_uint(t.x), __float_as_uint(t.y), 0x7632);
         };
         if constexpr (VEC) {
