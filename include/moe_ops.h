@@ -131,7 +131,8 @@ moe_status moe_unpermute_backward(int32_t dtype, int64_t T, int32_t d, int32_t k
  *   magnitudes, about 3e-7 of a result in practice.  fp32 values are split into
  *   three parts of 8 bits: below 2^-102 they are held to 2^-126, and a sum with
  *   an infinity in it may be NaN instead.)
- *   x [rows, K], out [rows, N] with row strides ldx, ldo; w contiguous.
+ *   x [rows, K], out [rows, N] with row strides ldx, ldo; w contiguous.  A
+ *   result overlaps no operand.
  *   offsets [G+1], not decreasing; NULL: G = 1, all rows.  Rows outside
  *   [offsets[0], offsets[G]) are neither used nor written.
  *   0 <= rows <= 2^28, 1 <= G <= 1024, 1 <= K, N <= 2^22, no array of more than

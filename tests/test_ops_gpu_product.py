@@ -205,6 +205,22 @@ def test_fp32_values_over_their_range():
     check_rows(x, w, off, out, "f32", False)
 
 
+def test_fp32_products_of_two_values():
+    """A value's three parts leave out at most 2^-24 + 2^-34 of a product; its small parts' five sums truncate
+    (each 2^-23 of less than 2^-7 of it), and the sum is rounded once (2^-24)."""
+    g = gen(9)
+    hard = torch.tensor([1.0, 1.0 + 2.0 ** -8 + 2.0 ** -17 + 2.0 ** -23, 1.0 + 2.0 ** -7 - 2.0 ** -16 + 2.0 ** -23,
+                         2.0 - 2.0 ** -23, 1.0 + 2.0 ** -7 - 2.0 ** -23, 1.0 + 2.0 ** -8 - 2.0 ** -17 - 2.0 ** -23], device="cuda")
+    x = torch.cat((hard, -hard, randn(g, 700))).reshape(-1, 1)
+    w = torch.cat((hard, randn(g, 506))).reshape(1, 1, -1)
+    R, N = x.shape[0], w.shape[2]
+    out = torch.empty(R, N, device="cuda")
+    ops.moe_grouped_product(x, w, offsets_of([R]), out, workspace(R, 1, N, 1))
+    want = x.double() @ w[0].double()
+    bound = 2.0 ** -23 + 2.0 ** -34 + 5 * 2.0 ** -30
+    assert bool(((out.double() - want).abs() <= bound * want.abs()).all())
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_no_rows(dt):
     t = DT[dt]
