@@ -116,9 +116,11 @@ MOE_DEV void tmem_add16(uint32_t taddr, float* v) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(r[i]);
 }
-// An arrival in the even CTA's barrier that orders nothing but this thread's TMEM reads,
-// which have ended: a release over the cluster would wait for the thread's stores to memory
-// (16384 rows into 64 weight gradients of 2048 x 1536: 151 us with it, 125 without).
+// An arrival in the even CTA's barrier, ordered behind what this thread did in its own CTA:
+// TMEM reads, which have ended, or writes to its shared memory (past their proxy fence),
+// which this SM's own tensor core reads.  A release over the cluster would wait for the
+// SM's stores to memory as well (16384 rows into 64 weight gradients of 2048 x 1536: 151 us
+// with releases, 125 without the epilogue's, 108 without those behind the zeroed ends).
 MOE_DEV void mbar_arrive_even(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(bar, 0)) : "memory");
 }
@@ -461,7 +463,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
         tph ^= 1u << s;
         const int left = left_of(t) - (steps - 1) * kBlkK;
         zero_rows(base + (uint32_t)s * stage_bytes, left, (left + 15) & ~15);
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&ready[s]), 0));
+        if (lane == 0) mbar_arrive_even(smem_u32(&ready[s]));
       }
       if (++s == S) s = 0;
     }
