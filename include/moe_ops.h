@@ -126,11 +126,14 @@ moe_status moe_unpermute_backward(int32_t dtype, int64_t T, int32_t d, int32_t k
  * form on dy [rows, N] with K and N changed places; that of the weights is
  * moe_grouped_product_dw.
  *   dtype: of x and w; odtype: of out, dtype or MOE_DT_F32.  Products and sums
- *   in fp32, each result rounded once.  (All run on the tensor cores, whose sums
- *   truncate: fp32 results are off by at most n 2^-23 of the sum of their n terms'
- *   magnitudes, about 3e-7 of a result in practice.  fp32 values are split into
- *   three parts of 8 bits: below 2^-102 they are held to 2^-126, and a sum with
- *   an infinity in it may be NaN instead.)
+ *   in fp32, each result rounded once.  (All run on the tensor cores, which add 16
+ *   terms at a time and truncate.  A sum there takes 512 terms, 1024 for 16-bit
+ *   results; longer ones are added up from several, rounded to nearest.  So the sums
+ *   are off by less than 2^-16 of their n terms' magnitudes and n 2^-33 of them, and
+ *   in practice by 5e-7 of a result whatever n (operands of 16 bits; of fp32 3e-7;
+ *   for 16-bit results 1e-6 before their rounding).  fp32 values are split into three
+ *   parts of 8 bits: below 2^-102 they are held to 2^-126, and a sum with an infinity
+ *   in it may be NaN instead.)
  *   x [rows, K], out [rows, N] with row strides ldx, ldo; w contiguous.  A
  *   result overlaps no operand.
  *   offsets [G+1], not decreasing; NULL: G = 1, all rows.  Rows outside

@@ -39,11 +39,15 @@
 // up to 15 rows of both operands that the last one still takes are overwritten with zeros
 // first (one of them would not do: what lies there may be NaN).
 //
-// Sums.  The tensor cores add to their fp32 accumulators by truncation, which a long
-// contraction shows in results of 32 bits (4e-6 of a weight gradient of 4096 rows).  For
-// those an accumulator takes 512 of the contraction and the epilogue adds the accumulators
-// up in registers, rounding to nearest (5e-7; 16384 rows of four experts into 7168 x 4096
-// 576 us, as without; with 256 of the contraction 2.4e-7 and 589 us).
+// Sums.  The tensor cores add to their fp32 accumulators by truncation, always towards zero:
+// 4e-6 of a weight gradient of 4096 rows, 4e-4 of one of 65536 rows whose terms have the same
+// sign (half of fp16's last place).  So an accumulator takes 512 of the contraction, 1024 for
+// results of 16 bits, and the epilogue adds the accumulators up, rounding to nearest: 5e-7,
+// whatever the length.  (16384 rows of four experts into 7168 x 4096, fp32: 576 us, as in one
+// accumulator; 256 of the contraction at a time 2.4e-7 and 589 us.  Their forward, 7168 long in
+// 1024s, 518 us, in 512s 521, in one 511.)  The sums are in registers, or, for 16-bit results
+// beside loading warps, which leave none for 256 rows, in the other accumulator's place: a
+// unit of more than 1024 keeps to one.
 //
 // fp32 operands.  A value is the sum of three of bf16, x = h + m + l exactly (h nearest to x,
 // m to x - h, l the rest: |m| <= 2^-8 |x|, |l| <= 2^-17 |x|), and
@@ -72,8 +76,8 @@ constexpr int kStagesP = 12;         // at most
 constexpr int kTablesP = 8704;       // static shared memory: the experts' rows and units, barriers
 constexpr int kSmemP = 232448 - kTablesP;
 constexpr int kRawRow = 144;         // TC_LOAD: 64 elements from anywhere in a 16-byte block
-// Stages that a 32-bit result's accumulator takes.
-constexpr int sum_steps(TcMode mode) { return mode == TC_SPLIT ? 4 : 8; }
+// Stages that an accumulator takes; longer contractions are added up from several.
+constexpr int sum_steps(TcMode mode, bool f32) { return mode == TC_SPLIT ? 4 : f32 ? 8 : 16; }
 
 constexpr int threads_of(TcMode mode) { return 64 + 32 * (kEpi + (loads(mode) ? kLoadWarps : 0)); }
 // D (+)= A B, 16-bit operands, K = 16; a and b are descriptors' low words.
@@ -116,6 +120,16 @@ MOE_DEV void tmem_add16(uint32_t taddr, float* v) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(r[i]);
 }
+// The same columns, written (tmem_st_wait before they are read).
+MOE_DEV void tmem_st16(uint32_t taddr, const float* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+      "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+      : "memory");
+}
+MOE_DEV void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // An arrival in the even CTA's barrier, ordered behind what this thread did in its own CTA:
 // TMEM reads, which have ended, or writes to its shared memory (past their proxy fence),
 // which this SM's own tensor core reads.  A release over the cluster would wait for the
@@ -170,17 +184,19 @@ struct TcUnit {
   bool end;              // whether the contraction ends with it
 };
 
-// F32: results of 32 bits.  PARTS: of parts of the contraction (F32; its own kernel, since
-// what it adds to a unit costs the others registers: 4096 fp32 rows of 8 experts, 1024 x
-// 1024, 86 us instead of 74).
-template <ProdForm FORM, TcMode MODE, bool F32, bool PARTS>
+// F32: results of 32 bits.  SUMS: contractions that more than one accumulator takes (always
+// with F32 and with loading warps; 32768 rows of 8 experts, 64 x 2048, 35 us without, 39
+// with).  PARTS: of parts of the contraction (F32; its own kernel, since what it adds to a
+// unit costs the others registers: 4096 fp32 rows of 8 experts, 1024 x 1024, 86 us instead
+// of 74).
+template <ProdForm FORM, TcMode MODE, bool F32, bool SUMS, bool PARTS>
 __global__ void __launch_bounds__(threads_of(MODE), 1)
     tc_product_kernel(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ CUtensorMap tm_n,
                       const __grid_constant__ CUtensorMap tm_n128, const ProdArgs p, const uint32_t formats) {
   constexpr bool PAIR = MODE == TC_PAIR, DW = FORM == PROD_DW;
   constexpr bool M_MN = FORM != PROD_ROWS_T, N_MN = DW;  // operands whose contraction is not contiguous
   constexpr int kCols = PAIR ? 2 * kBlkM : kBlkM;        // output columns of a unit
-  constexpr int kTileRows = tile_most(MODE, F32), kSumSteps = sum_steps(MODE);
+  constexpr int kTileRows = tile_most(MODE, F32), kSumSteps = sum_steps(MODE, F32);
   constexpr int kImages = MODE == TC_SPLIT ? 3 : 1;  // of each operand in a stage
   constexpr int kBoxRows = DW ? 64 : 32;                 // output rows of a box of the N side
   constexpr uint32_t kNBox = kBoxRows * 128;
@@ -281,6 +297,9 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
   };
   // what is left of the contraction where the unit begins
   auto left_of = [&](const TcUnit& t) { return (DW ? t.count : p.K) - t.kb0 * kBlkK; };
+  // whether a unit of so many stages keeps to one accumulator, the other's place holding its
+  // sums (the unit behind it begins with the same one, whose last arrival is behind them)
+  auto holds = [](int steps) { return MODE == TC_LOAD && !F32 && steps > kSumSteps; };
   const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty);
   // All lanes wait; the result is the same in each.
   auto wait_all = [&](uint32_t bar, uint32_t parity, int where) {
@@ -390,7 +409,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
       for (int kb = 0; kb < steps; ++kb) {
         const uint32_t d = tmem + (uint32_t)(acc * kAccCols);
         if (!more) {
-          if (!wait_all(smem_u32(&tempty[acc]), aph ^ 1u, 2100 + acc)) goto issued;
+          if (!wait_all(smem_u32(&tempty[acc]), ((aph >> acc) & 1u) ^ 1u, 2100 + acc)) goto issued;
         }
         if (!wait_all(full0 + 8u * s, ph, 2200 + s)) goto issued;
         if constexpr (DW && !loads(MODE)) {
@@ -434,13 +453,11 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
           s = 0;
           ph ^= 1u;
         }
-        if (kb == steps - 1 || (F32 && (kb + 1) % kSumSteps == 0)) {
+        if (kb == steps - 1 || (SUMS && (kb + 1) % kSumSteps == 0)) {
           tc_commit_on<PAIR>(leader, smem_u32(&tfull[acc]));
           more = 0;
-          if (++acc == 2) {
-            acc = 0;
-            aph ^= 1u;
-          }
+          aph ^= 1u << acc;
+          if (!holds(steps)) acc ^= 1;
         }
       }
     }
@@ -859,18 +876,17 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
     const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16);
     int acc = 0;
     uint32_t aph = 0;
-    auto done = [&]() {  // this accumulator may be filled again
+    auto done = [&](bool hold = false) {  // this accumulator may be filled again
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
         if constexpr (PAIR) mbar_arrive_even(smem_u32(&tempty[acc]));
         else mbar_arrive(&tempty[acc]);
       }
-      if (++acc == 2) {
-        acc = 0;
-        aph ^= 1u;
-      }
+      aph ^= 1u << acc;
+      if (!hold) acc ^= 1;
     };
+    auto filled = [&]() { return wait_all(smem_u32(&tfull[acc]), (aph >> acc) & 1u, 2500 + acc); };
     for (int u = unit0; u < total; u += unit_step) {
       const TcUnit t = unit_at(u);
       const int steps = t.steps;
@@ -888,7 +904,46 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
         else if (p.odt == MOE_DT_BF16) put_tile<__nv_bfloat16, DW>(p, at, nt - c0, v);
         else put_tile<__half, DW>(p, at, nt - c0, v);
       };
-      if constexpr (F32) {
+      if (!F32 && steps == 0) {
+        float v[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = 0.f;
+        for (int c0 = c_first; c0 < nt; c0 += kStep) store(c0, v);
+      } else if (!F32 && (!SUMS || steps <= kSumSteps)) {
+        if (!filled()) goto stored;
+        tc_fence_after();
+        for (int c0 = c_first; c0 < nt; c0 += kStep) {
+          float v[32];
+          tmem_ld32(tq + (uint32_t)(acc * kAccCols + c0), v);
+          store(c0, v);
+        }
+        done();
+      } else if constexpr (!SUMS) {
+        // (there is no longer contraction)
+      } else if constexpr (MODE == TC_LOAD && !F32) {
+        // each time the same thread has the same columns of both places
+        for (int k = 0; k < steps; k += kSumSteps) {
+          if (!filled()) goto stored;
+          tc_fence_after();
+          for (int c0 = c_first; c0 < nt; c0 += kStep) {
+            const uint32_t from = tq + (uint32_t)(acc * kAccCols + c0), sums = tq + (uint32_t)((acc ^ 1) * kAccCols + c0);
+            float v[32];
+            tmem_ld32(from, v);
+            if (k > 0) {
+              tmem_add16(sums, v);
+              tmem_add16(sums + 16, v + 16);
+            }
+            if (k + kSumSteps < steps) {
+              tmem_st16(sums, v);
+              tmem_st16(sums + 16, v + 16);
+            } else {
+              store(c0, v);
+            }
+          }
+          tmem_st_wait();
+          done(true);
+        }
+      } else {
         constexpr int kParts = kTileRows / kStep;
         float sum[kParts][32];
 #pragma unroll
@@ -896,7 +951,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) sum[i][j] = 0.f;
         for (int k = 0; k < steps; k += kSumSteps) {
-          if (!wait_all(smem_u32(&tfull[acc]), aph, 2500 + acc)) goto stored;
+          if (!filled()) goto stored;
           tc_fence_after();
 #pragma unroll
           for (int i = 0; i < kParts; ++i) {
@@ -923,20 +978,6 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
 #pragma unroll
         for (int i = 0; i < kParts; ++i)
           if (c_first + kStep * i < nt) store(c_first + kStep * i, sum[i]);
-      } else if (steps == 0) {
-        float v[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = 0.f;
-        for (int c0 = c_first; c0 < nt; c0 += kStep) store(c0, v);
-      } else {
-        if (!wait_all(smem_u32(&tfull[acc]), aph, 2500 + acc)) goto stored;
-        tc_fence_after();
-        for (int c0 = c_first; c0 < nt; c0 += kStep) {
-          float v[32];
-          tmem_ld32(tq + (uint32_t)(acc * kAccCols + c0), v);
-          store(c0, v);
-        }
-        done();
       }
     }
   stored:;
@@ -990,9 +1031,9 @@ bool tc_map(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <ProdForm FORM, TcMode MODE, bool F32, bool PARTS>
+template <ProdForm FORM, TcMode MODE, bool F32, bool SUMS, bool PARTS>
 cudaError_t launch_tc(const CUtensorMap* tm, const ProdArgs& p, uint32_t formats, cudaStream_t st) {
-  auto kern = tc_product_kernel<FORM, MODE, F32, PARTS>;
+  auto kern = tc_product_kernel<FORM, MODE, F32, SUMS, PARTS>;
   static SmemAllowed allowed;
   const cudaError_t e = allow_smem(kern, kSmemP, allowed);
   if (e != cudaSuccess) return e;
@@ -1029,7 +1070,13 @@ cudaError_t launch_tc(const CUtensorMap* tm, const ProdArgs& p, uint32_t formats
 template <ProdForm FORM, TcMode MODE, bool F32>
 cudaError_t launch_parts(const CUtensorMap* tm, const ProdArgs& p, uint32_t formats, cudaStream_t st) {
   const int splits = splits_of(FORM, MODE, p.rows, p.K, p.N, p.G);
-  if (splits <= 1) return launch_tc<FORM, MODE, F32, false>(tm, p, formats, st);
+  if (splits <= 1) {
+    if constexpr (!F32 && MODE != TC_LOAD) {
+      if ((FORM == PROD_DW ? p.rows : p.K) <= kBlkK * sum_steps(MODE, false))
+        return launch_tc<FORM, MODE, false, false, false>(tm, p, formats, st);
+    }
+    return launch_tc<FORM, MODE, F32, true, false>(tm, p, formats, st);
+  }
   ProdArgs q = p;
   const int64_t n = results_of(FORM, p.rows, p.K, p.N, p.G);
   q.out = p.ws;
@@ -1038,7 +1085,7 @@ cudaError_t launch_parts(const CUtensorMap* tm, const ProdArgs& p, uint32_t form
   q.accumulate = 0;
   q.splits = splits;
   q.split_stride = n;
-  cudaError_t e = launch_tc<FORM, MODE, true, true>(tm, q, formats, st);
+  cudaError_t e = launch_tc<FORM, MODE, true, true, true>(tm, q, formats, st);
   if (e != cudaSuccess) return e;
   const int64_t blocks = (n + 255) / 256, most = (int64_t)num_sms() * 8;
   return with_dtype(p.odt, [&](auto t) {
