@@ -555,11 +555,11 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
           blk = reinterpret_cast<const uint8_t*>(at.src + w7 * ld) - at.sh + off;
           copies = copies_of(BLK ? kBlkK : at.have, 2 * (BLK ? at.have : kBlkK) + at.sh);
           // (only the first stage can begin before the array's first whole block, only the last
-          // whole one, and what is left, end behind its last)
+          // whole one, and what is left, end behind its last; far rows are all loaded singly)
           const int whole = min(steps, at.left / kBlkK);
           const int64_t next = BLK ? kBlkK * ld : kBlkK;
           fast0 = whole > 0 && inside(at.src, kBlkK) ? 0 : 1;
-          fast1 = whole == 0 ? 0 : inside(at.src + (whole - 1) * next, kBlkK) ? whole : whole - 1;
+          fast1 = whole == 0 || !near ? 0 : inside(at.src + (whole - 1) * next, kBlkK) ? whole : whole - 1;
           return;
         }
         more = false;
