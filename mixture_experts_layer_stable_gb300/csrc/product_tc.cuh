@@ -130,14 +130,24 @@ MOE_DEV void tmem_st16(uint32_t taddr, const float* v) {
       : "memory");
 }
 MOE_DEV void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// An arrival in the even CTA's barrier, ordered behind what this thread did in its own CTA:
-// TMEM reads, which have ended, or writes to its shared memory (past their proxy fence),
-// which this SM's own tensor core reads.  A release over the cluster would wait for the
-// SM's stores to memory as well (16384 rows into 64 weight gradients of 2048 x 1536: 151 us
-// with releases, 125 without the epilogue's, 108 without those behind the zeroed ends).
+// An arrival in the even CTA's barrier behind TMEM reads.  Their values are in registers by
+// then and nothing was written that the other side reads, so there is nothing to release;
+// a release over the cluster would wait for the SM's stores to memory (16384 rows into 64
+// weight gradients of 2048 x 1536: 151 us with it, 129 without).
 MOE_DEV void mbar_arrive_even(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(bar, 0)) : "memory");
 }
+// The same behind the warp's writes to its CTA's shared memory (past their proxy fence and
+// the warp's barrier), which the even CTA's instructions read: a release over the cluster of
+// shared memory alone, which does not wait for the stores either (111 us; 129 with a release
+// of all memory here).  The other side is try_wait_cluster and acquire_smem_cluster.
+MOE_DEV void mbar_arrive_even_release(uint32_t bar) {
+  asm volatile(
+      "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(bar, 0))
+      : "memory");
+}
+MOE_DEV void acquire_smem_cluster() { asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory"); }
 // A wait for an arrival from the other CTA that orders what that one wrote.
 MOE_DEV bool try_wait_cluster(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -423,6 +433,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
                 ok = ok && __all_sync(0xffffffffu, try_wait_cluster(bar, par));
               }
               if (!ok) goto issued;
+              acquire_smem_cluster();
               tph ^= 1u << s;
             }
           }
@@ -480,7 +491,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
         tph ^= 1u << s;
         const int left = left_of(t) - (steps - 1) * kBlkK;
         zero_rows(base + (uint32_t)s * stage_bytes, left, (left + 15) & ~15);
-        if (lane == 0) mbar_arrive_even(smem_u32(&ready[s]));
+        if (lane == 0) mbar_arrive_even_release(smem_u32(&ready[s]));
       }
       if (++s == S) s = 0;
     }
