@@ -129,7 +129,7 @@ moe_status moe_unpermute_backward(int32_t dtype, int64_t T, int32_t d, int32_t k
  *   in fp32, each result rounded once.  (All run on the tensor cores, which add 16
  *   terms at a time and truncate.  A sum there takes 512 terms, 1024 for 16-bit
  *   results; longer ones are added up from several, rounded to nearest.  So the sums
- *   are off by less than 2^-16 of their n terms' magnitudes and n 2^-33 of them, and
+ *   are off by less than 2^-16 of their n terms' magnitudes and n 2^-32 of them, and
  *   in practice by 5e-7 of a result whatever n (operands of 16 bits; of fp32 3e-7;
  *   for 16-bit results 1e-6 before their rounding).  fp32 values are split into three
  *   parts of 8 bits: below 2^-102 they are held to 2^-126, and a sum with an infinity
@@ -142,8 +142,8 @@ moe_status moe_unpermute_backward(int32_t dtype, int64_t T, int32_t d, int32_t k
  *   2^40 elements.
  *   16-byte aligned x, w and row strides are the fast path.
  *   ws: 128-byte aligned, of moe_grouped_product_workspace_bytes(rows, K, N, G)
- *   bytes, which serve both calls and either form; calls that may overlap need
- *   one each.  moe_read_status(ws, stream) reports a wait that ran out in the
+ *   bytes, which serve both calls and either form, of these or fewer rows (at most
+ *   about 20 MB); calls that may overlap need one each.  moe_read_status(ws, stream) reports a wait that ran out in the
  *   last call that was given ws. */
 size_t moe_grouped_product_workspace_bytes(int64_t rows, int32_t K, int32_t N, int32_t G);
 moe_status moe_grouped_product(int32_t dtype, int32_t odtype, int64_t rows, int32_t K, int32_t N, int32_t G,

@@ -21,15 +21,28 @@ bool prod_sizes(int64_t rows, int32_t K, int32_t N, int32_t G) {
          G <= kMaxG && (int64_t)K * N <= most / G && rows <= most / (K > N ? K : N);
 }
 
-// Bytes of partial sums that a call can need.
-size_t partial_bytes(ProdForm form, int64_t rows, int K, int N, int G) {
+// Bytes of workspace: a status, and partial sums.
+size_t ws_bytes_of(int64_t floats) { return 128 + ((size_t)floats * sizeof(float) + 127) / 128 * 128; }
+
+// What a call needs, however its operands lie.
+size_t needed_bytes(ProdForm form, int64_t rows, int K, int N, int G) {
   int splits = 1;
   for (const TcMode mode : {TC_COPY, TC_PAIR, TC_LOAD}) {  // (fp32 operands' tiles are TC_LOAD's)
     if (mode == TC_PAIR && !takes_pairs(rows, N, G)) continue;
     const int s = splits_of(form, mode, rows, K, N, G);
     splits = s > splits ? s : splits;
   }
-  return splits > 1 ? (size_t)splits * results_of(form, rows, K, N, G) * sizeof(float) : 0;
+  return ws_bytes_of(splits > 1 ? splits * results_of(form, rows, K, N, G) : 0);
+}
+
+// At least what any call of up to `rows` rows needs.  (One call's need has no order in the
+// rows: fewer leave more workers without a unit.)  The parts are at most a quarter of the
+// stages, and so many that every worker has one tile at most.
+int64_t partials_most(ProdForm form, int64_t rows, int K, int N, int G) {
+  const int64_t stages = ((form == PROD_DW ? rows / G : K) + kBlkK - 1) / kBlkK;
+  if (stages < kSplitStages) return 0;
+  const int64_t tiles = (int64_t)num_sms() * 256 * kBlkM, results = results_of(form, rows, K, N, G);
+  return results >= tiles / (stages / 4) ? tiles : results * (stages / 4);
 }
 
 }  // namespace
@@ -43,13 +56,13 @@ extern "C" {
 size_t moe_grouped_product_workspace_bytes(int64_t rows, int32_t K, int32_t N, int32_t G) {
   if (!prod_sizes(rows, K, N, G)) return 0;
   // every form, K and N also in each other's place: both orders need the same
-  size_t most = 0;
+  int64_t most = 0;
   for (const ProdForm form : {PROD_ROWS, PROD_ROWS_T, PROD_DW}) {
-    const size_t a = partial_bytes(form, rows, K, N, G), b = partial_bytes(form, rows, N, K, G);
+    const int64_t a = partials_most(form, rows, K, N, G), b = partials_most(form, rows, N, K, G);
     most = most < a ? a : most;
     most = most < b ? b : most;
   }
-  return 128 + (most + 127) / 128 * 128;
+  return ws_bytes_of(most);
 }
 
 moe_status moe_grouped_product(int32_t dtype, int32_t odtype, int64_t rows, int32_t K, int32_t N, int32_t G,
@@ -58,7 +71,7 @@ moe_status moe_grouped_product(int32_t dtype, int32_t odtype, int64_t rows, int3
   if (!dtype_valid(dtype) || (odtype != dtype && odtype != MOE_DT_F32) || !prod_sizes(rows, K, N, G) || ldx < K ||
       ldo < N || (offsets == nullptr && G != 1) || ws == nullptr || !aligned_to(ws, 128))
     return MOE_ERR_INVALID_ARG;
-  if (ws_bytes < moe_grouped_product_workspace_bytes(rows, K, N, G)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (ws_bytes < needed_bytes(transposed ? PROD_ROWS_T : PROD_ROWS, rows, K, N, G)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (rows == 0) return clear_status(ws, st);
   const size_t es = dtype_bytes(dtype);
@@ -89,7 +102,7 @@ moe_status moe_grouped_product_dw(int32_t dtype, int32_t wdtype, int64_t rows, i
   if (!dtype_valid(dtype) || (wdtype != dtype && wdtype != MOE_DT_F32) || !prod_sizes(rows, K, N, G) || ldx < K ||
       lddy < N || (offsets == nullptr && G != 1) || ws == nullptr || !aligned_to(ws, 128))
     return MOE_ERR_INVALID_ARG;
-  if (ws_bytes < moe_grouped_product_workspace_bytes(rows, K, N, G)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (ws_bytes < needed_bytes(PROD_DW, rows, K, N, G)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const size_t es = dtype_bytes(dtype);
   if (!elem_ok(dw, dtype_bytes(wdtype)) ||

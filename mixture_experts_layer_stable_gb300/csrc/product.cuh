@@ -94,10 +94,11 @@ inline int64_t units_of(ProdForm form, TcMode mode, bool f32, int64_t rows, int 
 // leave every worker a unit where there are at most half as many units as workers, of four
 // stages at least.  (8 bf16 rows, 7168 to 256, two tiles: 29 us whole, 16 in parts; 3636
 // rows' gradient of 84 columns through 6373, 15 tiles of unaligned rows: 47 us in parts.)
+constexpr int kSplitStages = 16;  // shorter contractions stay whole
 inline int splits_of(ProdForm form, TcMode mode, int64_t rows, int K, int N, int G) {
   const int64_t units = units_of(form, mode, true, rows, K, N, G), workers = mode == TC_PAIR ? num_sms() / 2 : num_sms();
   const int64_t stages = ((form == PROD_DW ? rows / G : K) + kBlkK - 1) / kBlkK;
-  if (units < 1 || 2 * units > workers || stages < 16) return 1;
+  if (units < 1 || 2 * units > workers || stages < kSplitStages) return 1;
   const int64_t most = stages / 4, want = workers / units;
   return (int)(want < most ? want : most);
 }

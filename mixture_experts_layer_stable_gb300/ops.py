@@ -252,6 +252,7 @@ def moe_unpermute_backward(dout, y, weights, k, inv, offsets, dy, dw, stream=Non
 
 # ---------------------------------------------------------------- products by expert
 def moe_grouped_product_workspace_bytes(rows, K, N, G=1):
+    """Bytes for the products and gradients of up to `rows` rows."""
     return int(lib().moe_grouped_product_workspace_bytes(rows, K, N, G))
 
 
