@@ -54,27 +54,30 @@ class SwiGLUExperts:
         return next((e for e in map(B.moe_read_status, (self.ws1, self.ws2)) if e), 0)
 
     def forward(self, rows, offsets):
-        ops.moe_grouped_product(rows, self.W1, offsets, self.h, self.ws1)
-        ops.moe_swiglu_forward(self.h, self.a, self.hq, self.hs)
-        ops.moe_grouped_product(self.a, self.W2, offsets, self.y, self.ws2)
+        n = rows.shape[0]
+        h, a, y = self.h[:n], self.a[:n], self.y[:n]
+        ops.moe_grouped_product(rows, self.W1, offsets, h, self.ws1)
+        ops.moe_swiglu_forward(h, a, self.hq[:n], self.hs)
+        ops.moe_grouped_product(a, self.W2, offsets, y, self.ws2)
         if not self.keep_rows:
-            ops.moe_quantize_mxint8_rows(rows, self.xq, self.xs)
-        return self.y
+            ops.moe_quantize_mxint8_rows(rows, self.xq[:n], self.xs)
+        return y
 
     def backward(self, dy, rows, offsets):
         """The rows' gradient; of `rows` nothing is read unless keep_rows."""
-        add, da, dh = not self.fresh, self.a, self.h
-        ops.moe_grouped_product(dy, self.W2, offsets, da, self.ws2, transposed=True)
-        # h's place takes dh, da's the activation again
-        ops.moe_swiglu_backward(da, None, dh, self.a, self.hq, self.hs)
-        ops.moe_grouped_product_dw(self.a, dy, offsets, self.dW2, self.ws2, accumulate=add)
-        ops.moe_grouped_product(dh, self.W1, offsets, self.dx, self.ws1, transposed=True)
+        n = dy.shape[0]
+        # h's place takes dh, the activation's its gradient and then the activation again
+        add, a, dh, dx = not self.fresh, self.a[:n], self.h[:n], self.dx[:n]
+        ops.moe_grouped_product(dy, self.W2, offsets, a, self.ws2, transposed=True)
+        ops.moe_swiglu_backward(a, None, dh, a, self.hq[:n], self.hs)
+        ops.moe_grouped_product_dw(a, dy, offsets, self.dW2, self.ws2, accumulate=add)
+        ops.moe_grouped_product(dh, self.W1, offsets, dx, self.ws1, transposed=True)
         if not self.keep_rows:
-            rows = self.y
-            ops.moe_dequantize_mxint8_rows(self.xq, self.xs, rows)
+            rows = self.y[:n]
+            ops.moe_dequantize_mxint8_rows(self.xq[:n], self.xs, rows)
         ops.moe_grouped_product_dw(rows, dh, offsets, self.dW1, self.ws1, accumulate=add)
         self.fresh = False
-        return self.dx
+        return dx
 
 
 def main():
