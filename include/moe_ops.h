@@ -168,6 +168,9 @@ moe_status moe_grouped_product_dw(int32_t dtype, int32_t wdtype, int64_t rows, i
  * 2^(s-1) <= max |v| / 127.  (A block that ends in the last 2^122 of fp32's
  * range is cut to 63 * 2^122: finite values stay finite.)  A block with a NaN
  * or an infinity gets the scale byte 255 (NaN) and comes back as NaN.
+ * (The OCP MX format of this name counts its elements in 64ths, c / 64 * 2^s: the
+ * same codes have a scale byte that is 6 higher there.  What leaves the program for
+ * a reader of that format needs 6 added to each byte below 249.)
  *   codes [rows, n] contiguous, scale bytes (s + 127) [rows, ceil(n / 32)]
  *   contiguous.  Codes in 8-byte aligned rows take the fast path. */
 size_t moe_mxint8_scale_bytes(int64_t rows, int32_t n);
@@ -179,8 +182,9 @@ moe_status moe_dequantize_mxint8_rows(int32_t dtype, int64_t rows, int32_t n, co
 
 /* ---------------------------------------------------------------- SwiGLU
  * a = silu(g) * u of rows h = [g | u] of 2f elements, silu(g) = g / (1 + exp(-g)),
- * in fp32, rounded once.  (16-bit types: silu to 2^-18, and 0 for gates below
- * -87, where it is below 1e-36.)
+ * in fp32, rounded once.  (silu is within 2^-20 of itself in fp32; for 16-bit types
+ * within 2^-18 for gates from -20 on, 2^-16 down to -87, and 0 below, where it is
+ * below 1e-36.)
  *   q, scales: NULL, or a checkpoint of h for the backward: MXINT8 of the two
  *   halves of each row, codes [rows, 2f] and scales [rows, 2 * ceil(f / 32)]
  *   (moe_quantize_mxint8_rows of 2 * rows rows of f).
@@ -253,8 +257,8 @@ moe_status moe_dequantize_mxfp4_rows(int32_t dtype, int64_t rows, int32_t K, con
  *   (offsets NULL: G = 1, all rows).  wq, wscales: moe_quantize_mxfp4.
  *   act MOE_ACT_NONE: out [rows, N].  MOE_ACT_SWIGLU (paired weights): out
  *   [rows, N/2], out[p, i] = silu(h[2i]) * h[2i+1] of the fp32 products h.
- *   (silu to fp32 accuracy for fp32 results; for 16-bit ones to 2^-18, and 0
- *   for gates below -87, where it is below 1e-36.)
+ *   (silu to fp32 accuracy for fp32 results; for 16-bit ones to 2^-18 for gates
+ *   from -20 on, 2^-16 down to -87, and 0 below, where it is below 1e-36.)
  *   dtype: of out (row stride ldo).  Rows outside [offsets[0], offsets[G]) are
  *   not written.
  *   0 <= rows <= 2^28, 1 <= G <= 1024, N >= 1, K a multiple of 32, K >= 32.

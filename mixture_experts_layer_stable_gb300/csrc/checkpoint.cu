@@ -296,7 +296,8 @@ __global__ void __launch_bounds__(kThreadsCk)
 }
 
 // sigmoid(g) and 1 - sigmoid(g).  For 16-bit results from the hardware exponential and
-// reciprocal, as the layer's (2^-18, and 0 below -87); for fp32 ones from exp(-|g|), which
+// reciprocal, as the layer's (2^-18 from -20 on, where the exponential's 2 + 1.173 |g| ulp
+// begin to count 2^-16, and 0 below -87); for fp32 ones from exp(-|g|), which
 // cannot overflow.
 template <typename T>
 __device__ __forceinline__ void sigmoids(float g, float& s, float& c) {
