@@ -21,6 +21,10 @@ bool prod_sizes(int64_t rows, int32_t K, int32_t N, int32_t G) {
          G <= kMaxG && (int64_t)K * N <= most / G && rows <= most / (K > N ? K : N);
 }
 
+// The stride of `rows` rows of n: one row's says nothing (and may be past what a tensor map
+// holds, or keep it off 16 bytes).
+int64_t row_stride(int64_t rows, int64_t ld, int n) { return rows > 1 ? ld : (n + 7) / 8 * 8; }
+
 // Bytes of workspace: a status, and partial sums.
 size_t ws_bytes_of(int64_t floats) { return 128 + ((size_t)floats * sizeof(float) + 127) / 128 * 128; }
 
@@ -82,9 +86,9 @@ moe_status moe_grouped_product(int32_t dtype, int32_t odtype, int64_t rows, int3
   p.a = x;
   p.b = w;
   p.out = out;
-  p.lda = ldx;
+  p.lda = row_stride(rows, ldx, K);
   p.ldb = transposed ? K : N;
-  p.ldo = ldo;
+  p.ldo = row_stride(rows, ldo, N);
   p.status = static_cast<int*>(ws);
   p.ws = static_cast<char*>(ws) + 128;
   p.splits = 1;
@@ -113,8 +117,8 @@ moe_status moe_grouped_product_dw(int32_t dtype, int32_t wdtype, int64_t rows, i
   p.a = x;
   p.b = dy;
   p.out = dw;
-  p.lda = ldx;
-  p.ldb = lddy;
+  p.lda = row_stride(rows, ldx, K);
+  p.ldb = row_stride(rows, lddy, N);
   p.ldo = N;
   p.status = static_cast<int*>(ws);
   p.ws = static_cast<char*>(ws) + 128;

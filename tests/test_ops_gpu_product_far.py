@@ -43,3 +43,22 @@ def test_rows_far_apart(cuda_lib, dt, ld, first):
         close(dx[s], b @ c.t(), dt, N * 2.0 ** -23 * (b.abs() @ c.t().abs()), "their gradient")
         close(dw[e], a.t() @ b, dt, (n + 1) * 2.0 ** -23 * (a.t().abs() @ b.abs()), "weights' gradient")
     assert B.moe_read_status(ws) == 0
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("K,N", [(264, 136), (61, 45)])
+@pytest.mark.parametrize("ld", [(1 << 62) + 1, 1 << 44, 1001])
+def test_one_rows_stride_says_nothing(cuda_lib, dt, K, N, ld):
+    g = gen(2)
+    x, dy, w = randn(g, 1, K, dtype=DT[dt]), randn(g, 1, N, dtype=DT[dt]), randn(g, 1, K, N, dtype=DT[dt])
+    out, dx, dw = torch.empty_like(dy), torch.empty_like(x), torch.empty_like(w)
+    ws = torch.full((ops.moe_grouped_product_workspace_bytes(1, K, N, 1),), 255, dtype=torch.uint8, device="cuda")
+    L, t, st = ops.lib(), {"f32": 0, "bf16": 1}[dt], torch.cuda.current_stream().cuda_stream
+    at = [v.data_ptr() for v in (x, dy, w, out, dx, dw, ws)]
+    assert L.moe_grouped_product(t, t, 1, K, N, 1, None, at[0], ld, at[2], 0, at[3], ld, at[6], ws.nbytes, st) == 0
+    assert L.moe_grouped_product(t, t, 1, N, K, 1, None, at[1], ld, at[2], 1, at[4], ld, at[6], ws.nbytes, st) == 0
+    assert L.moe_grouped_product_dw(t, t, 1, K, N, 1, None, at[0], ld, at[1], ld, at[5], 0, at[6], ws.nbytes, st) == 0
+    a, b, c = x.double(), dy.double(), w[0].double()
+    close(out, a @ c, dt, K * 2.0 ** -23 * (a.abs() @ c.abs()))
+    close(dx, b @ c.t(), dt, N * 2.0 ** -23 * (b.abs() @ c.t().abs()))
+    close(dw[0], a.t() @ b, dt, 2 * 2.0 ** -23 * (a.t().abs() @ b.abs()))
