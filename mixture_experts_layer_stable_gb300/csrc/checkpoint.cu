@@ -375,6 +375,9 @@ __global__ void __launch_bounds__(kThreadsCk)
     }
     pd[i].load(da + at.row * ldda + c, n);
   }
+  // dh may be h and a may be da, and du needs no u, a no da: no store moves up over the loads
+  // (which the compiler does not know to read memory)
+  asm volatile("" ::: "memory");
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
     const int b = at.t / L + i * l.nq, c = b * 32 + sub * V;
