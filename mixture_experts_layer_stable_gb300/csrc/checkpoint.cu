@@ -22,7 +22,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreadsCk = 256;
-// Pieces of a thread: 16384 rows of 4096 bf16 to 8 bits 80 us with one, 68 with two, 66 with
+// Pieces of a thread: 32768 rows of 4096 bf16 to 8 bits 80 us with one, 68 with two, 66 with
 // four, back 76, 64, 66.
 constexpr int kPieces = 2;
 

@@ -30,8 +30,8 @@
 // by side.  Where experts' rows differ much they are taken from the front and the back of
 // that order in turns: experts with many rows (bound by the tensor cores) then run beside
 // experts with few (bound by their weights' way from HBM).  32768 rows skewed over 256
-// experts, 7168 x 4096: 1849 us, 1996 in one order; 16384 rows of four experts, where two
-// experts' operands at a time do not fit into L2: 541 us in turns, 514 in one order.
+// experts, 7168 x 4096: 1864 us, 2020 in one order; 16384 rows of four experts, where two
+// experts' operands at a time do not fit into L2: 557 us in turns, 526 in one order.
 //
 // Ragged edges.  Rows behind an expert's last are other experts': they fill accumulator
 // columns that are not stored.  The contraction over an expert's rows (the weights'
@@ -43,9 +43,9 @@
 // 4e-6 of a weight gradient of 4096 rows, 4e-4 of one of 65536 rows whose terms have the same
 // sign (half of fp16's last place).  So an accumulator takes 512 of the contraction, 1024 for
 // results of 16 bits, and the epilogue adds the accumulators up, rounding to nearest: 5e-7,
-// whatever the length.  (16384 rows of four experts into 7168 x 4096, fp32: 576 us, as in one
-// accumulator; 256 of the contraction at a time 2.4e-7 and 589 us.  Their forward, 7168 long in
-// 1024s, 518 us, in 512s 521, in one 511.)  The sums are in registers, or, for 16-bit results
+// whatever the length.  (16384 rows of four experts into 7168 x 4096, fp32: 570 us, as in one
+// accumulator; 256 of the contraction at a time 2.4e-7 and 2 % more.  Their forward, 7168 long
+// in 1024s, 518 us, in 512s 521, in one 511.)  The sums are in registers, or, for 16-bit results
 // beside loading warps, which leave none for 256 rows, in the other accumulator's place: a
 // unit of more than 1024 keeps to one.
 //
@@ -880,8 +880,8 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
     }
   } else if (warp > 1 && warp < 2 + kEpi) {
     // A lane holds an output column; a warp takes 32 rows in kStep of its quarter's 32 columns.
-    // (Sixteen warps, half of the sums each, are slower: 16384 rows of four experts into
-    // 7168 x 4096 711 us, not 653.)
+    // (Sixteen warps, half of the sums each, were 9 % slower for 16384 rows of four experts
+    // into 7168 x 4096.)
     constexpr int kStep = 8 * kEpi;
     const int q = warp & 3, c_first = 32 * ((warp - 2) >> 2);
     const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16);
